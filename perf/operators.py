@@ -295,10 +295,10 @@ def run(s):
         return out, idx, gates
     if not kept:
         kept["ws"] = moe.Workspace(moe.balance_workspace_size(case["T"], case["E"], case["S"]))
-    loss, counts, lse = moe.moe_balance(s["logits"], s["idx"], s["off"], s["coef"], ws=kept["ws"])
-    d = moe.moe_balance_backward(s["logits"], lse, counts, s["off"], s["coef"], s["d_loss"],
-                                 topk_idx=s["idx"], gates=s["gates"], d_gates=s["d_gates"],
-                                 ws=kept["ws"])
+    loss, counts, stats = moe.moe_balance(s["logits"], s["idx"], s["off"], s["coef"], ws=kept["ws"])
+    d = moe.moe_balance_backward(s["logits"], stats, counts, case["k"], s["off"], s["coef"],
+                                 s["d_loss"], topk_idx=s["idx"], gates=s["gates"],
+                                 d_gates=s["d_gates"])
     return loss, counts, d
 
 
