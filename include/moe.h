@@ -336,6 +336,128 @@ moe_status moe_forward_cached(moe_cache* cache, const moe_shape* shape, int32_t 
                               moe_bf16* const* out, void* ws, size_t ws_bytes,
                               moe_stream_t compute, moe_stream_t copy);
 
+/* ---- 8-bit experts ------------------------------------------------------ */
+
+/* The layer on experts held in 8-bit floating point: half the HBM and half
+ * the decode stream of bf16, and the tensor cores' 8-bit rate.  Not on the
+ * pages: their quantised experts are another format.
+ *
+ * Format: a value is e4m3 (one byte, largest finite value 448) and belongs to
+ * a block of 128 with one scale byte b, standing for 2^(b - 127).  Blocks are
+ * 1 x 128 along a row of activations and 128 x 128 in a weight matrix.  A
+ * block's scale is the smallest power of two, at least 2^-127, for which no
+ * finite value of the block exceeds 448 times it; values are rounded to
+ * nearest, ties to even; a value that is not finite becomes NaN and does not
+ * count towards its block's scale.  Scales are powers of two because the
+ * tensor cores apply such scales themselves; byte 255 stands for NaN. */
+
+/* Quantises rows x [rows, K] bf16 into q [rows, K] e4m3 and scales
+ * [rows, K / 128].  K: a positive multiple of 128, at most 16384; rows == 0 is
+ * a no-op. */
+moe_status moe_quantize_rows(const moe_bf16* x, int32_t rows, int32_t K, uint8_t* q,
+                             uint8_t* scales, moe_stream_t stream);
+
+/* Quantises n matrices W [n, N, K] bf16 into q [n, N, K] e4m3 and scales
+ * [n, N / 128, K / 128].  N and K: positive multiples of 128, at most 16384. */
+moe_status moe_quantize_weights(const moe_bf16* W, int32_t n, int32_t N, int32_t K, uint8_t* q,
+                                uint8_t* scales, moe_stream_t stream);
+
+/* Bytes of workspace moe_grouped_gemm_fp8 needs (0 for invalid arguments). */
+size_t moe_grouped_gemm_fp8_workspace_size(int32_t rows, int32_t E);
+
+/* Grouped matrix product of 8-bit operands: for rows offsets[e] <= p <
+ * offsets[e + 1] of group e
+ *   y[p, n] = bf16( sum_k x[p, k] W[e, n, k] ),
+ * each operand multiplied by its block's scale, fp32 accumulation, one
+ * rounding at the end.  E = 1 is the dense product x W^T.
+ *   x [rows, K] e4m3, x_scales [rows, K / 128]; W [E, N, K] e4m3, W_scales
+ *   [E, N / 128, K / 128]; offsets [E + 1] ascending with offsets[0] = 0 and
+ *   offsets[E] = rows, groups may be empty; y [rows, N] bf16 written.
+ *   N and K: positive multiples of 128, at most 16384; E <= 1024.
+ *   ws: moe_grouped_gemm_fp8_workspace_size() bytes, initialised once with
+ *   moe_workspace_init().  Offsets that are not as stated set
+ *   MOE_ERR_BAD_INDEX in the workspace status; rows of no group are then not
+ *   written.
+ * The gradient of x is the same product with each W[e] transposed (128 x 128
+ * blocks transpose into blocks of the same scale) and the quantised gradient
+ * of y. */
+moe_status moe_grouped_gemm_fp8(const uint8_t* x, const uint8_t* x_scales, int32_t rows,
+                                const int32_t* offsets, int32_t E, int32_t N, int32_t K,
+                                const uint8_t* W, const uint8_t* W_scales, moe_bf16* y, void* ws,
+                                size_t ws_bytes, moe_stream_t stream);
+
+/* A layer's experts in 8 bits: gate, up [E, I, H] and down [E, H, I] e4m3 with
+ * scales [E, I / 128, H / 128] and [E, H / 128, I / 128] (device pointers). */
+typedef struct {
+    const uint8_t* gate;
+    const uint8_t* gate_scales;
+    const uint8_t* up;
+    const uint8_t* up_scales;
+    const uint8_t* down;
+    const uint8_t* down_scales;
+} moe_fp8_experts;
+
+/* moe_expert_ffn on 8-bit experts.  x [T, H] bf16 is quantised by rows, the
+ * intermediate silu(gate) * up by rows from fp32, and
+ *   y_sorted[p] = bf16( W_down[e] . quantised( silu(W_gate[e] . x) * (W_up[e] . x) ) )
+ * with fp32 accumulation.  perm, offsets as moe_permute wrote them; the
+ * shape's fat_threshold and thin_mma_min do not apply.  ws:
+ * moe_expert_ffn_fp8_workspace_size() bytes, initialised once with
+ * moe_workspace_init(). */
+size_t moe_expert_ffn_fp8_workspace_size(const moe_shape* shape);
+moe_status moe_expert_ffn_fp8(const moe_shape* shape, const moe_bf16* x, const int32_t* perm,
+                              const int32_t* offsets, const moe_fp8_experts* experts,
+                              moe_bf16* y_sorted, void* ws, size_t ws_bytes,
+                              moe_stream_t stream);
+
+/* moe_forward on 8-bit experts: route -> permute -> 8-bit experts -> combine
+ * on one stream, no host synchronisation.  Arguments as moe_forward; ws:
+ * moe_fp8_workspace_size() bytes, initialised once with moe_workspace_init(). */
+size_t moe_fp8_workspace_size(const moe_shape* shape);
+moe_status moe_forward_fp8(const moe_shape* shape, const float* logits, const moe_bf16* x,
+                           const moe_fp8_experts* experts, moe_bf16* out, int32_t* topk_idx,
+                           float* gates, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---- the router's balance loss ------------------------------------------- */
+
+/* Per-expert counts and the balance loss of packed sequences, and the
+ * gradient of the router's logits.  With p_t = softmax(logits[t]) over all E
+ * experts, sequence s the n_s tokens seq_offsets[s] <= t < seq_offsets[s + 1],
+ * T' = sum_s n_s and counts[s, e] the slots that s routes to e:
+ *   loss = coef * sum_s (n_s / T') sum_e f_se P_se,
+ *   f_se = E counts[s, e] / (k n_s),   P_se = mean of p_te over the sequence.
+ * Evenly spread slots give loss = coef.  Sequences may be empty, and tokens
+ * outside [seq_offsets[0], seq_offsets[S]) (padding) take no part.  A token
+ * whose logits are all -inf has no probability anywhere: it adds nothing to P
+ * and has no gradient from the loss.  The pages do not train their model.
+ *   logits [T, E] fp32, topk_idx [T, k] int32 as moe_route wrote them;
+ *   seq_offsets [S + 1] int32 ascending in [0, T], or NULL with S = 1 (one
+ *   sequence of all tokens); loss [1] fp32, counts [S, E] int32 and stats
+ *   [T, 2] fp32 (for the backward call) written.  ws:
+ *   moe_balance_workspace_size() bytes, initialised once with
+ *   moe_workspace_init().  Sums are fp32 in a fixed order: repeated runs give
+ *   the same bits.  A routed index outside [0, E) is not counted and sets
+ *   MOE_ERR_BAD_INDEX in the workspace status. */
+size_t moe_balance_workspace_size(int32_t T, int32_t E, int32_t S);
+moe_status moe_balance(const float* logits, const int32_t* topk_idx, int32_t T, int32_t E,
+                       int32_t k, const int32_t* seq_offsets, int32_t S, float coef, float* loss,
+                       int32_t* counts, float* stats, void* ws, size_t ws_bytes,
+                       moe_stream_t stream);
+
+/* d_logits [T, E] fp32, written:
+ *   d_loss p_te (a_se - sum_j p_tj a_sj),  a_se = coef E counts[s, e] / (k n_s T')
+ * for the tokens of a sequence (0 for the others; the counts carry no
+ * gradient), plus, when topk_idx, gates and d_gates [T, k] are given (all or
+ * none), the gradient of the router's gates,
+ *   g_tj (d_gates_tj - sum_i g_ti d_gates_ti)  at expert topk_idx[t, j].
+ * logits, seq_offsets, k, S and coef as in the moe_balance call that wrote
+ * stats and counts; d_loss [1] fp32 on the device, NULL for 1. */
+moe_status moe_balance_backward(const float* logits, const float* stats, const int32_t* counts,
+                                const int32_t* seq_offsets, int32_t T, int32_t E, int32_t k,
+                                int32_t S, float coef, const float* d_loss,
+                                const int32_t* topk_idx, const float* gates, const float* d_gates,
+                                float* d_logits, moe_stream_t stream);
+
 /* ---- activations in host memory --------------------------------------- */
 
 /* The layer on host-resident activations, as a serving process feeds it:

@@ -12,4 +12,8 @@ from .binding import (  # noqa: F401
     PROFILE_EVENTS, PROFILE_STAGES, forward_launches, Stager, layer_weight_bytes,
     pack_layer_weights, Pipe, pipe_workspace_size, DecodeGraph, ExpertCache,
     debug_set_wait_limit,
+    moe_quantize_rows, moe_quantize_weights, moe_grouped_gemm_fp8,
+    grouped_gemm_fp8_workspace_size, Fp8Experts, quantize_experts, moe_expert_ffn_fp8,
+    expert_ffn_fp8_workspace_size, moe_forward_fp8, fp8_workspace_size, moe_balance,
+    moe_balance_backward, balance_workspace_size,
 )

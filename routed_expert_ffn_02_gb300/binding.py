@@ -39,7 +39,11 @@ EXPORTED = ("moe_route", "moe_permute_workspace_size", "moe_permute", "moe_permu
             "moe_workspace_status", "moe_last_error", "moe_version",
             "moe_pipe_workspace_size", "moe_pipe_create", "moe_pipe_destroy",
             "moe_forward_host", "moe_cache_bytes", "moe_cache_create", "moe_cache_destroy",
-            "moe_cache_stats", "moe_forward_cached", "moe_debug_set_wait_limit")
+            "moe_cache_stats", "moe_forward_cached", "moe_debug_set_wait_limit",
+            "moe_quantize_rows", "moe_quantize_weights", "moe_grouped_gemm_fp8_workspace_size",
+            "moe_grouped_gemm_fp8", "moe_expert_ffn_fp8_workspace_size", "moe_expert_ffn_fp8",
+            "moe_fp8_workspace_size", "moe_forward_fp8", "moe_balance_workspace_size",
+            "moe_balance", "moe_balance_backward")
 
 
 class MoeShape(ctypes.Structure):
@@ -47,6 +51,11 @@ class MoeShape(ctypes.Structure):
                 ("H", ctypes.c_int32), ("I", ctypes.c_int32),
                 ("fat_threshold", ctypes.c_int32),
                 ("thin_mma_min", ctypes.c_int32)]
+
+
+class MoeFp8Experts(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "gate_scales", "up", "up_scales",
+                                               "down", "down_scales")]
 
 
 @dataclass(frozen=True)
@@ -80,7 +89,22 @@ _i32 = ctypes.c_int32
 _sz = ctypes.c_size_t
 _SP = ctypes.POINTER(MoeShape)
 
+_WP = ctypes.POINTER(MoeFp8Experts)
+_f32 = ctypes.c_float
+
 _sig = {
+    "moe_quantize_rows": ([_P, _i32, _i32, _P, _P, _P], _i32),
+    "moe_quantize_weights": ([_P, _i32, _i32, _i32, _P, _P, _P], _i32),
+    "moe_grouped_gemm_fp8_workspace_size": ([_i32, _i32], _sz),
+    "moe_grouped_gemm_fp8": ([_P, _P, _i32, _P, _i32, _i32, _i32, _P, _P, _P, _P, _sz, _P], _i32),
+    "moe_expert_ffn_fp8_workspace_size": ([_SP], _sz),
+    "moe_expert_ffn_fp8": ([_SP, _P, _P, _P, _WP, _P, _P, _sz, _P], _i32),
+    "moe_fp8_workspace_size": ([_SP], _sz),
+    "moe_forward_fp8": ([_SP, _P, _P, _WP, _P, _P, _P, _P, _sz, _P], _i32),
+    "moe_balance_workspace_size": ([_i32, _i32, _i32], _sz),
+    "moe_balance": ([_P, _P, _i32, _i32, _i32, _P, _i32, _f32, _P, _P, _P, _P, _sz, _P], _i32),
+    "moe_balance_backward": ([_P, _P, _P, _P, _i32, _i32, _i32, _i32, _f32, _P, _P, _P, _P, _P,
+                              _P], _i32),
     "moe_route": ([_P, _i32, _i32, _i32, _P, _P, _P], _i32),
     "moe_permute_workspace_size": ([_i32, _i32, _i32], _sz),
     "moe_permute": ([_P, _i32, _i32, _i32, _P, _P, _P, _P, _P, _sz, _P], _i32),
@@ -130,6 +154,32 @@ def _ptr(t: torch.Tensor | None):
 def _host_ptr(t: torch.Tensor):
     assert not t.is_cuda and t.is_contiguous(), "expected a contiguous host tensor"
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _dtype(t: torch.Tensor, dtype, shape=None):
+    assert t.dtype == dtype, f"expected {dtype}, got {t.dtype}"
+    assert shape is None or tuple(t.shape) == tuple(shape), f"expected {shape}, got {tuple(t.shape)}"
+
+
+def _out(t: torch.Tensor | None, shape, dtype, device) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _dtype(t, dtype, shape)
+    return t
+
+
+def _fp8(q: torch.Tensor, scales: torch.Tensor, shape, scale_shape):
+    _dtype(q, torch.float8_e4m3fn, shape)
+    _dtype(scales, torch.uint8, scale_shape)
+
+
+def _sequences(seq_offsets) -> int:
+    if seq_offsets is None:
+        return 1
+    _dtype(seq_offsets, torch.int32)
+    assert seq_offsets.dim() == 1 and len(seq_offsets) >= 2, "seq_offsets is [S + 1], S >= 1"
+    return len(seq_offsets) - 1
 
 
 def _stream(stream):
@@ -509,6 +559,182 @@ class DecodeGraph:
         """Runs the captured layer on the current stream's timeline."""
         self.graph.replay()
         return self.out
+
+
+def moe_quantize_rows(x: torch.Tensor, q=None, scales=None, stream=None):
+    """x [rows, K] bf16 -> (q [rows, K] float8_e4m3fn, scales [rows, K/128]
+    uint8): one power-of-two scale 2^(byte - 127) per 128 values of a row."""
+    rows, K = x.shape
+    _dtype(x, torch.bfloat16)
+    q = _out(q, (rows, K), torch.float8_e4m3fn, x.device)
+    scales = _out(scales, (rows, K // 128), torch.uint8, x.device)
+    _check(_lib.moe_quantize_rows(_ptr(x), rows, K, _ptr(q), _ptr(scales), _stream(stream)),
+           "moe_quantize_rows")
+    return q, scales
+
+
+def moe_quantize_weights(W: torch.Tensor, q=None, scales=None, stream=None):
+    """W [E, N, K] bf16 -> (q [E, N, K] float8_e4m3fn, scales [E, N/128, K/128]
+    uint8): one power-of-two scale per 128 x 128 block."""
+    E, N, K = W.shape
+    _dtype(W, torch.bfloat16)
+    q = _out(q, (E, N, K), torch.float8_e4m3fn, W.device)
+    scales = _out(scales, (E, N // 128, K // 128), torch.uint8, W.device)
+    _check(_lib.moe_quantize_weights(_ptr(W), E, N, K, _ptr(q), _ptr(scales), _stream(stream)),
+           "moe_quantize_weights")
+    return q, scales
+
+
+def grouped_gemm_fp8_workspace_size(rows: int, E: int) -> int:
+    n = _lib.moe_grouped_gemm_fp8_workspace_size(rows, E)
+    if n == 0:
+        raise MoeError(1, "moe_grouped_gemm_fp8_workspace_size")
+    return n
+
+
+def moe_grouped_gemm_fp8(x, x_scales, offsets, W, W_scales, y=None, ws: Workspace | None = None,
+                         stream=None):
+    """y[p] = x[p] . W[e]^T for the rows offsets[e] <= p < offsets[e + 1], both
+    operands 8-bit with block scales (as moe_quantize_rows / _weights give
+    them); y [rows, N] bf16.  E = 1 (offsets [0, rows]) is the dense product."""
+    rows, K = x.shape
+    E, N, _ = W.shape
+    _fp8(x, x_scales, (rows, K), (rows, K // 128))
+    _fp8(W, W_scales, (E, N, K), (E, N // 128, K // 128))
+    _dtype(offsets, torch.int32, (E + 1,))
+    y = _out(y, (rows, N), torch.bfloat16, x.device)
+    ws = ws or Workspace(grouped_gemm_fp8_workspace_size(rows, E), x.device, stream)
+    _check(_lib.moe_grouped_gemm_fp8(_ptr(x), _ptr(x_scales), rows, _ptr(offsets), E, N, K, _ptr(W),
+                                     _ptr(W_scales), _ptr(y), ws.ptr, ws.nbytes, _stream(stream)),
+           "moe_grouped_gemm_fp8")
+    return y
+
+
+@dataclass(frozen=True)
+class Fp8Experts:
+    """A layer's experts in 8 bits: gate, up [E, I, H] and down [E, H, I]
+    float8_e4m3fn, each with its scales [E, rows/128, cols/128] uint8."""
+    gate: torch.Tensor
+    gate_scales: torch.Tensor
+    up: torch.Tensor
+    up_scales: torch.Tensor
+    down: torch.Tensor
+    down_scales: torch.Tensor
+
+    def c(self, shape: Shape) -> MoeFp8Experts:
+        E, H, I = shape.E, shape.H, shape.I
+        _fp8(self.gate, self.gate_scales, (E, I, H), (E, I // 128, H // 128))
+        _fp8(self.up, self.up_scales, (E, I, H), (E, I // 128, H // 128))
+        _fp8(self.down, self.down_scales, (E, H, I), (E, H // 128, I // 128))
+        return MoeFp8Experts(*[_ptr(t) for t in (self.gate, self.gate_scales, self.up,
+                                                 self.up_scales, self.down, self.down_scales)])
+
+
+def quantize_experts(W_gate, W_up, W_down, stream=None) -> Fp8Experts:
+    """bf16 experts (the layouts of moe_forward) -> Fp8Experts."""
+    return Fp8Experts(*moe_quantize_weights(W_gate, stream=stream),
+                      *moe_quantize_weights(W_up, stream=stream),
+                      *moe_quantize_weights(W_down, stream=stream))
+
+
+def expert_ffn_fp8_workspace_size(shape: Shape) -> int:
+    n = _lib.moe_expert_ffn_fp8_workspace_size(ctypes.byref(shape.c()))
+    if n == 0:
+        raise MoeError(1, "moe_expert_ffn_fp8_workspace_size")
+    return n
+
+
+def moe_expert_ffn_fp8(shape: Shape, x, perm, offsets, experts: Fp8Experts, y_sorted=None,
+                       ws: Workspace | None = None, stream=None):
+    """moe_expert_ffn on 8-bit experts (perm, offsets from moe_permute)."""
+    _dtype(x, torch.bfloat16, (shape.T, shape.H))
+    _dtype(perm, torch.int32, (shape.P,))
+    _dtype(offsets, torch.int32, (shape.E + 1,))
+    y_sorted = _out(y_sorted, (shape.P, shape.H), torch.bfloat16, x.device)
+    ws = ws or Workspace(expert_ffn_fp8_workspace_size(shape), x.device, stream)
+    w = experts.c(shape)
+    _check(_lib.moe_expert_ffn_fp8(ctypes.byref(shape.c()), _ptr(x), _ptr(perm), _ptr(offsets),
+                                   ctypes.byref(w), _ptr(y_sorted), ws.ptr, ws.nbytes,
+                                   _stream(stream)), "moe_expert_ffn_fp8")
+    return y_sorted
+
+
+def fp8_workspace_size(shape: Shape) -> int:
+    n = _lib.moe_fp8_workspace_size(ctypes.byref(shape.c()))
+    if n == 0:
+        raise MoeError(1, "moe_fp8_workspace_size")
+    return n
+
+
+def moe_forward_fp8(shape: Shape, logits, x, experts: Fp8Experts, out=None, topk_idx=None,
+                    gates=None, ws: Workspace | None = None, stream=None):
+    """moe_forward on 8-bit experts."""
+    _dtype(logits, torch.float32, (shape.T, shape.E))
+    _dtype(x, torch.bfloat16, (shape.T, shape.H))
+    if topk_idx is not None:
+        _dtype(topk_idx, torch.int32, (shape.T, shape.k))
+    if gates is not None:
+        _dtype(gates, torch.float32, (shape.T, shape.k))
+    out = _out(out, (shape.T, shape.H), torch.bfloat16, x.device)
+    ws = ws or Workspace(fp8_workspace_size(shape), x.device, stream)
+    w = experts.c(shape)
+    _check(_lib.moe_forward_fp8(ctypes.byref(shape.c()), _ptr(logits), _ptr(x), ctypes.byref(w),
+                                _ptr(out), _ptr(topk_idx), _ptr(gates), ws.ptr, ws.nbytes,
+                                _stream(stream)), "moe_forward_fp8")
+    return out
+
+
+def balance_workspace_size(T: int, E: int, S: int = 1) -> int:
+    n = _lib.moe_balance_workspace_size(T, E, S)
+    if n == 0:
+        raise MoeError(1, "moe_balance_workspace_size")
+    return n
+
+
+def moe_balance(logits, topk_idx, seq_offsets=None, coef: float = 1.0, loss=None, counts=None,
+                stats=None, ws: Workspace | None = None, stream=None):
+    """The router's balance loss over packed sequences (seq_offsets int32
+    [S + 1], None: one sequence of all tokens).  Returns (loss [] fp32, counts
+    [S, E] int32, stats [T, 2] fp32 for moe_balance_backward)."""
+    T, E = logits.shape
+    _dtype(logits, torch.float32)
+    k = topk_idx.shape[1]
+    _dtype(topk_idx, torch.int32, (T, k))
+    S = _sequences(seq_offsets)
+    dev = logits.device
+    loss = _out(loss, (), torch.float32, dev)
+    counts = _out(counts, (S, E), torch.int32, dev)
+    stats = _out(stats, (T, 2), torch.float32, dev)
+    ws = ws or Workspace(balance_workspace_size(T, E, S), dev, stream)
+    _check(_lib.moe_balance(_ptr(logits), _ptr(topk_idx), T, E, k, _ptr(seq_offsets), S, coef,
+                            _ptr(loss), _ptr(counts), _ptr(stats), ws.ptr, ws.nbytes,
+                            _stream(stream)), "moe_balance")
+    return loss, counts, stats
+
+
+def moe_balance_backward(logits, stats, counts, k: int, seq_offsets=None, coef: float = 1.0,
+                         d_loss=None, topk_idx=None, gates=None, d_gates=None, d_logits=None,
+                         stream=None):
+    """Gradient of the logits from the balance loss (d_loss: fp32 scalar on the
+    device, None for 1) and, where topk_idx, gates and d_gates are given, from
+    the router's gates.  Returns d_logits [T, E] fp32."""
+    T, E = logits.shape
+    _dtype(logits, torch.float32)
+    S = _sequences(seq_offsets)
+    _dtype(stats, torch.float32, (T, 2))
+    _dtype(counts, torch.int32, (S, E))
+    if d_loss is not None:
+        _dtype(d_loss, torch.float32)
+        assert d_loss.numel() == 1, "d_loss is one number"
+    for t, dt in ((topk_idx, torch.int32), (gates, torch.float32), (d_gates, torch.float32)):
+        if t is not None:
+            _dtype(t, dt, (T, k))
+    d_logits = _out(d_logits, (T, E), torch.float32, logits.device)
+    _check(_lib.moe_balance_backward(_ptr(logits), _ptr(stats), _ptr(counts), _ptr(seq_offsets), T,
+                                     E, k, S, coef, _ptr(d_loss), _ptr(topk_idx), _ptr(gates),
+                                     _ptr(d_gates), _ptr(d_logits), _stream(stream)),
+           "moe_balance_backward")
+    return d_logits
 
 
 def raw_lib():

@@ -122,6 +122,13 @@ moe_status check_shape(const moe_shape* sh) {
 
 moe_status moe::check_shape_status(const moe_shape* shape) { return check_shape(shape); }
 
+moe_status moe::current_device(int* num_sms) {
+    DeviceInfo dev;
+    const moe_status st = device_info(&dev);
+    if (st == MOE_OK) *num_sms = dev.num_sms;
+    return st;
+}
+
 
 namespace {
 

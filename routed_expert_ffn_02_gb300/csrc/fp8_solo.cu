@@ -1,0 +1,397 @@
+// fp8_solo.cu -- one-CTA grouped products of 8-bit block-scaled operands:
+// row tiles of at most 128 rows (experts with few rows, where the weights'
+// bytes count).
+//
+//   plain:    y[rows, n0:n0+256] = bf16( A W_e[n0:n0+256]^T )
+//   gate/up:  h[rows, n0:n0+128] = quantised( silu(A Wg_e^T) * (A Wu_e^T) ),
+//             the gate and up rows of the same 128 columns back to back in
+//             one N = 256 MMA; a thread holds a row's 128 columns, which are
+//             one block of 128, so it quantises them by itself.
+//
+// A is [rows, K] e4m3 with one scale byte per 128 of K, W [E, N, K] e4m3 with
+// one per 128 x 128; the tensor core applies both (fp8.cuh).
+//
+// Persistent CTAs, one per SM, warp-specialised: warp 0 TMA producer (one
+// lane), warp 1 MMA issuer (M = 128, N = 256, K = 32), warp 2 TMEM allocator,
+// warp 3 scale producer, warps 4-7 epilogue.  A ring of 4 stages of 128 of K
+// (16 KB of A, 32 KB of W) and a ring of 4 scale slots, each the scale words
+// of 512 of K: 128 rows of A and 256 rows of W, written to shared memory by
+// warp 3 and copied to TMEM by the MMA lane.  Slot i of the shared ring goes
+// to slot i of the TMEM ring, and a slot is refilled only after the MMAs that
+// read it have completed (its "empty" barrier), so no copy to TMEM overtakes
+// an MMA.  Every wait is bounded; on expiry the kernel records
+// MOE_ERR_TIMEOUT, drains its own copies and MMAs, frees TMEM and returns.
+#include <cuda.h>
+
+#include "fp8.cuh"
+#include "moe_internal.cuh"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace {
+
+using namespace ptx;
+using namespace tc;
+using fp8::kBlock;
+using fp8::kGroupBlocks;
+using fp8::kScaleBytes;
+using fp8::kScaleCols;
+
+constexpr int BM = kTileM;                      // 128 rows per tile
+constexpr int BN = 256;                         // MMA N
+constexpr int STAGES = 4;
+constexpr int A_BYTES = BM * kBlock;            // 16 KB
+constexpr int B_BYTES = BN * kBlock;            // 32 KB
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int SLOTS = 4;                        // scale ring
+constexpr int SLOT_BYTES = 3 * kScaleBytes;     // A, W rows 0-127, W rows 128-255
+constexpr int SLOT_COLS = 3 * kScaleCols;
+constexpr int TMEM_COLS = 512;
+constexpr int SCALE_COL = BN;                   // TMEM column of the scale ring
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SLOTS * SLOT_BYTES + 1024 + 256;
+constexpr uint32_t kIdesc = fp8::make_idesc(BM, BN);
+
+template <bool kGated>
+__global__ void __launch_bounds__(256, 1)
+fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
+                const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
+                Fp8Args args) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* base_ptr = smem_raw + (base - raw);
+    const uint32_t slots = base + STAGES * STAGE_BYTES;
+    const uint32_t bars = slots + SLOTS * SLOT_BYTES;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (STAGES + s); };
+    auto sfull_bar = [&](int s) { return bars + 8u * (2 * STAGES + s); };
+    auto sempty_bar = [&](int s) { return bars + 8u * (2 * STAGES + SLOTS + s); };
+    const uint32_t tfull_bar = bars + 8u * (2 * STAGES + 2 * SLOTS);
+    const uint32_t tempty_bar = tfull_bar + 8u;
+    const uint32_t done_bar = tfull_bar + 16u;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (done_bar + 8u - base));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    grid_dep_wait();
+    grid_dep_launch();
+    // Tiles: the pair list's (when no pair kernel runs), the solo tiles, the thin tiles.
+    const int n_pair = args.with_pairs ? args.hdr->n_fat_tiles : 0;
+    const int n_solo = n_pair + args.hdr->n_solo;
+    const int total = (n_solo + args.hdr->n_thin_mma) * args.n_blocks_n;
+    auto tile_at = [&](int i) {
+        return i < n_pair ? args.tiles[i]
+               : i < n_solo ? args.solo_tiles[i - n_pair] : args.thin_tiles[i - n_solo];
+    };
+    // Items go round-robin to the first `active` CTAs, as many as keep every
+    // wave full (see the bf16 one-CTA GEMM).
+    const int waves = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int active = waves > 0 ? (total + waves - 1) / waves : 0;
+    if ((int)blockIdx.x >= active) return;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(sfull_bar(s), 1);
+            mbar_init(sempty_bar(s), 1);
+        }
+        mbar_init(tfull_bar, 1);
+        mbar_init(tempty_bar, 128);
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_map(&tmA);
+        prefetch_map(&tmA32);
+        prefetch_map(&tmB0);
+        if (kGated) prefetch_map(&tmB1);
+    }
+    if (warp == 2) tmem_alloc(smem_u32(tmem_holder), TMEM_COLS);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    const int k_blocks = args.k_blocks;
+
+    if (warp == 0 && lane == 0) {
+        // ---------------- TMA producer ----------------
+        int stage = 0;
+        uint32_t phase = 0;
+        int pending[STAGES];
+        for (int s = 0; s < STAGES; ++s) pending[s] = -1;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < total; t += active) {
+            const FatTile ft = tile_at(t / args.n_blocks_n);
+            const int brow = ft.expert * args.n_rows + (t % args.n_blocks_n) * (kGated ? 128 : BN);
+            const bool small = ft.rows <= kThinMaxTokens;
+            const uint32_t bytes = (small ? kThinMaxTokens * kBlock : A_BYTES) + B_BYTES;
+            for (int kb = 0; kb < k_blocks; ++kb) {
+                if (!mbar_wait_for(empty_bar(stage), phase ^ 1u, args.wait_cycles, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sa = base + stage * STAGE_BYTES;
+                const uint32_t sb = sa + A_BYTES;
+                mbar_expect_tx(full_bar(stage), bytes);
+                tma_load_2d(sa, small ? &tmA32 : &tmA, full_bar(stage), kb * kBlock, ft.row0);
+                tma_load_2d(sb, &tmB0, full_bar(stage), kb * kBlock, brow);
+                if (kGated) tma_load_2d(sb + B_BYTES / 2, &tmB1, full_bar(stage), kb * kBlock, brow);
+                pending[stage] = (int)phase;
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            set_status(args.hdr, MOE_ERR_TIMEOUT);
+            for (int s = 0; s < STAGES; ++s)
+                if (pending[s] >= 0) (void)mbar_wait(full_bar(s), (uint32_t)pending[s]);
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ---------------- MMA issuer ----------------
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, sphase = 0;
+        int it = 0;
+        bool ok = true;
+        bool issued = false;
+        for (int t = blockIdx.x; ok && t < total; t += active, ++it) {
+            if (!mbar_wait_for(tempty_bar, (uint32_t)(it & 1) ^ 1u, args.wait_cycles, abort_flag)) {
+                ok = false;
+                break;
+            }
+            fence_after();
+            for (int kb = 0; kb < k_blocks; ++kb) {
+                const uint32_t sc = tmem_base + SCALE_COL + slot * SLOT_COLS;
+                if (kb % kGroupBlocks == 0) {
+                    if (!mbar_wait_for(sfull_bar(slot), sphase, args.wait_cycles, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        fp8::scale_copy(sc + i * kScaleCols,
+                                        fp8::scale_desc(slots + slot * SLOT_BYTES + i * kScaleBytes));
+                    issued = true;
+                }
+                if (!mbar_wait_for(full_bar(stage), phase, args.wait_cycles, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+                const uint32_t sa = base + stage * STAGE_BYTES;
+                const uint64_t ad = sw128_desc(sa);
+                const uint64_t bd = sw128_desc(sa + A_BYTES);
+                const uint32_t idesc = fp8::with_scale_byte(kIdesc, kb % kGroupBlocks);
+#pragma unroll
+                for (int kk = 0; kk < kBlock / 32; ++kk)   // +32 bytes per K step
+                    fp8::mma(tmem_base, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), idesc, sc,
+                             sc + kScaleCols, (kb > 0 || kk > 0) ? 1u : 0u);
+                commit(empty_bar(stage));
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                if (kb % kGroupBlocks == kGroupBlocks - 1 || kb == k_blocks - 1) {
+                    commit(sempty_bar(slot));
+                    if (++slot == SLOTS) {
+                        slot = 0;
+                        sphase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) break;
+            commit(tfull_bar);
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            set_status(args.hdr, MOE_ERR_TIMEOUT);
+            if (issued) {
+                commit(done_bar);
+                (void)mbar_wait(done_bar, 0);
+            }
+        }
+    } else if (warp == 3) {
+        // ---------------- scale producer ----------------
+        // Lane l holds rows l, l + 32, l + 64, l + 96 of the A tile; every
+        // 128 rows of W share one word, so its 512 bytes repeat it.
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const int groups = (k_blocks + kGroupBlocks - 1) / kGroupBlocks;
+        for (int t = blockIdx.x; ok && t < total; t += active) {
+            const FatTile ft = tile_at(t / args.n_blocks_n);
+            const int nt = t % args.n_blocks_n;
+            const uint8_t* ra[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // rows past the tile's only scale rows of D that are not stored
+                const int r = min(ft.row0 + lane + 32 * i, args.rows - 1);
+                ra[i] = args.a_scales + (int64_t)r * k_blocks;
+            }
+            const int64_t eb = (int64_t)ft.expert * (args.n_rows / kBlock);
+            const int last = args.n_rows / kBlock - 1;   // N is a multiple of 128, not of 256
+            const uint8_t* rb0 =
+                args.b0_scales + (eb + (kGated ? nt : min(2 * nt, last))) * k_blocks;
+            const uint8_t* rb1 =
+                kGated ? args.b1_scales + (eb + nt) * k_blocks
+                       : args.b0_scales + (eb + min(2 * nt + 1, last)) * k_blocks;
+            for (int g = 0; g < groups; ++g) {
+                uint32_t a[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = fp8::scale_word(ra[i], g, k_blocks);
+                const uint32_t b0 = fp8::scale_word(rb0, g, k_blocks);
+                const uint32_t b1 = fp8::scale_word(rb1, g, k_blocks);
+                if (!__all_sync(0xffffffffu, mbar_wait_for(sempty_bar(slot), phase ^ 1u,
+                                                           args.wait_cycles, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = slots + slot * SLOT_BYTES + lane * 16u;
+                st_shared_v4(dst, a[0], a[1], a[2], a[3]);
+                st_shared_v4(dst + kScaleBytes, b0, b0, b0, b0);
+                st_shared_v4(dst + 2 * kScaleBytes, b1, b1, b1, b1);
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sfull_bar(slot));
+                if (++slot == SLOTS) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            *abort_flag = 1;
+            set_status(args.hdr, MOE_ERR_TIMEOUT);
+        }
+    } else if (warp >= 4) {
+        // ---------------- epilogue ----------------
+        const int ew = warp - 4;   // TMEM lanes 32*ew .. 32*ew+31
+        const int row = ew * 32 + lane;
+        int it = 0;
+        for (int t = blockIdx.x; t < total; t += active, ++it) {
+            // the whole warp decides together (tcgen05.ld below is warp-wide)
+            if (!__all_sync(0xffffffffu, mbar_wait_for(tfull_bar, (uint32_t)(it & 1),
+                                                       args.wait_cycles, abort_flag))) {
+                *abort_flag = 1;
+                set_status(args.hdr, MOE_ERR_TIMEOUT);
+                break;
+            }
+            fence_after();
+            const FatTile ft = tile_at(t / args.n_blocks_n);
+            const int nt = t % args.n_blocks_n;
+            const int64_t out_row = (int64_t)ft.row0 + row;
+            const uint32_t taddr = tmem_base + ((uint32_t)(ew * 32) << 16);
+            if (ew * 32 < ft.rows) {   // uniform over the warp
+                if (kGated) {
+                    float h[kBlock];
+                    float m = 0.f;
+#pragma unroll
+                    for (int c = 0; c < kBlock; c += 32) {
+                        uint32_t g[32], u[32];
+                        tmem_ld32(taddr + c, g);
+                        tmem_ld32(taddr + 128 + c, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) {
+                            h[c + q] = swiglu(__uint_as_float(g[q]), __uint_as_float(u[q]));
+                            m = fmaxf(m, fp8::finite_abs(h[c + q]));
+                        }
+                    }
+                    const uint32_t sb = fp8::scale_byte(m);
+                    const float inv = fp8::inverse_scale(sb);
+                    if (row < ft.rows) {
+                        uint4* dst = reinterpret_cast<uint4*>(args.out_q + out_row * args.ld_out +
+                                                              (int64_t)nt * kBlock);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float* p = h + 16 * q + 4 * i;
+                                v[i] = fp8::pack_e4m3x4(fp8::scaled(p[0], inv), fp8::scaled(p[1], inv),
+                                                        fp8::scaled(p[2], inv), fp8::scaled(p[3], inv));
+                            }
+                            dst[q] = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                        args.out_scales[out_row * (args.ld_out / kBlock) + nt] = (uint8_t)sb;
+                    }
+                } else {
+                    __nv_bfloat16* dst = args.out + out_row * args.ld_out + (int64_t)nt * BN;
+                    const int cols = min(BN, (int)args.ld_out - nt * BN);
+#pragma unroll 1
+                    for (int c = 0; c < cols; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(taddr + c, v);
+                        tmem_ld_wait();
+                        if (row < ft.rows) {
+                            uint4* d4 = reinterpret_cast<uint4*>(dst + c);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                uint32_t o[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    o[i] = pack_bf16(__uint_as_float(v[8 * q + 2 * i]),
+                                                     __uint_as_float(v[8 * q + 2 * i + 1]));
+                                d4[q] = make_uint4(o[0], o[1], o[2], o[3]);
+                            }
+                        }
+                    }
+                }
+            }
+            fence_before();
+            mbar_arrive(tempty_bar);
+        }
+    }
+
+    fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        fence_after();
+        tmem_dealloc(tmem_base, TMEM_COLS);
+    }
+}
+
+template <bool kGated>
+cudaError_t set_smem_attr() {
+    static std::atomic<int> done[kMaxDevices];
+    return smem_limit_once(fp8_solo_kernel<kGated>, SMEM_BYTES, done);
+}
+
+template <bool kGated>
+cudaError_t launch(const uint8_t* a, int64_t rows, const uint8_t* b0, const uint8_t* b1,
+                   const Fp8Args& args, int E, int num_sms, cudaStream_t s) {
+    const uint64_t K = (uint64_t)args.k_blocks * kBlock;
+    CUtensorMap mA, mA32, mB0, mB1;
+    cudaError_t e;
+    if ((e = make_tma_map_u8(&mA, a, (uint64_t)rows, K, BM)) != cudaSuccess) return e;
+    if ((e = make_tma_map_u8(&mA32, a, (uint64_t)rows, K, kThinMaxTokens)) != cudaSuccess) return e;
+    const uint32_t box = kGated ? 128 : 256;
+    if ((e = make_tma_map_u8(&mB0, b0, (uint64_t)E * args.n_rows, K, box)) != cudaSuccess) return e;
+    if ((e = make_tma_map_u8(&mB1, b1, (uint64_t)E * args.n_rows, K, box)) != cudaSuccess) return e;
+    if ((e = set_smem_attr<kGated>()) != cudaSuccess) return e;
+    return launch_pdl(fp8_solo_kernel<kGated>, dim3(num_sms), dim3(256), SMEM_BYTES, s, mA, mA32,
+                      mB0, mB1, args);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_solo_gate_up(const uint8_t* a, int64_t rows, const uint8_t* b0,
+                                    const uint8_t* b1, const Fp8Args& args, int E, int num_sms,
+                                    cudaStream_t s) {
+    return launch<true>(a, rows, b0, b1, args, E, num_sms, s);
+}
+cudaError_t launch_fp8_solo(const uint8_t* a, int64_t rows, const uint8_t* b, const Fp8Args& args,
+                            int E, int num_sms, cudaStream_t s) {
+    return launch<false>(a, rows, b, b, args, E, num_sms, s);
+}
+
+}  // namespace moe

@@ -328,6 +328,66 @@ cudaError_t launch_combine(const __nv_bfloat16* y_sorted, const int32_t* inv_per
                            const float* gates, int T, int k, int H,
                            __nv_bfloat16* out, int num_sms, cudaStream_t s);
 
+// ---- 8-bit operands (fp8.cuh) ----
+
+// Quantises x [rows, K]: row r to row r of q / scales (dst == nullptr), or to
+// rows dst[r * k .. r * k + k), skipping positions outside [0, P).
+cudaError_t launch_quantize_rows(const __nv_bfloat16* x, int64_t rows, int K, const int32_t* dst,
+                                 int k, int64_t P, uint8_t* q, uint8_t* scales, int num_sms,
+                                 cudaStream_t s);
+// Quantises n matrices [N, K] in blocks of 128 x 128.
+cudaError_t launch_quantize_matrices(const __nv_bfloat16* w, int64_t n, int N, int K, uint8_t* q,
+                                     uint8_t* scales, cudaStream_t s);
+// inv[perm[p]] = p for the slots of perm [P] inside [0, P).
+cudaError_t launch_invert_perm(const int32_t* perm, int64_t P, int32_t* inv, int num_sms,
+                               cudaStream_t s);
+
+// Planner over caller-given group offsets [E + 1] of `rows` rows: the tile
+// lists of launch_plan with the offsets forced to be ascending inside
+// [0, rows] (MOE_ERR_BAD_INDEX recorded if they were not, or do not start at 0
+// and end at rows).
+cudaError_t launch_plan_groups(const int32_t* offsets, int rows, int E, const Plan& plan,
+                               cudaStream_t s);
+
+// Grouped product of 8-bit operands over the planner's tiles.
+struct Fp8Args {
+    const FatTile* tiles;        // pair tiles (experts of more than 128 rows)
+    const FatTile* solo_tiles;   // experts of 33 .. 128 rows
+    const FatTile* thin_tiles;   // experts of at most 32 rows
+    WsHeader* hdr;
+    int rows;                    // rows of A
+    int with_pairs;              // the one-CTA kernel runs the pair tiles too
+    int k_blocks;                // K / 128
+    int n_rows;                  // weight rows per expert
+    int n_blocks_n;              // column tiles per expert (128 gated, 256 plain)
+    const uint8_t* a_scales;     // [rows, K / 128]
+    const uint8_t* b0_scales;    // [E, n_rows / 128, K / 128]; gated: gate
+    const uint8_t* b1_scales;    // gated: up
+    __nv_bfloat16* out;          // plain: [rows, ld_out]
+    uint8_t* out_q;              // gated: [rows, ld_out] e4m3
+    uint8_t* out_scales;         // gated: [rows, ld_out / 128]
+    int64_t ld_out;
+    long long wait_cycles;
+};
+cudaError_t launch_fp8_solo_gate_up(const uint8_t* a, int64_t rows, const uint8_t* b0,
+                                    const uint8_t* b1, const Fp8Args& args, int E, int num_sms,
+                                    cudaStream_t s);
+cudaError_t launch_fp8_solo(const uint8_t* a, int64_t rows, const uint8_t* b, const Fp8Args& args,
+                            int E, int num_sms, cudaStream_t s);
+
+// ---- balance loss (balance.cu) ----
+constexpr int kBalanceChunk = 64;    // tokens per CTA of the forward pass
+int64_t balance_partial_rows(int T, int S);
+cudaError_t launch_balance(const float* logits, const int32_t* idx, int T, int E, int k,
+                           const int32_t* seq, int S, float coef, float* loss, int32_t* counts,
+                           float2* stats, float* part_p, int32_t* part_c, float* seq_loss,
+                           WsHeader* hdr, cudaStream_t s);
+cudaError_t launch_balance_backward(const float* logits, const float2* stats,
+                                    const int32_t* counts, const int32_t* seq, int T, int E, int k,
+                                    int S, float coef, const float* d_loss, const int32_t* idx,
+                                    const float* gates, const float* d_gates, float* d_logits,
+                                    int num_sms, cudaStream_t s);
+
 // Experts to copy: entry j copies expert src_e[j] of the source matrices
 // into block dst_e[j] of the destination matrices.
 struct ExpertCopyList {
@@ -363,6 +423,9 @@ moe_status forward_blocks(const moe_shape* shape, const float* logits, const moe
 
 // Validates a moe_shape as every entry point does (sets moe_last_error()).
 moe_status check_shape_status(const moe_shape* shape);
+
+// Checks that the current device runs this library and reads its SM count.
+moe_status current_device(int* num_sms);
 
 // Sets the calling thread's moe_last_error() message (printf format).
 void set_last_error(const char* fmt, ...);

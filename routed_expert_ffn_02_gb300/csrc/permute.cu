@@ -381,6 +381,37 @@ plan_kernel(const int32_t* __restrict__ counts, const int32_t* __restrict__ offs
     block_plan<1024>(cnt, off, E, plan, ta, tb, ws);
 }
 
+// plan_kernel over group offsets alone, checked: offset e becomes the largest
+// of offsets 0..e, inside [0, rows], so the groups never overlap and the tile
+// lists never hold more rows than exist.
+__global__ void __launch_bounds__(1024)
+plan_groups_kernel(const int32_t* __restrict__ offsets, int rows, int E, Plan plan) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    __shared__ int cnt[kMaxE], off[kMaxE + 1], ta[kMaxE], tb[kMaxE];
+    __shared__ int ws[33];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int e = threadIdx.x;
+    const int given = e < E ? offsets[e] : 0, end = offsets[E];
+    int v = min(max(given, 0), rows);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v = max(v, u);
+    }
+    if (lane == 31) ws[w] = v;
+    __syncthreads();
+    for (int i = 0; i < w; ++i) v = max(v, ws[i]);
+    if (e < E) off[e] = v;
+    if (e == E - 1) off[E] = max(v, min(max(end, 0), rows));
+    if ((e < E && v != given) || (e == 0 && (given != 0 || end != rows)))
+        set_status(plan.hdr, MOE_ERR_BAD_INDEX);
+    __syncthreads();
+    if (e < E) cnt[e] = off[e + 1] - off[e];
+    __syncthreads();
+    block_plan<1024>(cnt, off, E, plan, ta, tb, ws);
+}
+
 // x_sorted[p] = x[perm[p] / k] for the rows of the fat tiles (paired and
 // solo) and of the tensor-core streaming tiles (all of them, or one of the
 // two gather parts); one warp per row, 16-byte vectors.
@@ -430,6 +461,11 @@ cudaError_t launch_permute(const int32_t* idx, int T, int E, int k,
 cudaError_t launch_plan(const int32_t* counts, const int32_t* offsets, int E,
                         const Plan& plan, cudaStream_t s) {
     return launch_pdl(plan_kernel, dim3(1), dim3(1024), 0, s, counts, offsets, E, plan);
+}
+
+cudaError_t launch_plan_groups(const int32_t* offsets, int rows, int E, const Plan& plan,
+                               cudaStream_t s) {
+    return launch_pdl(plan_groups_kernel, dim3(1), dim3(1024), 0, s, offsets, rows, E, plan);
 }
 
 cudaError_t launch_gather(const __nv_bfloat16* x, const int32_t* perm, int k,

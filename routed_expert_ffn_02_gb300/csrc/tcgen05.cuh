@@ -131,5 +131,8 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // (128 bytes) x box_rows, 128-byte swizzle, zero fill outside the tensor.
 cudaError_t make_tma_map_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
                               uint32_t box_rows);
+// Same over 8-bit values: box = 128 columns (128 bytes) x box_rows.
+cudaError_t make_tma_map_u8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
+                            uint32_t box_rows);
 
 }  // namespace moe
