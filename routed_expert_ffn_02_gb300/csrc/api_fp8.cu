@@ -96,7 +96,6 @@ Fp8Args args_of(const Lists& l, int64_t rows, int K, int N, bool gated) {
     a.thin_tiles = l.thin;
     a.hdr = l.hdr;
     a.rows = (int)rows;
-    a.with_pairs = 1;
     a.k_blocks = K / kSide;
     a.n_rows = N;
     a.n_blocks_n = gated ? N / kSide : (N + 255) / 256;
@@ -169,9 +168,19 @@ moe_status check_experts(const moe_fp8_experts* w) {
     return MOE_OK;
 }
 
+// Which kernels can have work, from sizes the host knows: `most` bounds any
+// expert's rows.  One expert of all rows has either pair tiles or a one-CTA
+// tile; with several, small ones cannot be ruled out.
+struct Kernels {
+    bool pair, solo;
+};
+Kernels kernels_for(int64_t rows, int64_t most, int E) {
+    return {most > kTileM, !(E == 1 && rows > kTileM)};
+}
+
 // Quantised rows in place (xq, xs): gate/up, then down into y [P, H].
 moe_status run_ffn(const moe_shape* sh, const FfnBufs& b, const moe_fp8_experts* w,
-                   __nv_bfloat16* y, int num_sms, cudaStream_t s) {
+                   __nv_bfloat16* y, int64_t most, int num_sms, cudaStream_t s) {
     const int64_t P = (int64_t)sh->T * sh->k;
     Fp8Args a = args_of(b.l, P, sh->H, sh->I, true);
     a.a_scales = b.xs;
@@ -179,13 +188,21 @@ moe_status run_ffn(const moe_shape* sh, const FfnBufs& b, const moe_fp8_experts*
     a.b1_scales = w->up_scales;
     a.out_q = b.hq;
     a.out_scales = b.hs;
-    CUDA_TRY(launch_fp8_solo_gate_up(b.xq, P, w->gate, w->up, a, sh->E, num_sms, s),
-             "8-bit gate/up");
+    const Kernels kn = kernels_for(P, most, sh->E);
+    if (kn.pair)
+        CUDA_TRY(launch_fp8_pair_gate_up(b.xq, P, w->gate, w->up, a, sh->E, num_sms, s),
+                 "8-bit gate/up (pairs)");
+    if (kn.solo)
+        CUDA_TRY(launch_fp8_solo_gate_up(b.xq, P, w->gate, w->up, a, sh->E, num_sms, s),
+                 "8-bit gate/up");
     Fp8Args d = args_of(b.l, P, sh->I, sh->H, false);
     d.a_scales = b.hs;
     d.b0_scales = w->down_scales;
     d.out = y;
-    CUDA_TRY(launch_fp8_solo(b.hq, P, w->down, d, sh->E, num_sms, s), "8-bit down");
+    if (kn.pair)
+        CUDA_TRY(launch_fp8_pair(b.hq, P, w->down, d, sh->E, num_sms, s), "8-bit down (pairs)");
+    if (kn.solo)
+        CUDA_TRY(launch_fp8_solo(b.hq, P, w->down, d, sh->E, num_sms, s), "8-bit down");
     return MOE_OK;
 }
 
@@ -273,7 +290,9 @@ moe_status moe_grouped_gemm_fp8(const uint8_t* x, const uint8_t* x_scales, int32
     a.a_scales = x_scales;
     a.b0_scales = W_scales;
     a.out = (__nv_bfloat16*)y;
-    CUDA_TRY(launch_fp8_solo(x, rows, W, a, E, sms, s), "8-bit product");
+    const Kernels kn = kernels_for(rows, rows, E);
+    if (kn.pair) CUDA_TRY(launch_fp8_pair(x, rows, W, a, E, sms, s), "8-bit product (pairs)");
+    if (kn.solo) CUDA_TRY(launch_fp8_solo(x, rows, W, a, E, sms, s), "8-bit product");
     return ok();
 }
 
@@ -304,7 +323,7 @@ moe_status moe_expert_ffn_fp8(const moe_shape* shape, const moe_bf16* x, const i
     CUDA_TRY(launch_invert_perm(perm, P, b.inv_perm, sms, s), "invert perm");
     CUDA_TRY(launch_quantize_rows((const __nv_bfloat16*)x, shape->T, shape->H, b.inv_perm,
                                   shape->k, P, b.xq, b.xs, sms, s), "quantize rows");
-    STATUS_TRY(run_ffn(shape, b, experts, (__nv_bfloat16*)y_sorted, sms, s));
+    STATUS_TRY(run_ffn(shape, b, experts, (__nv_bfloat16*)y_sorted, P, sms, s));
     return ok();
 }
 
@@ -340,7 +359,7 @@ moe_status moe_forward_fp8(const moe_shape* shape, const float* logits, const mo
                             b.chunk + nch * E, b.f.l.hdr, &plan, s), "permute");
     CUDA_TRY(launch_quantize_rows((const __nv_bfloat16*)x, T, shape->H, b.f.inv_perm, k, P,
                                   b.f.xq, b.f.xs, sms, s), "quantize rows");
-    STATUS_TRY(run_ffn(shape, b.f, experts, b.y, sms, s));
+    STATUS_TRY(run_ffn(shape, b.f, experts, b.y, T, sms, s));
     CUDA_TRY(launch_combine(b.y, b.f.inv_perm, g, T, k, shape->H, (__nv_bfloat16*)out, sms, s),
              "combine");
     return ok();

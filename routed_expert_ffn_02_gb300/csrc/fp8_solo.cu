@@ -77,13 +77,10 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
     grid_dep_wait();
     grid_dep_launch();
-    // Tiles: the pair list's (when no pair kernel runs), the solo tiles, the thin tiles.
-    const int n_pair = args.with_pairs ? args.hdr->n_fat_tiles : 0;
-    const int n_solo = n_pair + args.hdr->n_solo;
+    const int n_solo = args.hdr->n_solo;
     const int total = (n_solo + args.hdr->n_thin_mma) * args.n_blocks_n;
     auto tile_at = [&](int i) {
-        return i < n_pair ? args.tiles[i]
-               : i < n_solo ? args.solo_tiles[i - n_pair] : args.thin_tiles[i - n_solo];
+        return i < n_solo ? args.solo_tiles[i] : args.thin_tiles[i - n_solo];
     };
     // Items go round-robin to the first `active` CTAs, as many as keep every
     // wave full (see the bf16 one-CTA GEMM).

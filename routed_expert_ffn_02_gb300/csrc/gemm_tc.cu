@@ -63,6 +63,7 @@
 
 #include "gather_dev.cuh"
 #include "moe_internal.cuh"
+#include "pair_dev.cuh"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
 
@@ -109,40 +110,6 @@ struct GemmArgs {
                            // warps then gather the other rows), 2 the rest
     GatherRows gather;     // part 1 of gate/up: the rows of part 2
 };
-
-// Stage rounds filled into stage s by a producer that filled `fills` stages
-// in ring order.
-__device__ __forceinline__ int rounds_filled(int fills, int s) {
-    return fills > s ? (fills - s + STAGES - 1) / STAGES : 0;
-}
-
-// After an abort, run by one thread of the even CTA once both CTAs' roles
-// have stopped (fills_even / fills_odd: the stages each CTA's producer
-// filled).  Every round of a stage that either CTA filled completes on the
-// even CTA's full barrier; the two producers differ by at most one round per
-// stage (a round needs the previous one consumed, which needs both CTAs'
-// bytes).  A round only the odd CTA filled is armed here for its bytes; a
-// round only the even CTA filled is credited the odd CTA's missing bytes.
-// Then each last round is waited for with the full bound, so every copy of
-// both CTAs has landed.
-__device__ __forceinline__ void drain_pair(uint32_t full0, int fills_even, int fills_odd,
-                                           uint32_t stage_bytes) {
-    for (int s = 0; s < STAGES; ++s) {
-        const uint32_t bar = full0 + 8u * s;
-        const int re = rounds_filled(fills_even, s) - 1, ro = rounds_filled(fills_odd, s) - 1;
-        if (re < 0 && ro < 0) continue;
-        if (ro == re + 1) {
-            if (re >= 0) (void)ptx::mbar_wait(bar, (uint32_t)(re & 1));
-            ptx::mbar_expect_tx(bar, stage_bytes);
-            (void)ptx::mbar_wait(bar, (uint32_t)(ro & 1));
-        } else if (re == ro + 1) {
-            ptx::mbar_complete_tx(bar, stage_bytes);
-            (void)ptx::mbar_wait(bar, (uint32_t)(re & 1));
-        } else {
-            (void)ptx::mbar_wait(bar, (uint32_t)(re & 1));
-        }
-    }
-}
 
 // B rows of N tile nt: gated: 128 rows of Wg (even CTA) or Wu (odd CTA);
 // down: rows [256 nt, 256 nt + 256) of Wd, the odd CTA taking the upper 128.
@@ -413,7 +380,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     // Both CTAs read the same two flags here, so they agree on the drain.
     if (*abort_flag || ld_shared_cluster(peer_abort) != 0) {
         if (rank == 0 && threadIdx.x == 0)
-            drain_pair(full_bar(0), *fills_out,
+            drain_pair<STAGES>(full_bar(0), *fills_out,
                        (int)ld_shared_cluster(mapa_shared(smem_u32(fills_out), 1)),
                        (uint32_t)STAGE_BYTES);
         cluster_sync();
@@ -450,33 +417,6 @@ template <bool kGated>
 cudaError_t set_smem_attr() {
     static std::atomic<int> done[kMaxDevices];
     return smem_limit_once(grouped_gemm_kernel<kGated>, SMEM_BYTES, done);
-}
-
-// CTAs to launch: two per co-resident cluster (an SM pair whose partner is
-// busy or absent cannot host a cluster, so this can be below the SM count).
-template <bool kGated>
-cudaError_t pair_grid(int num_sms, int* grid) {
-    constexpr int kMaxDev = kMaxDevices;
-    static int cached[kMaxDev] = {};
-    static std::mutex mu;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lk(mu);
-    if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
-    if (!cached[dev]) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(num_sms & ~1), 1, 1);
-        cfg.blockDim = dim3(256, 1, 1);
-        cfg.dynamicSmemBytes = SMEM_BYTES;
-        int clusters = 0;
-        e = cudaOccupancyMaxActiveClusters(&clusters, grouped_gemm_kernel<kGated>, &cfg);
-        if (e != cudaSuccess) return e;
-        if (clusters < 1) return cudaErrorInvalidConfiguration;
-        cached[dev] = 2 * std::min(clusters, num_sms / 2);
-    }
-    *grid = cached[dev];
-    return cudaSuccess;
 }
 
 }  // namespace
@@ -523,7 +463,7 @@ cudaError_t launch_gemm_gate_up(const __nv_bfloat16* x_sorted, int64_t rows_allo
     if ((e = make_tma_map_bf16(&mO, h, (uint64_t)rows_alloc, (uint64_t)I, 32)) != cudaSuccess) return e;
     if ((e = set_smem_attr<true>()) != cudaSuccess) return e;
     int grid = 0;
-    if ((e = pair_grid<true>(num_sms, &grid)) != cudaSuccess) return e;
+    if ((e = pair_grid<grouped_gemm_kernel<true>, SMEM_BYTES>(num_sms, &grid)) != cudaSuccess) return e;
     GemmArgs a;
     a.tiles = plan.tiles;
     a.wslot = plan.wslot;
@@ -561,7 +501,7 @@ cudaError_t launch_gemm_down(const __nv_bfloat16* h, int64_t rows_alloc,
     if ((e = make_tma_map_bf16(&mO, y_sorted, (uint64_t)rows_alloc, (uint64_t)H, 32)) != cudaSuccess) return e;
     if ((e = set_smem_attr<false>()) != cudaSuccess) return e;
     int grid = 0;
-    if ((e = pair_grid<false>(num_sms, &grid)) != cudaSuccess) return e;
+    if ((e = pair_grid<grouped_gemm_kernel<false>, SMEM_BYTES>(num_sms, &grid)) != cudaSuccess) return e;
     GemmArgs a;
     a.tiles = plan.tiles;
     a.wslot = plan.wslot;

@@ -356,7 +356,6 @@ struct Fp8Args {
     const FatTile* thin_tiles;   // experts of at most 32 rows
     WsHeader* hdr;
     int rows;                    // rows of A
-    int with_pairs;              // the one-CTA kernel runs the pair tiles too
     int k_blocks;                // K / 128
     int n_rows;                  // weight rows per expert
     int n_blocks_n;              // column tiles per expert (128 gated, 256 plain)
@@ -369,6 +368,12 @@ struct Fp8Args {
     int64_t ld_out;
     long long wait_cycles;
 };
+// On CTA pairs: the pair tiles.  One-CTA kernel: the solo and thin tiles.
+cudaError_t launch_fp8_pair_gate_up(const uint8_t* a, int64_t rows, const uint8_t* b0,
+                                    const uint8_t* b1, const Fp8Args& args, int E, int num_sms,
+                                    cudaStream_t s);
+cudaError_t launch_fp8_pair(const uint8_t* a, int64_t rows, const uint8_t* b, const Fp8Args& args,
+                            int E, int num_sms, cudaStream_t s);
 cudaError_t launch_fp8_solo_gate_up(const uint8_t* a, int64_t rows, const uint8_t* b0,
                                     const uint8_t* b1, const Fp8Args& args, int E, int num_sms,
                                     cudaStream_t s);

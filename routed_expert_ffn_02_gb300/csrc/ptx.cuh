@@ -105,6 +105,29 @@ __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, lon
     return true;
 }
 
+// mbar_wait_for that also acquires what threads of other CTAs of the cluster
+// released by arriving on `bar`.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, long long limit,
+                                                  const volatile int* abort) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const long long start = clock64();
+    while (!mbar_try_wait_cluster(bar, parity)) {
+        if ((abort && *abort) || clock64() - start > limit) return false;
+    }
+    return true;
+}
+
 // Invalidates a barrier so its shared memory can be used again (for another
 // barrier or data); no thread may be waiting on it.
 __device__ __forceinline__ void mbar_inval(uint32_t bar) {
