@@ -69,8 +69,12 @@ class Shape:
     thin_mma_min: int = 0     # 0: library default; > fat_threshold - 1: CUDA cores only
 
     def c(self) -> MoeShape:
-        return MoeShape(self.T, self.E, self.k, self.H, self.I, self.fat_threshold,
-                        self.thin_mma_min)
+        c = self.__dict__.get("_c")
+        if c is None:
+            c = MoeShape(self.T, self.E, self.k, self.H, self.I, self.fat_threshold,
+                         self.thin_mma_min)
+            object.__setattr__(self, "_c", c)
+        return c
 
     @property
     def P(self) -> int:
@@ -156,30 +160,35 @@ def _host_ptr(t: torch.Tensor):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _dtype(t: torch.Tensor, dtype, shape=None):
-    assert t.dtype == dtype, f"expected {dtype}, got {t.dtype}"
-    assert shape is None or tuple(t.shape) == tuple(shape), f"expected {shape}, got {tuple(t.shape)}"
+# The 8-bit operators and the balance loss run in microseconds, so their
+# arguments take a short path: one condition and a plain integer per tensor.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_BF16, _F32, _I32, _U8, _E4M3 = (torch.bfloat16, torch.float32, torch.int32, torch.uint8,
+                                 torch.float8_e4m3fn)
 
 
-def _out(t: torch.Tensor | None, shape, dtype, device) -> torch.Tensor:
-    """The caller's output tensor, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _dtype(t, dtype, shape)
-    return t
+def _in(t: torch.Tensor, dtype, shape) -> int:
+    """Address of a contiguous CUDA tensor of this type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise AssertionError(f"expected a contiguous CUDA tensor {dtype} {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
 
 
-def _fp8(q: torch.Tensor, scales: torch.Tensor, shape, scale_shape):
-    _dtype(q, torch.float8_e4m3fn, shape)
-    _dtype(scales, torch.uint8, scale_shape)
+def _opt(t: torch.Tensor | None, dtype, shape):
+    return None if t is None else _in(t, dtype, shape)
+
+
+def _on(stream, t: torch.Tensor) -> int:
+    """The stream to launch on: the caller's, or the current one of t's device."""
+    return stream.cuda_stream if stream is not None else _raw_stream(t.get_device())
 
 
 def _sequences(seq_offsets) -> int:
     if seq_offsets is None:
         return 1
-    _dtype(seq_offsets, torch.int32)
-    assert seq_offsets.dim() == 1 and len(seq_offsets) >= 2, "seq_offsets is [S + 1], S >= 1"
-    return len(seq_offsets) - 1
+    assert seq_offsets.dim() == 1 and seq_offsets.shape[0] >= 2, "seq_offsets is [S + 1], S >= 1"
+    return seq_offsets.shape[0] - 1
 
 
 def _stream(stream):
@@ -213,11 +222,12 @@ class Workspace:
         off = (-self._buf.data_ptr()) % 256
         self.tensor = self._buf[off:off + nbytes]
         self.nbytes = nbytes
+        self.addr = self.tensor.data_ptr()
         _check(_lib.moe_workspace_init(self.ptr, nbytes, _stream(stream)), "moe_workspace_init")
 
     @property
     def ptr(self):
-        return ctypes.c_void_p(self.tensor.data_ptr())
+        return ctypes.c_void_p(self.addr)
 
     def status(self, clear: bool = True, stream=None) -> int:
         """Synchronises the stream and returns the device status code."""
@@ -565,11 +575,15 @@ def moe_quantize_rows(x: torch.Tensor, q=None, scales=None, stream=None):
     """x [rows, K] bf16 -> (q [rows, K] float8_e4m3fn, scales [rows, K/128]
     uint8): one power-of-two scale 2^(byte - 127) per 128 values of a row."""
     rows, K = x.shape
-    _dtype(x, torch.bfloat16)
-    q = _out(q, (rows, K), torch.float8_e4m3fn, x.device)
-    scales = _out(scales, (rows, K // 128), torch.uint8, x.device)
-    _check(_lib.moe_quantize_rows(_ptr(x), rows, K, _ptr(q), _ptr(scales), _stream(stream)),
-           "moe_quantize_rows")
+    shape = (rows, K // 128)
+    if q is None:
+        q = torch.empty((rows, K), dtype=_E4M3, device=x.device)
+    if scales is None:
+        scales = torch.empty(shape, dtype=_U8, device=x.device)
+    st = _lib.moe_quantize_rows(_in(x, _BF16, (rows, K)), rows, K, _in(q, _E4M3, (rows, K)),
+                                _in(scales, _U8, shape), _on(stream, x))
+    if st:
+        raise MoeError(st, "moe_quantize_rows")
     return q, scales
 
 
@@ -577,11 +591,15 @@ def moe_quantize_weights(W: torch.Tensor, q=None, scales=None, stream=None):
     """W [E, N, K] bf16 -> (q [E, N, K] float8_e4m3fn, scales [E, N/128, K/128]
     uint8): one power-of-two scale per 128 x 128 block."""
     E, N, K = W.shape
-    _dtype(W, torch.bfloat16)
-    q = _out(q, (E, N, K), torch.float8_e4m3fn, W.device)
-    scales = _out(scales, (E, N // 128, K // 128), torch.uint8, W.device)
-    _check(_lib.moe_quantize_weights(_ptr(W), E, N, K, _ptr(q), _ptr(scales), _stream(stream)),
-           "moe_quantize_weights")
+    shape = (E, N // 128, K // 128)
+    if q is None:
+        q = torch.empty((E, N, K), dtype=_E4M3, device=W.device)
+    if scales is None:
+        scales = torch.empty(shape, dtype=_U8, device=W.device)
+    st = _lib.moe_quantize_weights(_in(W, _BF16, (E, N, K)), E, N, K, _in(q, _E4M3, (E, N, K)),
+                                   _in(scales, _U8, shape), _on(stream, W))
+    if st:
+        raise MoeError(st, "moe_quantize_weights")
     return q, scales
 
 
@@ -599,21 +617,24 @@ def moe_grouped_gemm_fp8(x, x_scales, offsets, W, W_scales, y=None, ws: Workspac
     them); y [rows, N] bf16.  E = 1 (offsets [0, rows]) is the dense product."""
     rows, K = x.shape
     E, N, _ = W.shape
-    _fp8(x, x_scales, (rows, K), (rows, K // 128))
-    _fp8(W, W_scales, (E, N, K), (E, N // 128, K // 128))
-    _dtype(offsets, torch.int32, (E + 1,))
-    y = _out(y, (rows, N), torch.bfloat16, x.device)
+    if y is None:
+        y = torch.empty((rows, N), dtype=_BF16, device=x.device)
     ws = ws or Workspace(grouped_gemm_fp8_workspace_size(rows, E), x.device, stream)
-    _check(_lib.moe_grouped_gemm_fp8(_ptr(x), _ptr(x_scales), rows, _ptr(offsets), E, N, K, _ptr(W),
-                                     _ptr(W_scales), _ptr(y), ws.ptr, ws.nbytes, _stream(stream)),
-           "moe_grouped_gemm_fp8")
+    st = _lib.moe_grouped_gemm_fp8(
+        _in(x, _E4M3, (rows, K)), _in(x_scales, _U8, (rows, K // 128)), rows,
+        _in(offsets, _I32, (E + 1,)), E, N, K, _in(W, _E4M3, (E, N, K)),
+        _in(W_scales, _U8, (E, N // 128, K // 128)), _in(y, _BF16, (rows, N)), ws.addr, ws.nbytes,
+        _on(stream, x))
+    if st:
+        raise MoeError(st, "moe_grouped_gemm_fp8")
     return y
 
 
 @dataclass(frozen=True)
 class Fp8Experts:
     """A layer's experts in 8 bits: gate, up [E, I, H] and down [E, H, I]
-    float8_e4m3fn, each with its scales [E, rows/128, cols/128] uint8."""
+    float8_e4m3fn, each with its scales [E, rows/128, cols/128] uint8.  The
+    tensors are checked and their addresses taken here, once."""
     gate: torch.Tensor
     gate_scales: torch.Tensor
     up: torch.Tensor
@@ -621,13 +642,20 @@ class Fp8Experts:
     down: torch.Tensor
     down_scales: torch.Tensor
 
-    def c(self, shape: Shape) -> MoeFp8Experts:
-        E, H, I = shape.E, shape.H, shape.I
-        _fp8(self.gate, self.gate_scales, (E, I, H), (E, I // 128, H // 128))
-        _fp8(self.up, self.up_scales, (E, I, H), (E, I // 128, H // 128))
-        _fp8(self.down, self.down_scales, (E, H, I), (E, H // 128, I // 128))
-        return MoeFp8Experts(*[_ptr(t) for t in (self.gate, self.gate_scales, self.up,
-                                                 self.up_scales, self.down, self.down_scales)])
+    def __post_init__(self):
+        E, I, H = self.gate.shape
+        a, b = (E, I // 128, H // 128), (E, H // 128, I // 128)
+        c = MoeFp8Experts(_in(self.gate, _E4M3, (E, I, H)), _in(self.gate_scales, _U8, a),
+                          _in(self.up, _E4M3, (E, I, H)), _in(self.up_scales, _U8, a),
+                          _in(self.down, _E4M3, (E, H, I)), _in(self.down_scales, _U8, b))
+        object.__setattr__(self, "_sizes", (E, H, I))
+        object.__setattr__(self, "_c", c)
+
+    def ref(self, shape: Shape):
+        """The C structure, for a layer of these sizes."""
+        assert self._sizes == (shape.E, shape.H, shape.I), \
+            f"experts of (E, H, I) = {self._sizes}, layer of {(shape.E, shape.H, shape.I)}"
+        return ctypes.byref(self._c)
 
 
 def quantize_experts(W_gate, W_up, W_down, stream=None) -> Fp8Experts:
@@ -647,15 +675,16 @@ def expert_ffn_fp8_workspace_size(shape: Shape) -> int:
 def moe_expert_ffn_fp8(shape: Shape, x, perm, offsets, experts: Fp8Experts, y_sorted=None,
                        ws: Workspace | None = None, stream=None):
     """moe_expert_ffn on 8-bit experts (perm, offsets from moe_permute)."""
-    _dtype(x, torch.bfloat16, (shape.T, shape.H))
-    _dtype(perm, torch.int32, (shape.P,))
-    _dtype(offsets, torch.int32, (shape.E + 1,))
-    y_sorted = _out(y_sorted, (shape.P, shape.H), torch.bfloat16, x.device)
+    P, T, H = shape.P, shape.T, shape.H
+    if y_sorted is None:
+        y_sorted = torch.empty((P, H), dtype=_BF16, device=x.device)
     ws = ws or Workspace(expert_ffn_fp8_workspace_size(shape), x.device, stream)
-    w = experts.c(shape)
-    _check(_lib.moe_expert_ffn_fp8(ctypes.byref(shape.c()), _ptr(x), _ptr(perm), _ptr(offsets),
-                                   ctypes.byref(w), _ptr(y_sorted), ws.ptr, ws.nbytes,
-                                   _stream(stream)), "moe_expert_ffn_fp8")
+    st = _lib.moe_expert_ffn_fp8(
+        ctypes.byref(shape.c()), _in(x, _BF16, (T, H)), _in(perm, _I32, (P,)),
+        _in(offsets, _I32, (shape.E + 1,)), experts.ref(shape), _in(y_sorted, _BF16, (P, H)),
+        ws.addr, ws.nbytes, _on(stream, x))
+    if st:
+        raise MoeError(st, "moe_expert_ffn_fp8")
     return y_sorted
 
 
@@ -669,18 +698,16 @@ def fp8_workspace_size(shape: Shape) -> int:
 def moe_forward_fp8(shape: Shape, logits, x, experts: Fp8Experts, out=None, topk_idx=None,
                     gates=None, ws: Workspace | None = None, stream=None):
     """moe_forward on 8-bit experts."""
-    _dtype(logits, torch.float32, (shape.T, shape.E))
-    _dtype(x, torch.bfloat16, (shape.T, shape.H))
-    if topk_idx is not None:
-        _dtype(topk_idx, torch.int32, (shape.T, shape.k))
-    if gates is not None:
-        _dtype(gates, torch.float32, (shape.T, shape.k))
-    out = _out(out, (shape.T, shape.H), torch.bfloat16, x.device)
+    T, H, k = shape.T, shape.H, shape.k
+    if out is None:
+        out = torch.empty((T, H), dtype=_BF16, device=x.device)
     ws = ws or Workspace(fp8_workspace_size(shape), x.device, stream)
-    w = experts.c(shape)
-    _check(_lib.moe_forward_fp8(ctypes.byref(shape.c()), _ptr(logits), _ptr(x), ctypes.byref(w),
-                                _ptr(out), _ptr(topk_idx), _ptr(gates), ws.ptr, ws.nbytes,
-                                _stream(stream)), "moe_forward_fp8")
+    st = _lib.moe_forward_fp8(
+        ctypes.byref(shape.c()), _in(logits, _F32, (T, shape.E)), _in(x, _BF16, (T, H)),
+        experts.ref(shape), _in(out, _BF16, (T, H)), _opt(topk_idx, _I32, (T, k)),
+        _opt(gates, _F32, (T, k)), ws.addr, ws.nbytes, _on(stream, x))
+    if st:
+        raise MoeError(st, "moe_forward_fp8")
     return out
 
 
@@ -697,18 +724,22 @@ def moe_balance(logits, topk_idx, seq_offsets=None, coef: float = 1.0, loss=None
     [S + 1], None: one sequence of all tokens).  Returns (loss [] fp32, counts
     [S, E] int32, stats [T, 2] fp32 for moe_balance_backward)."""
     T, E = logits.shape
-    _dtype(logits, torch.float32)
     k = topk_idx.shape[1]
-    _dtype(topk_idx, torch.int32, (T, k))
     S = _sequences(seq_offsets)
     dev = logits.device
-    loss = _out(loss, (), torch.float32, dev)
-    counts = _out(counts, (S, E), torch.int32, dev)
-    stats = _out(stats, (T, 2), torch.float32, dev)
+    if loss is None:
+        loss = torch.empty((), dtype=_F32, device=dev)
+    if counts is None:
+        counts = torch.empty((S, E), dtype=_I32, device=dev)
+    if stats is None:
+        stats = torch.empty((T, 2), dtype=_F32, device=dev)
     ws = ws or Workspace(balance_workspace_size(T, E, S), dev, stream)
-    _check(_lib.moe_balance(_ptr(logits), _ptr(topk_idx), T, E, k, _ptr(seq_offsets), S, coef,
-                            _ptr(loss), _ptr(counts), _ptr(stats), ws.ptr, ws.nbytes,
-                            _stream(stream)), "moe_balance")
+    st = _lib.moe_balance(
+        _in(logits, _F32, (T, E)), _in(topk_idx, _I32, (T, k)), T, E, k,
+        _opt(seq_offsets, _I32, (S + 1,)), S, coef, _in(loss, _F32, ()), _in(counts, _I32, (S, E)),
+        _in(stats, _F32, (T, 2)), ws.addr, ws.nbytes, _on(stream, logits))
+    if st:
+        raise MoeError(st, "moe_balance")
     return loss, counts, stats
 
 
@@ -719,21 +750,16 @@ def moe_balance_backward(logits, stats, counts, k: int, seq_offsets=None, coef: 
     device, None for 1) and, where topk_idx, gates and d_gates are given, from
     the router's gates.  Returns d_logits [T, E] fp32."""
     T, E = logits.shape
-    _dtype(logits, torch.float32)
     S = _sequences(seq_offsets)
-    _dtype(stats, torch.float32, (T, 2))
-    _dtype(counts, torch.int32, (S, E))
-    if d_loss is not None:
-        _dtype(d_loss, torch.float32)
-        assert d_loss.numel() == 1, "d_loss is one number"
-    for t, dt in ((topk_idx, torch.int32), (gates, torch.float32), (d_gates, torch.float32)):
-        if t is not None:
-            _dtype(t, dt, (T, k))
-    d_logits = _out(d_logits, (T, E), torch.float32, logits.device)
-    _check(_lib.moe_balance_backward(_ptr(logits), _ptr(stats), _ptr(counts), _ptr(seq_offsets), T,
-                                     E, k, S, coef, _ptr(d_loss), _ptr(topk_idx), _ptr(gates),
-                                     _ptr(d_gates), _ptr(d_logits), _stream(stream)),
-           "moe_balance_backward")
+    if d_logits is None:
+        d_logits = torch.empty((T, E), dtype=_F32, device=logits.device)
+    st = _lib.moe_balance_backward(
+        _in(logits, _F32, (T, E)), _in(stats, _F32, (T, 2)), _in(counts, _I32, (S, E)),
+        _opt(seq_offsets, _I32, (S + 1,)), T, E, k, S, coef, _opt(d_loss, _F32, ()),
+        _opt(topk_idx, _I32, (T, k)), _opt(gates, _F32, (T, k)), _opt(d_gates, _F32, (T, k)),
+        _in(d_logits, _F32, (T, E)), _on(stream, logits))
+    if st:
+        raise MoeError(st, "moe_balance_backward")
     return d_logits
 
 

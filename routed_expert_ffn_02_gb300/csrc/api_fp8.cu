@@ -1,8 +1,6 @@
 // api_fp8.cu -- the C ABI of the 8-bit operators and of the balance loss
 // (include/moe.h): argument validation, workspace layout and the launch
 // sequence of each entry point.
-#include <cstdarg>
-#include <cstdio>
 
 #include "fp8.cuh"
 #include "moe_internal.cuh"
@@ -169,13 +167,21 @@ moe_status check_experts(const moe_fp8_experts* w) {
 }
 
 // Which kernels can have work, from sizes the host knows: `most` bounds any
-// expert's rows.  One expert of all rows has either pair tiles or a one-CTA
-// tile; with several, small ones cannot be ruled out.
+// expert's rows.  One expert holds all rows; with several, small ones cannot
+// be ruled out.
 struct Kernels {
     bool pair, solo;
 };
 Kernels kernels_for(int64_t rows, int64_t most, int E) {
     return {most > kTileM, !(E == 1 && rows > kTileM)};
+}
+
+// The grouped product y = A W^T (plain) over the planner's lists.
+moe_status run_product(const uint8_t* x, const uint8_t* W, const Fp8Args& a, const Kernels& kn,
+                       int E, int num_sms, cudaStream_t s) {
+    if (kn.pair) CUDA_TRY(launch_fp8_pair(x, a.rows, W, a, E, num_sms, s), "8-bit product (pairs)");
+    if (kn.solo) CUDA_TRY(launch_fp8_solo(x, a.rows, W, a, E, num_sms, s), "8-bit product (one-CTA)");
+    return MOE_OK;
 }
 
 // Quantised rows in place (xq, xs): gate/up, then down into y [P, H].
@@ -194,16 +200,13 @@ moe_status run_ffn(const moe_shape* sh, const FfnBufs& b, const moe_fp8_experts*
                  "8-bit gate/up (pairs)");
     if (kn.solo)
         CUDA_TRY(launch_fp8_solo_gate_up(b.xq, P, w->gate, w->up, a, sh->E, num_sms, s),
-                 "8-bit gate/up");
+                 "8-bit gate/up (one-CTA)");
     Fp8Args d = args_of(b.l, P, sh->I, sh->H, false);
+    d.early_weights = 1;   // the lists precede the quantised rows, these the gate/up kernels
     d.a_scales = b.hs;
     d.b0_scales = w->down_scales;
     d.out = y;
-    if (kn.pair)
-        CUDA_TRY(launch_fp8_pair(b.hq, P, w->down, d, sh->E, num_sms, s), "8-bit down (pairs)");
-    if (kn.solo)
-        CUDA_TRY(launch_fp8_solo(b.hq, P, w->down, d, sh->E, num_sms, s), "8-bit down");
-    return MOE_OK;
+    return run_product(b.hq, w->down, d, kn, sh->E, num_sms, s);
 }
 
 // C++ exceptions never leave a C entry point: nothing here allocates or throws.
@@ -290,9 +293,7 @@ moe_status moe_grouped_gemm_fp8(const uint8_t* x, const uint8_t* x_scales, int32
     a.a_scales = x_scales;
     a.b0_scales = W_scales;
     a.out = (__nv_bfloat16*)y;
-    const Kernels kn = kernels_for(rows, rows, E);
-    if (kn.pair) CUDA_TRY(launch_fp8_pair(x, rows, W, a, E, sms, s), "8-bit product (pairs)");
-    if (kn.solo) CUDA_TRY(launch_fp8_solo(x, rows, W, a, E, sms, s), "8-bit product");
+    STATUS_TRY(run_product(x, W, a, kernels_for(rows, rows, E), E, sms, s));
     return ok();
 }
 

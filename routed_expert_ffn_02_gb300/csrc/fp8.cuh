@@ -61,6 +61,24 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
     return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
 }
 
+// Sixteen consecutive values as e4m3 bytes.
+__device__ __forceinline__ uint4 quantize16(const float* v, float inv) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o[i] = pack_e4m3x4(scaled(v[4 * i], inv), scaled(v[4 * i + 1], inv),
+                           scaled(v[4 * i + 2], inv), scaled(v[4 * i + 3], inv));
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// silu(g) * u in fp32, by the hardware's approximate reciprocal (about one
+// ulp): the result is rounded to 4 significant bits next.
+__device__ __forceinline__ float swiglu(float g, float u) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
+    return g * r * u;
+}
+
 // ---- tensor core ---------------------------------------------------------
 
 // Instruction descriptor, kind::mxf8f6f4, e4m3 x e4m3, both K-major, scales
@@ -126,9 +144,9 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64
 __device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int w, int nb) {
     if ((nb & 3) == 0) return __ldg(reinterpret_cast<const uint32_t*>(row) + w);
     uint32_t v = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        v |= (4 * w + i < nb ? (uint32_t)__ldg(row + 4 * w + i) : 127u) << (8 * i);
+#pragma unroll 1   // rare; unrolled, the loads of several words raise the kernels' registers
+    for (int i = 3; i >= 0; --i)
+        v = (v << 8) | (4 * w + i < nb ? (uint32_t)__ldg(row + 4 * w + i) : 127u);
     return v;
 }
 

@@ -366,7 +366,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     if (c == 32) drained();
 #pragma unroll
                     for (int q = 0; q < 32; ++q) {
-                        h[c + q] = swiglu(__uint_as_float(g[q]), __uint_as_float(u[q]));
+                        h[c + q] = fp8::swiglu(__uint_as_float(g[q]), __uint_as_float(u[q]));
                         m = fmaxf(m, fp8::finite_abs(h[c + q]));
                     }
                 }

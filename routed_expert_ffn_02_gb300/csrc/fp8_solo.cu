@@ -1,15 +1,15 @@
 // fp8_solo.cu -- one-CTA grouped products of 8-bit block-scaled operands:
-// row tiles of at most 128 rows (experts with few rows, where the weights'
-// bytes count).
+// experts of at most 128 rows, one row tile each.
 //
 //   plain:    y[rows, n0:n0+256] = bf16( A W_e[n0:n0+256]^T )
 //   gate/up:  h[rows, n0:n0+128] = quantised( silu(A Wg_e^T) * (A Wu_e^T) ),
 //             the gate and up rows of the same 128 columns back to back in
-//             one N = 256 MMA; a thread holds a row's 128 columns, which are
-//             one block of 128, so it quantises them by itself.
+//             one N = 256 MMA; the 128 columns of a row are one block of 128.
 //
 // A is [rows, K] e4m3 with one scale byte per 128 of K, W [E, N, K] e4m3 with
-// one per 128 x 128; the tensor core applies both (fp8.cuh).
+// one per 128 x 128; the tensor core applies both (fp8.cuh).  Each weight byte
+// is read from HBM once and used for one tile of rows, so the kernel is a
+// weight stream bound by HBM; the MMAs take a third of the time.
 //
 // Persistent CTAs, one per SM, warp-specialised: warp 0 TMA producer (one
 // lane), warp 1 MMA issuer (M = 128, N = 256, K = 32), warp 2 TMEM allocator,
@@ -19,8 +19,18 @@
 // warp 3 and copied to TMEM by the MMA lane.  Slot i of the shared ring goes
 // to slot i of the TMEM ring, and a slot is refilled only after the MMAs that
 // read it have completed (its "empty" barrier), so no copy to TMEM overtakes
-// an MMA.  Every wait is bounded; on expiry the kernel records
-// MOE_ERR_TIMEOUT, drains its own copies and MMAs, frees TMEM and returns.
+// an MMA.  The two accumulators overlap in TMEM as in the pair kernel
+// (fp8_pair.cu): an item's epilogue runs under the next item's stream.
+//
+// Thin tiles (at most 32 rows).  A TMEM lane is a row of A and a warp reads
+// only its own 32 lanes, so a few rows would leave the whole epilogue to one
+// warp (its 128 SwiGLUs per lane took longer than the ring could bridge: a
+// decode batch of 24 streamed at 75% of HBM, 94% in the down product that has
+// none).  The 32 rows are therefore loaded into all four quarters of A: every
+// warp finds them in its lanes and does a quarter of the columns.
+//
+// Every wait is bounded; on expiry the kernel records MOE_ERR_TIMEOUT, drains
+// its own copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
 
 #include "fp8.cuh"
@@ -48,9 +58,11 @@ constexpr int SLOTS = 4;                        // scale ring
 constexpr int SLOT_BYTES = 3 * kScaleBytes;     // A, W rows 0-127, W rows 128-255
 constexpr int SLOT_COLS = 3 * kScaleCols;
 constexpr int TMEM_COLS = 512;
-constexpr int SCALE_COL = BN;                   // TMEM column of the scale ring
+constexpr int SCALE_COL = TMEM_COLS - SLOTS * SLOT_COLS;   // 464
+constexpr int ACC1_COL = SCALE_COL - BN;                   // 208: the accumulators overlap
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SLOTS * SLOT_BYTES + 1024 + 256;
 constexpr uint32_t kIdesc = fp8::make_idesc(BM, BN);
+static_assert(BN - ACC1_COL <= 64, "the overlap lies in the part that the epilogue reads first");
 
 template <bool kGated>
 __global__ void __launch_bounds__(256, 1)
@@ -68,25 +80,41 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     auto sfull_bar = [&](int s) { return bars + 8u * (2 * STAGES + s); };
     auto sempty_bar = [&](int s) { return bars + 8u * (2 * STAGES + SLOTS + s); };
     const uint32_t tfull_bar = bars + 8u * (2 * STAGES + 2 * SLOTS);
-    const uint32_t tempty_bar = tfull_bar + 8u;
-    const uint32_t done_bar = tfull_bar + 16u;
+    const uint32_t drained_bar = tfull_bar + 8u;    // the overlap of an item has been read
+    const uint32_t max_bar = tfull_bar + 16u;       // thin gate/up: four warps' maxima are in
+    const uint32_t done_bar = tfull_bar + 24u;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (done_bar + 8u - base));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    __shared__ float part_max[2][4][32];   // thin gate/up: a row's maximum, by warp; items
+                                           // alternate, so a reader is never overwritten
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
-    grid_dep_wait();
-    grid_dep_launch();
-    const int n_solo = args.hdr->n_solo;
-    const int total = (n_solo + args.hdr->n_thin_mma) * args.n_blocks_n;
+    // With early_weights the tile lists were complete before the previous
+    // kernel started (see Fp8Args), so they and the weights are read before
+    // the wait for that kernel; reads go to L2, past this SM's L1.
+    if (!args.early_weights) {
+        grid_dep_wait();
+        grid_dep_launch();
+    }
+    const int n_solo = __ldcg(&args.hdr->n_solo);
+    const int total = (n_solo + __ldcg(&args.hdr->n_thin_mma)) * args.n_blocks_n;
     auto tile_at = [&](int i) {
-        return i < n_solo ? args.solo_tiles[i] : args.thin_tiles[i - n_solo];
+        const int4 v = __ldcg(reinterpret_cast<const int4*>(
+            i < n_solo ? args.solo_tiles + i : args.thin_tiles + (i - n_solo)));
+        return FatTile{v.x, v.y, v.z, v.w};
     };
     // Items go round-robin to the first `active` CTAs, as many as keep every
     // wave full (see the bf16 one-CTA GEMM).
     const int waves = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     const int active = waves > 0 ? (total + waves - 1) / waves : 0;
-    if ((int)blockIdx.x >= active) return;
+    if ((int)blockIdx.x >= active) {
+        if (args.early_weights) {
+            grid_dep_wait();
+            grid_dep_launch();
+        }
+        return;
+    }
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -98,7 +126,8 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             mbar_init(sempty_bar(s), 1);
         }
         mbar_init(tfull_bar, 1);
-        mbar_init(tempty_bar, 128);
+        mbar_init(drained_bar, 4);
+        mbar_init(max_bar, 4);
         mbar_init(done_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -115,6 +144,10 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     fence_after();
     const uint32_t tmem_base = *tmem_holder;
     const int k_blocks = args.k_blocks;
+    if (args.early_weights && warp != 0) {
+        grid_dep_wait();
+        grid_dep_launch();
+    }
 
     if (warp == 0 && lane == 0) {
         // ---------------- TMA producer ----------------
@@ -123,22 +156,50 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         int pending[STAGES];
         for (int s = 0; s < STAGES; ++s) pending[s] = -1;
         bool ok = true;
+        auto load_w = [&](uint32_t sb, uint32_t bar, int x, int y) {
+            tma_load_2d(sb, &tmB0, bar, x, y);
+            if (kGated) tma_load_2d(sb + B_BYTES / 2, &tmB1, bar, x, y);
+        };
+        auto load_a = [&](uint32_t sa, uint32_t bar, int x, const FatTile& ft) {
+            if (ft.rows > kThinMaxTokens) {
+                tma_load_2d(sa, &tmA, bar, x, ft.row0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tma_load_2d(sa + i * (A_BYTES / 4), &tmA32, bar, x, ft.row0);
+            }
+        };
+        // The first stages' weights do not depend on the previous kernel.
+        int early = 0;
+        if (args.early_weights) {
+            const FatTile ft = tile_at(blockIdx.x / args.n_blocks_n);
+            const int brow = ft.expert * args.n_rows +
+                             ((int)blockIdx.x % args.n_blocks_n) * (kGated ? 128 : BN);
+            for (early = 0; early < min(STAGES, k_blocks); ++early) {
+                mbar_expect_tx(full_bar(early), STAGE_BYTES);
+                load_w(base + early * STAGE_BYTES + A_BYTES, full_bar(early), early * kBlock, brow);
+            }
+            grid_dep_wait();
+            grid_dep_launch();
+            // the rows come from the previous kernel's ordinary stores
+            fence_proxy_async_global();
+        }
         for (int t = blockIdx.x; ok && t < total; t += active) {
             const FatTile ft = tile_at(t / args.n_blocks_n);
             const int brow = ft.expert * args.n_rows + (t % args.n_blocks_n) * (kGated ? 128 : BN);
-            const bool small = ft.rows <= kThinMaxTokens;
-            const uint32_t bytes = (small ? kThinMaxTokens * kBlock : A_BYTES) + B_BYTES;
             for (int kb = 0; kb < k_blocks; ++kb) {
                 if (!mbar_wait_for(empty_bar(stage), phase ^ 1u, args.wait_cycles, abort_flag)) {
                     ok = false;
                     break;
                 }
                 const uint32_t sa = base + stage * STAGE_BYTES;
-                const uint32_t sb = sa + A_BYTES;
-                mbar_expect_tx(full_bar(stage), bytes);
-                tma_load_2d(sa, small ? &tmA32 : &tmA, full_bar(stage), kb * kBlock, ft.row0);
-                tma_load_2d(sb, &tmB0, full_bar(stage), kb * kBlock, brow);
-                if (kGated) tma_load_2d(sb + B_BYTES / 2, &tmB1, full_bar(stage), kb * kBlock, brow);
+                if (early > 0) {
+                    --early;
+                } else {
+                    mbar_expect_tx(full_bar(stage), STAGE_BYTES);
+                    load_w(sa + A_BYTES, full_bar(stage), kb * kBlock, brow);
+                }
+                load_a(sa, full_bar(stage), kb * kBlock, ft);
                 pending[stage] = (int)phase;
                 if (++stage == STAGES) {
                     stage = 0;
@@ -160,11 +221,15 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         bool ok = true;
         bool issued = false;
         for (int t = blockIdx.x; ok && t < total; t += active, ++it) {
-            if (!mbar_wait_for(tempty_bar, (uint32_t)(it & 1) ^ 1u, args.wait_cycles, abort_flag)) {
+            // the previous item's epilogue has read the overlap (and with it,
+            // being in order, all of this buffer's previous item)
+            if (it > 0 && !mbar_wait_for(drained_bar, (uint32_t)((it - 1) & 1), args.wait_cycles,
+                                         abort_flag)) {
                 ok = false;
                 break;
             }
             fence_after();
+            const uint32_t d_tmem = tmem_base + (uint32_t)((it & 1) ? ACC1_COL : 0);
             for (int kb = 0; kb < k_blocks; ++kb) {
                 const uint32_t sc = tmem_base + SCALE_COL + slot * SLOT_COLS;
                 if (kb % kGroupBlocks == 0) {
@@ -190,7 +255,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 const uint32_t idesc = fp8::with_scale_byte(kIdesc, kb % kGroupBlocks);
 #pragma unroll
                 for (int kk = 0; kk < kBlock / 32; ++kk)   // +32 bytes per K step
-                    fp8::mma(tmem_base, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), idesc, sc,
+                    fp8::mma(d_tmem, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), idesc, sc,
                              sc + kScaleCols, (kb > 0 || kk > 0) ? 1u : 0u);
                 commit(empty_bar(stage));
                 if (++stage == STAGES) {
@@ -230,8 +295,10 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             const uint8_t* ra[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                // rows past the tile's only scale rows of D that are not stored
-                const int r = min(ft.row0 + lane + 32 * i, args.rows - 1);
+                // rows past the tile's only scale rows of D that are not stored;
+                // a thin tile's rows repeat in every quarter
+                const int r = min(ft.row0 + lane + (ft.rows > kThinMaxTokens ? 32 * i : 0),
+                                  args.rows - 1);
                 ra[i] = args.a_scales + (int64_t)r * k_blocks;
             }
             const int64_t eb = (int64_t)ft.expert * (args.n_rows / kBlock);
@@ -272,8 +339,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     } else if (warp >= 4) {
         // ---------------- epilogue ----------------
         const int ew = warp - 4;   // TMEM lanes 32*ew .. 32*ew+31
-        const int row = ew * 32 + lane;
-        int it = 0;
+        int it = 0, n_thin = 0;
         for (int t = blockIdx.x; t < total; t += active, ++it) {
             // the whole warp decides together (tcgen05.ld below is warp-wide)
             if (!__all_sync(0xffffffffu, mbar_wait_for(tfull_bar, (uint32_t)(it & 1),
@@ -285,67 +351,113 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             fence_after();
             const FatTile ft = tile_at(t / args.n_blocks_n);
             const int nt = t % args.n_blocks_n;
+            const int odd = it & 1;
+            const bool thin = ft.rows <= kThinMaxTokens;
+            const int row = thin ? lane : ew * 32 + lane;
+            const bool valid = row < ft.rows;
             const int64_t out_row = (int64_t)ft.row0 + row;
-            const uint32_t taddr = tmem_base + ((uint32_t)(ew * 32) << 16);
-            if (ew * 32 < ft.rows) {   // uniform over the warp
-                if (kGated) {
-                    float h[kBlock];
-                    float m = 0.f;
+            const uint32_t taddr =
+                tmem_base + ((uint32_t)(ew * 32) << 16) + (uint32_t)(odd ? ACC1_COL : 0);
+            auto drained = [&]() {   // the columns shared with the other buffer have been read
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(drained_bar);
+            };
+            if (kGated && thin) {
+                // 32 of the 128 columns per warp; the row's maximum over the four warps
+                const int f = 32 * ew;
+                uint32_t g[32], u[32];
+                tmem_ld32(taddr + f, g);
+                tmem_ld32(taddr + 128 + f, u);
+                tmem_ld_wait();
+                drained();
+                float h[32];
+                float m = 0.f;
 #pragma unroll
-                    for (int c = 0; c < kBlock; c += 32) {
-                        uint32_t g[32], u[32];
-                        tmem_ld32(taddr + c, g);
-                        tmem_ld32(taddr + 128 + c, u);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int q = 0; q < 32; ++q) {
-                            h[c + q] = swiglu(__uint_as_float(g[q]), __uint_as_float(u[q]));
-                            m = fmaxf(m, fp8::finite_abs(h[c + q]));
-                        }
-                    }
-                    const uint32_t sb = fp8::scale_byte(m);
-                    const float inv = fp8::inverse_scale(sb);
-                    if (row < ft.rows) {
-                        uint4* dst = reinterpret_cast<uint4*>(args.out_q + out_row * args.ld_out +
-                                                              (int64_t)nt * kBlock);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            uint32_t v[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float* p = h + 16 * q + 4 * i;
-                                v[i] = fp8::pack_e4m3x4(fp8::scaled(p[0], inv), fp8::scaled(p[1], inv),
-                                                        fp8::scaled(p[2], inv), fp8::scaled(p[3], inv));
-                            }
-                            dst[q] = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
+                for (int q = 0; q < 32; ++q) {
+                    h[q] = fp8::swiglu(__uint_as_float(g[q]), __uint_as_float(u[q]));
+                    m = fmaxf(m, fp8::finite_abs(h[q]));
+                }
+                float(*pm)[32] = part_max[n_thin & 1];
+                pm[ew][lane] = m;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(max_bar);
+                if (!__all_sync(0xffffffffu, mbar_wait_for(max_bar, (uint32_t)(n_thin & 1),
+                                                           args.wait_cycles, abort_flag))) {
+                    *abort_flag = 1;
+                    set_status(args.hdr, MOE_ERR_TIMEOUT);
+                    break;
+                }
+                ++n_thin;
+                m = fmaxf(fmaxf(pm[0][lane], pm[1][lane]), fmaxf(pm[2][lane], pm[3][lane]));
+                const uint32_t sb = fp8::scale_byte(m);
+                const float inv = fp8::inverse_scale(sb);
+                if (valid) {
+                    uint4* dst = reinterpret_cast<uint4*>(args.out_q + out_row * args.ld_out +
+                                                          (int64_t)nt * kBlock + f);
+                    dst[0] = fp8::quantize16(h, inv);
+                    dst[1] = fp8::quantize16(h + 16, inv);
+                    if (ew == 0)
                         args.out_scales[out_row * (args.ld_out / kBlock) + nt] = (uint8_t)sb;
+                }
+            } else if (kGated) {
+                // first the 64 columns whose TMEM columns overlap: the upper
+                // ones of buffer 0 (up columns 208-255), the lower of buffer 1
+                const int first = odd ? 0 : 64;
+                float h[kBlock];
+                float m = 0.f;
+#pragma unroll
+                for (int c = 0; c < kBlock; c += 32) {
+                    const int f = (first + c) & 127;
+                    uint32_t g[32], u[32];
+                    tmem_ld32(taddr + f, g);
+                    tmem_ld32(taddr + 128 + f, u);
+                    tmem_ld_wait();
+                    if (c == 32) drained();
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) {
+                        h[c + q] = fp8::swiglu(__uint_as_float(g[q]), __uint_as_float(u[q]));
+                        m = fmaxf(m, fp8::finite_abs(h[c + q]));
                     }
-                } else {
-                    __nv_bfloat16* dst = args.out + out_row * args.ld_out + (int64_t)nt * BN;
-                    const int cols = min(BN, (int)args.ld_out - nt * BN);
+                }
+                const uint32_t sb = fp8::scale_byte(m);
+                const float inv = fp8::inverse_scale(sb);
+                if (valid) {
+                    uint4* dst = reinterpret_cast<uint4*>(args.out_q + out_row * args.ld_out +
+                                                          (int64_t)nt * kBlock);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)   // h is in the order read
+                        dst[(first / 16 + q) & 7] = fp8::quantize16(h + 16 * q, inv);
+                    args.out_scales[out_row * (args.ld_out / kBlock) + nt] = (uint8_t)sb;
+                }
+            } else {
+                __nv_bfloat16* dst = args.out + out_row * args.ld_out + (int64_t)nt * BN;
+                const int cols = (int)min((int64_t)BN, args.ld_out - (int64_t)nt * BN);
 #pragma unroll 1
-                    for (int c = 0; c < cols; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(taddr + c, v);
+                for (int i = 0; i < (thin ? 1 : 4); ++i) {
+                    // 64 columns at a time, the overlapping ones first; of a
+                    // thin tile each warp does 64
+                    const int c = thin ? 64 * ew : odd ? 64 * i : 64 * ((i + 3) & 3);
+                    uint32_t v[32];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t d[32];
+                        tmem_ld32(taddr + c + 32 * half, d);
                         tmem_ld_wait();
-                        if (row < ft.rows) {
-                            uint4* d4 = reinterpret_cast<uint4*>(dst + c);
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                uint32_t o[4];
+                        for (int q = 0; q < 16; ++q)
+                            v[16 * half + q] = pack_bf16(__uint_as_float(d[2 * q]),
+                                                         __uint_as_float(d[2 * q + 1]));
+                    }
+                    if (i == 0) drained();
+                    if (valid && c < cols) {
+                        uint4* d4 = reinterpret_cast<uint4*>(dst + c);
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    o[i] = pack_bf16(__uint_as_float(v[8 * q + 2 * i]),
-                                                     __uint_as_float(v[8 * q + 2 * i + 1]));
-                                d4[q] = make_uint4(o[0], o[1], o[2], o[3]);
-                            }
-                        }
+                        for (int q = 0; q < 8; ++q)
+                            d4[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                     }
                 }
             }
-            fence_before();
-            mbar_arrive(tempty_bar);
         }
     }
 

@@ -356,6 +356,9 @@ struct Fp8Args {
     const FatTile* thin_tiles;   // experts of at most 32 rows
     WsHeader* hdr;
     int rows;                    // rows of A
+    int early_weights;           // one-CTA kernel: the tile lists come from a kernel
+                                 // before the previous one, so weights may be copied
+                                 // before the dependency wait
     int k_blocks;                // K / 128
     int n_rows;                  // weight rows per expert
     int n_blocks_n;              // column tiles per expert (128 gated, 256 plain)
