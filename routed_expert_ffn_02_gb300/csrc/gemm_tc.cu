@@ -377,8 +377,12 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     fence_before();
     __syncthreads();
     cluster_sync();   // both CTAs' roles have stopped
-    // Both CTAs read the same two flags here, so they agree on the drain.
-    if (*abort_flag || ld_shared_cluster(peer_abort) != 0) {
+    // Both CTAs read the same two flags here, so they agree on the drain.  The
+    // barrier after it keeps a CTA from exiting while a slower warp of its
+    // peer still reads its shared memory (a fault of the whole launch).
+    const bool aborted = *abort_flag || ld_shared_cluster(peer_abort) != 0;
+    cluster_sync();
+    if (aborted) {
         if (rank == 0 && threadIdx.x == 0)
             drain_pair<STAGES>(full_bar(0), *fills_out,
                        (int)ld_shared_cluster(mapa_shared(smem_u32(fills_out), 1)),
