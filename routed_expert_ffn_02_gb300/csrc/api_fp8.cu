@@ -202,7 +202,7 @@ moe_status run_ffn(const moe_shape* sh, const FfnBufs& b, const moe_fp8_experts*
         CUDA_TRY(launch_fp8_solo_gate_up(b.xq, P, w->gate, w->up, a, sh->E, num_sms, s),
                  "8-bit gate/up (one-CTA)");
     Fp8Args d = args_of(b.l, P, sh->I, sh->H, false);
-    d.early_weights = 1;   // the lists precede the quantised rows, these the gate/up kernels
+    d.early_weights = 1;   // the lists were complete before the gate/up kernels started
     d.a_scales = b.hs;
     d.b0_scales = w->down_scales;
     d.out = y;
@@ -288,8 +288,9 @@ moe_status moe_grouped_gemm_fp8(const uint8_t* x, const uint8_t* x_scales, int32
     Lists l;
     take_lists(&c, rows, E, &l);
     const PdlScope pdl(rows <= kPermChunk);
-    CUDA_TRY(launch_plan_groups(offsets, rows, E, plan_of(l, E), s), "plan");
     Fp8Args a = args_of(l, rows, K, N, false);
+    if (E == 1) a.group = offsets;
+    else CUDA_TRY(launch_plan_groups(offsets, rows, E, plan_of(l, E), s), "plan");
     a.a_scales = x_scales;
     a.b0_scales = W_scales;
     a.out = (__nv_bfloat16*)y;
@@ -355,11 +356,17 @@ moe_status moe_forward_fp8(const moe_shape* shape, const float* logits, const mo
     float* g = gates ? gates : b.gates;
     const Plan plan = plan_of(b.f.l, E);
     const int64_t nch = (P + kPermChunk - 1) / kPermChunk;
-    CUDA_TRY(launch_route(logits, T, E, k, idx, g, s), "route");
-    CUDA_TRY(launch_permute(idx, T, E, k, b.counts, b.offsets, b.perm, b.f.inv_perm, b.chunk,
-                            b.chunk + nch * E, b.f.l.hdr, &plan, s), "permute");
-    CUDA_TRY(launch_quantize_rows((const __nv_bfloat16*)x, T, shape->H, b.f.inv_perm, k, P,
-                                  b.f.xq, b.f.xs, sms, s), "quantize rows");
+    if (fp8_prologue_fits(T)) {
+        CUDA_TRY(launch_fp8_prologue(logits, (const __nv_bfloat16*)x, T, E, k, shape->H, idx, g,
+                                     b.f.inv_perm, b.f.l.thin, b.f.l.hdr, b.f.xq, b.f.xs, s),
+                 "prologue");
+    } else {
+        CUDA_TRY(launch_route(logits, T, E, k, idx, g, s), "route");
+        CUDA_TRY(launch_permute(idx, T, E, k, b.counts, b.offsets, b.perm, b.f.inv_perm, b.chunk,
+                                b.chunk + nch * E, b.f.l.hdr, &plan, s), "permute");
+        CUDA_TRY(launch_quantize_rows((const __nv_bfloat16*)x, T, shape->H, b.f.inv_perm, k, P,
+                                      b.f.xq, b.f.xs, sms, s), "quantize rows");
+    }
     STATUS_TRY(run_ffn(shape, b.f, experts, b.y, T, sms, s));
     CUDA_TRY(launch_combine(b.y, b.f.inv_perm, g, T, k, shape->H, (__nv_bfloat16*)out, sms, s),
              "combine");

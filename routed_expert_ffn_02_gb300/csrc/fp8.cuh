@@ -139,6 +139,23 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate));
 }
 
+// The tiles of a launch: the planner's lists, or, for a single expert, the
+// rows [lo, lo + n) that its two offsets give, cut into tiles here (no planner
+// launch; offsets outside [0, rows] are cut, and recorded by the first CTA).
+struct OneGroup {
+    int lo, n;
+};
+__device__ __forceinline__ OneGroup one_group(const Fp8Args& args) {
+    const int a = __ldg(args.group), b = __ldg(args.group + 1);
+    const int lo = min(max(a, 0), args.rows);
+    if ((a != 0 || b != args.rows) && blockIdx.x == 0 && threadIdx.x == 0)
+        set_status(args.hdr, MOE_ERR_BAD_INDEX);
+    return {lo, max(0, min(b, args.rows) - lo)};
+}
+__device__ __forceinline__ FatTile group_tile(const OneGroup& g, int i) {
+    return FatTile{0, g.lo + i * kTileM, max(0, min(kTileM, g.n - i * kTileM)), 0};
+}
+
 // Scale word w (bytes 4w .. 4w+3) of a row of nb scale bytes; bytes past nb
 // read as 127 (a factor of one, for operands that TMA filled with zeros).
 __device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int w, int nb) {

@@ -130,10 +130,15 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     grid_dep_wait();      // everything above overlaps the previous kernel
     grid_dep_launch();
 
-    const int total = (args.hdr->n_fat_tiles >> 1) * args.n_blocks_n;
+    const fp8::OneGroup grp = args.group ? fp8::one_group(args) : fp8::OneGroup{0, 0};
+    const int n_pairs = args.group ? (grp.n + 2 * BM - 1) / (2 * BM) : args.hdr->n_fat_tiles >> 1;
+    const int total = n_pairs * args.n_blocks_n;
     const int k_blocks = args.k_blocks;
     const int k_stages = (k_blocks + KSUB - 1) / KSUB;
-    auto tile_at = [&](int w) { return args.tiles[2 * (w / args.n_blocks_n) + (int)rank]; };
+    auto tile_at = [&](int w) {
+        const int i = 2 * (w / args.n_blocks_n) + (int)rank;
+        return args.group ? fp8::group_tile(grp, i) : args.tiles[i];
+    };
 
     if (warp == 0 && lane == 0) {
         // ---------------- TMA producer (both CTAs) ----------------
@@ -326,6 +331,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 tma_store_2d(&tmOut, buf, x, y);
                 bulk_commit();
             }
+            __syncwarp();
             stored = true;
         };
         for (int w = cluster; w < total; w += n_clusters, ++it) {
@@ -349,6 +355,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(drained0);
+                __syncwarp();   // converged for the warp-wide TMEM loads that follow
             };
             if (kGated) {
                 // first the 64 features whose columns overlap: the upper ones
@@ -397,6 +404,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         d4[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                 }
                 if (valid) args.out_scales[out_row * (args.ld_out / kBlock) + nt] = (uint8_t)sb;
+                __syncwarp();
             } else {
                 const int cols = (int)min((int64_t)BN, args.ld_out - (int64_t)nt * BN);
 #pragma unroll 1
@@ -425,6 +433,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         for (int q = 0; q < 8; ++q)
                             d4[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                     }
+                    __syncwarp();
                 }
             }
         }
@@ -435,8 +444,12 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     fence_before();
     __syncthreads();
     cluster_sync();   // both CTAs' roles have stopped
-    // Both CTAs read the same two flags here, so they agree on the drain.
-    if (*abort_flag || ld_shared_cluster(peer_abort) != 0) {
+    // Both CTAs read the same two flags here, so they agree on the drain.  The
+    // barrier after it keeps a CTA from exiting while a slower warp of its
+    // peer still reads its shared memory (a fault of the whole launch).
+    const bool aborted = *abort_flag || ld_shared_cluster(peer_abort) != 0;
+    cluster_sync();
+    if (aborted) {
         if (rank == 0 && threadIdx.x == 0)
             drain_pair<STAGES>(full_bar(0), *fills_out,
                                (int)ld_shared_cluster(mapa_shared(smem_u32(fills_out), 1)),

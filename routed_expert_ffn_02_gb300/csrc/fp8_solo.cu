@@ -97,9 +97,12 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         grid_dep_wait();
         grid_dep_launch();
     }
-    const int n_solo = __ldcg(&args.hdr->n_solo);
-    const int total = (n_solo + __ldcg(&args.hdr->n_thin_mma)) * args.n_blocks_n;
+    const fp8::OneGroup grp = args.group ? fp8::one_group(args) : fp8::OneGroup{0, 0};
+    const int n_solo = args.group ? 0 : __ldcg(&args.hdr->n_solo);
+    const int n_tiles = args.group ? (grp.n > 0) : n_solo + __ldcg(&args.hdr->n_thin_mma);
+    const int total = n_tiles * args.n_blocks_n;
     auto tile_at = [&](int i) {
+        if (args.group) return fp8::group_tile(grp, 0);
         const int4 v = __ldcg(reinterpret_cast<const int4*>(
             i < n_solo ? args.solo_tiles + i : args.thin_tiles + (i - n_solo)));
         return FatTile{v.x, v.y, v.z, v.w};
@@ -362,6 +365,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(drained_bar);
+                __syncwarp();   // converged for the warp-wide TMEM loads that follow
             };
             if (kGated && thin) {
                 // 32 of the 128 columns per warp; the row's maximum over the four warps
@@ -456,8 +460,10 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         for (int q = 0; q < 8; ++q)
                             d4[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                     }
+                    __syncwarp();
                 }
             }
+            __syncwarp();
         }
     }
 

@@ -342,6 +342,14 @@ cudaError_t launch_quantize_matrices(const __nv_bfloat16* w, int64_t n, int N, i
 cudaError_t launch_invert_perm(const int32_t* perm, int64_t P, int32_t* inv, int num_sms,
                                cudaStream_t s);
 
+// Routing, route lists, tile list and quantised rows of a small batch, in one
+// launch (fp8_prologue.cu), where it fits.
+bool fp8_prologue_fits(int T);
+cudaError_t launch_fp8_prologue(const float* logits, const __nv_bfloat16* x, int T, int E, int k,
+                                int H, int32_t* idx, float* gates, int32_t* inv_perm,
+                                FatTile* thin_tiles, WsHeader* hdr, uint8_t* xq, uint8_t* xs,
+                                cudaStream_t s);
+
 // Planner over caller-given group offsets [E + 1] of `rows` rows: the tile
 // lists of launch_plan with the offsets forced to be ascending inside
 // [0, rows] (MOE_ERR_BAD_INDEX recorded if they were not, or do not start at 0
@@ -356,6 +364,7 @@ struct Fp8Args {
     const FatTile* thin_tiles;   // experts of at most 32 rows
     WsHeader* hdr;
     int rows;                    // rows of A
+    const int32_t* group;        // one expert: its offsets [2] in place of the lists
     int early_weights;           // one-CTA kernel: the tile lists come from a kernel
                                  // before the previous one, so weights may be copied
                                  // before the dependency wait

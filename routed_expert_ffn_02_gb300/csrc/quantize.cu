@@ -12,22 +12,12 @@
 //   matrices  one CTA per 128 x 128 block, 64 values per thread in registers.
 #include <algorithm>
 
-#include "fp8.cuh"
+#include "quantize_dev.cuh"
 
 namespace moe {
 namespace {
 
 using namespace fp8;
-
-__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
-    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 a = __bfloat1622float2(p[i]);
-        f[2 * i] = a.x;
-        f[2 * i + 1] = a.y;
-    }
-}
 
 // Thread i quantises values [16 i, 16 i + 16) of x [rows, K]; dst == nullptr
 // writes row r to q row r, else to rows dst[r * k .. r * k + k) (a position
@@ -40,25 +30,9 @@ quantize_rows_kernel(const uint4* __restrict__ x, int64_t n16, int per_row,
     ptx::grid_dep_launch();
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n16;
          i += (int64_t)gridDim.x * blockDim.x) {
-        const uint4 a = __ldg(x + 2 * i), b = __ldg(x + 2 * i + 1);
-        float f[16];
-        unpack8(a, f);
-        unpack8(b, f + 8);
-        float m = 0.f;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) m = fmaxf(m, finite_abs(f[j]));
         // n16 is a multiple of 8, so the eight lanes of a block are together
-        const unsigned lanes = 0xffu << (threadIdx.x & 24);
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, o));
-        const uint32_t sb = scale_byte(m);
-        const float inv = inverse_scale(sb);
-        uint4 o;
-        uint32_t* po = reinterpret_cast<uint32_t*>(&o);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            po[j] = pack_e4m3x4(scaled(f[4 * j], inv), scaled(f[4 * j + 1], inv),
-                                scaled(f[4 * j + 2], inv), scaled(f[4 * j + 3], inv));
+        uint32_t sb;
+        const uint4 o = quantize_lane16(__ldg(x + 2 * i), __ldg(x + 2 * i + 1), &sb);
         const int64_t r = i / per_row;
         const int c = (int)(i - r * per_row);
         if (!dst) {
