@@ -179,6 +179,14 @@ def _opt(t: torch.Tensor | None, dtype, shape):
     return None if t is None else _in(t, dtype, shape)
 
 
+def _out(t: torch.Tensor | None, shape, dtype, like: torch.Tensor):
+    """The caller's output tensor, checked, or a new one, and its address."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+        return t, t.data_ptr()
+    return t, _in(t, dtype, shape)
+
+
 def _on(stream, t: torch.Tensor) -> int:
     """The stream to launch on: the caller's, or the current one of t's device."""
     return stream.cuda_stream if stream is not None else _raw_stream(t.get_device())
@@ -575,13 +583,9 @@ def moe_quantize_rows(x: torch.Tensor, q=None, scales=None, stream=None):
     """x [rows, K] bf16 -> (q [rows, K] float8_e4m3fn, scales [rows, K/128]
     uint8): one power-of-two scale 2^(byte - 127) per 128 values of a row."""
     rows, K = x.shape
-    shape = (rows, K // 128)
-    if q is None:
-        q = torch.empty((rows, K), dtype=_E4M3, device=x.device)
-    if scales is None:
-        scales = torch.empty(shape, dtype=_U8, device=x.device)
-    st = _lib.moe_quantize_rows(_in(x, _BF16, (rows, K)), rows, K, _in(q, _E4M3, (rows, K)),
-                                _in(scales, _U8, shape), _on(stream, x))
+    q, qp = _out(q, (rows, K), _E4M3, x)
+    scales, sp = _out(scales, (rows, K // 128), _U8, x)
+    st = _lib.moe_quantize_rows(_in(x, _BF16, (rows, K)), rows, K, qp, sp, _on(stream, x))
     if st:
         raise MoeError(st, "moe_quantize_rows")
     return q, scales
@@ -591,13 +595,9 @@ def moe_quantize_weights(W: torch.Tensor, q=None, scales=None, stream=None):
     """W [E, N, K] bf16 -> (q [E, N, K] float8_e4m3fn, scales [E, N/128, K/128]
     uint8): one power-of-two scale per 128 x 128 block."""
     E, N, K = W.shape
-    shape = (E, N // 128, K // 128)
-    if q is None:
-        q = torch.empty((E, N, K), dtype=_E4M3, device=W.device)
-    if scales is None:
-        scales = torch.empty(shape, dtype=_U8, device=W.device)
-    st = _lib.moe_quantize_weights(_in(W, _BF16, (E, N, K)), E, N, K, _in(q, _E4M3, (E, N, K)),
-                                   _in(scales, _U8, shape), _on(stream, W))
+    q, qp = _out(q, (E, N, K), _E4M3, W)
+    scales, sp = _out(scales, (E, N // 128, K // 128), _U8, W)
+    st = _lib.moe_quantize_weights(_in(W, _BF16, (E, N, K)), E, N, K, qp, sp, _on(stream, W))
     if st:
         raise MoeError(st, "moe_quantize_weights")
     return q, scales
@@ -617,13 +617,12 @@ def moe_grouped_gemm_fp8(x, x_scales, offsets, W, W_scales, y=None, ws: Workspac
     them); y [rows, N] bf16.  E = 1 (offsets [0, rows]) is the dense product."""
     rows, K = x.shape
     E, N, _ = W.shape
-    if y is None:
-        y = torch.empty((rows, N), dtype=_BF16, device=x.device)
+    y, yp = _out(y, (rows, N), _BF16, x)
     ws = ws or Workspace(grouped_gemm_fp8_workspace_size(rows, E), x.device, stream)
     st = _lib.moe_grouped_gemm_fp8(
         _in(x, _E4M3, (rows, K)), _in(x_scales, _U8, (rows, K // 128)), rows,
         _in(offsets, _I32, (E + 1,)), E, N, K, _in(W, _E4M3, (E, N, K)),
-        _in(W_scales, _U8, (E, N // 128, K // 128)), _in(y, _BF16, (rows, N)), ws.addr, ws.nbytes,
+        _in(W_scales, _U8, (E, N // 128, K // 128)), yp, ws.addr, ws.nbytes,
         _on(stream, x))
     if st:
         raise MoeError(st, "moe_grouped_gemm_fp8")
@@ -676,12 +675,11 @@ def moe_expert_ffn_fp8(shape: Shape, x, perm, offsets, experts: Fp8Experts, y_so
                        ws: Workspace | None = None, stream=None):
     """moe_expert_ffn on 8-bit experts (perm, offsets from moe_permute)."""
     P, T, H = shape.P, shape.T, shape.H
-    if y_sorted is None:
-        y_sorted = torch.empty((P, H), dtype=_BF16, device=x.device)
+    y_sorted, yp = _out(y_sorted, (P, H), _BF16, x)
     ws = ws or Workspace(expert_ffn_fp8_workspace_size(shape), x.device, stream)
     st = _lib.moe_expert_ffn_fp8(
         ctypes.byref(shape.c()), _in(x, _BF16, (T, H)), _in(perm, _I32, (P,)),
-        _in(offsets, _I32, (shape.E + 1,)), experts.ref(shape), _in(y_sorted, _BF16, (P, H)),
+        _in(offsets, _I32, (shape.E + 1,)), experts.ref(shape), yp,
         ws.addr, ws.nbytes, _on(stream, x))
     if st:
         raise MoeError(st, "moe_expert_ffn_fp8")
@@ -699,12 +697,11 @@ def moe_forward_fp8(shape: Shape, logits, x, experts: Fp8Experts, out=None, topk
                     gates=None, ws: Workspace | None = None, stream=None):
     """moe_forward on 8-bit experts."""
     T, H, k = shape.T, shape.H, shape.k
-    if out is None:
-        out = torch.empty((T, H), dtype=_BF16, device=x.device)
+    out, op = _out(out, (T, H), _BF16, x)
     ws = ws or Workspace(fp8_workspace_size(shape), x.device, stream)
     st = _lib.moe_forward_fp8(
         ctypes.byref(shape.c()), _in(logits, _F32, (T, shape.E)), _in(x, _BF16, (T, H)),
-        experts.ref(shape), _in(out, _BF16, (T, H)), _opt(topk_idx, _I32, (T, k)),
+        experts.ref(shape), op, _opt(topk_idx, _I32, (T, k)),
         _opt(gates, _F32, (T, k)), ws.addr, ws.nbytes, _on(stream, x))
     if st:
         raise MoeError(st, "moe_forward_fp8")
@@ -726,18 +723,13 @@ def moe_balance(logits, topk_idx, seq_offsets=None, coef: float = 1.0, loss=None
     T, E = logits.shape
     k = topk_idx.shape[1]
     S = _sequences(seq_offsets)
-    dev = logits.device
-    if loss is None:
-        loss = torch.empty((), dtype=_F32, device=dev)
-    if counts is None:
-        counts = torch.empty((S, E), dtype=_I32, device=dev)
-    if stats is None:
-        stats = torch.empty((T, 2), dtype=_F32, device=dev)
-    ws = ws or Workspace(balance_workspace_size(T, E, S), dev, stream)
+    loss, lp = _out(loss, (), _F32, logits)
+    counts, cp = _out(counts, (S, E), _I32, logits)
+    stats, sp = _out(stats, (T, 2), _F32, logits)
+    ws = ws or Workspace(balance_workspace_size(T, E, S), logits.device, stream)
     st = _lib.moe_balance(
         _in(logits, _F32, (T, E)), _in(topk_idx, _I32, (T, k)), T, E, k,
-        _opt(seq_offsets, _I32, (S + 1,)), S, coef, _in(loss, _F32, ()), _in(counts, _I32, (S, E)),
-        _in(stats, _F32, (T, 2)), ws.addr, ws.nbytes, _on(stream, logits))
+        _opt(seq_offsets, _I32, (S + 1,)), S, coef, lp, cp, sp, ws.addr, ws.nbytes, _on(stream, logits))
     if st:
         raise MoeError(st, "moe_balance")
     return loss, counts, stats
@@ -751,13 +743,12 @@ def moe_balance_backward(logits, stats, counts, k: int, seq_offsets=None, coef: 
     the router's gates.  Returns d_logits [T, E] fp32."""
     T, E = logits.shape
     S = _sequences(seq_offsets)
-    if d_logits is None:
-        d_logits = torch.empty((T, E), dtype=_F32, device=logits.device)
+    d_logits, dp = _out(d_logits, (T, E), _F32, logits)
     st = _lib.moe_balance_backward(
         _in(logits, _F32, (T, E)), _in(stats, _F32, (T, 2)), _in(counts, _I32, (S, E)),
         _opt(seq_offsets, _I32, (S + 1,)), T, E, k, S, coef, _opt(d_loss, _F32, ()),
         _opt(topk_idx, _I32, (T, k)), _opt(gates, _F32, (T, k)), _opt(d_gates, _F32, (T, k)),
-        _in(d_logits, _F32, (T, E)), _on(stream, logits))
+        dp, _on(stream, logits))
     if st:
         raise MoeError(st, "moe_balance_backward")
     return d_logits

@@ -144,18 +144,12 @@ size_t carve_fwd(const moe_shape* sh, void* ws, FwdBufs* b) {
     return align_up(c.off, 256);
 }
 
-struct BalanceBufs {
-    WsHeader* hdr;
-    float *part_p, *seq_loss;
-    int32_t* part_c;
-};
-size_t carve_balance(int32_t T, int32_t E, int32_t S, void* ws, BalanceBufs* b) {
-    const size_t n = (size_t)(balance_partial_rows(T, S) * E);
+// Places the scratch of the balance loss; returns its bytes.
+size_t carve_balance(void* ws, BalanceArgs* a) {
     Carver c(ws);
-    b->hdr = c.take<WsHeader>(1);
-    b->seq_loss = c.take<float>((size_t)S);
-    b->part_p = c.take<float>(n);
-    b->part_c = c.take<int32_t>(n);
+    a->hdr = c.take<WsHeader>(1);
+    a->shares = c.take<float>((size_t)balance_shares(a->E, a->S));
+    a->part = c.take<float2>((size_t)(balance_partial_rows(a->T, a->S) * a->E));
     return align_up(c.off, 256);
 }
 
@@ -218,7 +212,7 @@ moe_status check_balance_args(int32_t T, int32_t E, int32_t k, int32_t S, bool h
     if ((int64_t)T * k > (int64_t)INT32_MAX - kTileM)
         return fail(MOE_ERR_INVALID_ARG, "T*k = %lld too large", (long long)T * k);
     if (S < 1) return fail(MOE_ERR_INVALID_ARG, "S = %d < 1", S);
-    if (S > INT32_MAX - kBalanceChunk - T)
+    if (S > INT32_MAX / 2)
         return fail(MOE_ERR_INVALID_ARG, "S = %d too large", S);
     if (!have_seq && S != 1)
         return fail(MOE_ERR_INVALID_ARG, "S = %d without seq_offsets", S);
@@ -375,8 +369,11 @@ moe_status moe_forward_fp8(const moe_shape* shape, const float* logits, const mo
 
 size_t moe_balance_workspace_size(int32_t T, int32_t E, int32_t S) {
     if (check_balance_args(T, E, 1, S, true) != MOE_OK) return 0;
-    BalanceBufs b;
-    return carve_balance(T, E, S, nullptr, &b);
+    BalanceArgs a = {};
+    a.T = T;
+    a.E = E;
+    a.S = S;
+    return carve_balance(nullptr, &a);
 }
 
 moe_status moe_balance(const float* logits, const int32_t* topk_idx, int32_t T, int32_t E,
@@ -387,15 +384,22 @@ moe_status moe_balance(const float* logits, const int32_t* topk_idx, int32_t T, 
     if (!loss || !counts || (T > 0 && (!logits || !topk_idx || !stats)))
         return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
     if (!aligned(stats, 8)) return fail(MOE_ERR_INVALID_ARG, "stats is not 8-byte aligned");
-    BalanceBufs b;
-    STATUS_TRY(check_ws(ws, ws_bytes, carve_balance(T, E, S, nullptr, &b)));
-    carve_balance(T, E, S, ws, &b);
+    BalanceArgs a = {};
+    a.T = T;
+    a.E = E;
+    a.k = k;
+    a.S = S;
+    a.seq = seq_offsets;
+    a.coef = coef;
+    a.loss = loss;
+    a.counts = counts;
+    STATUS_TRY(check_ws(ws, ws_bytes, carve_balance(nullptr, &a)));
+    carve_balance(ws, &a);
     int sms = 0;
     STATUS_TRY(current_device(&sms));
     const PdlScope pdl(true);
-    CUDA_TRY(launch_balance(logits, topk_idx, T, E, k, seq_offsets, S, coef, loss, counts,
-                            (float2*)stats, b.part_p, b.part_c, b.seq_loss, b.hdr,
-                            (cudaStream_t)stream), "balance");
+    CUDA_TRY(launch_balance(logits, topk_idx, (float2*)stats, a, sms, (cudaStream_t)stream),
+             "balance");
     return ok();
 }
 
@@ -412,10 +416,18 @@ moe_status moe_balance_backward(const float* logits, const float* stats, const i
         return fail(MOE_ERR_INVALID_ARG, "topk_idx, gates and d_gates come together");
     int sms = 0;
     STATUS_TRY(current_device(&sms));
+    BalanceArgs a = {};
+    a.T = T;
+    a.E = E;
+    a.k = k;
+    a.S = S;
+    a.seq = seq_offsets;
+    a.coef = coef;
+    a.counts = const_cast<int32_t*>(counts);   // read only there
     const PdlScope pdl(true);
-    CUDA_TRY(launch_balance_backward(logits, (const float2*)stats, counts, seq_offsets, T, E, k, S,
-                                     coef, d_loss, topk_idx, gates, d_gates, d_logits, sms,
-                                     (cudaStream_t)stream), "balance backward");
+    CUDA_TRY(launch_balance_backward(logits, (const float2*)stats, d_loss, topk_idx, gates,
+                                     d_gates, d_logits, a, sms, (cudaStream_t)stream),
+             "balance backward");
     return ok();
 }
 

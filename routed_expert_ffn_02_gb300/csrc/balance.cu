@@ -14,23 +14,32 @@
 // the second line being the gradient of the router's gates (the softmax over
 // the selected logits), added when the gates' gradient is given.
 //
-// Forward: a CTA takes kBalanceChunk tokens, a warp per token, the row in
-// registers; probabilities add up per lane over the warp's tokens, then over
-// the CTA's warps in order, then (second kernel) over the chunks in order, all
-// fp32: no floating-point atomics, so repeated runs give the same bits.  A
-// chunk that several sequences share writes one partial row per sequence:
-// chunk c and sequence s meet in row c + s, which no other pair of the
-// staircase uses.
+// Forward: bound by HBM (4 T E bytes read) for large batches, by latency for
+// small ones.  One CTA per SM takes a chunk of consecutive tokens, a warp per
+// token, the row in registers (16-byte loads); probabilities add up per lane
+// over the warp's tokens, then over the CTA's warps in order, then over the
+// chunks in order, all fp32: no floating-point atomics, so repeated runs give
+// the same bits.  A chunk that several sequences share writes one partial row
+// per sequence: chunk c and sequence s meet in row c + s, which no other pair
+// of the staircase uses.  The last CTA to finish adds the chunks up; with more
+// than kFusedSequences sequences that would be one CTA's work for too many
+// rows, and a second kernel does it with a CTA per sequence (a second launch
+// for the usual one sequence cost 2 us of a 30 us host-bound call).
+//
+// Backward: bound by HBM (4 T E read, 4 T E written).  A warp per token, as
+// many consecutive ones as fill the GPU once, so that the coefficients a_se of
+// their common sequence stay in registers.
 #include <algorithm>
 
 #include "moe_internal.cuh"
 #include "ptx.cuh"
-#include "route_dev.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kFusedChunks = 4;
+constexpr int kSlice = 32;           // experts per CTA of the second kernel
+constexpr int kFold = 8;             // shared rows that a CTA's warps add into in turn
 
 // Token range of sequence s, inside [0, T]; seq == nullptr: one sequence.
 struct SeqRange {
@@ -56,6 +65,10 @@ __device__ __forceinline__ int tokens_of(const int32_t* seq, int S, int T) {
     const int b = min(max(__ldg(seq), 0), T), e = min(max(__ldg(seq + S), 0), T);
     return max(e - b, 0);
 }
+// a_se per counted slot: coef E / (k n_s T').
+__device__ __forceinline__ float slot_weight(float coef, int E, int k, int n, int total) {
+    return n > 0 ? coef * (float)E / ((float)k * (float)n * (float)max(total, 1)) : 0.f;
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -68,236 +81,399 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
-// Partial sums of one chunk: part_p[c + s][e], part_c[c + s][e], and each
-// token's (row maximum, 1 / sum of exponentials).  A row of -inf alone has
-// the pair (0, 0): no probability anywhere.
-template <int EPL>
-__global__ void __launch_bounds__(32 * kWarps)
-balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx, int T,
-                       int E, int k, const int32_t* __restrict__ seq, int S,
-                       float2* __restrict__ stats, float* __restrict__ part_p,
-                       int32_t* __restrict__ part_c, WsHeader* hdr) {
+// A row of E values in registers: lane l holds values 4 (l + 32 v) + c at
+// [4 v + c].  vec: the rows are 16-byte aligned and E a multiple of 4.
+template <int V>
+__device__ __forceinline__ void load_row(const float* row, int E, bool vec, float fill,
+                                         float (&r)[4 * V]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = 4 * (lane + 32 * v);
+        if (vec) {
+            float4 x = make_float4(fill, fill, fill, fill);
+            if (e < E) x = __ldg(reinterpret_cast<const float4*>(row + e));
+            r[4 * v] = x.x;
+            r[4 * v + 1] = x.y;
+            r[4 * v + 2] = x.z;
+            r[4 * v + 3] = x.w;
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) r[4 * v + c] = e + c < E ? __ldg(row + e + c) : fill;
+        }
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_row(float* row, int E, bool vec, const float (&r)[4 * V]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = 4 * (lane + 32 * v);
+        if (vec) {
+            if (e < E)
+                *reinterpret_cast<float4*>(row + e) =
+                    make_float4(r[4 * v], r[4 * v + 1], r[4 * v + 2], r[4 * v + 3]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (e + c < E) row[e + c] = r[4 * v + c];
+        }
+    }
+}
+
+// Chunks of sequence s and its a_se per counted slot.
+struct SeqSum {
+    int c0, c1;
+    float w;
+};
+__device__ __forceinline__ SeqSum seq_sum(const BalanceArgs& a, int s) {
+    const SeqRange r = seq_range(a.seq, s, a.T);
+    const int n = r.end - r.beg;
+    const int c0 = r.beg / a.chunk;
+    return {c0, n > 0 ? (r.end - 1) / a.chunk + 1 : c0,
+            slot_weight(a.coef, a.E, a.k, n, tokens_of(a.seq, a.S, a.T))};
+}
+
+// Partial sums of one chunk: part[c + s][e] = (sum of p, count), and each
+// token's (row maximum, 1 / sum of exponentials).  A row of -inf alone has the
+// pair (0, 0): no probability anywhere.
+template <int V, int W>
+__global__ void __launch_bounds__(32 * W)
+balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
+               float2* __restrict__ stats, BalanceArgs a, int fused) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    __shared__ float sum[kWarps][kMaxE];
-    __shared__ int hist[kMaxE];
+    __shared__ __align__(16) float sum[kFold][128 * V];
+    __shared__ int hist[128 * V];
+    __shared__ float red[W];
+    __shared__ int last;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int c = blockIdx.x;
-    const int beg = c * kBalanceChunk, end = min(T, beg + kBalanceChunk);
-    for (int s = seq_of(seq, S, beg); s < S; ++s) {
-        const SeqRange r = seq_range(seq, s, T);
+    const int c = blockIdx.x, E = a.E, k = a.k;
+    const int beg = c * a.chunk, end = min(a.T, beg + a.chunk);
+    const bool vec = a.vec;
+    for (int s = seq_of(a.seq, a.S, beg); s < a.S; ++s) {
+        const SeqRange r = seq_range(a.seq, s, a.T);
         if (r.beg >= end) break;
         const int t0 = max(beg, r.beg), t1 = min(end, r.end);
         if (t0 >= t1) continue;
-        for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
+        for (int e = threadIdx.x; e < E; e += 32 * W) hist[e] = 0;
         __syncthreads();
-        for (int i = t0 * k + threadIdx.x; i < t1 * k; i += blockDim.x) {
+        for (int i = t0 * k + threadIdx.x; i < t1 * k; i += 32 * W) {
             const int e = __ldg(idx + i);
             if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
-            else set_status(hdr, MOE_ERR_BAD_INDEX);
+            else set_status(a.hdr, MOE_ERR_BAD_INDEX);
         }
-        float acc[EPL];
+        float acc[4 * V];
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) acc[j] = 0.f;
-        for (int t = t0 + w; t < t1; t += kWarps) {
-            const float* row = logits + (int64_t)t * E;
-            float v[EPL];
+        for (int j = 0; j < 4 * V; ++j) acc[j] = 0.f;
+        float next[4 * V];
+        if (t0 + w < t1) load_row<V>(logits + (int64_t)(t0 + w) * E, E, vec, -INFINITY, next);
+        for (int t = t0 + w; t < t1; t += W) {
+            float v[4 * V];
             float m = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) {
-                const int e = lane + 32 * j;
-                v[j] = e < E ? __ldg(row + e) : -INFINITY;
+            for (int j = 0; j < 4 * V; ++j) {
+                v[j] = next[j];
                 m = fmaxf(m, v[j]);
             }
+            if (t + W < t1) load_row<V>(logits + (int64_t)(t + W) * E, E, vec, -INFINITY, next);
             m = warp_max(m);
             if (m == -INFINITY) m = 0.f;
             float z = 0.f;
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) {
+            for (int j = 0; j < 4 * V; ++j) {
                 v[j] = expf(v[j] - m);
                 z += v[j];
             }
             z = warp_sum(z);
             const float inv = z == 0.f ? 0.f : 1.f / z;
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) acc[j] = fmaf(v[j], inv, acc[j]);
+            for (int j = 0; j < 4 * V; ++j) acc[j] = fmaf(v[j], inv, acc[j]);
             if (lane == 0) stats[t] = make_float2(m, inv);
         }
+        // warps 0-7 store their sums, 8-15 add theirs, ...
 #pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (lane + 32 * j < E) sum[w][lane + 32 * j] = acc[j];
-        __syncthreads();
+        for (int f = 0; f < W / kFold; ++f) {
+            if (w / kFold == f) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float4* p = reinterpret_cast<float4*>(&sum[w % kFold][4 * (lane + 32 * v)]);
+                    float4 x = f ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x.x += acc[4 * v];
+                    x.y += acc[4 * v + 1];
+                    x.z += acc[4 * v + 2];
+                    x.w += acc[4 * v + 3];
+                    *p = x;
+                }
+            }
+            __syncthreads();
+        }
         const int64_t out = (int64_t)(c + s) * E;
-        for (int e = threadIdx.x; e < E; e += blockDim.x) {
-            float a = 0.f;
+        for (int e = threadIdx.x; e < E; e += 32 * W) {
+            float x = 0.f;
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) a += sum[i][e];
-            part_p[out + e] = a;
-            part_c[out + e] = hist[e];
+            for (int i = 0; i < kFold; ++i) x += sum[i][e];
+            a.part[out + e] = make_float2(x, __int_as_float(hist[e]));
         }
         __syncthreads();
     }
-}
-
-// One CTA per sequence: counts and the sequence's share of the loss; the last
-// CTA adds the shares in order.
-__global__ void __launch_bounds__(256)
-balance_finish_kernel(const float* __restrict__ part_p, const int32_t* __restrict__ part_c, int T,
-                      int E, int k, const int32_t* __restrict__ seq, int S, float coef,
-                      int32_t* __restrict__ counts, float* seq_loss, float* loss, WsHeader* hdr) {
-    ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
-    __shared__ float red[8];
-    __shared__ int last;
-    const int s = blockIdx.x;
-    const SeqRange r = seq_range(seq, s, T);
-    const int n = r.end - r.beg;
-    const int c0 = r.beg / kBalanceChunk, c1 = n > 0 ? (r.end - 1) / kBalanceChunk + 1 : c0;
-    const float total = (float)max(tokens_of(seq, S, T), 1);
-    const float scale = n > 0 ? coef * (float)E / ((float)k * (float)n * total) : 0.f;
-    float mine = 0.f;
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        float p = 0.f;
-        int q = 0;
-        for (int c = c0; c < c1; ++c) {
-            p += part_p[(int64_t)(c + s) * E + e];
-            q += part_c[(int64_t)(c + s) * E + e];
-        }
-        counts[(int64_t)s * E + e] = q;
-        mine = fmaf(scale * (float)q, p, mine);
-    }
-    mine = warp_sum(mine);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mine;
+    if (!fused) return;
+    __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
-        float a = 0.f;
-        for (int i = 0; i < 8; ++i) a += red[i];
-        seq_loss[s] = a;
-        __threadfence();
-        last = atomicAdd(&hdr->ticket, 1) == S - 1;
-        if (last) hdr->ticket = 0;
+        last = atomicAdd(&a.hdr->ticket, 1) == (int)gridDim.x - 1;
+        if (last) a.hdr->ticket = 0;
     }
     __syncthreads();
-    if (!last || threadIdx.x >= 32) return;
+    if (!last) return;
     __threadfence();
-    float a = 0.f;
-    for (int i = threadIdx.x; i < S; i += 32) a += __ldcg(seq_loss + i);
-    a = warp_sum(a);
-    if (threadIdx.x == 0) *loss = a;
+    // one sequence of at most kFusedChunks chunks
+    const SeqSum q = seq_sum(a, 0);
+    float mine = 0.f;
+    for (int e = threadIdx.x; e < E; e += 32 * W) {
+        float p = 0.f;
+        int n = 0;
+        for (int i = q.c0; i < q.c1; ++i) {
+            const float2 v = __ldcg(a.part + (int64_t)i * E + e);
+            p += v.x;
+            n += __float_as_int(v.y);
+        }
+        a.counts[e] = n;
+        mine = fmaf(q.w * (float)n, p, mine);
+    }
+    mine = warp_sum(mine);
+    if (lane == 0) red[w] = mine;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float loss = 0.f;
+        for (int i = 0; i < W; ++i) loss += red[i];
+        *a.loss = loss;
+    }
 }
 
-template <int EPL>
-__global__ void __launch_bounds__(32 * kWarps)
+// CTA (x, y): kSlice experts (a lane each) of sequences y, y + gridDim.y, ...;
+// warp w adds chunks w, w + 8, ..., then the warps' sums are added in order.
+// The last CTA adds the slices' shares of the loss.
+__global__ void __launch_bounds__(256)
+balance_finish_kernel(BalanceArgs a) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    __shared__ float sum[8][kSlice];
+    __shared__ int count[8][kSlice];
+    __shared__ float red[8];
+    __shared__ int last;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int e = blockIdx.x * kSlice + lane;
+    float share = 0.f;
+    for (int s = blockIdx.y; s < a.S; s += gridDim.y) {
+        const SeqSum q = seq_sum(a, s);
+        float p = 0.f;
+        int n = 0;
+        if (e < a.E) {
+#pragma unroll 8
+            for (int c = q.c0 + w; c < q.c1; c += 8) {
+                const float2 v = __ldg(a.part + (int64_t)(c + s) * a.E + e);
+                p += v.x;
+                n += __float_as_int(v.y);
+            }
+        }
+        sum[w][lane] = p;
+        count[w][lane] = n;
+        __syncthreads();
+        if (w == 0) {
+#pragma unroll
+            for (int i = 1; i < 8; ++i) {
+                p += sum[i][lane];
+                n += count[i][lane];
+            }
+            if (e < a.E) a.counts[(int64_t)s * a.E + e] = n;
+            share = fmaf(q.w * (float)n, p, share);
+        }
+        __syncthreads();
+    }
+    if (w == 0) {
+        share = warp_sum(share);
+        if (lane == 0) {
+            a.shares[blockIdx.y * gridDim.x + blockIdx.x] = share;
+            __threadfence();
+            const int n = (int)(gridDim.x * gridDim.y);
+            last = atomicAdd(&a.hdr->ticket, 1) == n - 1;
+            if (last) a.hdr->ticket = 0;
+        }
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    float loss = 0.f;
+    for (int i = threadIdx.x; i < (int)(gridDim.x * gridDim.y); i += 256) loss += __ldcg(a.shares + i);
+    loss = warp_sum(loss);
+    if (lane == 0) red[w] = loss;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float v = 0.f;
+        for (int i = 0; i < 8; ++i) v += red[i];
+        *a.loss = v;
+    }
+}
+
+template <int V>
+__global__ void __launch_bounds__(256, V <= 3 ? 3 : 2)
 balance_backward_kernel(const float* __restrict__ logits, const float2* __restrict__ stats,
-                        const int32_t* __restrict__ counts, const int32_t* __restrict__ seq, int T,
-                        int E, int k, int S, float coef, const float* __restrict__ d_loss,
+                        const int32_t* __restrict__ counts, const float* __restrict__ d_loss,
                         const int32_t* __restrict__ idx, const float* __restrict__ gates,
-                        const float* __restrict__ d_gates, float* __restrict__ d_logits) {
+                        const float* __restrict__ d_gates, float* __restrict__ d_logits,
+                        BalanceArgs a) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int lane = threadIdx.x & 31;
-    const float total = (float)max(tokens_of(seq, S, T), 1);
+    const int E = a.E, k = a.k;
+    const bool vec = a.vec;
+    const int total = tokens_of(a.seq, a.S, a.T);
     const float up = d_loss ? __ldg(d_loss) : 1.f;
-    for (int t = blockIdx.x * kWarps + (threadIdx.x >> 5); t < T; t += gridDim.x * kWarps) {
-        const int s = seq_of(seq, S, t);
-        const SeqRange r = seq_range(seq, s, T);
+    const int t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * a.chunk, t1 = min(a.T, t0 + a.chunk);
+    int s = -1;
+    SeqRange r{0, 0};
+    float coef[4 * V];   // d_loss * a_se of the current sequence
+    float next[4 * V];   // the next token's row (read also for tokens of no sequence)
+    float2 st_next = make_float2(0.f, 0.f);
+    auto fetch = [&](int t) {
+        load_row<V>(logits + (int64_t)t * E, E, vec, -INFINITY, next);
+        st_next = __ldg(stats + t);
+    };
+    if (t0 < t1) fetch(t0);
+    for (int t = t0; t < t1; ++t) {
+        if (s < 0 || t >= r.end) {
+            s = seq_of(a.seq, a.S, t);
+            r = seq_range(a.seq, s, a.T);
+            const float w = up * slot_weight(a.coef, E, k, r.end - r.beg, total);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int e = 4 * (lane + 32 * v) + c;
+                    coef[4 * v + c] = e < E ? w * (float)__ldg(counts + (int64_t)s * E + e) : 0.f;
+                }
+        }
         const bool inside = t >= r.beg && t < r.end;
-        const float a0 = inside ? coef * (float)E / ((float)k * (float)(r.end - r.beg) * total) : 0.f;
-        float d[EPL];
+        float d[4 * V];
+        int e_sel = -1;
+        float add = 0.f;
+        if (idx && lane < k) {
+            e_sel = __ldg(idx + (int64_t)t * k + lane);
+            add = __ldg(gates + (int64_t)t * k + lane);
+        }
+        const float dg = idx && lane < k ? __ldg(d_gates + (int64_t)t * k + lane) : 0.f;
+        float p[4 * V];
+#pragma unroll
+        for (int j = 0; j < 4 * V; ++j) p[j] = next[j];
+        const float2 st = st_next;
+        if (t + 1 < t1) fetch(t + 1);
         if (inside) {
-            const float* row = logits + (int64_t)t * E;
-            const int32_t* cnt = counts + (int64_t)s * E;
-            const float2 st = __ldg(stats + t);
-            float p[EPL];
             float dot = 0.f;
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) {
-                const int e = lane + 32 * j;
-                p[j] = e < E ? expf(__ldg(row + e) - st.x) * st.y : 0.f;
-                d[j] = e < E ? a0 * (float)__ldg(cnt + e) : 0.f;
-                dot = fmaf(p[j], d[j], dot);
+            for (int j = 0; j < 4 * V; ++j) {
+                p[j] = expf(p[j] - st.x) * st.y;
+                dot = fmaf(p[j], coef[j], dot);
             }
             dot = warp_sum(dot);
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) d[j] = up * p[j] * (d[j] - dot);
+            for (int j = 0; j < 4 * V; ++j) d[j] = p[j] * (coef[j] - dot);
         } else {
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) d[j] = 0.f;
+            for (int j = 0; j < 4 * V; ++j) d[j] = 0.f;
         }
         if (idx) {
-            const float g = lane < k ? __ldg(gates + (int64_t)t * k + lane) : 0.f;
-            const float dg = lane < k ? __ldg(d_gates + (int64_t)t * k + lane) : 0.f;
-            const int e = lane < k ? __ldg(idx + (int64_t)t * k + lane) : -1;
-            const float add = g * (dg - warp_sum(g * dg));
+            // Lane j of the first k holds slot j's gradient; value e lives in
+            // lane (e / 4) mod 32.  Each pass hands every lane the first of
+            // its slots (k slots over 32 lanes: one or two passes).
+            add *= dg - warp_sum(add * dg);
+            unsigned left = 0;
             for (int i = 0; i < k; ++i) {
-                const int ei = __shfl_sync(0xffffffffu, e, i);
-                const float ai = __shfl_sync(0xffffffffu, add, i);
+                const int e = __shfl_sync(0xffffffffu, e_sel, i);
+                if (((e >> 2) & 31) == lane && (unsigned)e < (unsigned)E) left |= 1u << i;
+            }
+            while (__any_sync(0xffffffffu, left != 0)) {
+                const int i = left ? __ffs(left) - 1 : 0;
+                const int e = __shfl_sync(0xffffffffu, e_sel, i);
+                const float x = __shfl_sync(0xffffffffu, add, i);
+                const int at = left ? (e >> 7) * 4 + (e & 3) : -1;
 #pragma unroll
-                for (int j = 0; j < EPL; ++j)
-                    if (ei == lane + 32 * j) d[j] += ai;
+                for (int j = 0; j < 4 * V; ++j)
+                    if (j == at) d[j] += x;
+                left &= left - 1;
             }
         }
-        float* out = d_logits + (int64_t)t * E;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (lane + 32 * j < E) out[lane + 32 * j] = d[j];
+        store_row<V>(d_logits + (int64_t)t * E, E, vec, d);
     }
 }
+
+bool rows_aligned(const void* p, int E) {
+    return E % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+}
+
+// Calls f.template operator()<V>() for the smallest V with 128 V >= E.
+template <typename F>
+cudaError_t with_width(int E, F&& f) {
+    switch ((E + 127) / 128) {
+        case 1: return f.template operator()<1>();
+        case 2: return f.template operator()<2>();
+        case 3: return f.template operator()<3>();
+        case 4: return f.template operator()<4>();
+        case 5:
+        case 6: return f.template operator()<6>();
+        default: return f.template operator()<8>();
+    }
+}
+
+constexpr int kMaxChunks = 512;   // CTAs of the forward pass
+constexpr int kMaxRows = 256;     // CTAs per slice of the second kernel
+constexpr int warps_for(int V) { return V <= 3 ? 32 : 16; }   // 64 / 128 registers a thread
 
 }  // namespace
 
 int64_t balance_partial_rows(int T, int S) {
-    return ((int64_t)T + kBalanceChunk - 1) / kBalanceChunk + S;
+    return std::min<int64_t>(((int64_t)T + 15) / 16, kMaxChunks) + S;
 }
 
-cudaError_t launch_balance(const float* logits, const int32_t* idx, int T, int E, int k,
-                           const int32_t* seq, int S, float coef, float* loss, int32_t* counts,
-                           float2* stats, float* part_p, int32_t* part_c, float* seq_loss,
-                           WsHeader* hdr, cudaStream_t s) {
-    const int chunks = (T + kBalanceChunk - 1) / kBalanceChunk;
+int64_t balance_shares(int E, int S) {
+    return (int64_t)((E + kSlice - 1) / kSlice) * std::min(S, kMaxRows);
+}
+
+cudaError_t launch_balance(const float* logits, const int32_t* idx, float2* stats, BalanceArgs a,
+                           int num_sms, cudaStream_t s) {
+    bool fused = false;
+    a.vec = rows_aligned(logits, a.E);
+    a.chunk = 16;
     cudaError_t e = cudaSuccess;
-    auto go = [&](auto kernel) {
-        return launch_pdl(kernel, dim3(chunks), dim3(32 * kWarps), 0, s, logits, idx, T, E, k, seq,
-                          S, stats, part_p, part_c, hdr);
-    };
-    if (chunks > 0) {
-        switch (routing::candidates_per_lane(E)) {
-            case 1: e = go(balance_partial_kernel<1>); break;
-            case 2: e = go(balance_partial_kernel<2>); break;
-            case 4: e = go(balance_partial_kernel<4>); break;
-            case 8: e = go(balance_partial_kernel<8>); break;
-            case 12: e = go(balance_partial_kernel<12>); break;
-            case 16: e = go(balance_partial_kernel<16>); break;
-            case 24: e = go(balance_partial_kernel<24>); break;
-            default: e = go(balance_partial_kernel<32>); break;
-        }
+    if (a.T > 0) {
+        e = with_width(a.E, [&]<int V>() {
+            constexpr int W = warps_for(V);
+            const int most = std::min(num_sms, kMaxChunks);
+            a.chunk = std::max(W, (a.T + most - 1) / most);
+            const int chunks = (a.T + a.chunk - 1) / a.chunk;
+            fused = a.S == 1 && chunks <= kFusedChunks;
+            return launch_pdl(balance_kernel<V, W>, dim3(chunks), dim3(32 * W), 0, s, logits, idx,
+                              stats, a, (int)fused);
+        });
     }
-    if (e != cudaSuccess) return e;
-    return launch_pdl(balance_finish_kernel, dim3(S), dim3(256), 0, s, (const float*)part_p,
-                      (const int32_t*)part_c, T, E, k, seq, S, coef, counts, seq_loss, loss, hdr);
+    if (e != cudaSuccess || fused) return e;
+    return launch_pdl(balance_finish_kernel,
+                      dim3((a.E + kSlice - 1) / kSlice, std::min(a.S, kMaxRows)), dim3(256), 0, s, a);
 }
 
-cudaError_t launch_balance_backward(const float* logits, const float2* stats,
-                                    const int32_t* counts, const int32_t* seq, int T, int E, int k,
-                                    int S, float coef, const float* d_loss, const int32_t* idx,
-                                    const float* gates, const float* d_gates, float* d_logits,
-                                    int num_sms, cudaStream_t s) {
-    if (T == 0) return cudaSuccess;
-    const int blocks = (int)std::min<int64_t>((T + kWarps - 1) / kWarps, (int64_t)num_sms * 16);
-    auto go = [&](auto kernel) {
-        return launch_pdl(kernel, dim3(blocks), dim3(32 * kWarps), 0, s, logits, stats, counts, seq,
-                          T, E, k, S, coef, d_loss, idx, gates, d_gates, d_logits);
-    };
-    switch (routing::candidates_per_lane(E)) {
-        case 1: return go(balance_backward_kernel<1>);
-        case 2: return go(balance_backward_kernel<2>);
-        case 4: return go(balance_backward_kernel<4>);
-        case 8: return go(balance_backward_kernel<8>);
-        case 12: return go(balance_backward_kernel<12>);
-        case 16: return go(balance_backward_kernel<16>);
-        case 24: return go(balance_backward_kernel<24>);
-        default: return go(balance_backward_kernel<32>);
-    }
+cudaError_t launch_balance_backward(const float* logits, const float2* stats, const float* d_loss,
+                                    const int32_t* idx, const float* gates, const float* d_gates,
+                                    float* d_logits, BalanceArgs a, int num_sms, cudaStream_t s) {
+    if (a.T == 0) return cudaSuccess;
+    a.vec = rows_aligned(logits, a.E) && rows_aligned(d_logits, a.E);
+    const int warps = num_sms * (a.E <= 384 ? 24 : 16);   // resident at once
+    a.chunk = (a.T + warps - 1) / warps;
+    const int per_block = 8 * a.chunk;
+    return with_width(a.E, [&]<int V>() {
+        return launch_pdl(balance_backward_kernel<V>, dim3((a.T + per_block - 1) / per_block),
+                          dim3(256), 0, s, logits, stats, (const int32_t*)a.counts, d_loss, idx,
+                          gates, d_gates, d_logits, a);
+    });
 }
 
 }  // namespace moe

@@ -393,17 +393,25 @@ cudaError_t launch_fp8_solo(const uint8_t* a, int64_t rows, const uint8_t* b, co
                             int E, int num_sms, cudaStream_t s);
 
 // ---- balance loss (balance.cu) ----
-constexpr int kBalanceChunk = 64;    // tokens per CTA of the forward pass
+struct BalanceArgs {
+    int T, E, k, S;
+    const int32_t* seq;    // [S + 1], or nullptr: one sequence of all tokens
+    float coef;
+    float* loss;           // [1]
+    int32_t* counts;       // [S, E]
+    float2* part;          // [balance_partial_rows, E]: (sum of p, count)
+    float* shares;         // [balance_shares]: parts of the loss
+    WsHeader* hdr;
+    int chunk;             // consecutive tokens per CTA (backward: per warp); set by the launchers
+    int vec;               // rows are 16-byte aligned; set by the launchers
+};
 int64_t balance_partial_rows(int T, int S);
-cudaError_t launch_balance(const float* logits, const int32_t* idx, int T, int E, int k,
-                           const int32_t* seq, int S, float coef, float* loss, int32_t* counts,
-                           float2* stats, float* part_p, int32_t* part_c, float* seq_loss,
-                           WsHeader* hdr, cudaStream_t s);
-cudaError_t launch_balance_backward(const float* logits, const float2* stats,
-                                    const int32_t* counts, const int32_t* seq, int T, int E, int k,
-                                    int S, float coef, const float* d_loss, const int32_t* idx,
-                                    const float* gates, const float* d_gates, float* d_logits,
-                                    int num_sms, cudaStream_t s);
+int64_t balance_shares(int E, int S);
+cudaError_t launch_balance(const float* logits, const int32_t* idx, float2* stats, BalanceArgs a,
+                           int num_sms, cudaStream_t s);
+cudaError_t launch_balance_backward(const float* logits, const float2* stats, const float* d_loss,
+                                    const int32_t* idx, const float* gates, const float* d_gates,
+                                    float* d_logits, BalanceArgs a, int num_sms, cudaStream_t s);
 
 // Experts to copy: entry j copies expert src_e[j] of the source matrices
 // into block dst_e[j] of the destination matrices.

@@ -5,7 +5,7 @@
 // 1 + 1/16384 (matrices) written per value.
 //
 //   rows      eight lanes hold a 1 x 128 block, 16 values (32 bytes) each:
-//             two 16-byte loads, three shuffles for the maximum, one 16-byte
+//             one 32-byte load, three shuffles for the maximum, one 16-byte
 //             store.  The same kernel writes the rows of the experts' input:
 //             token t's quantised row goes to its k sorted positions, so a
 //             token is read and quantised once however many experts it has.
@@ -19,38 +19,50 @@ namespace {
 
 using namespace fp8;
 
-// Thread i quantises values [16 i, 16 i + 16) of x [rows, K]; dst == nullptr
+// Vector i is the values [16 i, 16 i + 16) of x [rows, K]; dst == nullptr
 // writes row r to q row r, else to rows dst[r * k .. r * k + k) (a position
 // outside [0, P) is skipped: route lists of a bad index leave it unset).
+template <int U>
 __global__ void __launch_bounds__(256)
 quantize_rows_kernel(const uint4* __restrict__ x, int64_t n16, int per_row,
                      const int32_t* __restrict__ dst, int k, int64_t P, uint4* __restrict__ q,
                      uint8_t* __restrict__ scales) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n16;
-         i += (int64_t)gridDim.x * blockDim.x) {
-        // n16 is a multiple of 8, so the eight lanes of a block are together
-        uint32_t sb;
-        const uint4 o = quantize_lane16(__ldg(x + 2 * i), __ldg(x + 2 * i + 1), &sb);
-        const int64_t r = i / per_row;
-        const int c = (int)(i - r * per_row);
+    auto put = [&](int64_t i, const uint4& o, uint32_t sb) {
         if (!dst) {
             q[i] = o;
             if ((threadIdx.x & 7) == 0) scales[i >> 3] = (uint8_t)sb;
-        } else {
-            for (int j = 0; j < k; ++j) {
-                const int64_t p = dst[r * k + j];
-                if (p < 0 || p >= P) continue;
-                q[p * per_row + c] = o;
-                if ((threadIdx.x & 7) == 0) scales[(p * per_row + c) >> 3] = (uint8_t)sb;
-            }
+            return;
         }
+        const int64_t r = i / per_row;
+        const int c = (int)(i - r * per_row);
+        for (int j = 0; j < k; ++j) {
+            const int64_t p = dst[r * k + j];
+            if (p < 0 || p >= P) continue;
+            q[p * per_row + c] = o;
+            if ((threadIdx.x & 7) == 0) scales[(p * per_row + c) >> 3] = (uint8_t)sb;
+        }
+    };
+    // the CTA's first vector, U per thread 256 apart: n16 and the offsets are
+    // multiples of 8, so the eight lanes of a block are together
+    const bool wide = reinterpret_cast<uintptr_t>(x) % 32 == 0;
+    const int64_t i0 = (int64_t)blockIdx.x * (256 * U) + threadIdx.x;
+    Vec32 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (i0 + 256 * u < n16) v[u] = load32(x + 2 * (i0 + 256 * u), wide);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (i0 + 256 * u >= n16) break;
+        uint32_t sb;
+        const uint4 o = quantize_lane16(v[u].a, v[u].b, &sb);
+        put(i0 + 256 * u, o, sb);
     }
 }
 
-__global__ void __launch_bounds__(256)
-quantize_matrices_kernel(const uint4* __restrict__ w, int n_rb, int n_cb, uint2* __restrict__ q,
+__global__ void __launch_bounds__(256, 3)
+quantize_matrices_kernel(const uint4* __restrict__ w, int n_cb, uint4* __restrict__ q,
                          uint8_t* __restrict__ scales) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
@@ -58,20 +70,21 @@ quantize_matrices_kernel(const uint4* __restrict__ w, int n_rb, int n_cb, uint2*
     const int64_t blk = blockIdx.x;               // (matrix, row block), column block
     const int64_t rb = blk / n_cb;
     const int cb = (int)(blk - rb * n_cb);
-    (void)n_rb;
-    const int64_t ld = (int64_t)n_cb * (kBlock / 8);       // 8-value vectors per row
-    const int64_t base = rb * kBlock * ld + (int64_t)cb * (kBlock / 8) +
-                         (int64_t)(threadIdx.x >> 4) * ld + (threadIdx.x & 15);
-    uint4 v[8];
+    const bool wide = reinterpret_cast<uintptr_t>(w) % 32 == 0;
+    const int64_t ld = (int64_t)n_cb * (kBlock / 16);      // 16-value vectors per row
+    const int64_t base = rb * kBlock * ld + (int64_t)cb * (kBlock / 16) +
+                         (int64_t)(threadIdx.x >> 3) * ld + (threadIdx.x & 7);
+    Vec32 v[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __ldg(w + base + (int64_t)(16 * i) * ld);
+    for (int i = 0; i < 4; ++i) v[i] = load32(w + 2 * (base + (int64_t)(32 * i) * ld), wide);
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float f[8];
-        unpack8(v[i], f);
+    for (int i = 0; i < 4; ++i) {
+        float f[16];
+        unpack8(v[i].a, f);
+        unpack8(v[i].b, f + 8);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(f[j]));
+        for (int j = 0; j < 16; ++j) m = fmaxf(m, finite_abs(f[j]));
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -83,13 +96,11 @@ quantize_matrices_kernel(const uint4* __restrict__ w, int n_rb, int n_cb, uint2*
     const float inv = inverse_scale(sb);
     if (threadIdx.x == 0) scales[blk] = (uint8_t)sb;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float f[8];
-        unpack8(v[i], f);
-        uint2 o;
-        o.x = pack_e4m3x4(scaled(f[0], inv), scaled(f[1], inv), scaled(f[2], inv), scaled(f[3], inv));
-        o.y = pack_e4m3x4(scaled(f[4], inv), scaled(f[5], inv), scaled(f[6], inv), scaled(f[7], inv));
-        q[base + (int64_t)(16 * i) * ld] = o;
+    for (int i = 0; i < 4; ++i) {
+        float f[16];
+        unpack8(v[i].a, f);
+        unpack8(v[i].b, f + 8);
+        q[base + (int64_t)(32 * i) * ld] = quantize16(f, inv);
     }
 }
 
@@ -112,10 +123,14 @@ cudaError_t launch_quantize_rows(const __nv_bfloat16* x, int64_t rows, int K, co
                                  cudaStream_t s) {
     const int64_t n16 = rows * K / 16;
     if (n16 == 0) return cudaSuccess;
-    const int64_t blocks = std::min<int64_t>((n16 + 255) / 256, (int64_t)num_sms * 16);
-    return launch_pdl(quantize_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, s,
-                      reinterpret_cast<const uint4*>(x), n16, K / 16, dst, k, P,
-                      reinterpret_cast<uint4*>(q), scales);
+    // Four vectors per thread (128 bytes in flight) once they fill the GPU
+    // twice, else one, which spreads a small batch over more SMs.
+    auto go = [&]<int U>() {
+        return launch_pdl(quantize_rows_kernel<U>, dim3((unsigned)((n16 + 256 * U - 1) / (256 * U))),
+                          dim3(256), 0, s, reinterpret_cast<const uint4*>(x), n16, K / 16, dst, k, P,
+                          reinterpret_cast<uint4*>(q), scales);
+    };
+    return n16 >= (int64_t)num_sms * 2048 ? go.template operator()<4>() : go.template operator()<1>();
 }
 
 cudaError_t launch_quantize_matrices(const __nv_bfloat16* w, int64_t n, int N, int K, uint8_t* q,
@@ -123,8 +138,8 @@ cudaError_t launch_quantize_matrices(const __nv_bfloat16* w, int64_t n, int N, i
     const int64_t blocks = n * (N / fp8::kBlock) * (K / fp8::kBlock);
     if (blocks == 0) return cudaSuccess;
     return launch_pdl(quantize_matrices_kernel, dim3((unsigned)blocks), dim3(256), 0, s,
-                      reinterpret_cast<const uint4*>(w), N / fp8::kBlock, K / fp8::kBlock,
-                      reinterpret_cast<uint2*>(q), scales);
+                      reinterpret_cast<const uint4*>(w), K / fp8::kBlock,
+                      reinterpret_cast<uint4*>(q), scales);
 }
 
 cudaError_t launch_invert_perm(const int32_t* perm, int64_t P, int32_t* inv, int num_sms,

@@ -17,6 +17,24 @@ __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
     }
 }
 
+// 32 bytes in one load, for data read once (p 32-byte aligned).
+struct Vec32 {
+    uint4 a, b;
+};
+__device__ __forceinline__ Vec32 load32(const void* p) {
+    Vec32 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v.a.x), "=r"(v.a.y), "=r"(v.a.z), "=r"(v.a.w), "=r"(v.b.x), "=r"(v.b.y),
+                   "=r"(v.b.z), "=r"(v.b.w)
+                 : "l"(p));
+    return v;
+}
+// The same where p is 16-byte aligned only.
+__device__ __forceinline__ Vec32 load32(const uint4* p, bool wide) {
+    if (wide) return load32(p);
+    return {__ldg(p), __ldg(p + 1)};
+}
+
 // Sixteen consecutive bf16 values (a, b) of a row as e4m3 and their block's
 // scale byte.  The eight lanes 8i .. 8i+7 of a warp hold one block of 128 and
 // call it together.
