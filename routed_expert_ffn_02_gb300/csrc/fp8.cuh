@@ -111,11 +111,6 @@ __device__ __forceinline__ void scale_copy(uint32_t tmem, uint64_t sdesc) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(sdesc)
                  : "memory");
 }
-__device__ __forceinline__ void scale_copy_pair(uint32_t tmem, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(sdesc)
-                 : "memory");
-}
-
 // D[tmem] (+)= (A[smem] scaled by sa[tmem]) (B[smem] scaled by sb[tmem])^T,
 // K = 32, one elected thread.
 __device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,

@@ -10,11 +10,17 @@
 // kernel takes: stages of 256 of K (two 128-byte swizzle atoms per operand,
 // 64 KB per CTA, 3 stages), the even CTA's lane issuing the MMAs of both.
 //
-// Scales.  Warp 3 of each CTA writes the scale words of 512 of K (its own 128
-// rows of A, all 256 rows of W) into a ring of 4 slots; both arrive on the
-// even CTA's barrier, whose MMA lane copies a slot of both CTAs to TMEM.  A
-// slot is refilled after the MMAs that read it completed, shared memory and
-// TMEM alike.
+// Scales.  Warps 8-11 of each CTA write the scale words of 512 of K (the CTA's
+// own 128 rows of A, all 256 rows of W) straight to TMEM, each warp its 32
+// lanes (the hardware reads the words of a row from every quarter), into a
+// ring of 4 slots that the MMAs' completion frees.  That keeps the tensor
+// pipe to MMAs: with copies from shared memory on it (tcgen05.cp, three per
+// 512 of K) 16384 x 4096 x 4096 took 200.6 us, with these stores 197.1.
+//
+// What bounds it: power, and the copies.  In a loop the chip sits at its 1.4
+// kW limit at 1.72 GHz; with operands of zeros (2.03 GHz) the same product
+// takes 167 us, 88 GB/s into each SM, and with half of its MMAs left out 153:
+// the stages arrive little faster than they are multiplied.
 //
 // TMEM.  Two 256-column accumulators and the 48 columns of scales do not fit
 // in 512 columns, so the accumulators overlap: buffer 0 is columns [0, 256),
@@ -23,7 +29,7 @@
 // MMAs wait for a quarter to a half of an epilogue, not for all of it.
 //
 // Roles as in the bf16 pair GEMM: warp 0 TMA producer, warp 1 MMA issuer
-// (even CTA), warp 2 TMEM allocator, warp 3 scales, warps 4-7 epilogue.
+// (even CTA), warp 2 TMEM allocator, warps 4-7 epilogue, warps 8-11 scales.
 // Every wait is bounded; on expiry the role records MOE_ERR_TIMEOUT, both
 // CTAs stop issuing, issued MMAs and copies are waited for, TMEM is freed.
 #include <cuda.h>
@@ -41,7 +47,6 @@ using namespace ptx;
 using namespace tc;
 using fp8::kBlock;
 using fp8::kGroupBlocks;
-using fp8::kScaleBytes;
 using fp8::kScaleCols;
 
 constexpr int BM = kTileM;                         // A rows per CTA (M = 256 per pair)
@@ -51,22 +56,22 @@ constexpr int STAGES = 3;
 constexpr int A_BYTES = BM * kBlock * KSUB;        // 32 KB
 constexpr int B_BYTES = (BN / 2) * kBlock * KSUB;  // 32 KB
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int THREADS = 384;
 constexpr int SLOTS = 4;
-constexpr int SLOT_BYTES = 3 * kScaleBytes;        // A, W rows 0-127, W rows 128-255
-constexpr int SLOT_COLS = 3 * kScaleCols;
+constexpr int SLOT_COLS = 3 * kScaleCols;          // A, W rows 0-127, W rows 128-255
 constexpr int TMEM_COLS = 512;
 constexpr int SCALE_COL = TMEM_COLS - SLOTS * SLOT_COLS;   // 464
 constexpr int ACC1_COL = SCALE_COL - BN;                   // 208
 constexpr int OUT_BUF_BYTES = 32 * 128;            // one 32-row, 128-byte box per warp
 constexpr int STAGING_BYTES = 4 * OUT_BUF_BYTES;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + SLOTS * SLOT_BYTES + 1024 + 256;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024 + 256;
 constexpr uint32_t kIdesc = fp8::make_idesc(2 * BM, BN);
 constexpr uint16_t kPairMask = 0x3;
 static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 static_assert(BN - ACC1_COL <= 64, "the overlap lies in the part that the epilogue reads first");
 
 template <bool kGated>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                 const __grid_constant__ CUtensorMap tmB1,
                 const __grid_constant__ CUtensorMap tmOut, Fp8Args args) {
@@ -75,8 +80,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* base_ptr = smem_raw + (base - raw);
     const uint32_t staging = base + STAGES * STAGE_BYTES;
-    const uint32_t slots = staging + STAGING_BYTES;
-    const uint32_t bars = slots + SLOTS * SLOT_BYTES;
+    const uint32_t bars = staging + STAGING_BYTES;
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (STAGES + s); };
     auto sfull_bar = [&](int s) { return bars + 8u * (2 * STAGES + s); };
@@ -106,7 +110,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             mbar_init(empty_bar(s), 1);    // the pair's MMA commit
         }
         for (int s = 0; s < SLOTS; ++s) {
-            mbar_init(sfull_bar(s), 2);    // both CTAs' scale warps
+            mbar_init(sfull_bar(s), 8);    // 4 scale warps x 2 CTAs
             mbar_init(sempty_bar(s), 1);
         }
         mbar_init(tfull_bar, 1);
@@ -206,12 +210,6 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         break;
                     }
                     fence_after();
-#pragma unroll
-                    for (int i = 0; i < 3; ++i)
-                        fp8::scale_copy_pair(
-                            sc + i * kScaleCols,
-                            fp8::scale_desc(slots + slot * SLOT_BYTES + i * kScaleBytes));
-                    issued = true;
                 }
                 if (!mbar_wait_for(full_bar(stage), phase, args.wait_cycles, abort_flag)) {
                     ok = false;
@@ -231,6 +229,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         fp8::mma_pair(d_tmem, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), idesc,
                                       sc, sc + kScaleCols, (kb > 0 || kk > 0) ? 1u : 0u);
                 }
+                issued = true;
                 commit_pair_multicast(empty_bar(stage), kPairMask);
                 if (++stage == STAGES) {
                     stage = 0;
@@ -254,10 +253,11 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 (void)mbar_wait(done_bar, 0);
             }
         }
-    } else if (warp == 3) {
-        // ---------------- scale producer (both CTAs) ----------------
-        // Lane l holds rows l, l + 32, l + 64, l + 96 of this CTA's A tile;
-        // every 128 rows of W share one word, so its 512 bytes repeat it.
+    } else if (warp >= 8) {
+        // ---------------- scale producers (both CTAs) ----------------
+        // Lane l holds rows l, l + 32, l + 64, l + 96 of this CTA's A tile
+        // (TMEM columns 0-3 of the slot); every 128 rows of W share one word.
+        const uint32_t tscale = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + SCALE_COL;
         const uint32_t sfull0 = mapa_shared(sfull_bar(0), 0);
         int slot = 0;
         uint32_t phase = 0;
@@ -291,11 +291,13 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     ok = false;
                     break;
                 }
-                const uint32_t dst = slots + slot * SLOT_BYTES + lane * 16u;
-                st_shared_v4(dst, a[0], a[1], a[2], a[3]);
-                st_shared_v4(dst + kScaleBytes, b0, b0, b0, b0);
-                st_shared_v4(dst + 2 * kScaleBytes, b1, b1, b1, b1);
-                fence_proxy_async_shared();
+                fence_after();
+                const uint32_t t = tscale + slot * SLOT_COLS;
+                tmem_st4(t, a[0], a[1], a[2], a[3]);
+                tmem_st4(t + kScaleCols, b0, b0, b0, b0);
+                tmem_st4(t + 2 * kScaleCols, b1, b1, b1, b1);
+                tmem_st_wait();
+                fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(sfull0 + 8u * slot);
                 if (++slot == SLOTS) {
@@ -305,7 +307,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             }
         }
         if (!ok && lane == 0 && !*abort_flag) give_up();
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 8) {
         // ---------------- epilogue (both CTAs) ----------------
         const int ew = warp - 4;              // TMEM lanes 32*ew .. 32*ew+31
         const int row = ew * 32 + lane;
@@ -358,41 +360,55 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 __syncwarp();   // converged for the warp-wide TMEM loads that follow
             };
             if (kGated) {
-                // first the 64 features whose columns overlap: the upper ones
-                // of buffer 0 (up columns 208-255), the lower ones of buffer 1
+                // First the 64 features whose columns overlap: the upper ones
+                // of buffer 0 (up columns 208-255), the lower of buffer 1.
+                // They stay in registers until the row's maximum is known; the
+                // other 64 are computed for the maximum and once more after
+                // it, which keeps the kernel within 168 registers.
                 const int first = odd ? 0 : 64;
-                float h[kBlock];
+                float h[64], x[32];
                 float m = 0.f;
-#pragma unroll
-                for (int c = 0; c < kBlock; c += 32) {
-                    const int f = (first + c) & 127;
+                auto features = [&](int f, float* dst) {
                     uint32_t g[32], u[32];
                     tmem_ld32(taddr + f, g);
                     tmem_ld32(taddr + 128 + f, u);
                     tmem_ld_wait();
-                    if (c == 32) drained();
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) {
-                        h[c + q] = fp8::swiglu(__uint_as_float(g[q]), __uint_as_float(u[q]));
-                        m = fmaxf(m, fp8::finite_abs(h[c + q]));
-                    }
+                    for (int q = 0; q < 32; ++q)
+                        dst[q] = fp8::swiglu(__uint_as_float(g[q]), __uint_as_float(u[q]));
+                };
+                features(first, h);
+                features(first + 32, h + 32);
+                drained();
+#pragma unroll
+                for (int q = 0; q < 64; ++q) m = fmaxf(m, fp8::finite_abs(h[q]));
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    features((first ^ 64) + c, x);
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) m = fmaxf(m, fp8::finite_abs(x[q]));
                 }
                 const uint32_t sb = fp8::scale_byte(m);
                 const float inv = fp8::inverse_scale(sb);
-                uint32_t lo[16], hi[16];   // 64 features each, in the order read
+                uint32_t mine[16], rest[16];   // 64 features each, in the order read
+                auto pack = [&](const float* p, uint32_t* o) {
 #pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const float* p = h + 4 * q;
-                    lo[q] = fp8::pack_e4m3x4(fp8::scaled(p[0], inv), fp8::scaled(p[1], inv),
-                                             fp8::scaled(p[2], inv), fp8::scaled(p[3], inv));
-                    hi[q] = fp8::pack_e4m3x4(fp8::scaled(p[64], inv), fp8::scaled(p[65], inv),
-                                             fp8::scaled(p[66], inv), fp8::scaled(p[67], inv));
+                    for (int q = 0; q < 8; ++q)
+                        o[q] = fp8::pack_e4m3x4(fp8::scaled(p[4 * q], inv), fp8::scaled(p[4 * q + 1], inv),
+                                                fp8::scaled(p[4 * q + 2], inv), fp8::scaled(p[4 * q + 3], inv));
+                };
+                pack(h, mine);
+                pack(h + 32, mine + 8);
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    features((first ^ 64) + c, x);
+                    pack(x, rest + c / 4);
                 }
                 uint32_t v[32];
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
-                    v[q] = odd ? lo[q] : hi[q];
-                    v[16 + q] = odd ? hi[q] : lo[q];
+                    v[q] = odd ? mine[q] : rest[q];
+                    v[16 + q] = odd ? rest[q] : mine[q];
                 }
                 if (whole) {
                     store_box(v, nt * kBlock, ft.row0 + ew * 32);
@@ -482,8 +498,8 @@ cudaError_t launch(const uint8_t* a, int64_t rows, const uint8_t* b0, const uint
     if (e != cudaSuccess) return e;
     if ((e = set_smem_attr<kGated>()) != cudaSuccess) return e;
     int grid = 0;
-    if ((e = pair_grid<fp8_pair_kernel<kGated>, SMEM_BYTES>(num_sms, &grid)) != cudaSuccess) return e;
-    return launch_pdl(fp8_pair_kernel<kGated>, dim3(grid), dim3(256), SMEM_BYTES, s, mA, mB0, mB1,
+    if ((e = pair_grid<fp8_pair_kernel<kGated>, SMEM_BYTES, THREADS>(num_sms, &grid)) != cudaSuccess) return e;
+    return launch_pdl(fp8_pair_kernel<kGated>, dim3(grid), dim3(THREADS), SMEM_BYTES, s, mA, mB0, mB1,
                       mO, args);
 }
 

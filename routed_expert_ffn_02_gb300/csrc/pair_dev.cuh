@@ -48,7 +48,7 @@ __device__ __forceinline__ void drain_pair(uint32_t full0, int fills_even, int f
 
 // CTAs to launch: two per co-resident cluster (an SM pair whose partner is
 // busy or absent cannot host a cluster, so this can be below the SM count).
-template <auto kKernel, int kSmemBytes>
+template <auto kKernel, int kSmemBytes, int kThreads = 256>
 cudaError_t pair_grid(int num_sms, int* grid) {
     constexpr int kMaxDev = kMaxDevices;
     static int cached[kMaxDev] = {};
@@ -61,7 +61,7 @@ cudaError_t pair_grid(int num_sms, int* grid) {
     if (!cached[dev]) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(num_sms & ~1), 1, 1);
-        cfg.blockDim = dim3(256, 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
         cfg.dynamicSmemBytes = kSmemBytes;
         int clusters = 0;
         e = cudaOccupancyMaxActiveClusters(&clusters, kKernel, &cfg);
