@@ -90,35 +90,6 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
-    // With early_weights the tile lists were complete before the previous
-    // kernel started (see Fp8Args), so they and the weights are read before
-    // the wait for that kernel; reads go to L2, past this SM's L1.
-    if (!args.early_weights) {
-        grid_dep_wait();
-        grid_dep_launch();
-    }
-    const fp8::OneGroup grp = args.group ? fp8::one_group(args) : fp8::OneGroup{0, 0};
-    const int n_solo = args.group ? 0 : __ldcg(&args.hdr->n_solo);
-    const int n_tiles = args.group ? (grp.n > 0) : n_solo + __ldcg(&args.hdr->n_thin_mma);
-    const int total = n_tiles * args.n_blocks_n;
-    auto tile_at = [&](int i) {
-        if (args.group) return fp8::group_tile(grp, 0);
-        const int4 v = __ldcg(reinterpret_cast<const int4*>(
-            i < n_solo ? args.solo_tiles + i : args.thin_tiles + (i - n_solo)));
-        return FatTile{v.x, v.y, v.z, v.w};
-    };
-    // Items go round-robin to the first `active` CTAs, as many as keep every
-    // wave full (see the bf16 one-CTA GEMM).
-    const int waves = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-    const int active = waves > 0 ? (total + waves - 1) / waves : 0;
-    if ((int)blockIdx.x >= active) {
-        if (args.early_weights) {
-            grid_dep_wait();
-            grid_dep_launch();
-        }
-        return;
-    }
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_bar(s), 1);
@@ -147,11 +118,37 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     fence_after();
     const uint32_t tmem_base = *tmem_holder;
     const int k_blocks = args.k_blocks;
-    if (args.early_weights && warp != 0) {
+
+    // Everything above overlaps the previous kernel.  With early_weights the
+    // tile lists were complete before that kernel started (see Fp8Args), so
+    // they and the weights are read before the wait for it; reads go to L2,
+    // past this SM's L1.
+    if (!args.early_weights) {
         grid_dep_wait();
         grid_dep_launch();
     }
-
+    auto list_tile = [](const FatTile* p) {
+        const int4 v = __ldcg(reinterpret_cast<const int4*>(p));
+        return FatTile{v.x, v.y, v.z, v.w};
+    };
+    const fp8::OneGroup grp = args.group ? fp8::one_group(args) : fp8::OneGroup{0, 0};
+    const int n_solo = args.group ? 0 : __ldcg(&args.hdr->n_solo);
+    const int n_tiles = args.group ? (grp.n > 0) : n_solo + __ldcg(&args.hdr->n_thin_mma);
+    const int total = n_tiles * args.n_blocks_n;
+    auto tile_at = [&](int i) {
+        if (args.group) return fp8::group_tile(grp, 0);
+        return list_tile(i < n_solo ? args.solo_tiles + i : args.thin_tiles + (i - n_solo));
+    };
+    // Items go round-robin to the first `active` CTAs, as many as keep every
+    // wave full (see the bf16 one-CTA GEMM).
+    const int waves = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int active = waves > 0 ? (total + waves - 1) / waves : 0;
+    // A CTA without items takes no role; total_mine ends its loops at once.
+    const int total_mine = (int)blockIdx.x < active ? total : 0;
+    if (args.early_weights && (warp != 0 || total_mine == 0)) {
+        grid_dep_wait();
+        grid_dep_launch();
+    }
     if (warp == 0 && lane == 0) {
         // ---------------- TMA producer ----------------
         int stage = 0;
@@ -174,7 +171,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         };
         // The first stages' weights do not depend on the previous kernel.
         int early = 0;
-        if (args.early_weights) {
+        if (args.early_weights && total_mine > 0) {
             const FatTile ft = tile_at(blockIdx.x / args.n_blocks_n);
             const int brow = ft.expert * args.n_rows +
                              ((int)blockIdx.x % args.n_blocks_n) * (kGated ? 128 : BN);
@@ -187,7 +184,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             // the rows come from the previous kernel's ordinary stores
             fence_proxy_async_global();
         }
-        for (int t = blockIdx.x; ok && t < total; t += active) {
+        for (int t = blockIdx.x; ok && t < total_mine; t += active) {
             const FatTile ft = tile_at(t / args.n_blocks_n);
             const int brow = ft.expert * args.n_rows + (t % args.n_blocks_n) * (kGated ? 128 : BN);
             for (int kb = 0; kb < k_blocks; ++kb) {
@@ -223,7 +220,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         int it = 0;
         bool ok = true;
         bool issued = false;
-        for (int t = blockIdx.x; ok && t < total; t += active, ++it) {
+        for (int t = blockIdx.x; ok && t < total_mine; t += active, ++it) {
             // the previous item's epilogue has read the overlap (and with it,
             // being in order, all of this buffer's previous item)
             if (it > 0 && !mbar_wait_for(drained_bar, (uint32_t)((it - 1) & 1), args.wait_cycles,
@@ -292,7 +289,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         uint32_t phase = 0;
         bool ok = true;
         const int groups = (k_blocks + kGroupBlocks - 1) / kGroupBlocks;
-        for (int t = blockIdx.x; ok && t < total; t += active) {
+        for (int t = blockIdx.x; ok && t < total_mine; t += active) {
             const FatTile ft = tile_at(t / args.n_blocks_n);
             const int nt = t % args.n_blocks_n;
             const uint8_t* ra[4];
@@ -313,10 +310,10 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                        : args.b0_scales + (eb + min(2 * nt + 1, last)) * k_blocks;
             for (int g = 0; g < groups; ++g) {
                 uint32_t a[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = fp8::scale_word(ra[i], g, k_blocks);
                 const uint32_t b0 = fp8::scale_word(rb0, g, k_blocks);
                 const uint32_t b1 = fp8::scale_word(rb1, g, k_blocks);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = fp8::scale_word(ra[i], g, k_blocks);
                 if (!__all_sync(0xffffffffu, mbar_wait_for(sempty_bar(slot), phase ^ 1u,
                                                            args.wait_cycles, abort_flag))) {
                     ok = false;
@@ -343,7 +340,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         // ---------------- epilogue ----------------
         const int ew = warp - 4;   // TMEM lanes 32*ew .. 32*ew+31
         int it = 0, n_thin = 0;
-        for (int t = blockIdx.x; t < total; t += active, ++it) {
+        for (int t = blockIdx.x; t < total_mine; t += active, ++it) {
             // the whole warp decides together (tcgen05.ld below is warp-wide)
             if (!__all_sync(0xffffffffu, mbar_wait_for(tfull_bar, (uint32_t)(it & 1),
                                                        args.wait_cycles, abort_flag))) {
