@@ -192,26 +192,25 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         bool ok = true;
         bool issued = false;
         for (int w = cluster; ok && w < total; w += n_clusters, ++it) {
-            // the previous tile's epilogue has read the overlap (and with it,
-            // being in order, all of this buffer's previous tile)
-            if (it > 0 && !mbar_wait_cluster(drained_bar, (uint32_t)((it - 1) & 1),
-                                             args.wait_cycles, abort_flag)) {
-                ok = false;
-                break;
-            }
-            fence_after();
             const uint32_t d_tmem = tmem_base + (uint32_t)((it & 1) ? ACC1_COL : 0);
             for (int ks = 0; ks < k_stages; ++ks) {
                 const int kb0 = ks * KSUB;
                 const uint32_t sc = tmem_base + SCALE_COL + slot * SLOT_COLS;
-                if (kb0 % kGroupBlocks == 0) {
-                    if (!mbar_wait_cluster(sfull_bar(slot), sphase, args.wait_cycles, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    fence_after();
+                // (the fence below orders the scale stores before the MMAs)
+                if (kb0 % kGroupBlocks == 0 &&
+                    !mbar_wait_for(sfull_bar(slot), sphase, args.wait_cycles, abort_flag)) {
+                    ok = false;
+                    break;
                 }
                 if (!mbar_wait_for(full_bar(stage), phase, args.wait_cycles, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                // Last, so that a tile's first operands are known to be there:
+                // the previous tile's epilogue has read the overlap (and with
+                // it, being in order, all of this buffer's previous tile).
+                if (ks == 0 && it > 0 &&
+                    !mbar_wait_for(drained_bar, (uint32_t)((it - 1) & 1), args.wait_cycles, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -299,7 +298,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 tmem_st_wait();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(sfull0 + 8u * slot);
+                if (lane == 0) mbar_arrive_cluster_tmem(sfull0 + 8u * slot);
                 if (++slot == SLOTS) {
                     slot = 0;
                     phase ^= 1u;
@@ -339,13 +338,6 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         for (int w = cluster; w < total; w += n_clusters, ++it) {
             const FatTile ft = ft_next;
             if (w + n_clusters < total) ft_next = tile_at(w + n_clusters);
-            // the whole warp decides together (tcgen05.ld below is warp-wide)
-            if (!__all_sync(0xffffffffu, mbar_wait_for(tfull_bar, (uint32_t)(it & 1),
-                                                       args.wait_cycles, abort_flag))) {
-                if (!*abort_flag) give_up();
-                break;
-            }
-            fence_after();
             const int nt = w % args.n_blocks_n;
             const bool valid = row < ft.rows;
             const bool whole = ew * 32 + 32 <= ft.rows;   // else each valid lane stores its row
@@ -353,16 +345,33 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             const int64_t out_row = (int64_t)ft.row0 + row;
             const uint32_t taddr =
                 tmem_base + ((uint32_t)(ew * 32) << 16) + (uint32_t)(odd ? ACC1_COL : 0);
+            // the 64 columns that hold those shared with the other buffer
+            const uint32_t shared_cols = taddr + (odd ? 0u : (uint32_t)(BN - 64));
+            // the whole warp decides together (tcgen05.ld below is warp-wide)
+            if (!__all_sync(0xffffffffu, mbar_wait_for(tfull_bar, (uint32_t)(it & 1),
+                                                       args.wait_cycles, abort_flag))) {
+                if (!*abort_flag) give_up();
+                break;
+            }
+            fence_after();
+            // They are read before anything else: the next tile's MMAs wait for
+            // this (2,500 cycles per tile when the epilogue did its first
+            // quarter first).
+            uint32_t early[64];
+            tmem_ld32(shared_cols, *reinterpret_cast<uint32_t(*)[32]>(early));
+            tmem_ld32(shared_cols + 32, *reinterpret_cast<uint32_t(*)[32]>(early + 32));
+            tmem_ld_wait();
             auto drained = [&]() {   // the columns shared with the other buffer have been read
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(drained0);
+                if (lane == 0) mbar_arrive_cluster_tmem(drained0);
                 __syncwarp();   // converged for the warp-wide TMEM loads that follow
             };
+            drained();
             if (kGated) {
-                // First the 64 features whose columns overlap: the upper ones
-                // of buffer 0 (up columns 208-255), the lower of buffer 1.
-                // They stay in registers until the row's maximum is known; the
+                // The columns read are the up values of features 64-127 (buffer
+                // 0) or the gate values of 0-63 (buffer 1).  Those 64 features
+                // stay in registers until the row's maximum is known; the
                 // other 64 are computed for the maximum and once more after
                 // it, which keeps the kernel within 168 registers.
                 const int first = odd ? 0 : 64;
@@ -377,9 +386,16 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     for (int q = 0; q < 32; ++q)
                         dst[q] = fp8::swiglu(__uint_as_float(g[q]), __uint_as_float(u[q]));
                 };
-                features(first, h);
-                features(first + 32, h + 32);
-                drained();
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(taddr + (odd ? 128 : 0) + first + c, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 32; ++q)
+                        h[c + q] = fp8::swiglu(__uint_as_float(odd ? early[c + q] : o[q]),
+                                               __uint_as_float(odd ? o[q] : early[c + q]));
+                }
 #pragma unroll
                 for (int q = 0; q < 64; ++q) m = fmaxf(m, fp8::finite_abs(h[q]));
 #pragma unroll
@@ -425,20 +441,17 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 const int cols = (int)min((int64_t)BN, args.ld_out - (int64_t)nt * BN);
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
-                    // 64 columns at a time, the overlapping ones first
+                    // 64 columns at a time, the ones already read first
                     const int c = odd ? 64 * i : 64 * ((i + 3) & 3);
+                    if (i > 0) {
+                        tmem_ld32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(early));
+                        tmem_ld32(taddr + c + 32, *reinterpret_cast<uint32_t(*)[32]>(early + 32));
+                        tmem_ld_wait();
+                    }
                     uint32_t v[32];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t d[32];
-                        tmem_ld32(taddr + c + 32 * half, d);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int q = 0; q < 16; ++q)
-                            v[16 * half + q] = pack_bf16(__uint_as_float(d[2 * q]),
-                                                         __uint_as_float(d[2 * q + 1]));
-                    }
-                    if (i == 0) drained();
+                    for (int q = 0; q < 32; ++q)
+                        v[q] = pack_bf16(__uint_as_float(early[2 * q]), __uint_as_float(early[2 * q + 1]));
                     if (c >= cols) continue;
                     if (whole) {
                         store_box(v, nt * BN + c, ft.row0 + ew * 32);
