@@ -411,8 +411,11 @@ moe_status moe_expert_ffn_fp8(const moe_shape* shape, const moe_bf16* x, const i
                               moe_stream_t stream);
 
 /* moe_forward on 8-bit experts: route -> permute -> 8-bit experts -> combine
- * on one stream, no host synchronisation.  Arguments as moe_forward; ws:
- * moe_fp8_workspace_size() bytes, initialised once with moe_workspace_init(). */
+ * on one stream, no host synchronisation.  Batches of at most 128 tokens keep
+ * the experts' outputs in fp32 up to the one rounding of out; larger ones round
+ * them to bf16 as moe_expert_ffn_fp8 does, and give the bits of the separate
+ * entry points.  Arguments as moe_forward; ws: moe_fp8_workspace_size() bytes,
+ * initialised once with moe_workspace_init(). */
 size_t moe_fp8_workspace_size(const moe_shape* shape);
 moe_status moe_forward_fp8(const moe_shape* shape, const float* logits, const moe_bf16* x,
                            const moe_fp8_experts* experts, moe_bf16* out, int32_t* topk_idx,

@@ -128,8 +128,12 @@ struct FwdBufs {
     FfnBufs f;
     int32_t *idx, *counts, *offsets, *perm, *chunk;
     float* gates;
-    __nv_bfloat16* y;
+    uint8_t* y;   // [P, H] bf16, or fp32 (fp32_y)
 };
+// y of a batch that cannot have pair tiles stays in L2 (at most 128 tokens),
+// where four bytes a value cost nothing measurable (decode batch 24: 160.7 us
+// either way), and the output is then rounded once instead of twice.
+bool fp32_y(const moe_shape* sh) { return sh->T <= kTileM; }
 size_t carve_fwd(const moe_shape* sh, void* ws, FwdBufs* b) {
     const int64_t P = (int64_t)sh->T * sh->k;
     Carver c(ws);
@@ -140,7 +144,7 @@ size_t carve_fwd(const moe_shape* sh, void* ws, FwdBufs* b) {
     b->offsets = c.take<int32_t>((size_t)sh->E + 1);
     b->perm = c.take<int32_t>((size_t)P);
     b->chunk = c.take<int32_t>(permute_scratch_ints(P, sh->E));
-    b->y = c.take<__nv_bfloat16>((size_t)(P * sh->H));
+    b->y = c.take<uint8_t>((size_t)(P * sh->H) * (fp32_y(sh) ? 4 : 2));
     return align_up(c.off, 256);
 }
 
@@ -178,9 +182,10 @@ moe_status run_product(const uint8_t* x, const uint8_t* W, const Fp8Args& a, con
     return MOE_OK;
 }
 
-// Quantised rows in place (xq, xs): gate/up, then down into y [P, H].
+// Quantised rows in place (xq, xs): gate/up, then down into y [P, H], or y32
+// where no expert can have pair tiles.
 moe_status run_ffn(const moe_shape* sh, const FfnBufs& b, const moe_fp8_experts* w,
-                   __nv_bfloat16* y, int64_t most, int num_sms, cudaStream_t s) {
+                   __nv_bfloat16* y, float* y32, int64_t most, int num_sms, cudaStream_t s) {
     const int64_t P = (int64_t)sh->T * sh->k;
     Fp8Args a = args_of(b.l, P, sh->H, sh->I, true);
     a.a_scales = b.xs;
@@ -200,6 +205,7 @@ moe_status run_ffn(const moe_shape* sh, const FfnBufs& b, const moe_fp8_experts*
     d.a_scales = b.hs;
     d.b0_scales = w->down_scales;
     d.out = y;
+    d.out32 = y32;
     return run_product(b.hq, w->down, d, kn, sh->E, num_sms, s);
 }
 
@@ -319,7 +325,7 @@ moe_status moe_expert_ffn_fp8(const moe_shape* shape, const moe_bf16* x, const i
     CUDA_TRY(launch_invert_perm(perm, P, b.inv_perm, sms, s), "invert perm");
     CUDA_TRY(launch_quantize_rows((const __nv_bfloat16*)x, shape->T, shape->H, b.inv_perm,
                                   shape->k, P, b.xq, b.xs, sms, s), "quantize rows");
-    STATUS_TRY(run_ffn(shape, b, experts, (__nv_bfloat16*)y_sorted, P, sms, s));
+    STATUS_TRY(run_ffn(shape, b, experts, (__nv_bfloat16*)y_sorted, nullptr, P, sms, s));
     return ok();
 }
 
@@ -361,9 +367,15 @@ moe_status moe_forward_fp8(const moe_shape* shape, const float* logits, const mo
         CUDA_TRY(launch_quantize_rows((const __nv_bfloat16*)x, T, shape->H, b.f.inv_perm, k, P,
                                       b.f.xq, b.f.xs, sms, s), "quantize rows");
     }
-    STATUS_TRY(run_ffn(shape, b.f, experts, b.y, T, sms, s));
-    CUDA_TRY(launch_combine(b.y, b.f.inv_perm, g, T, k, shape->H, (__nv_bfloat16*)out, sms, s),
-             "combine");
+    __nv_bfloat16* y = (__nv_bfloat16*)b.y;
+    float* y32 = fp32_y(shape) ? (float*)b.y : nullptr;
+    STATUS_TRY(run_ffn(shape, b.f, experts, y, y32, T, sms, s));
+    if (y32)
+        CUDA_TRY(launch_combine_f32(y32, b.f.inv_perm, g, T, k, shape->H, (__nv_bfloat16*)out, s),
+                 "combine");
+    else
+        CUDA_TRY(launch_combine(y, b.f.inv_perm, g, T, k, shape->H, (__nv_bfloat16*)out, sms, s),
+                 "combine");
     return ok();
 }
 

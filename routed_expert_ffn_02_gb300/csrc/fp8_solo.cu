@@ -432,30 +432,36 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     args.out_scales[out_row * (args.ld_out / kBlock) + nt] = (uint8_t)sb;
                 }
             } else {
-                __nv_bfloat16* dst = args.out + out_row * args.ld_out + (int64_t)nt * BN;
+                const int64_t at = out_row * args.ld_out + (int64_t)nt * BN;
                 const int cols = (int)min((int64_t)BN, args.ld_out - (int64_t)nt * BN);
 #pragma unroll 1
                 for (int i = 0; i < (thin ? 1 : 4); ++i) {
                     // 64 columns at a time, the overlapping ones first; of a
                     // thin tile each warp does 64
                     const int c = thin ? 64 * ew : odd ? 64 * i : 64 * ((i + 3) & 3);
-                    uint32_t v[32];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t d[32];
-                        tmem_ld32(taddr + c + 32 * half, d);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int q = 0; q < 16; ++q)
-                            v[16 * half + q] = pack_bf16(__uint_as_float(d[2 * q]),
-                                                         __uint_as_float(d[2 * q + 1]));
-                    }
+                    uint32_t d[64];
+                    tmem_ld32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(d));
+                    tmem_ld32(taddr + c + 32, *reinterpret_cast<uint32_t(*)[32]>(d + 32));
+                    tmem_ld_wait();
                     if (i == 0) drained();
                     if (valid && c < cols) {
-                        uint4* d4 = reinterpret_cast<uint4*>(dst + c);
+                        if (args.out32) {
+                            uint4* d4 = reinterpret_cast<uint4*>(args.out32 + at + c);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            d4[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                            for (int q = 0; q < 16; ++q)
+                                d4[q] = make_uint4(d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]);
+                        } else {
+                            uint4* d4 = reinterpret_cast<uint4*>(args.out + at + c);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                uint32_t o[4];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    o[j] = pack_bf16(__uint_as_float(d[8 * q + 2 * j]),
+                                                     __uint_as_float(d[8 * q + 2 * j + 1]));
+                                d4[q] = make_uint4(o[0], o[1], o[2], o[3]);
+                            }
+                        }
                     }
                     __syncwarp();
                 }

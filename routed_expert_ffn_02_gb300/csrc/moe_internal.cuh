@@ -375,6 +375,7 @@ struct Fp8Args {
     const uint8_t* b0_scales;    // [E, n_rows / 128, K / 128]; gated: gate
     const uint8_t* b1_scales;    // gated: up
     __nv_bfloat16* out;          // plain: [rows, ld_out]
+    float* out32;                // plain, one-CTA kernel: [rows, ld_out] in place of out
     uint8_t* out_q;              // gated: [rows, ld_out] e4m3
     uint8_t* out_scales;         // gated: [rows, ld_out / 128]
     int64_t ld_out;
@@ -412,6 +413,10 @@ cudaError_t launch_balance(const float* logits, const int32_t* idx, float2* stat
 cudaError_t launch_balance_backward(const float* logits, const float2* stats, const float* d_loss,
                                     const int32_t* idx, const float* gates, const float* d_gates,
                                     float* d_logits, BalanceArgs a, int num_sms, cudaStream_t s);
+
+// launch_combine over fp32 y.
+cudaError_t launch_combine_f32(const float* y_sorted, const int32_t* inv_perm, const float* gates,
+                               int T, int k, int H, __nv_bfloat16* out, cudaStream_t s);
 
 // Experts to copy: entry j copies expert src_e[j] of the source matrices
 // into block dst_e[j] of the destination matrices.

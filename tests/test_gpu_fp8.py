@@ -198,11 +198,15 @@ def test_layer(moe, T, E, k, H, I, zipf):
     want, y = plain.layer(x, idx, gates, parts)
     assert rel_rms(out, want) <= REL_RMS_TOL
     assert torch.equal(out, moe.moe_forward_fp8(shape, lg, x, ex, ws=ws)), "repeated run differs"
-    # the separate entry points give the same bits
+    # the separate entry points give the same bits (above 128 tokens)
     counts, offsets, perm, inv = moe.moe_permute(idx, E)
     ys = moe.moe_expert_ffn_fp8(shape, x, perm, offsets, ex)
     assert rel_rms(ys[inv.long()].view(T, k, H), y) <= REL_RMS_TOL
-    assert torch.equal(moe.moe_combine(ys, inv, gates, T, k, H), out)
+    combined = moe.moe_combine(ys, inv, gates, T, k, H)
+    if T > 128:
+        assert torch.equal(combined, out)
+    else:    # y kept in fp32: one rounding to bf16 (1.7e-3) and not two
+        assert rel_rms(out, want) <= 2e-3 and rel_rms(out, combined.double()) <= REL_RMS_TOL
 
 
 def test_layer_against_bf16_experts(moe):
