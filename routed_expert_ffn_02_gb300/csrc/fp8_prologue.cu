@@ -53,7 +53,7 @@ fp8_prologue_kernel(const float* __restrict__ logits, const uint4* __restrict__ 
         const int v = tid + i * threads;
         if (v < per_row) {
             const uint4* src = x + 2 * ((int64_t)t * per_row + v);
-            q[i] = fp8::quantize_lane16(__ldg(src), __ldg(src + 1), &sb[i]);
+            q[i] = fp8::quantize_lane16({__ldg(src), __ldg(src + 1)}, &sb[i]);
         }
     }
     for (int r = warp; r < T; r += threads / 32)

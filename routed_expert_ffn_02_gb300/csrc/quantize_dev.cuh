@@ -35,21 +35,53 @@ __device__ __forceinline__ Vec32 load32(const uint4* p, bool wide) {
     return {__ldg(p), __ldg(p + 1)};
 }
 
-// Sixteen consecutive bf16 values (a, b) of a row as e4m3 and their block's
-// scale byte.  The eight lanes 8i .. 8i+7 of a warp hold one block of 128 and
-// call it together.
-__device__ __forceinline__ uint4 quantize_lane16(const uint4& a, const uint4& b, uint32_t* sb) {
-    float f[16];
-    unpack8(a, f);
-    unpack8(b, f + 8);
-    float m = 0.f;
+// Largest magnitude of 16 bf16 values, NaN apart; two values per instruction.
+__device__ __forceinline__ float amax16(const Vec32& v) {
+    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+    __nv_bfloat162 m = __habs2(p[0]);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) m = fmaxf(m, finite_abs(f[j]));
+    for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(p[i]));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+// The same over finite values only.
+__device__ __forceinline__ float amax16_finite(const Vec32& v) {
+    float f[16], m = 0.f;
+    unpack8(v.a, f);
+    unpack8(v.b, f + 8);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, finite_abs(f[i]));
+    return m;
+}
+// e4m3 of 16 values.  has_inf: infinities must become NaN (the conversion
+// would saturate them); NaN stays NaN by itself.
+__device__ __forceinline__ uint4 convert16(const Vec32& v, float inv, bool has_inf) {
+    float f[16];
+    unpack8(v.a, f);
+    unpack8(v.b, f + 8);
+    if (has_inf) return quantize16(f, inv);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o[i] = pack_e4m3x4(f[4 * i] * inv, f[4 * i + 1] * inv, f[4 * i + 2] * inv, f[4 * i + 3] * inv);
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Sixteen consecutive bf16 values of a row as e4m3 and their block's scale
+// byte.  The eight lanes 8i .. 8i+7 of a warp hold one block of 128 and call
+// it together.
+__device__ __forceinline__ uint4 quantize_lane16(const Vec32& v, uint32_t* sb) {
     const unsigned lanes = 0xffu << (threadIdx.x & 24);
+    float m = amax16(v);
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, o));
+    const bool has_inf = m > 3.402823466e38f;   // the same for the eight lanes
+    if (has_inf) {
+        m = amax16_finite(v);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, o));
+    }
     *sb = scale_byte(m);
-    return quantize16(f, inverse_scale(*sb));
+    return convert16(v, inverse_scale(*sb), has_inf);
 }
 
 }  // namespace fp8
