@@ -164,14 +164,20 @@ moe_status check_experts(const moe_fp8_experts* w) {
     return MOE_OK;
 }
 
-// Which kernels can have work, from sizes the host knows: `most` bounds any
-// expert's rows.  One expert holds all rows; with several, small ones cannot
-// be ruled out.
+// Which kernels run, from sizes the host knows: `most` bounds any expert's
+// rows.  A single expert takes one kernel by its rows.  With several, small
+// experts cannot be ruled out, so the pair kernel is a launch more, and up to
+// kPairRows rows the one-CTA kernel takes the pair tiles as well (measured, us
+// with / without the pair kernel: 777 rows over 48 experts, N = 640, K = 1152:
+// 23.0 / 16.7; 4096 over 16, 4096 x 2048: 56.0 / 53.3; 8192 over 16: 67.6 /
+// 78.6; a layer of 512 tokens, 64 experts, 2048 x 1024: 162 / 134).
 struct Kernels {
     bool pair, solo;
 };
+constexpr int64_t kPairRows = 4096;
 Kernels kernels_for(int64_t rows, int64_t most, int E) {
-    return {most > kTileM, !(E == 1 && rows > kTileM)};
+    const bool pair = most > kTileM && (E == 1 || rows > kPairRows);
+    return {pair, !(E == 1 && pair)};
 }
 
 // The grouped product y = A W^T (plain) over the planner's lists.
@@ -194,6 +200,7 @@ moe_status run_ffn(const moe_shape* sh, const FfnBufs& b, const moe_fp8_experts*
     a.out_q = b.hq;
     a.out_scales = b.hs;
     const Kernels kn = kernels_for(P, most, sh->E);
+    a.with_pairs = !kn.pair;
     if (kn.pair)
         CUDA_TRY(launch_fp8_pair_gate_up(b.xq, P, w->gate, w->up, a, sh->E, num_sms, s),
                  "8-bit gate/up (pairs)");
@@ -201,6 +208,7 @@ moe_status run_ffn(const moe_shape* sh, const FfnBufs& b, const moe_fp8_experts*
         CUDA_TRY(launch_fp8_solo_gate_up(b.xq, P, w->gate, w->up, a, sh->E, num_sms, s),
                  "8-bit gate/up (one-CTA)");
     Fp8Args d = args_of(b.l, P, sh->I, sh->H, false);
+    d.with_pairs = !kn.pair;
     d.early_weights = 1;   // the lists were complete before the gate/up kernels started
     d.a_scales = b.hs;
     d.b0_scales = w->down_scales;
@@ -294,7 +302,9 @@ moe_status moe_grouped_gemm_fp8(const uint8_t* x, const uint8_t* x_scales, int32
     a.a_scales = x_scales;
     a.b0_scales = W_scales;
     a.out = (__nv_bfloat16*)y;
-    STATUS_TRY(run_product(x, W, a, kernels_for(rows, rows, E), E, sms, s));
+    const Kernels kn = kernels_for(rows, rows, E);
+    a.with_pairs = !kn.pair;
+    STATUS_TRY(run_product(x, W, a, kn, E, sms, s));
     return ok();
 }
 

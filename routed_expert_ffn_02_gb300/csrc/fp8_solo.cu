@@ -1,5 +1,6 @@
 // fp8_solo.cu -- one-CTA grouped products of 8-bit block-scaled operands:
-// experts of at most 128 rows, one row tile each.
+// experts of at most 128 rows, one row tile each, and, in products of few rows
+// (Fp8Args::with_pairs), the larger experts' 128-row tiles too.
 //
 //   plain:    y[rows, n0:n0+256] = bf16( A W_e[n0:n0+256]^T )
 //   gate/up:  h[rows, n0:n0+128] = quantised( silu(A Wg_e^T) * (A Wu_e^T) ),
@@ -132,12 +133,17 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         return FatTile{v.x, v.y, v.z, v.w};
     };
     const fp8::OneGroup grp = args.group ? fp8::one_group(args) : fp8::OneGroup{0, 0};
-    const int n_solo = args.group ? 0 : __ldcg(&args.hdr->n_solo);
-    const int n_tiles = args.group ? (grp.n > 0) : n_solo + __ldcg(&args.hdr->n_thin_mma);
+    const bool with_pairs = args.with_pairs && !args.group;
+    const int n_pair = with_pairs ? __ldcg(&args.hdr->n_fat_tiles) : 0;
+    const int n_solo = args.group ? 0 : n_pair + __ldcg(&args.hdr->n_solo);
+    const int n_tiles = args.group ? (grp.n + BM - 1) / BM : n_solo + __ldcg(&args.hdr->n_thin_mma);
     const int total = n_tiles * args.n_blocks_n;
+    // (the second tile of an expert's last pair may be empty)
     auto tile_at = [&](int i) {
-        if (args.group) return fp8::group_tile(grp, 0);
-        return list_tile(i < n_solo ? args.solo_tiles + i : args.thin_tiles + (i - n_solo));
+        if (args.group) return fp8::group_tile(grp, i);
+        return list_tile(i < n_pair   ? args.tiles + i
+                         : i < n_solo ? args.solo_tiles + (i - n_pair)
+                                      : args.thin_tiles + (i - n_solo));
     };
     // Items go round-robin to the first `active` CTAs, as many as keep every
     // wave full (see the bf16 one-CTA GEMM).
@@ -186,6 +192,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         }
         for (int t = blockIdx.x; ok && t < total_mine; t += active) {
             const FatTile ft = tile_at(t / args.n_blocks_n);
+            if (ft.rows == 0) continue;
             const int brow = ft.expert * args.n_rows + (t % args.n_blocks_n) * (kGated ? 128 : BN);
             for (int kb = 0; kb < k_blocks; ++kb) {
                 if (!mbar_wait_for(empty_bar(stage), phase ^ 1u, args.wait_cycles, abort_flag)) {
@@ -220,7 +227,8 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         int it = 0;
         bool ok = true;
         bool issued = false;
-        for (int t = blockIdx.x; ok && t < total_mine; t += active, ++it) {
+        for (int t = blockIdx.x; ok && t < total_mine; t += active) {
+            if (with_pairs && tile_at(t / args.n_blocks_n).rows == 0) continue;
             // the previous item's epilogue has read the overlap (and with it,
             // being in order, all of this buffer's previous item)
             if (it > 0 && !mbar_wait_for(drained_bar, (uint32_t)((it - 1) & 1), args.wait_cycles,
@@ -272,6 +280,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             }
             if (!ok) break;
             commit(tfull_bar);
+            ++it;
         }
         if (!ok) {
             *abort_flag = 1;
@@ -291,6 +300,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         const int groups = (k_blocks + kGroupBlocks - 1) / kGroupBlocks;
         for (int t = blockIdx.x; ok && t < total_mine; t += active) {
             const FatTile ft = tile_at(t / args.n_blocks_n);
+            if (ft.rows == 0) continue;
             const int nt = t % args.n_blocks_n;
             const uint8_t* ra[4];
 #pragma unroll
@@ -340,7 +350,9 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         // ---------------- epilogue ----------------
         const int ew = warp - 4;   // TMEM lanes 32*ew .. 32*ew+31
         int it = 0, n_thin = 0;
-        for (int t = blockIdx.x; t < total_mine; t += active, ++it) {
+        for (int t = blockIdx.x; t < total_mine; t += active) {
+            const FatTile ft = tile_at(t / args.n_blocks_n);
+            if (ft.rows == 0) continue;
             // the whole warp decides together (tcgen05.ld below is warp-wide)
             if (!__all_sync(0xffffffffu, mbar_wait_for(tfull_bar, (uint32_t)(it & 1),
                                                        args.wait_cycles, abort_flag))) {
@@ -349,7 +361,6 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 break;
             }
             fence_after();
-            const FatTile ft = tile_at(t / args.n_blocks_n);
             const int nt = t % args.n_blocks_n;
             const int odd = it & 1;
             const bool thin = ft.rows <= kThinMaxTokens;
@@ -467,6 +478,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 }
             }
             __syncwarp();
+            ++it;
         }
     }
 

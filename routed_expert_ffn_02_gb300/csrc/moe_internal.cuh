@@ -365,6 +365,7 @@ struct Fp8Args {
     WsHeader* hdr;
     int rows;                    // rows of A
     const int32_t* group;        // one expert: its offsets [2] in place of the lists
+    int with_pairs;              // the one-CTA kernel runs the pair tiles too
     int early_weights;           // one-CTA kernel: the tile lists come from a kernel
                                  // before the previous one, so weights may be copied
                                  // before the dependency wait
@@ -381,7 +382,8 @@ struct Fp8Args {
     int64_t ld_out;
     long long wait_cycles;
 };
-// On CTA pairs: the pair tiles.  One-CTA kernel: the solo and thin tiles.
+// On CTA pairs: the pair tiles.  One-CTA kernel: the solo and thin tiles (and,
+// with_pairs, the pair tiles).
 cudaError_t launch_fp8_pair_gate_up(const uint8_t* a, int64_t rows, const uint8_t* b0,
                                     const uint8_t* b1, const Fp8Args& args, int E, int num_sms,
                                     cudaStream_t s);
