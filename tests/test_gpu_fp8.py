@@ -114,6 +114,14 @@ def test_product(moe, counts, N, K):
     assert torch.equal(y, moe.moe_grouped_gemm_fp8(*args, ws=ws)), "repeated run differs"
 
 
+@pytest.mark.parametrize("counts", [[255, 256, 257, 1, 3900], [129, 0, 385, 33, 4000, 128, 31], [4097, 512]],
+                         ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("N,K", [(128, 128), (384, 640), (640, 1152), (1024, 256)])
+def test_product_many_rows(moe, counts, N, K):
+    """More than 4096 rows: the CTA-pair kernel beside the one-CTA kernel."""
+    test_product(moe, counts, N, K)
+
+
 @pytest.mark.parametrize("counts,N,K", [([1], 16384, 256), ([40], 256, 16384), ([200], 384, 16384),
                                         ([3] * 1024, 128, 256), ([0, 4097, 0, 12], 512, 2048)])
 def test_product_limits(moe, counts, N, K):
@@ -265,7 +273,8 @@ def test_decode_step_in_a_graph(moe):
         assert torch.equal(out.clone(), moe.moe_forward_fp8(shape, lg, x, ex))
 
 
-@pytest.mark.parametrize("T,E,k,H,I", [(700, 6, 2, 512, 256), (64, 16, 2, 512, 256)])
+@pytest.mark.parametrize("T,E,k,H,I", [(700, 6, 2, 512, 256), (64, 16, 2, 512, 256),
+                                       (2500, 6, 2, 512, 256), (4, 16, 2, 512, 512)])
 def test_wait_expiry(moe, T, E, k, H, I):
     """Waits given up after one cycle: the status says so, and the next call
     on the same workspace gives the outputs of the call before."""
