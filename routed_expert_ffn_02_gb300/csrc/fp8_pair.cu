@@ -17,10 +17,10 @@
 // pipe to MMAs: with copies from shared memory on it (tcgen05.cp, three per
 // 512 of K) 16384 x 4096 x 4096 took 200.6 us, with these stores 197.1.
 //
-// What bounds it: power, and the copies.  In a loop the chip sits at its 1.4
-// kW limit at 1.72 GHz; with operands of zeros (2.03 GHz) the same product
-// takes 167 us, 88 GB/s into each SM, and with half of its MMAs left out 153:
-// the stages arrive little faster than they are multiplied.
+// What bounds it: power.  16384 x 4096 x 4096 takes 184 us (2.99 PFLOP/s) with
+// the chip at its 1.4 kW limit and 1.72 GHz; with operands of zeros, at 2.03
+// GHz, 168.  Per tile of 4096 of K about 18,000 cycles of issue against 16,400
+// of MMA, and about 1,000 from one tile to the next.
 //
 // TMEM.  Two 256-column accumulators and the 48 columns of scales do not fit
 // in 512 columns, so the accumulators overlap: buffer 0 is columns [0, 256),
@@ -355,8 +355,9 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             }
             fence_after();
             // They are read before anything else: the next tile's MMAs wait for
-            // this (2,500 cycles per tile when the epilogue did its first
-            // quarter first).
+            // this (2,500 cycles per tile, 197 us in place of 184, when the
+            // epilogue did its first quarter first and released with cluster
+            // scope).
             uint32_t early[64];
             tmem_ld32(shared_cols, *reinterpret_cast<uint32_t(*)[32]>(early));
             tmem_ld32(shared_cols + 32, *reinterpret_cast<uint32_t(*)[32]>(early + 32));
