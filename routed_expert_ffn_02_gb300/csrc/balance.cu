@@ -159,7 +159,7 @@ balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx
         for (int e = threadIdx.x; e < E; e += 32 * W) hist[e] = 0;
         __syncthreads();
         for (int i = t0 * k + threadIdx.x; i < t1 * k; i += 32 * W) {
-            const int e = __ldg(idx + i);
+            const int e = __ldca(idx + i);
             if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
             else set_status(a.hdr, MOE_ERR_BAD_INDEX);
         }
@@ -272,7 +272,7 @@ balance_finish_kernel(BalanceArgs a) {
         if (e < a.E) {
 #pragma unroll 8
             for (int c = q.c0 + w; c < q.c1; c += 8) {
-                const float2 v = __ldg(a.part + (int64_t)(c + s) * a.E + e);
+                const float2 v = __ldca(a.part + (int64_t)(c + s) * a.E + e);
                 p += v.x;
                 n += __float_as_int(v.y);
             }
@@ -338,7 +338,7 @@ balance_backward_kernel(const float* __restrict__ logits, const float2* __restri
     float2 st_next = make_float2(0.f, 0.f);
     auto fetch = [&](int t) {
         load_row<V>(logits + (int64_t)t * E, E, vec, -INFINITY, next);
-        st_next = __ldg(stats + t);
+        st_next = __ldca(stats + t);
     };
     if (t0 < t1) fetch(t0);
     for (int t = t0; t < t1; ++t) {
@@ -351,7 +351,7 @@ balance_backward_kernel(const float* __restrict__ logits, const float2* __restri
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int e = 4 * (lane + 32 * v) + c;
-                    coef[4 * v + c] = e < E ? w * (float)__ldg(counts + (int64_t)s * E + e) : 0.f;
+                    coef[4 * v + c] = e < E ? w * (float)__ldca(counts + (int64_t)s * E + e) : 0.f;
                 }
         }
         const bool inside = t >= r.beg && t < r.end;
@@ -359,8 +359,8 @@ balance_backward_kernel(const float* __restrict__ logits, const float2* __restri
         int e_sel = -1;
         float add = 0.f;
         if (idx && lane < k) {
-            e_sel = __ldg(idx + (int64_t)t * k + lane);
-            add = __ldg(gates + (int64_t)t * k + lane);
+            e_sel = __ldca(idx + (int64_t)t * k + lane);
+            add = __ldca(gates + (int64_t)t * k + lane);
         }
         const float dg = idx && lane < k ? __ldg(d_gates + (int64_t)t * k + lane) : 0.f;
         float p[4 * V];

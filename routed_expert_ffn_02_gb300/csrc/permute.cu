@@ -395,7 +395,7 @@ plan_groups_kernel(const int32_t* __restrict__ offsets, int rows, int E, Plan pl
     __shared__ unsigned long long warp_sum[32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int e = threadIdx.x;
-    const int given = e < E ? offsets[e] : 0, end = offsets[E];
+    const int given = e < E ? __ldcg(offsets + e) : 0, end = __ldcg(offsets + E);
     int v = min(max(given, 0), rows);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

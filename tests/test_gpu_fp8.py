@@ -162,6 +162,22 @@ def test_product_bad_offsets(moe, off, written):
         assert bool((y[written:10] == 0).all())
 
 
+@pytest.mark.parametrize("rows", [10, 300])
+@pytest.mark.parametrize("off,lo,hi", [([0, 7], 0, 7), ([2, 10**6], 2, None), ([-5, 4], 0, 4), ([9, 3], 0, 0)])
+def test_product_bad_offsets_of_one_group(moe, rows, off, lo, hi):
+    """One group takes no planner launch: the same rules hold."""
+    q, sq, _, Wq, sW = product_case(moe, [rows], 256, 256)
+    good = moe.moe_grouped_gemm_fp8(q, sq, torch.tensor([0, rows], dtype=torch.int32, device="cuda"), Wq, sW)
+    y = torch.zeros((rows + 2, 256), dtype=torch.bfloat16, device="cuda")
+    ws = moe.Workspace(moe.grouped_gemm_fp8_workspace_size(rows, 1))
+    moe.moe_grouped_gemm_fp8(q, sq, torch.tensor(off, dtype=torch.int32, device="cuda"), Wq, sW,
+                             y=y[:rows], ws=ws)
+    assert ws.status() == MOE_ERR_BAD_INDEX
+    hi = rows if hi is None else hi
+    assert torch.equal(y[lo:hi], good[lo:hi])
+    assert not y[:lo].any() and not y[hi:].any()
+
+
 def test_product_as_input_gradient(moe):
     """dX = dY W by the same entry point on the transposed matrix, whose
     blocks keep their scales."""
