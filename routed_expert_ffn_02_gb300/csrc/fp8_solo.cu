@@ -28,7 +28,8 @@
 // warp (its 128 SwiGLUs per lane took longer than the ring could bridge: a
 // decode batch of 24 streamed at 75% of HBM, 94% in the down product that has
 // none).  The 32 rows are therefore loaded into all four quarters of A: every
-// warp finds them in its lanes and does a quarter of the columns.
+// warp finds them in its lanes and does a quarter of the columns.  Tiles of at
+// most 8 rows load only 8 per quarter, which takes 12 of 48 KB off each stage.
 //
 // Every wait is bounded; on expiry the kernel records MOE_ERR_TIMEOUT, drains
 // its own copies and MMAs, frees TMEM and returns.
@@ -68,8 +69,8 @@ static_assert(BN - ACC1_COL <= 64, "the overlap lies in the part that the epilog
 template <bool kGated>
 __global__ void __launch_bounds__(256, 1)
 fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
-                const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
-                Fp8Args args) {
+                const __grid_constant__ CUtensorMap tmA8, const __grid_constant__ CUtensorMap tmB0,
+                const __grid_constant__ CUtensorMap tmB1, Fp8Args args) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -110,6 +111,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     if (warp == 0 && lane == 0) {
         prefetch_map(&tmA);
         prefetch_map(&tmA32);
+        prefetch_map(&tmA8);
         prefetch_map(&tmB0);
         if (kGated) prefetch_map(&tmB1);
     }
@@ -170,10 +172,14 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             if (ft.rows > kThinMaxTokens) {
                 tma_load_2d(sa, &tmA, bar, x, ft.row0);
             } else {
+                // the rest of a quarter keeps what it held: rows of D that are not read
+                const CUtensorMap* map = ft.rows > 8 ? &tmA32 : &tmA8;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tma_load_2d(sa + i * (A_BYTES / 4), &tmA32, bar, x, ft.row0);
+                for (int i = 0; i < 4; ++i) tma_load_2d(sa + i * (A_BYTES / 4), map, bar, x, ft.row0);
             }
+        };
+        auto stage_bytes = [](const FatTile& ft) {
+            return (uint32_t)(B_BYTES + (ft.rows > 8 ? A_BYTES : 4 * 8 * kBlock));
         };
         // The first stages' weights do not depend on the previous kernel.
         int early = 0;
@@ -182,7 +188,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             const int brow = ft.expert * args.n_rows +
                              ((int)blockIdx.x % args.n_blocks_n) * (kGated ? 128 : BN);
             for (early = 0; early < min(STAGES, k_blocks); ++early) {
-                mbar_expect_tx(full_bar(early), STAGE_BYTES);
+                mbar_expect_tx(full_bar(early), stage_bytes(ft));
                 load_w(base + early * STAGE_BYTES + A_BYTES, full_bar(early), early * kBlock, brow);
             }
             grid_dep_wait();
@@ -203,7 +209,7 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 if (early > 0) {
                     --early;
                 } else {
-                    mbar_expect_tx(full_bar(stage), STAGE_BYTES);
+                    mbar_expect_tx(full_bar(stage), stage_bytes(ft));
                     load_w(sa + A_BYTES, full_bar(stage), kb * kBlock, brow);
                 }
                 load_a(sa, full_bar(stage), kb * kBlock, ft);
@@ -500,16 +506,17 @@ template <bool kGated>
 cudaError_t launch(const uint8_t* a, int64_t rows, const uint8_t* b0, const uint8_t* b1,
                    const Fp8Args& args, int E, int num_sms, cudaStream_t s) {
     const uint64_t K = (uint64_t)args.k_blocks * kBlock;
-    CUtensorMap mA, mA32, mB0, mB1;
+    CUtensorMap mA, mA32, mA8, mB0, mB1;
     cudaError_t e;
     if ((e = make_tma_map_u8(&mA, a, (uint64_t)rows, K, BM)) != cudaSuccess) return e;
     if ((e = make_tma_map_u8(&mA32, a, (uint64_t)rows, K, kThinMaxTokens)) != cudaSuccess) return e;
+    if ((e = make_tma_map_u8(&mA8, a, (uint64_t)rows, K, 8)) != cudaSuccess) return e;
     const uint32_t box = kGated ? 128 : 256;
     if ((e = make_tma_map_u8(&mB0, b0, (uint64_t)E * args.n_rows, K, box)) != cudaSuccess) return e;
     if ((e = make_tma_map_u8(&mB1, b1, (uint64_t)E * args.n_rows, K, box)) != cudaSuccess) return e;
     if ((e = set_smem_attr<kGated>()) != cudaSuccess) return e;
     return launch_pdl(fp8_solo_kernel<kGated>, dim3(num_sms), dim3(256), SMEM_BYTES, s, mA, mA32,
-                      mB0, mB1, args);
+                      mA8, mB0, mB1, args);
 }
 
 }  // namespace
