@@ -1,6 +1,6 @@
 // api_fp8.cu -- the C ABI of the 8-bit operators and of the balance loss
 // (include/moe.h): argument validation, workspace layout and the launch
-// sequence of each entry point.
+// sequence of each entry point.  Nothing here allocates or throws.
 
 #include "fp8.cuh"
 #include "moe_internal.cuh"
@@ -217,7 +217,6 @@ moe_status run_ffn(const moe_shape* sh, const FfnBufs& b, const moe_fp8_experts*
     return run_product(b.hq, w->down, d, kn, sh->E, num_sms, s);
 }
 
-// C++ exceptions never leave a C entry point: nothing here allocates or throws.
 moe_status check_balance_args(int32_t T, int32_t E, int32_t k, int32_t S, bool have_seq) {
     if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T = %d < 0", T);
     if (E < 1 || E > kMaxE) return fail(MOE_ERR_INVALID_ARG, "E = %d outside [1, %d]", E, kMaxE);
