@@ -31,6 +31,7 @@
 // their common sequence stay in registers.
 #include <algorithm>
 
+#include "ld_dev.cuh"
 #include "moe_internal.cuh"
 #include "ptx.cuh"
 
@@ -47,7 +48,7 @@ struct SeqRange {
 };
 __device__ __forceinline__ SeqRange seq_range(const int32_t* seq, int s, int T) {
     if (!seq) return {0, T};
-    const int b = min(max(__ldg(seq + s), 0), T), e = min(max(__ldg(seq + s + 1), 0), T);
+    const int b = min(max(ld::i32(seq + s), 0), T), e = min(max(ld::i32(seq + s + 1), 0), T);
     return {b, max(b, e)};
 }
 // The last sequence s in [0, S) with seq[s] <= t (0 if there is none).
@@ -56,13 +57,13 @@ __device__ __forceinline__ int seq_of(const int32_t* seq, int S, int t) {
     int lo = 0, hi = S - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(seq + mid) <= t) lo = mid; else hi = mid - 1;
+        if (ld::i32(seq + mid) <= t) lo = mid; else hi = mid - 1;
     }
     return lo;
 }
 __device__ __forceinline__ int tokens_of(const int32_t* seq, int S, int T) {
     if (!seq) return T;
-    const int b = min(max(__ldg(seq), 0), T), e = min(max(__ldg(seq + S), 0), T);
+    const int b = min(max(ld::i32(seq), 0), T), e = min(max(ld::i32(seq + S), 0), T);
     return max(e - b, 0);
 }
 // a_se per counted slot: coef E / (k n_s T').
@@ -92,14 +93,14 @@ __device__ __forceinline__ void load_row(const float* row, int E, bool vec, floa
         const int e = 4 * (lane + 32 * v);
         if (vec) {
             float4 x = make_float4(fill, fill, fill, fill);
-            if (e < E) x = __ldg(reinterpret_cast<const float4*>(row + e));
+            if (e < E) x = ld::f32x4(reinterpret_cast<const float4*>(row + e));
             r[4 * v] = x.x;
             r[4 * v + 1] = x.y;
             r[4 * v + 2] = x.z;
             r[4 * v + 3] = x.w;
         } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) r[4 * v + c] = e + c < E ? __ldg(row + e + c) : fill;
+            for (int c = 0; c < 4; ++c) r[4 * v + c] = e + c < E ? ld::f32(row + e + c) : fill;
         }
     }
 }
@@ -159,7 +160,7 @@ balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx
         for (int e = threadIdx.x; e < E; e += 32 * W) hist[e] = 0;
         __syncthreads();
         for (int i = t0 * k + threadIdx.x; i < t1 * k; i += 32 * W) {
-            const int e = __ldca(idx + i);
+            const int e = ld::i32(idx + i);
             if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
             else set_status(a.hdr, MOE_ERR_BAD_INDEX);
         }
@@ -234,7 +235,7 @@ balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx
         float p = 0.f;
         int n = 0;
         for (int i = q.c0; i < q.c1; ++i) {
-            const float2 v = __ldcg(a.part + (int64_t)i * E + e);
+            const float2 v = ld::f32x2_cg(a.part + (int64_t)i * E + e);
             p += v.x;
             n += __float_as_int(v.y);
         }
@@ -272,7 +273,7 @@ balance_finish_kernel(BalanceArgs a) {
         if (e < a.E) {
 #pragma unroll 8
             for (int c = q.c0 + w; c < q.c1; c += 8) {
-                const float2 v = __ldca(a.part + (int64_t)(c + s) * a.E + e);
+                const float2 v = ld::f32x2(a.part + (int64_t)(c + s) * a.E + e);
                 p += v.x;
                 n += __float_as_int(v.y);
             }
@@ -305,7 +306,7 @@ balance_finish_kernel(BalanceArgs a) {
     if (!last) return;
     __threadfence();
     float loss = 0.f;
-    for (int i = threadIdx.x; i < (int)(gridDim.x * gridDim.y); i += 256) loss += __ldcg(a.shares + i);
+    for (int i = threadIdx.x; i < (int)(gridDim.x * gridDim.y); i += 256) loss += ld::f32_cg(a.shares + i);
     loss = warp_sum(loss);
     if (lane == 0) red[w] = loss;
     __syncthreads();
@@ -329,7 +330,7 @@ balance_backward_kernel(const float* __restrict__ logits, const float2* __restri
     const int E = a.E, k = a.k;
     const bool vec = a.vec;
     const int total = tokens_of(a.seq, a.S, a.T);
-    const float up = d_loss ? __ldg(d_loss) : 1.f;
+    const float up = d_loss ? ld::f32(d_loss) : 1.f;
     const int t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * a.chunk, t1 = min(a.T, t0 + a.chunk);
     int s = -1;
     SeqRange r{0, 0};
@@ -338,7 +339,7 @@ balance_backward_kernel(const float* __restrict__ logits, const float2* __restri
     float2 st_next = make_float2(0.f, 0.f);
     auto fetch = [&](int t) {
         load_row<V>(logits + (int64_t)t * E, E, vec, -INFINITY, next);
-        st_next = __ldca(stats + t);
+        st_next = ld::f32x2(stats + t);
     };
     if (t0 < t1) fetch(t0);
     for (int t = t0; t < t1; ++t) {
@@ -351,7 +352,7 @@ balance_backward_kernel(const float* __restrict__ logits, const float2* __restri
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int e = 4 * (lane + 32 * v) + c;
-                    coef[4 * v + c] = e < E ? w * (float)__ldca(counts + (int64_t)s * E + e) : 0.f;
+                    coef[4 * v + c] = e < E ? w * (float)ld::i32(counts + (int64_t)s * E + e) : 0.f;
                 }
         }
         const bool inside = t >= r.beg && t < r.end;
@@ -359,10 +360,10 @@ balance_backward_kernel(const float* __restrict__ logits, const float2* __restri
         int e_sel = -1;
         float add = 0.f;
         if (idx && lane < k) {
-            e_sel = __ldca(idx + (int64_t)t * k + lane);
-            add = __ldca(gates + (int64_t)t * k + lane);
+            e_sel = ld::i32(idx + (int64_t)t * k + lane);
+            add = ld::f32(gates + (int64_t)t * k + lane);
         }
-        const float dg = idx && lane < k ? __ldg(d_gates + (int64_t)t * k + lane) : 0.f;
+        const float dg = idx && lane < k ? ld::f32(d_gates + (int64_t)t * k + lane) : 0.f;
         float p[4 * V];
 #pragma unroll
         for (int j = 0; j < 4 * V; ++j) p[j] = next[j];

@@ -6,6 +6,7 @@
 // 16-byte vectors.
 #include "moe_internal.cuh"
 #include "combine_dev.cuh"
+#include "ld_dev.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -48,10 +49,10 @@ combine_f32_kernel(const float4* __restrict__ y, const int32_t* __restrict__ inv
 #pragma unroll
     for (int j = 0; j < kMaxK; ++j) {
         if (j >= k) continue;
-        const int64_t row = (int64_t)__ldca(inv_perm + t * k + j) * vec + v;
-        a[j] = __ldca(y + 2 * row);
-        b[j] = __ldca(y + 2 * row + 1);
-        g[j] = __ldca(gates + t * k + j);
+        const int64_t row = (int64_t)ld::i32(inv_perm + t * k + j) * vec + v;
+        a[j] = ld::f32x4(y + 2 * row);
+        b[j] = ld::f32x4(y + 2 * row + 1);
+        g[j] = ld::f32(gates + t * k + j);
     }
     float s[8] = {};
 #pragma unroll

@@ -20,6 +20,7 @@
 #include <cuda.h>
 #include <stdint.h>
 
+#include "ld_dev.cuh"
 #include "moe_internal.cuh"
 #include "ptx.cuh"
 
@@ -141,7 +142,7 @@ struct OneGroup {
     int lo, n;
 };
 __device__ __forceinline__ OneGroup one_group(const Fp8Args& args) {
-    const int a = __ldcg(args.group), b = __ldcg(args.group + 1);
+    const int a = ld::i32_cg(args.group), b = ld::i32_cg(args.group + 1);
     const int lo = min(max(a, 0), args.rows);
     if ((a != 0 || b != args.rows) && blockIdx.x == 0 && threadIdx.x == 0)
         set_status(args.hdr, MOE_ERR_BAD_INDEX);
@@ -154,13 +155,11 @@ __device__ __forceinline__ FatTile group_tile(const OneGroup& g, int i) {
 // Scale word w (bytes 4w .. 4w+3) of a row of nb scale bytes; bytes past nb
 // read as 127 (a factor of one, for operands that TMA filled with zeros).
 __device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int w, int nb) {
-    // coherent loads: the rows' bytes may be written while the kernel already
-    // waits for the one before it
-    if ((nb & 3) == 0) return __ldca(reinterpret_cast<const uint32_t*>(row) + w);
+    if ((nb & 3) == 0) return ld::u32(reinterpret_cast<const uint32_t*>(row) + w);
     uint32_t v = 0;
 #pragma unroll 1   // rare; unrolled, the loads of several words raise the kernels' registers
     for (int i = 3; i >= 0; --i)
-        v = (v << 8) | (4 * w + i < nb ? (uint32_t)__ldca(row + 4 * w + i) : 127u);
+        v = (v << 8) | (4 * w + i < nb ? ld::u8(row + 4 * w + i) : 127u);
     return v;
 }
 

@@ -135,7 +135,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     grid_dep_launch();
 
     const fp8::OneGroup grp = args.group ? fp8::one_group(args) : fp8::OneGroup{0, 0};
-    const int n_pairs = args.group ? (grp.n + 2 * BM - 1) / (2 * BM) : args.hdr->n_fat_tiles >> 1;
+    const int n_pairs = args.group ? (grp.n + 2 * BM - 1) / (2 * BM) : ld::i32_cg(&args.hdr->n_fat_tiles) >> 1;
     const int total = n_pairs * args.n_blocks_n;
     const int k_blocks = args.k_blocks;
     const int k_stages = (k_blocks + KSUB - 1) / KSUB;

@@ -14,6 +14,7 @@
 #include <algorithm>
 
 #include "fp8.cuh"
+#include "ld_dev.cuh"
 #include "moe_internal.cuh"
 #include "ptx.cuh"
 #include "quantize_dev.cuh"
@@ -53,7 +54,7 @@ fp8_prologue_kernel(const float* __restrict__ logits, const uint4* __restrict__ 
         const int v = tid + i * threads;
         if (v < per_row) {
             const uint4* src = x + 2 * ((int64_t)t * per_row + v);
-            q[i] = fp8::quantize_lane16({__ldg(src), __ldg(src + 1)}, &sb[i]);
+            q[i] = fp8::quantize_lane16({ld::u32x4(src), ld::u32x4(src + 1)}, &sb[i]);
         }
     }
     for (int r = warp; r < T; r += threads / 32)

@@ -131,14 +131,14 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         grid_dep_launch();
     }
     auto list_tile = [](const FatTile* p) {
-        const int4 v = __ldcg(reinterpret_cast<const int4*>(p));
-        return FatTile{v.x, v.y, v.z, v.w};
+        const uint4 v = ld::u32x4_cg(p);
+        return FatTile{(int)v.x, (int)v.y, (int)v.z, (int)v.w};
     };
     const fp8::OneGroup grp = args.group ? fp8::one_group(args) : fp8::OneGroup{0, 0};
     const bool with_pairs = args.with_pairs && !args.group;
-    const int n_pair = with_pairs ? __ldcg(&args.hdr->n_fat_tiles) : 0;
-    const int n_solo = args.group ? 0 : n_pair + __ldcg(&args.hdr->n_solo);
-    const int n_tiles = args.group ? (grp.n + BM - 1) / BM : n_solo + __ldcg(&args.hdr->n_thin_mma);
+    const int n_pair = with_pairs ? ld::i32_cg(&args.hdr->n_fat_tiles) : 0;
+    const int n_solo = args.group ? 0 : n_pair + ld::i32_cg(&args.hdr->n_solo);
+    const int n_tiles = args.group ? (grp.n + BM - 1) / BM : n_solo + ld::i32_cg(&args.hdr->n_thin_mma);
     const int total = n_tiles * args.n_blocks_n;
     // (the second tile of an expert's last pair may be empty)
     auto tile_at = [&](int i) {

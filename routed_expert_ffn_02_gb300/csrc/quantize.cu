@@ -16,6 +16,7 @@
 //   matrices  one CTA per 128 x 128 block, 64 values per thread in registers.
 #include <algorithm>
 
+#include "ld_dev.cuh"
 #include "quantize_dev.cuh"
 
 namespace moe {
@@ -42,7 +43,7 @@ quantize_rows_kernel(const uint4* __restrict__ x, int64_t n16, int per_row,
         const int64_t r = i / per_row;
         const int c = (int)(i - r * per_row);
         for (int j = 0; j < k; ++j) {
-            const int64_t p = __ldca(dst + r * k + j);
+            const int64_t p = ld::i32(dst + r * k + j);
             if (p < 0 || p >= P) continue;
             q[p * per_row + c] = o;
             if ((threadIdx.x & 7) == 0) scales[(p * per_row + c) >> 3] = (uint8_t)sb;
@@ -111,7 +112,7 @@ invert_perm_kernel(const int32_t* __restrict__ perm, int64_t P, int32_t* __restr
     ptx::grid_dep_launch();
     for (int64_t p = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; p < P;
          p += (int64_t)gridDim.x * blockDim.x) {
-        const int32_t s = __ldca(perm + p);
+        const int32_t s = ld::i32(perm + p);
         if (s >= 0 && s < P) inv[s] = (int32_t)p;
     }
 }

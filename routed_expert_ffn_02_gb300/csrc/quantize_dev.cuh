@@ -3,6 +3,7 @@
 #pragma once
 
 #include "fp8.cuh"
+#include "ld_dev.cuh"
 
 namespace moe {
 namespace fp8 {
@@ -26,13 +27,14 @@ __device__ __forceinline__ Vec32 load32(const void* p) {
     asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(v.a.x), "=r"(v.a.y), "=r"(v.a.z), "=r"(v.a.w), "=r"(v.b.x), "=r"(v.b.y),
                    "=r"(v.b.z), "=r"(v.b.w)
-                 : "l"(p));
+                 : "l"(p)
+                 : "memory");
     return v;
 }
 // The same where p is 16-byte aligned only.
 __device__ __forceinline__ Vec32 load32(const uint4* p, bool wide) {
     if (wide) return load32(p);
-    return {__ldg(p), __ldg(p + 1)};
+    return {ld::u32x4(p), ld::u32x4(p + 1)};
 }
 
 // Largest magnitude of 16 bf16 values, NaN apart; two values per instruction.
