@@ -181,13 +181,20 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         auto stage_bytes = [](const FatTile& ft) {
             return (uint32_t)(B_BYTES + (ft.rows > 8 ? A_BYTES : 4 * 8 * kBlock));
         };
-        // The first stages' weights do not depend on the previous kernel.
+        // The first stages' weights do not depend on the previous kernel.  They
+        // are those of the CTA's first item with rows: the loop below skips
+        // empty tiles, so what is started here has to be what it runs first.
         int early = 0;
         if (args.early_weights && total_mine > 0) {
-            const FatTile ft = tile_at(blockIdx.x / args.n_blocks_n);
-            const int brow = ft.expert * args.n_rows +
-                             ((int)blockIdx.x % args.n_blocks_n) * (kGated ? 128 : BN);
-            for (early = 0; early < min(STAGES, k_blocks); ++early) {
+            FatTile ft = {};
+            int t = blockIdx.x;
+            for (; t < total_mine; t += active) {
+                ft = tile_at(t / args.n_blocks_n);
+                if (ft.rows > 0) break;
+            }
+            const int brow = ft.expert * args.n_rows + (t % args.n_blocks_n) * (kGated ? 128 : BN);
+            const int stages = ft.rows > 0 ? min(STAGES, k_blocks) : 0;
+            for (; early < stages; ++early) {
                 mbar_expect_tx(full_bar(early), stage_bytes(ft));
                 load_w(base + early * STAGE_BYTES + A_BYTES, full_bar(early), early * kBlock, brow);
             }
