@@ -32,7 +32,9 @@
 // most 8 rows load only 8 per quarter, which takes 12 of 48 KB off each stage.
 //
 // Every wait is bounded; on expiry the kernel records MOE_ERR_TIMEOUT, drains
-// its own copies and MMAs, frees TMEM and returns.
+// its own copies and MMAs, frees TMEM and returns.  The draining waits run in
+// every launch (whichever role gave up, or none): each role's waits expire by
+// themselves, so a role that ran to its end cannot know that another did not.
 #include <cuda.h>
 
 #include "fp8.cuh"
@@ -184,7 +186,8 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         // The first stages' weights do not depend on the previous kernel.  They
         // are those of the CTA's first item with rows: the loop below skips
         // empty tiles, so what is started here has to be what it runs first.
-        int early = 0;
+        int early = 0, early_end = 0;   // stages [early_end - early, early_end) lack their rows
+        uint32_t early_rows = 0;        // bytes of them per stage
         if (args.early_weights && total_mine > 0) {
             FatTile ft = {};
             int t = blockIdx.x;
@@ -198,6 +201,8 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 mbar_expect_tx(full_bar(early), stage_bytes(ft));
                 load_w(base + early * STAGE_BYTES + A_BYTES, full_bar(early), early * kBlock, brow);
             }
+            early_end = early;
+            early_rows = stage_bytes(ft) - B_BYTES;
             grid_dep_wait();
             grid_dep_launch();
             // the rows come from the previous kernel's ordinary stores
@@ -230,9 +235,15 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         if (!ok) {
             *abort_flag = 1;
             set_status(args.hdr, MOE_ERR_TIMEOUT);
-            for (int s = 0; s < STAGES; ++s)
-                if (pending[s] >= 0) (void)mbar_wait(full_bar(s), (uint32_t)pending[s]);
+            for (int s = early_end - early; s < early_end; ++s) {
+                mbar_complete_tx(full_bar(s), early_rows);
+                pending[s] = 0;
+            }
         }
+        // Every copy has landed before the CTA leaves.  Also where this loop
+        // ran to its end: the MMA lane may have given up on the last stages.
+        for (int s = 0; s < STAGES; ++s)
+            if (pending[s] >= 0) (void)mbar_wait(full_bar(s), (uint32_t)pending[s]);
     } else if (warp == 1 && lane == 0) {
         // ---------------- MMA issuer ----------------
         int stage = 0, slot = 0;
@@ -298,10 +309,12 @@ fp8_solo_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         if (!ok) {
             *abort_flag = 1;
             set_status(args.hdr, MOE_ERR_TIMEOUT);
-            if (issued) {
-                commit(done_bar);
-                (void)mbar_wait(done_bar, 0);
-            }
+        }
+        // Every MMA has completed before TMEM is freed.  Also where this loop
+        // ran to its end: the epilogue may have given up on the last tile.
+        if (issued) {
+            commit(done_bar);
+            (void)mbar_wait(done_bar, 0);
         }
     } else if (warp == 3) {
         // ---------------- scale producer ----------------

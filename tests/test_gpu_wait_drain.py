@@ -1,0 +1,51 @@
+"""GPU: expert kernels whose waits expire leave nothing behind, also where one
+role had already issued all it had to (few blocks of K: the producer never
+waits), so that only the others gave up.
+
+Each round launches a call whose main-loop waits give up after one cycle and,
+without a pause, the same call with the default bound: its CTAs take over the
+shared memory and tensor memory at once, so a copy or MMA still on its way
+would land in theirs.  Its outputs have to be the bits of an undisturbed call."""
+import pytest
+import torch
+
+import synth
+from test_gpu_fp8 import layer_case
+
+pytestmark = pytest.mark.gpu
+MOE_ERR_TIMEOUT = 5
+ROUNDS = 20
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import routed_expert_ffn_02_gb300 as m
+    return m
+
+
+def check(moe, call, ws):
+    ref = call().clone()
+    torch.cuda.synchronize()
+    assert ws.status() == 0
+    outs = []
+    for _ in range(ROUNDS):
+        moe.debug_set_wait_limit(1)
+        try:
+            call()
+        finally:
+            moe.debug_set_wait_limit(0)
+        outs.append(call().clone())
+    torch.cuda.synchronize()
+    assert ws.status(clear=True) == MOE_ERR_TIMEOUT
+    assert all(torch.equal(o, ref) for o in outs)
+    assert torch.equal(call(), ref) and ws.status() == 0
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(4, 64, 8, 512, 256),       # thin tiles
+                                       (40, 2, 2, 512, 512),       # 33-128 rows
+                                       (300, 64, 2, 512, 512),     # padded pair tiles, early weights
+                                       (700, 3, 2, 2048, 1024)])
+def test_8bit_one_cta_kernel(moe, T, E, k, H, I):
+    shape, lg, x, ex, _ = layer_case(moe, T, E, k, H, I, 1.1)
+    ws = moe.Workspace(moe.fp8_workspace_size(shape))
+    check(moe, lambda: moe.moe_forward_fp8(shape, lg, x, ex, ws=ws), ws)
