@@ -149,9 +149,11 @@ grouped_gemm_solo_kernel(const __grid_constant__ CUtensorMap tmA,
         if (!ok) {
             *abort_flag = 1;
             set_status(args.hdr, MOE_ERR_TIMEOUT);
-            for (int s = 0; s < STAGES; ++s)
-                if (pending[s] >= 0) (void)mbar_wait(full_bar(s), (uint32_t)pending[s]);
         }
+        // Every copy has landed before the CTA leaves.  Also where this loop
+        // ran to its end: the MMA lane may have given up on the last stages.
+        for (int s = 0; s < STAGES; ++s)
+            if (pending[s] >= 0) (void)mbar_wait(full_bar(s), (uint32_t)pending[s]);
     } else if (warp == 1 && lane == 0) {
         // ---------------- MMA issuer ----------------
         int stage = 0;
@@ -193,10 +195,12 @@ grouped_gemm_solo_kernel(const __grid_constant__ CUtensorMap tmA,
         if (!ok) {
             *abort_flag = 1;
             set_status(args.hdr, MOE_ERR_TIMEOUT);
-            if (issued) {
-                commit(done_bar);
-                (void)mbar_wait(done_bar, 0);
-            }
+        }
+        // Every MMA has completed before TMEM is freed.  Also where this loop
+        // ran to its end: the epilogue may have given up on the last item.
+        if (issued) {
+            commit(done_bar);
+            (void)mbar_wait(done_bar, 0);
         }
     } else if (warp >= 4) {
         // ---------------- epilogue ----------------

@@ -49,3 +49,18 @@ def test_8bit_one_cta_kernel(moe, T, E, k, H, I):
     shape, lg, x, ex, _ = layer_case(moe, T, E, k, H, I, 1.1)
     ws = moe.Workspace(moe.fp8_workspace_size(shape))
     check(moe, lambda: moe.moe_forward_fp8(shape, lg, x, ex, ws=ws), ws)
+
+
+def experts_case(moe, T, E, k, H, I, thr, mma):
+    """moe_expert_ffn on bf16 experts, as a call."""
+    d = {n: v.cuda() for n, v in synth.make_layer(synth.Shape(T=T, E=E, k=k, H=H, I=I), seed=7).items()}
+    shape = moe.Shape(T, E, k, H, I, fat_threshold=thr, thin_mma_min=mma)
+    counts, offsets, perm, _ = moe.moe_permute(moe.moe_route(d["logits"], k)[0], E)
+    ws = moe.Workspace(moe.expert_ffn_workspace_size(shape))
+    return (lambda: moe.moe_expert_ffn(shape, d["x"], perm, offsets, counts, d["Wg"], d["Wu"], d["Wd"],
+                                       ws=ws)), ws
+
+
+@pytest.mark.parametrize("H,I", [(256, 256), (2048, 512)])
+def test_bf16_one_cta_gemm(moe, H, I):
+    check(moe, *experts_case(moe, 64, 16, 2, H, I, 1, 0))
