@@ -200,9 +200,11 @@ thin_mma_kernel(const __grid_constant__ CUtensorMap tmX,
         if (!ok) {
             *abort_flag = 1;
             set_status(args.hdr, MOE_ERR_TIMEOUT);
-            for (int s = 0; s < C::kStages; ++s)
-                if (pending[s] >= 0) (void)mbar_wait(full_bar(s), (uint32_t)pending[s]);
         }
+        // Every copy has landed before the CTA leaves.  Also where this loop
+        // ran to its end: the MMA lane may have given up on the last stages.
+        for (int s = 0; s < C::kStages; ++s)
+            if (pending[s] >= 0) (void)mbar_wait(full_bar(s), (uint32_t)pending[s]);
     } else if (warp == 1 && lane == 0) {
         // ---------------- MMA issuer ----------------
         int stage = 0;
@@ -248,10 +250,12 @@ thin_mma_kernel(const __grid_constant__ CUtensorMap tmX,
         if (!ok) {
             *abort_flag = 1;
             set_status(args.hdr, MOE_ERR_TIMEOUT);
-            if (issued) {
-                commit(done_bar);
-                (void)mbar_wait(done_bar, 0);
-            }
+        }
+        // Every MMA has completed before TMEM is freed.  Also where this loop
+        // ran to its end: the epilogue may have given up on the last item.
+        if (issued) {
+            commit(done_bar);
+            (void)mbar_wait(done_bar, 0);
         }
     } else if (warp >= 4) {
         // ---------------- epilogue ----------------

@@ -64,3 +64,8 @@ def experts_case(moe, T, E, k, H, I, thr, mma):
 @pytest.mark.parametrize("H,I", [(256, 256), (2048, 512)])
 def test_bf16_one_cta_gemm(moe, H, I):
     check(moe, *experts_case(moe, 64, 16, 2, H, I, 1, 0))
+
+
+@pytest.mark.parametrize("H,I", [(256, 256), (2048, 1024)])
+def test_tensor_core_streaming(moe, H, I):
+    check(moe, *experts_case(moe, 64, 16, 2, H, I, 33, 1))
