@@ -269,8 +269,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, long lo
 // the consumers have released the unit that used that buffer before.  Items
 // [0, pre) (pre <= slots) were already issued into slots [0, pre).  While a
 // slot is still in use the lane sleeps in try_wait.  Each wait gives up after
-// `limit` cycles; then the copies already issued are waited for (full bound)
-// and it returns false.
+// `limit` cycles, and it returns false.  The copies it issued are waited for
+// (full bound) before it returns.
 template <int kBufs = 1, typename ItemFn, typename ActFn>
 __device__ bool produce(const Smem& m, int producer, const Range& rg, bool stager,
                         ItemFn copy_item, ActFn copy_act, long long limit, int pre = 0) {
@@ -323,15 +323,14 @@ __device__ bool produce(const Smem& m, int producer, const Range& rg, bool stage
         }
         stage_next();
     }
-    if (!ok) {
-        // Let the copies already issued land before the CTA exits.
-        for (int s = 0; s < m.slots; ++s)
-            if (last_round[s] >= 0)
-                (void)mbar_wait(m.full_of(producer, s), (uint32_t)(last_round[s] & 1));
-        for (int b = 0; b < kBufs; ++b) {
-            const int uses = (act_issued - b + kBufs - 1) / kBufs;   // units staged in b
-            if (uses > 0) (void)mbar_wait(m.act_full(b), (uint32_t)((uses - 1) & 1));
-        }
+    // Every copy has landed before the CTA exits.  Also where all of them could
+    // be issued: a consumer may have given up.
+    for (int s = 0; s < m.slots; ++s)
+        if (last_round[s] >= 0)
+            (void)mbar_wait(m.full_of(producer, s), (uint32_t)(last_round[s] & 1));
+    for (int b = 0; b < kBufs; ++b) {
+        const int uses = (act_issued - b + kBufs - 1) / kBufs;   // units staged in b
+        if (uses > 0) (void)mbar_wait(m.act_full(b), (uint32_t)((uses - 1) & 1));
     }
     return ok;
 }

@@ -89,8 +89,8 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
         fence_proxy_async_global();
         __threadfence();
         failed = __syncthreads_or(!ok);
-        // after a timeout the ring may still have copies in flight: the CTA
-        // then skips the down phase (the status already records the error)
+        // after a timeout a barrier of the ring may be in an unfinished phase:
+        // the CTA then skips the down phase (the status already records it)
         if (!failed) smem_teardown(m);
     }
     if (threadIdx.x == 0) {   // arrive; the down producer waits for the whole grid

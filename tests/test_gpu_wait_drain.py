@@ -69,3 +69,18 @@ def test_bf16_one_cta_gemm(moe, H, I):
 @pytest.mark.parametrize("H,I", [(256, 256), (2048, 1024)])
 def test_tensor_core_streaming(moe, H, I):
     check(moe, *experts_case(moe, 64, 16, 2, H, I, 33, 1))
+
+
+@pytest.mark.parametrize("H,I", [(256, 256), (2048, 1024)])
+def test_cuda_core_streaming(moe, H, I):
+    check(moe, *experts_case(moe, 64, 16, 2, H, I, 33, 33))
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 256, 256), (2, 1024, 2048), (1, 2048, 1024), (2, 2048, 1024)])
+def test_self_routed_decode(moe, T, H, I):
+    """Two launches, or the whole layer in one."""
+    Wg, Wu, Wd = synth.make_weights(16, H, I, seed=7, layer=0, device="cuda")
+    shape = moe.Shape(T, 16, 8, H, I, fat_threshold=32, thin_mma_min=33)
+    x, lg = synth.make_x(T, H, seed=7).cuda(), synth.make_logits(T, 16, seed=7).cuda()
+    ws = moe.Workspace(moe.workspace_size(shape))
+    check(moe, lambda: moe.moe_forward(shape, lg, x, Wg, Wu, Wd, ws=ws), ws)
