@@ -245,12 +245,12 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             if (!ok) break;
             commit_pair_multicast(tfull_bar, kPairMask);
         }
-        if (!ok) {
-            if (!*abort_flag) give_up();
-            if (issued) {
-                commit_pair_multicast(done_bar, 0x1);
-                (void)mbar_wait(done_bar, 0);
-            }
+        if (!ok && !*abort_flag) give_up();
+        // Every MMA has completed before TMEM is freed.  Also where this loop
+        // ran to its end: an epilogue may have given up on the last tile.
+        if (issued) {
+            commit_pair_multicast(done_bar, 0x1);
+            (void)mbar_wait(done_bar, 0);
         }
     } else if (warp >= 8) {
         // ---------------- scale producers (both CTAs) ----------------

@@ -268,13 +268,12 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             if (!ok) break;
             commit_pair_multicast(tfull_bar(acc), kPairMask);
         }
-        if (!ok) {
-            if (!*abort_flag) give_up();
-            if (issued) {
-                // Wait for every MMA issued so far before TMEM is freed.
-                commit_pair_multicast(done_bar, 0x1);
-                (void)mbar_wait(done_bar, 0);
-            }
+        if (!ok && !*abort_flag) give_up();
+        // Every MMA has completed before TMEM is freed.  Also where this loop
+        // ran to its end: an epilogue may have given up on the last tile.
+        if (issued) {
+            commit_pair_multicast(done_bar, 0x1);
+            (void)mbar_wait(done_bar, 0);
         }
     } else if (kGated && args.part == 1 && (warp == 2 || warp == 3)) {
         // ---------------- gather of the later pair tiles' rows ----------------

@@ -84,3 +84,15 @@ def test_self_routed_decode(moe, T, H, I):
     x, lg = synth.make_x(T, H, seed=7).cuda(), synth.make_logits(T, 16, seed=7).cuda()
     ws = moe.Workspace(moe.workspace_size(shape))
     check(moe, lambda: moe.moe_forward(shape, lg, x, Wg, Wu, Wd, ws=ws), ws)
+
+
+@pytest.mark.parametrize("H,I", [(256, 256), (1024, 768)])
+def test_bf16_pair_gemm(moe, H, I):
+    check(moe, *experts_case(moe, 1000, 4, 2, H, I, 1, 0))
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(300, 1, 1, 256, 256), (2500, 6, 2, 512, 256), (2500, 2, 2, 2048, 1024)])
+def test_8bit_pair_kernel(moe, T, E, k, H, I):
+    shape, lg, x, ex, _ = layer_case(moe, T, E, k, H, I, 1.1)
+    ws = moe.Workspace(moe.fp8_workspace_size(shape))
+    check(moe, lambda: moe.moe_forward_fp8(shape, lg, x, ex, ws=ws), ws)
