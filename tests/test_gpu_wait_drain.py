@@ -76,7 +76,7 @@ def test_cuda_core_streaming(moe, H, I):
     check(moe, *experts_case(moe, 64, 16, 2, H, I, 33, 33))
 
 
-@pytest.mark.parametrize("T,H,I", [(1, 256, 256), (2, 1024, 2048), (1, 2048, 1024), (2, 2048, 1024)])
+@pytest.mark.parametrize("T,H,I", [(2, 1024, 2048), (1, 2048, 1024), (2, 2048, 1024)])
 def test_self_routed_decode(moe, T, H, I):
     """Two launches, or the whole layer in one."""
     Wg, Wu, Wd = synth.make_weights(16, H, I, seed=7, layer=0, device="cuda")
