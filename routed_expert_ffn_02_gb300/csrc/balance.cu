@@ -150,7 +150,8 @@ balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx
     __shared__ int last;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x, E = a.E, k = a.k;
-    const int beg = c * a.chunk, end = min(a.T, beg + a.chunk);
+    // (T and T k may reach 2^31 - 129: what may pass them by a block is 64-bit)
+    const int beg = c * a.chunk, end = a.T - beg < a.chunk ? a.T : beg + a.chunk;
     const bool vec = a.vec;
     for (int s = seq_of(a.seq, a.S, beg); s < a.S; ++s) {
         const SeqRange r = seq_range(a.seq, s, a.T);
@@ -159,7 +160,7 @@ balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx
         if (t0 >= t1) continue;
         for (int e = threadIdx.x; e < E; e += 32 * W) hist[e] = 0;
         __syncthreads();
-        for (int i = t0 * k + threadIdx.x; i < t1 * k; i += 32 * W) {
+        for (int64_t i = (int64_t)t0 * k + threadIdx.x; i < (int64_t)t1 * k; i += 32 * W) {
             const int e = ld::i32(idx + i);
             if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
             else set_status(a.hdr, MOE_ERR_BAD_INDEX);
@@ -331,7 +332,8 @@ balance_backward_kernel(const float* __restrict__ logits, const float2* __restri
     const bool vec = a.vec;
     const int total = tokens_of(a.seq, a.S, a.T);
     const float up = d_loss ? ld::f32(d_loss) : 1.f;
-    const int t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * a.chunk, t1 = min(a.T, t0 + a.chunk);
+    const int64_t first = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * a.chunk;
+    const int t0 = (int)min(first, (int64_t)a.T), t1 = (int)min(first + a.chunk, (int64_t)a.T);
     int s = -1;
     SeqRange r{0, 0};
     float coef[4 * V];   // d_loss * a_se of the current sequence
@@ -450,8 +452,8 @@ cudaError_t launch_balance(const float* logits, const int32_t* idx, float2* stat
         e = with_width(a.E, [&]<int V>() {
             constexpr int W = warps_for(V);
             const int most = std::min(num_sms, kMaxChunks);
-            a.chunk = std::max(W, (a.T + most - 1) / most);
-            const int chunks = (a.T + a.chunk - 1) / a.chunk;
+            a.chunk = std::max(W, (int)(((int64_t)a.T + most - 1) / most));
+            const int chunks = (int)(((int64_t)a.T + a.chunk - 1) / a.chunk);
             fused = a.S == 1 && chunks <= kFusedChunks;
             return launch_pdl(balance_kernel<V, W>, dim3(chunks), dim3(32 * W), 0, s, logits, idx,
                               stats, a, (int)fused);
@@ -468,10 +470,10 @@ cudaError_t launch_balance_backward(const float* logits, const float2* stats, co
     if (a.T == 0) return cudaSuccess;
     a.vec = rows_aligned(logits, a.E) && rows_aligned(d_logits, a.E);
     const int warps = num_sms * (a.E <= 384 ? 24 : 16);   // resident at once
-    a.chunk = (a.T + warps - 1) / warps;
-    const int per_block = 8 * a.chunk;
+    a.chunk = (int)(((int64_t)a.T + warps - 1) / warps);
+    const int64_t per_block = 8 * (int64_t)a.chunk;
     return with_width(a.E, [&]<int V>() {
-        return launch_pdl(balance_backward_kernel<V>, dim3((a.T + per_block - 1) / per_block),
+        return launch_pdl(balance_backward_kernel<V>, dim3((unsigned)((a.T + per_block - 1) / per_block)),
                           dim3(256), 0, s, logits, stats, (const int32_t*)a.counts, d_loss, idx,
                           gates, d_gates, d_logits, a);
     });
