@@ -440,7 +440,10 @@ moe_status moe_forward_fp8(const moe_shape* shape, const float* logits, const mo
  *   moe_balance_workspace_size() bytes, initialised once with
  *   moe_workspace_init().  Sums are fp32 in a fixed order: repeated runs give
  *   the same bits.  A routed index outside [0, E) is not counted and sets
- *   MOE_ERR_BAD_INDEX in the workspace status. */
+ *   MOE_ERR_BAD_INDEX in the workspace status.  So do offsets outside [0, T],
+ *   which are held inside it, and offsets that descend anywhere: no token then
+ *   takes part (loss and counts are 0, stats are not written; the backward
+ *   call gives no gradient from the loss). */
 size_t moe_balance_workspace_size(int32_t T, int32_t E, int32_t S);
 moe_status moe_balance(const float* logits, const int32_t* topk_idx, int32_t T, int32_t E,
                        int32_t k, const int32_t* seq_offsets, int32_t S, float coef, float* loss,

@@ -66,6 +66,20 @@ __device__ __forceinline__ int tokens_of(const int32_t* seq, int S, int T) {
     const int b = min(max(ld::i32(seq), 0), T), e = min(max(ld::i32(seq + S), 0), T);
     return max(e - b, 0);
 }
+// Whether the offsets descend anywhere; all threads of a block together.  A
+// sequence then has no meaning (chunks would meet in one partial row, and rows
+// that nobody wrote would be added up), so no token takes part.  Offsets that
+// descend or lie outside [0, T] are recorded by the block that `records`.
+__device__ __forceinline__ bool offsets_descend(const BalanceArgs& a, bool records) {
+    if (!a.seq) return false;
+    int down = 0;
+    for (int64_t s = threadIdx.x; s < a.S; s += blockDim.x) {
+        const int b = ld::i32(a.seq + s), e = ld::i32(a.seq + s + 1);
+        down |= b > e;
+        if (records && (b > e || b < 0 || e > a.T)) set_status(a.hdr, MOE_ERR_BAD_INDEX);
+    }
+    return __syncthreads_or(down) != 0;
+}
 // a_se per counted slot: coef E / (k n_s T').
 __device__ __forceinline__ float slot_weight(float coef, int E, int k, int n, int total) {
     return n > 0 ? coef * (float)E / ((float)k * (float)n * (float)max(total, 1)) : 0.f;
@@ -127,7 +141,8 @@ struct SeqSum {
     int c0, c1;
     float w;
 };
-__device__ __forceinline__ SeqSum seq_sum(const BalanceArgs& a, int s) {
+__device__ __forceinline__ SeqSum seq_sum(const BalanceArgs& a, int s, bool none) {
+    if (none) return {0, 0, 0.f};
     const SeqRange r = seq_range(a.seq, s, a.T);
     const int n = r.end - r.beg;
     const int c0 = r.beg / a.chunk;
@@ -153,7 +168,8 @@ balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx
     // (T and T k may reach 2^31 - 129: what may pass them by a block is 64-bit)
     const int beg = c * a.chunk, end = a.T - beg < a.chunk ? a.T : beg + a.chunk;
     const bool vec = a.vec;
-    for (int s = seq_of(a.seq, a.S, beg); s < a.S; ++s) {
+    const bool none = offsets_descend(a, c == 0);
+    for (int s = none ? a.S : seq_of(a.seq, a.S, beg); s < a.S; ++s) {
         const SeqRange r = seq_range(a.seq, s, a.T);
         if (r.beg >= end) break;
         const int t0 = max(beg, r.beg), t1 = min(end, r.end);
@@ -230,7 +246,7 @@ balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx
     if (!last) return;
     __threadfence();
     // one sequence of at most kFusedChunks chunks
-    const SeqSum q = seq_sum(a, 0);
+    const SeqSum q = seq_sum(a, 0, none);
     float mine = 0.f;
     for (int e = threadIdx.x; e < E; e += 32 * W) {
         float p = 0.f;
@@ -266,9 +282,10 @@ balance_finish_kernel(BalanceArgs a) {
     __shared__ int last;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int e = blockIdx.x * kSlice + lane;
+    const bool none = offsets_descend(a, blockIdx.x == 0 && blockIdx.y == 0);
     float share = 0.f;
     for (int s = blockIdx.y; s < a.S; s += gridDim.y) {
-        const SeqSum q = seq_sum(a, s);
+        const SeqSum q = seq_sum(a, s, none);
         float p = 0.f;
         int n = 0;
         if (e < a.E) {
@@ -330,6 +347,7 @@ balance_backward_kernel(const float* __restrict__ logits, const float2* __restri
     const int lane = threadIdx.x & 31;
     const int E = a.E, k = a.k;
     const bool vec = a.vec;
+    const bool none = offsets_descend(a, false);
     const int total = tokens_of(a.seq, a.S, a.T);
     const float up = d_loss ? ld::f32(d_loss) : 1.f;
     const int64_t first = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * a.chunk;
@@ -357,7 +375,7 @@ balance_backward_kernel(const float* __restrict__ logits, const float2* __restri
                     coef[4 * v + c] = e < E ? w * (float)ld::i32(counts + (int64_t)s * E + e) : 0.f;
                 }
         }
-        const bool inside = t >= r.beg && t < r.end;
+        const bool inside = !none && t >= r.beg && t < r.end;
         float d[4 * V];
         int e_sel = -1;
         float add = 0.f;

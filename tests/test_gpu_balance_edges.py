@@ -28,3 +28,56 @@ def test_as_many_slots_as_fit_31_bits(moe, E, k):
     d = torch.full((T, E), 7.0, device="cuda")
     moe.moe_balance_backward(lg, stats, counts, k, coef=0.5, d_logits=d)
     assert not d.any()
+
+
+def poisoned(moe, T, E, S):
+    """A workspace whose scratch holds large numbers."""
+    ws = moe.Workspace(moe.balance_workspace_size(T, E, S))
+    ws.tensor[256:].view(torch.float32).fill_(1e6)
+    return ws
+
+
+@pytest.mark.parametrize("T", [100, 3000])
+@pytest.mark.parametrize("off", [[0, 80, 40, 100], [90, 10], [0, 50, 50, 49], [0, 2000, 30, 100]])
+def test_descending_offsets(moe, T, off):
+    """Recorded, and no token takes part: nothing of the scratch's former
+    contents reaches the outputs."""
+    E, k, S = 40, 4, len(off) - 1
+    lg = torch.randn((T, E), device="cuda")
+    idx, gates = moe.moe_route(lg, k)
+    seq = torch.tensor(off, dtype=torch.int32, device="cuda")
+    ws = poisoned(moe, T, E, S)
+    stats = torch.full((T, 2), float("nan"), device="cuda")
+    loss, counts, _ = moe.moe_balance(lg, idx, seq, 1.0, stats=stats, ws=ws)
+    assert ws.status(clear=True) == MOE_ERR_BAD_INDEX
+    assert loss.item() == 0 and not counts.any()
+    d = moe.moe_balance_backward(lg, stats, counts, k, seq, 1.0)
+    assert not d.any()
+    dg = torch.randn((T, k), device="cuda")
+    both = moe.moe_balance_backward(lg, stats, counts, k, seq, 1.0, topk_idx=idx, gates=gates, d_gates=dg)
+    ok = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    _, c1, s1 = moe.moe_balance(lg, idx, ok, 0.0)
+    assert torch.equal(both, moe.moe_balance_backward(lg, s1, c1, k, ok, 0.0, topk_idx=idx, gates=gates,
+                                                      d_gates=dg))
+
+
+@pytest.mark.parametrize("off,held", [([-5, 40, 1000], [0, 40, 100]), ([0, 101], [0, 100]), ([-1, 100], [0, 100])])
+def test_offsets_out_of_range_are_held_and_recorded(moe, off, held):
+    lg = torch.randn((100, 8), device="cuda")
+    idx, _ = moe.moe_route(lg, 2)
+    a, b = (torch.tensor(o, dtype=torch.int32, device="cuda") for o in (off, held))
+    ws = poisoned(moe, 100, 8, len(off) - 1)
+    loss, counts, stats = moe.moe_balance(lg, idx, a, ws=ws)
+    assert ws.status(clear=True) == MOE_ERR_BAD_INDEX
+    want = moe.moe_balance(lg, idx, b, ws=ws)
+    assert ws.status() == 0
+    assert torch.equal(loss, want[0]) and torch.equal(counts, want[1]) and torch.equal(stats, want[2])
+
+
+def test_no_tokens_with_offsets(moe):
+    z, i = torch.empty((0, 8), device="cuda"), torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    ws = poisoned(moe, 0, 8, 2)
+    loss, counts, _ = moe.moe_balance(z, i, torch.zeros(3, dtype=torch.int32, device="cuda"), ws=ws)
+    assert ws.status() == 0 and loss.item() == 0 and not counts.any()
+    moe.moe_balance(z, i, torch.tensor([0, 1, 0], dtype=torch.int32, device="cuda"), ws=ws)
+    assert ws.status(clear=True) == MOE_ERR_BAD_INDEX
