@@ -37,13 +37,14 @@ __device__ __forceinline__ Vec32 load32(const uint4* p, bool wide) {
     return {ld::u32x4(p), ld::u32x4(p + 1)};
 }
 
-// Largest magnitude of 16 bf16 values, NaN apart; two values per instruction.
+// Largest magnitude of 16 bf16 values, NaN apart (0 if there is nothing else);
+// two values per instruction.
 __device__ __forceinline__ float amax16(const Vec32& v) {
     const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
     __nv_bfloat162 m = __habs2(p[0]);
 #pragma unroll
     for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(p[i]));
-    return fmaxf(__low2float(m), __high2float(m));
+    return fmaxf(0.f, fmaxf(__low2float(m), __high2float(m)));   // 0: both may be NaN
 }
 // The same over finite values only.
 __device__ __forceinline__ float amax16_finite(const Vec32& v) {
