@@ -400,7 +400,9 @@ typedef struct {
 /* moe_expert_ffn on 8-bit experts.  x [T, H] bf16 is quantised by rows, the
  * intermediate silu(gate) * up by rows from fp32, and
  *   y_sorted[p] = bf16( W_down[e] . quantised( silu(W_gate[e] . x) * (W_up[e] . x) ) )
- * with fp32 accumulation.  perm, offsets as moe_permute wrote them; the
+ * with fp32 accumulation.  perm, offsets as moe_permute wrote them (where it
+ * skipped a routed index outside [0, E), the rows of the other slots are as
+ * stated and the rows after the last of them unspecified); the
  * shape's fat_threshold and thin_mma_min do not apply.  ws:
  * moe_expert_ffn_fp8_workspace_size() bytes, initialised once with
  * moe_workspace_init(). */

@@ -338,7 +338,8 @@ cudaError_t launch_quantize_rows(const __nv_bfloat16* x, int64_t rows, int K, co
 // Quantises n matrices [N, K] in blocks of 128 x 128.
 cudaError_t launch_quantize_matrices(const __nv_bfloat16* w, int64_t n, int N, int K, uint8_t* q,
                                      uint8_t* scales, cudaStream_t s);
-// inv[perm[p]] = p for the slots of perm [P] inside [0, P).
+// inv[perm[p]] = p for the slots of perm [P] inside [0, P), the first p where
+// several hold one slot; -1 for slots that perm does not hold.
 cudaError_t launch_invert_perm(const int32_t* perm, int64_t P, int32_t* inv, int num_sms,
                                cudaStream_t s);
 

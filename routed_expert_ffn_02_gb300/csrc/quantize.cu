@@ -26,7 +26,7 @@ using namespace fp8;
 
 // Vector i is the values [16 i, 16 i + 16) of x [rows, K]; dst == nullptr
 // writes row r to q row r, else to rows dst[r * k .. r * k + k) (a position
-// outside [0, P) is skipped: route lists of a bad index leave it unset).
+// outside [0, P) is skipped: the slot of a bad index has none).
 template <int U>
 __global__ void __launch_bounds__(256)
 quantize_rows_kernel(const uint4* __restrict__ x, int64_t n16, int per_row,
@@ -105,7 +105,19 @@ quantize_matrices_kernel(const uint4* __restrict__ w, int n_cb, uint4* __restric
     for (int i = 0; i < 4; ++i) q[base + (int64_t)(32 * i) * ld] = convert16(v[i], inv, has_inf);
 }
 
-// inv_perm[perm[p]] = p for the slots in range.
+__global__ void __launch_bounds__(256)
+clear_inverse_kernel(int64_t P, int32_t* __restrict__ inv) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    for (int64_t p = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; p < P;
+         p += (int64_t)gridDim.x * blockDim.x)
+        inv[p] = -1;
+}
+
+// inv[perm[p]] = p for the slots in range, over -1 (unsigned: the largest).  A
+// route list of a bad index ends in entries that nobody wrote: of two entries
+// for one slot the first stands, and a slot without one keeps -1, so whatever
+// they hold, no other token's row is written to its place.
 __global__ void __launch_bounds__(256)
 invert_perm_kernel(const int32_t* __restrict__ perm, int64_t P, int32_t* __restrict__ inv) {
     ptx::grid_dep_wait();
@@ -113,7 +125,7 @@ invert_perm_kernel(const int32_t* __restrict__ perm, int64_t P, int32_t* __restr
     for (int64_t p = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; p < P;
          p += (int64_t)gridDim.x * blockDim.x) {
         const int32_t s = ld::i32(perm + p);
-        if (s >= 0 && s < P) inv[s] = (int32_t)p;
+        if (s >= 0 && s < P) atomicMin(reinterpret_cast<unsigned*>(inv + s), (unsigned)p);
     }
 }
 
@@ -148,6 +160,9 @@ cudaError_t launch_invert_perm(const int32_t* perm, int64_t P, int32_t* inv, int
                                cudaStream_t s) {
     if (P == 0) return cudaSuccess;
     const int64_t blocks = std::min<int64_t>((P + 255) / 256, (int64_t)num_sms * 8);
+    const cudaError_t e =
+        launch_pdl(clear_inverse_kernel, dim3((unsigned)blocks), dim3(256), 0, s, P, inv);
+    if (e != cudaSuccess) return e;
     return launch_pdl(invert_perm_kernel, dim3((unsigned)blocks), dim3(256), 0, s, perm, P, inv);
 }
 

@@ -1,9 +1,11 @@
-"""GPU: the quantiser on blocks without a finite value.  Exact."""
+"""GPU: the 8-bit operators on blocks without a finite value and on route lists of
+bad indices.  The quantiser is exact; tolerances else as in test_gpu_fp8.py."""
 import pytest
 import torch
 
 import fp8_plain as plain
-from test_gpu_fp8 import randn, same
+from parity import REL_RMS_TOL
+from test_gpu_fp8 import layer_case, randn, rel_rms, same
 
 pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
@@ -39,7 +41,6 @@ def test_block_without_finite_values(moe, fill):
 @pytest.mark.parametrize("T", [3, 40, 300])
 def test_token_without_finite_values(moe, T):
     """In the layer: NaN outputs for that token alone, whichever launch quantises."""
-    from test_gpu_fp8 import layer_case
     shape, lg, x, ex, _ = layer_case(moe, T, 8, 2, 512, 256)
     ref = moe.moe_forward_fp8(shape, lg, x, ex)
     x[1] = NAN
@@ -47,3 +48,26 @@ def test_token_without_finite_values(moe, T):
     assert torch.isnan(out[1]).all()
     rest = [t for t in range(T) if t != 1]
     assert torch.equal(out[rest], ref[rest])
+
+
+@pytest.mark.parametrize("T,E,k", [(200, 8, 2), (3000, 16, 4)])
+def test_experts_after_bad_indices(moe, T, E, k):
+    """Slots of bad indices are skipped; the tail of perm that nobody writes holds
+    slots of other tokens here, whose rows must come out right all the same."""
+    shape, lg, x, ex, parts = layer_case(moe, T, E, k, 512, 256)
+    idx, gates = moe.moe_route(lg, k)
+    bad = torch.zeros((T, k), dtype=torch.bool, device="cuda")
+    bad[T // 2:, 1] = True
+    n_bad, P = int(bad.sum()), T * k
+    sent = torch.where(bad, E + 3, idx).int()
+    out = tuple(torch.arange(n, dtype=torch.int32, device="cuda") for n in (E, E + 1, P, P))
+    out[2][-n_bad:] = torch.arange(n_bad, device="cuda")     # slots of the first tokens
+    pws = moe.Workspace(moe.permute_workspace_size(T, E, k))
+    _, offsets, perm, inv = moe.moe_permute(sent, E, ws=pws, out=out)
+    assert pws.status(clear=True) == 6       # MOE_ERR_BAD_INDEX
+    ws = moe.Workspace(moe.expert_ffn_fp8_workspace_size(shape))
+    ws.tensor[256:].zero_()                  # as stale as a workspace can be: all positions 0
+    ys = moe.moe_expert_ffn_fp8(shape, x, perm, offsets, ex, ws=ws)
+    _, y = plain.layer(x, idx, gates, parts)
+    good = ~bad.flatten()
+    assert rel_rms(ys[inv[good].long()], y.view(P, 512)[good]) <= REL_RMS_TOL
