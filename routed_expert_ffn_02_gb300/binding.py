@@ -3,8 +3,9 @@
 Argument marshalling only: every step of the layer runs in libmoe's CUDA
 kernels.  Tensors are torch CUDA tensors; their data pointers and the current
 torch stream are handed to the C entry points.  Missing outputs and
-workspaces are allocated with torch (device memory is torch's job here).  If
-libmoe.so is missing this module raises on import: there is no fallback.
+workspaces are allocated with torch (device memory is torch's job here), as
+under torch.cuda.stream(stream) where a call is given a stream.  If libmoe.so
+is missing this module raises on import: there is no fallback.
 """
 from __future__ import annotations
 
@@ -155,6 +156,17 @@ def _ptr(t: torch.Tensor | None):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    """A tensor for a call on `stream` (None: the current one), out of that
+    stream's memory: torch hands memory out again in its stream's order, so
+    other streams' work is neither still using it nor given it before the call
+    has run."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _host_ptr(t: torch.Tensor):
     assert not t.is_cuda and t.is_contiguous(), "expected a contiguous host tensor"
     return ctypes.c_void_p(t.data_ptr())
@@ -179,10 +191,10 @@ def _opt(t: torch.Tensor | None, dtype, shape):
     return None if t is None else _in(t, dtype, shape)
 
 
-def _out(t: torch.Tensor | None, shape, dtype, like: torch.Tensor):
+def _out(t: torch.Tensor | None, shape, dtype, like: torch.Tensor, stream):
     """The caller's output tensor, checked, or a new one, and its address."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=like.device)
+        t = _empty(shape, dtype, like.device, stream)
         return t, t.data_ptr()
     return t, _in(t, dtype, shape)
 
@@ -221,12 +233,13 @@ def debug_set_wait_limit(cycles: int) -> None:
 
 
 class Workspace:
-    """Device scratch for libmoe calls: a 256-byte-aligned torch buffer whose
-    status word is cleared once at creation."""
+    """Device scratch for libmoe calls on one stream (None: the current one): a
+    256-byte-aligned torch buffer whose status word is cleared once at
+    creation."""
 
     def __init__(self, nbytes: int, device=None, stream=None):
         device = device or torch.device("cuda", torch.cuda.current_device())
-        self._buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+        self._buf = _empty(nbytes + 256, torch.uint8, device, stream)
         off = (-self._buf.data_ptr()) % 256
         self.tensor = self._buf[off:off + nbytes]
         self.nbytes = nbytes
@@ -266,8 +279,8 @@ def expert_ffn_workspace_size(shape: Shape) -> int:
 def moe_route(logits: torch.Tensor, k: int, topk_idx=None, gates=None, stream=None):
     T, E = logits.shape
     dev = logits.device
-    topk_idx = topk_idx if topk_idx is not None else torch.empty((T, k), dtype=torch.int32, device=dev)
-    gates = gates if gates is not None else torch.empty((T, k), dtype=torch.float32, device=dev)
+    topk_idx = topk_idx if topk_idx is not None else _empty((T, k), torch.int32, dev, stream)
+    gates = gates if gates is not None else _empty((T, k), torch.float32, dev, stream)
     _check(_lib.moe_route(_ptr(logits), T, E, k, _ptr(topk_idx), _ptr(gates), _stream(stream)),
            "moe_route")
     return topk_idx, gates
@@ -280,10 +293,9 @@ def moe_permute(topk_idx: torch.Tensor, E: int, ws: Workspace | None = None, out
     dev = topk_idx.device
     P = T * k
     if out is None:
-        out = (torch.empty(E, dtype=torch.int32, device=dev),
-               torch.empty(E + 1, dtype=torch.int32, device=dev),
-               torch.empty(max(P, 1), dtype=torch.int32, device=dev)[:P],
-               torch.empty(max(P, 1), dtype=torch.int32, device=dev)[:P])
+        out = (_empty(E, torch.int32, dev, stream), _empty(E + 1, torch.int32, dev, stream),
+               _empty(max(P, 1), torch.int32, dev, stream)[:P],
+               _empty(max(P, 1), torch.int32, dev, stream)[:P])
     counts, offsets, perm, inv_perm = out
     ws = ws or Workspace(permute_workspace_size(T, E, k), dev, stream)
     _check(_lib.moe_permute(_ptr(topk_idx), T, E, k, _ptr(counts), _ptr(offsets), _ptr(perm),
@@ -306,8 +318,8 @@ def moe_permute_noalloc(topk_idx: torch.Tensor, E: int, out, device_status=None,
 def moe_expert_ffn(shape: Shape, x, perm, offsets, counts, W_gate, W_up, W_down,
                    y_sorted=None, ws: Workspace | None = None, stream=None):
     dev = x.device
-    y_sorted = y_sorted if y_sorted is not None else torch.empty(
-        (shape.P, shape.H), dtype=torch.bfloat16, device=dev)
+    y_sorted = y_sorted if y_sorted is not None else _empty(
+        (shape.P, shape.H), torch.bfloat16, dev, stream)
     ws = ws or Workspace(expert_ffn_workspace_size(shape), dev, stream)
     _check(_lib.moe_expert_ffn(ctypes.byref(shape.c()), _ptr(x), _ptr(perm), _ptr(offsets),
                                _ptr(counts), _ptr(W_gate), _ptr(W_up), _ptr(W_down),
@@ -317,8 +329,7 @@ def moe_expert_ffn(shape: Shape, x, perm, offsets, counts, W_gate, W_up, W_down,
 
 
 def moe_combine(y_sorted, inv_perm, gates, T: int, k: int, H: int, out=None, stream=None):
-    out = out if out is not None else torch.empty((T, H), dtype=torch.bfloat16,
-                                                  device=y_sorted.device)
+    out = out if out is not None else _empty((T, H), torch.bfloat16, y_sorted.device, stream)
     _check(_lib.moe_combine(_ptr(y_sorted), _ptr(inv_perm), _ptr(gates), T, k, H, _ptr(out),
                             _stream(stream)), "moe_combine")
     return out
@@ -327,8 +338,7 @@ def moe_combine(y_sorted, inv_perm, gates, T: int, k: int, H: int, out=None, str
 def moe_forward(shape: Shape, logits, x, W_gate, W_up, W_down, out=None, topk_idx=None,
                 gates=None, ws: Workspace | None = None, stream=None):
     dev = x.device
-    out = out if out is not None else torch.empty((shape.T, shape.H), dtype=torch.bfloat16,
-                                                  device=dev)
+    out = out if out is not None else _empty((shape.T, shape.H), torch.bfloat16, dev, stream)
     ws = ws or Workspace(workspace_size(shape), dev, stream)
     _check(_lib.moe_forward(ctypes.byref(shape.c()), _ptr(logits), _ptr(x), _ptr(W_gate),
                             _ptr(W_up), _ptr(W_down), _ptr(out), _ptr(topk_idx), _ptr(gates),
@@ -348,8 +358,7 @@ def moe_forward_profiled(shape: Shape, logits, x, W_gate, W_up, W_down, events, 
     created with enable_timing=True) at the stage boundaries."""
     assert len(events) == PROFILE_EVENTS
     dev = x.device
-    out = out if out is not None else torch.empty((shape.T, shape.H), dtype=torch.bfloat16,
-                                                  device=dev)
+    out = out if out is not None else _empty((shape.T, shape.H), torch.bfloat16, dev, stream)
     ws = ws or Workspace(workspace_size(shape), dev, stream)
     for e in events:
         if e.cuda_event == 0:   # torch creates the CUDA event on first record
@@ -419,7 +428,7 @@ class Stager:
         L = len(host_weights)
         dev = x.device
         outs = outs if outs is not None else [
-            torch.empty((shape.T, shape.H), dtype=torch.bfloat16, device=dev) for _ in range(L)]
+            _empty((shape.T, shape.H), torch.bfloat16, dev, compute) for _ in range(L)]
         ws = ws or Workspace(workspace_size(shape), dev, compute)
         compute = compute if compute is not None else torch.cuda.current_stream()
         copy = copy if copy is not None else torch.cuda.Stream(device=dev)
@@ -527,7 +536,7 @@ class ExpertCache:
         dev = x.device
         shape = self.shape
         outs = outs if outs is not None else [
-            torch.empty((shape.T, shape.H), dtype=torch.bfloat16, device=dev) for _ in range(L)]
+            _empty((shape.T, shape.H), torch.bfloat16, dev, compute) for _ in range(L)]
         ws = ws or Workspace(workspace_size(shape), dev, compute)
         compute = compute if compute is not None else torch.cuda.current_stream()
         copy = copy if copy is not None else torch.cuda.Stream(device=dev)
@@ -583,8 +592,8 @@ def moe_quantize_rows(x: torch.Tensor, q=None, scales=None, stream=None):
     """x [rows, K] bf16 -> (q [rows, K] float8_e4m3fn, scales [rows, K/128]
     uint8): one power-of-two scale 2^(byte - 127) per 128 values of a row."""
     rows, K = x.shape
-    q, qp = _out(q, (rows, K), _E4M3, x)
-    scales, sp = _out(scales, (rows, K // 128), _U8, x)
+    q, qp = _out(q, (rows, K), _E4M3, x, stream)
+    scales, sp = _out(scales, (rows, K // 128), _U8, x, stream)
     st = _lib.moe_quantize_rows(_in(x, _BF16, (rows, K)), rows, K, qp, sp, _on(stream, x))
     if st:
         raise MoeError(st, "moe_quantize_rows")
@@ -595,8 +604,8 @@ def moe_quantize_weights(W: torch.Tensor, q=None, scales=None, stream=None):
     """W [E, N, K] bf16 -> (q [E, N, K] float8_e4m3fn, scales [E, N/128, K/128]
     uint8): one power-of-two scale per 128 x 128 block."""
     E, N, K = W.shape
-    q, qp = _out(q, (E, N, K), _E4M3, W)
-    scales, sp = _out(scales, (E, N // 128, K // 128), _U8, W)
+    q, qp = _out(q, (E, N, K), _E4M3, W, stream)
+    scales, sp = _out(scales, (E, N // 128, K // 128), _U8, W, stream)
     st = _lib.moe_quantize_weights(_in(W, _BF16, (E, N, K)), E, N, K, qp, sp, _on(stream, W))
     if st:
         raise MoeError(st, "moe_quantize_weights")
@@ -617,7 +626,7 @@ def moe_grouped_gemm_fp8(x, x_scales, offsets, W, W_scales, y=None, ws: Workspac
     them); y [rows, N] bf16.  E = 1 (offsets [0, rows]) is the dense product."""
     rows, K = x.shape
     E, N, _ = W.shape
-    y, yp = _out(y, (rows, N), _BF16, x)
+    y, yp = _out(y, (rows, N), _BF16, x, stream)
     ws = ws or Workspace(grouped_gemm_fp8_workspace_size(rows, E), x.device, stream)
     st = _lib.moe_grouped_gemm_fp8(
         _in(x, _E4M3, (rows, K)), _in(x_scales, _U8, (rows, K // 128)), rows,
@@ -675,7 +684,7 @@ def moe_expert_ffn_fp8(shape: Shape, x, perm, offsets, experts: Fp8Experts, y_so
                        ws: Workspace | None = None, stream=None):
     """moe_expert_ffn on 8-bit experts (perm, offsets from moe_permute)."""
     P, T, H = shape.P, shape.T, shape.H
-    y_sorted, yp = _out(y_sorted, (P, H), _BF16, x)
+    y_sorted, yp = _out(y_sorted, (P, H), _BF16, x, stream)
     ws = ws or Workspace(expert_ffn_fp8_workspace_size(shape), x.device, stream)
     st = _lib.moe_expert_ffn_fp8(
         ctypes.byref(shape.c()), _in(x, _BF16, (T, H)), _in(perm, _I32, (P,)),
@@ -697,7 +706,7 @@ def moe_forward_fp8(shape: Shape, logits, x, experts: Fp8Experts, out=None, topk
                     gates=None, ws: Workspace | None = None, stream=None):
     """moe_forward on 8-bit experts."""
     T, H, k = shape.T, shape.H, shape.k
-    out, op = _out(out, (T, H), _BF16, x)
+    out, op = _out(out, (T, H), _BF16, x, stream)
     ws = ws or Workspace(fp8_workspace_size(shape), x.device, stream)
     st = _lib.moe_forward_fp8(
         ctypes.byref(shape.c()), _in(logits, _F32, (T, shape.E)), _in(x, _BF16, (T, H)),
@@ -723,9 +732,9 @@ def moe_balance(logits, topk_idx, seq_offsets=None, coef: float = 1.0, loss=None
     T, E = logits.shape
     k = topk_idx.shape[1]
     S = _sequences(seq_offsets)
-    loss, lp = _out(loss, (), _F32, logits)
-    counts, cp = _out(counts, (S, E), _I32, logits)
-    stats, sp = _out(stats, (T, 2), _F32, logits)
+    loss, lp = _out(loss, (), _F32, logits, stream)
+    counts, cp = _out(counts, (S, E), _I32, logits, stream)
+    stats, sp = _out(stats, (T, 2), _F32, logits, stream)
     ws = ws or Workspace(balance_workspace_size(T, E, S), logits.device, stream)
     st = _lib.moe_balance(
         _in(logits, _F32, (T, E)), _in(topk_idx, _I32, (T, k)), T, E, k,
@@ -743,7 +752,7 @@ def moe_balance_backward(logits, stats, counts, k: int, seq_offsets=None, coef: 
     the router's gates.  Returns d_logits [T, E] fp32."""
     T, E = logits.shape
     S = _sequences(seq_offsets)
-    d_logits, dp = _out(d_logits, (T, E), _F32, logits)
+    d_logits, dp = _out(d_logits, (T, E), _F32, logits, stream)
     st = _lib.moe_balance_backward(
         _in(logits, _F32, (T, E)), _in(stats, _F32, (T, 2)), _in(counts, _I32, (S, E)),
         _opt(seq_offsets, _I32, (S + 1,)), T, E, k, S, coef, _opt(d_loss, _F32, ()),
