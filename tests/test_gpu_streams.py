@@ -53,11 +53,11 @@ def test_outputs_are_not_memory_that_another_stream_still_writes(moe, name):
     torch.cuda.empty_cache()
     torch.cuda._sleep(HOLD)
     for t in want:           # written late by the current stream, freed at once
-        torch.empty_like(t).view(torch.uint8).fill_(0x55)
+        torch.empty_like(t).reshape(-1).view(torch.uint8).fill_(0x55)
     got = call(side)
     torch.cuda.synchronize()
     for g, w in zip(got, want):
-        assert torch.equal(g.view(torch.uint8), w.view(torch.uint8))
+        assert torch.equal(g.reshape(-1).view(torch.uint8), w.reshape(-1).view(torch.uint8))
 
 
 def layers(moe):
