@@ -642,7 +642,8 @@ def moe_grouped_gemm_fp8(x, x_scales, offsets, W, W_scales, y=None, ws: Workspac
 class Fp8Experts:
     """A layer's experts in 8 bits: gate, up [E, I, H] and down [E, H, I]
     float8_e4m3fn, each with its scales [E, rows/128, cols/128] uint8.  The
-    tensors are checked and their addresses taken here, once."""
+    tensors are checked here, and again by a call that finds one of them in
+    another place (its storage was replaced)."""
     gate: torch.Tensor
     gate_scales: torch.Tensor
     up: torch.Tensor
@@ -653,14 +654,23 @@ class Fp8Experts:
     def __post_init__(self):
         E, I, H = self.gate.shape
         a, b = (E, I // 128, H // 128), (E, H // 128, I // 128)
-        c = MoeFp8Experts(_in(self.gate, _E4M3, (E, I, H)), _in(self.gate_scales, _U8, a),
-                          _in(self.up, _E4M3, (E, I, H)), _in(self.up_scales, _U8, a),
-                          _in(self.down, _E4M3, (E, H, I)), _in(self.down_scales, _U8, b))
+        at = (_in(self.gate, _E4M3, (E, I, H)), _in(self.gate_scales, _U8, a),
+              _in(self.up, _E4M3, (E, I, H)), _in(self.up_scales, _U8, a),
+              _in(self.down, _E4M3, (E, H, I)), _in(self.down_scales, _U8, b))
         object.__setattr__(self, "_sizes", (E, H, I))
-        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_at", at)
+        object.__setattr__(self, "_c", MoeFp8Experts(*at))
+
+    def _tensors(self):
+        return (self.gate, self.gate_scales, self.up, self.up_scales, self.down, self.down_scales)
+
+    def __reduce__(self):      # copies and pickles are of the tensors
+        return Fp8Experts, self._tensors()
 
     def ref(self, shape: Shape):
         """The C structure, for a layer of these sizes."""
+        if tuple(t.data_ptr() for t in self._tensors()) != self._at:
+            self.__post_init__()
         assert self._sizes == (shape.E, shape.H, shape.I), \
             f"experts of (E, H, I) = {self._sizes}, layer of {(shape.E, shape.H, shape.I)}"
         return ctypes.byref(self._c)

@@ -71,3 +71,30 @@ def test_experts_after_bad_indices(moe, T, E, k):
     _, y = plain.layer(x, idx, gates, parts)
     good = ~bad.flatten()
     assert rel_rms(ys[inv[good].long()], y.view(P, 512)[good]) <= REL_RMS_TOL
+
+
+def test_experts_whose_storage_is_replaced(moe):
+    """The tensors of an Fp8Experts are used where they are at the call."""
+    shape, lg, x, ex, _ = layer_case(moe, 40, 8, 2, 512, 256, seed=1)
+    other = layer_case(moe, 40, 8, 2, 512, 256, seed=2)[3]
+    first, second = (moe.moe_forward_fp8(shape, lg, x, e) for e in (ex, other))
+    assert not torch.equal(first, second)
+    kept = [t.data for t in ex._tensors()]       # so that the old places stay readable
+    for a, b in zip(ex._tensors(), other._tensors()):
+        a.data = b.data
+    assert torch.equal(moe.moe_forward_fp8(shape, lg, x, ex), second)
+    ex.up.data = ex.up.data[:, :128].contiguous()            # no longer these sizes: refused
+    with pytest.raises(AssertionError):
+        moe.moe_forward_fp8(shape, lg, x, ex)
+    del kept
+
+
+def test_experts_copy_and_pickle(moe):
+    import copy
+    import pickle
+    shape, lg, x, ex, _ = layer_case(moe, 40, 8, 2, 512, 256)
+    want = moe.moe_forward_fp8(shape, lg, x, ex)
+    for e in (copy.copy(ex), copy.deepcopy(ex), pickle.loads(pickle.dumps(ex))):
+        assert torch.equal(moe.moe_forward_fp8(shape, lg, x, e), want)
+    deep = copy.deepcopy(ex)
+    assert deep.gate.data_ptr() != ex.gate.data_ptr()
