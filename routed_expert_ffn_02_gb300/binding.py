@@ -239,6 +239,7 @@ class Workspace:
 
     def __init__(self, nbytes: int, device=None, stream=None):
         device = device or torch.device("cuda", torch.cuda.current_device())
+        assert torch.device(device).type == "cuda", f"workspace on {device}: expected a CUDA device"
         self._buf = _empty(nbytes + 256, torch.uint8, device, stream)
         off = (-self._buf.data_ptr()) % 256
         self.tensor = self._buf[off:off + nbytes]

@@ -91,3 +91,26 @@ def test_balance_refusals(lib):
                 dict(idx=GOOD), dict(idx=GOOD, g=GOOD), dict(dg=GOOD)):
         assert bwd(**bad) == INVALID, bad
     assert bwd(T=0, logits=None, d=None) == OK
+
+
+def test_host_tensors_without_a_workspace_are_refused():
+    """Before a workspace is made beside them and its status word is cleared on
+    the device."""
+    import torch
+    import routed_expert_ffn_02_gb300 as m
+
+    def z(*shape, dtype=torch.bfloat16):
+        return torch.zeros(shape, dtype=dtype)
+    f8, u8, i32 = torch.float8_e4m3fn, torch.uint8, torch.int32
+    shape = m.Shape(4, 4, 2, 256, 256)
+    for call in (
+            lambda: m.Workspace(1024, "cpu"),
+            lambda: m.moe_grouped_gemm_fp8(z(4, 256, dtype=f8), z(4, 2, dtype=u8), z(3, dtype=i32),
+                                           z(2, 256, 256, dtype=f8), z(2, 2, 2, dtype=u8)),
+            lambda: m.moe_expert_ffn_fp8(shape, z(4, 256), z(8, dtype=i32), z(5, dtype=i32), None),
+            lambda: m.moe_forward_fp8(shape, z(4, 4, dtype=torch.float32), z(4, 256), None),
+            lambda: m.moe_balance(z(4, 4, dtype=torch.float32), z(4, 2, dtype=i32)),
+            lambda: m.moe_permute(z(4, 2, dtype=i32), 4),
+            lambda: m.moe_forward(shape, z(4, 4, dtype=torch.float32), z(4, 256), *[z(4, 256, 256)] * 3)):
+        with pytest.raises(AssertionError, match="CUDA"):
+            call()
