@@ -13,13 +13,12 @@ namespace moe {
 namespace {
 
 __global__ void __launch_bounds__(256)
-combine_kernel(const uint4* __restrict__ y, const int32_t* __restrict__ inv_perm,
-               const float* __restrict__ gates, int T, int k, int H,
+combine_kernel(const uint4* y, const int32_t* inv_perm, const float* gates, int T, int k, int H,
                uint4* __restrict__ out) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int vec = H / 8;
-    auto load = [&](int64_t i) { return __ldg(y + i); };
+    auto load = [&](int64_t i) { return y[i]; };
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
         int64_t src[kMaxK];
         float g[kMaxK];
@@ -36,9 +35,8 @@ combine_kernel(const uint4* __restrict__ y, const int32_t* __restrict__ inv_perm
 // The same over fp32 y: 8-bit experts of a small batch, whose y stays in L2, so
 // that the output is rounded once.  One thread per 8 output values.
 __global__ void __launch_bounds__(256)
-combine_f32_kernel(const float4* __restrict__ y, const int32_t* __restrict__ inv_perm,
-                   const float* __restrict__ gates, int k, int vec, int64_t n,
-                   uint4* __restrict__ out) {
+combine_f32_kernel(const float4* y, const int32_t* inv_perm, const float* gates, int k, int vec,
+                   int64_t n, uint4* __restrict__ out) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;

@@ -2,7 +2,10 @@
 // starts while the one before it still runs may load that kernel's results
 // only after griddepcontrol.wait.  __ldg, __ldca and __ldcg promise no order
 // against it: the compiler may take them to depend on no store and move them
-// up.  These are volatile with a memory clobber, and keep their place.
+// up.  The same holds for ordinary loads through const __restrict__ kernel
+// arguments, which it may turn into such loads.  These are volatile with a
+// memory clobber, and keep their place (as ordinary loads through plain
+// pointers do).
 // _cg: past L1.
 #pragma once
 

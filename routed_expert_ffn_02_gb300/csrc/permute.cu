@@ -185,7 +185,7 @@ __device__ __forceinline__ unsigned lanemask_lt() {
 // ---- large path -------------------------------------------------------
 
 __global__ void __launch_bounds__(256)
-hist_kernel(const int32_t* __restrict__ idx, int64_t P, int E,
+hist_kernel(const int32_t* idx, int64_t P, int E,
             int32_t* __restrict__ chunk_hist, WsHeader* hdr) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
@@ -205,7 +205,7 @@ hist_kernel(const int32_t* __restrict__ idx, int64_t P, int E,
 }
 
 __global__ void __launch_bounds__(1024)
-scan_kernel(const int32_t* __restrict__ chunk_hist, int nchunks, int E,
+scan_kernel(const int32_t* chunk_hist, int nchunks, int E,
             int32_t* __restrict__ chunk_base, int32_t* __restrict__ counts,
             int32_t* __restrict__ offsets, int64_t P, Plan plan, int do_plan) {
     ptx::grid_dep_wait();
@@ -247,9 +247,9 @@ scan_kernel(const int32_t* __restrict__ chunk_hist, int nchunks, int E,
 }
 
 __global__ void __launch_bounds__(32 * kScatterWarps)
-scatter_kernel(const int32_t* __restrict__ idx, int64_t P, int E,
-               const int32_t* __restrict__ chunk_base,
-               const int32_t* __restrict__ offsets,
+scatter_kernel(const int32_t* idx, int64_t P, int E,
+               const int32_t* chunk_base,
+               const int32_t* offsets,
                int32_t* __restrict__ perm, int32_t* __restrict__ inv_perm) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
@@ -301,7 +301,7 @@ scatter_kernel(const int32_t* __restrict__ idx, int64_t P, int E,
 // ---- small path: everything in one block -------------------------------
 
 __global__ void __launch_bounds__(32 * kScatterWarps)
-permute_small_kernel(const int32_t* __restrict__ idx, int P, int E,
+permute_small_kernel(const int32_t* idx, int P, int E,
                      int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                      int32_t* __restrict__ perm, int32_t* __restrict__ inv_perm,
                      WsHeader* hdr, Plan plan, int do_plan) {
@@ -367,7 +367,7 @@ permute_small_kernel(const int32_t* __restrict__ idx, int P, int E,
 }
 
 __global__ void __launch_bounds__(1024)
-plan_kernel(const int32_t* __restrict__ counts, const int32_t* __restrict__ offsets,
+plan_kernel(const int32_t* counts, const int32_t* offsets,
             int E, Plan plan) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
@@ -385,7 +385,7 @@ plan_kernel(const int32_t* __restrict__ counts, const int32_t* __restrict__ offs
 // solo) and of the tensor-core streaming tiles (all of them, or one of the
 // two gather parts); one warp per row, 16-byte vectors.
 __global__ void __launch_bounds__(256)
-gather_kernel(GatherRows g, const WsHeader* __restrict__ hdr, int part) {
+gather_kernel(GatherRows g, const WsHeader* hdr, int part) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int64_t warp = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);

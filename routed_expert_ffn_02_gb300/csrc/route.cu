@@ -12,7 +12,7 @@ namespace {
 
 template <int EPL>   // candidates per lane
 __global__ void __launch_bounds__(256)
-route_kernel(const float* __restrict__ logits, int T, int E, int k,
+route_kernel(const float* logits, int T, int E, int k,
              int32_t* __restrict__ idx, float* __restrict__ gates) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
@@ -33,7 +33,7 @@ cudaError_t launch_epl(const float* logits, int T, int E, int k, int32_t* idx,
 // flags[idx[s]] = 1 for every routed slot (every writer stores the same
 // value, so the races are benign); indices outside [0, E) are skipped.
 __global__ void __launch_bounds__(256)
-mark_touched_kernel(const int32_t* __restrict__ idx, int64_t P, int E, uint8_t* flags) {
+mark_touched_kernel(const int32_t* idx, int64_t P, int E, uint8_t* flags) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     for (int64_t s = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; s < P;

@@ -41,14 +41,14 @@ __device__ __forceinline__ float order_to_float(uint32_t o) {
 // and each round is two warp reductions deep rather than a five-step
 // shuffle tree of 64-bit keys.
 template <int EPL>   // candidates per lane
-__device__ __forceinline__ void route_row(const float* __restrict__ row, int E, int k,
+__device__ __forceinline__ void route_row(const float* row, int E, int k,
                                           int32_t* __restrict__ idx, float* __restrict__ gates) {
     const int lane = threadIdx.x & 31;
     uint64_t key[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const int e = lane + 32 * j;
-        key[j] = (e < E) ? ((uint64_t)float_order(__ldg(row + e)) << 32) |
+        key[j] = (e < E) ? ((uint64_t)float_order(row[e]) << 32) |
                                (uint64_t)(~(uint32_t)e)
                          : 0ull;
     }
