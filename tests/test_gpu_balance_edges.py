@@ -1,6 +1,10 @@
-"""GPU: the balance loss at the ends of its range of tokens and offsets."""
+"""GPU: the balance loss at the ends of its range of tokens and offsets, and its
+gradient against extrapolated differences."""
 import pytest
 import torch
+
+import fp8_plain as plain
+import synth
 
 pytestmark = pytest.mark.gpu
 MOE_ERR_BAD_INDEX = 6
@@ -81,3 +85,46 @@ def test_no_tokens_with_offsets(moe):
     assert ws.status() == 0 and loss.item() == 0 and not counts.any()
     moe.moe_balance(z, i, torch.tensor([0, 1, 0], dtype=torch.int32, device="cuda"), ws=ws)
     assert ws.status(clear=True) == MOE_ERR_BAD_INDEX
+
+
+def fixed_slots(lg, idx, off, coef, d_loss, dg):
+    """d_loss * loss + sum of dg * gates over the selected slots, in 64 bits."""
+    loss, _ = plain.balance(lg, idx, off, coef)
+    gates = torch.softmax(lg.gather(1, idx.long()), 1)
+    return (d_loss * loss + (dg.double() * gates).sum()).item()
+
+
+@pytest.mark.parametrize("T,E,k,off", [(300, 24, 3, [0, 120, 300]), (130, 200, 8, [10, 10, 77, 130])])
+def test_gradient_against_extrapolated_differences(moe, T, E, k, off):
+    """Along random directions the kernel's gradient has to give the slope of the
+    definition in 64 bits: central differences at h and h / 2, extrapolated, are
+    off by about h^4 of the fifth derivative (h = 0.01: 1e-9 of the slope).  The
+    gradient's own rounding is held as in test_gpu_balance.py, and is under a
+    hundredth of the slope, so that no term of it can be missing."""
+    coef, d_loss = 1.0, 1.7
+    lg = synth.make_logits(T, E, seed=4, zipf_s=1.1).cuda()
+    idx, gates = moe.moe_route(lg, k)
+    seq = torch.tensor(off, dtype=torch.int32, device="cuda")
+    dg = torch.randn((T, k), generator=torch.Generator().manual_seed(1)).cuda() * 1e-2
+    loss, counts, stats = moe.moe_balance(lg, idx, seq, coef)
+    d = moe.moe_balance_backward(lg, stats, counts, k, seq, coef, torch.tensor(d_loss, device="cuda"),
+                                 topk_idx=idx, gates=gates, d_gates=dg).double()
+    tol = (64 + T / 64) * 2.0 ** -23
+    p, g, b = torch.softmax(lg.double(), 1), gates.double(), dg.double().abs()
+    a = torch.zeros_like(p)
+    for s, (lo, hi) in enumerate(zip(off[:-1], off[1:])):
+        if hi > lo:
+            a[lo:hi] = coef * E * counts[s].double() / (k * (hi - lo) * (off[-1] - off[0]))
+    size = d_loss * p * (a + (p * a).sum(1, keepdim=True))
+    size = size.scatter_add(1, idx.long(), g * (b + (g * b).sum(1, keepdim=True)))
+    for seed in range(4):
+        v = torch.randn((T, E), generator=torch.Generator().manual_seed(seed), dtype=torch.float64).cuda()
+        v += 2 * torch.sign(d)      # a slope that does not cancel
+
+        def slope(h):
+            f = [fixed_slots(lg.double() + s * h * v, idx, off, coef, d_loss, dg) for s in (-1, 1)]
+            return (f[1] - f[0]) / (2 * h)
+        want = slope(0.005) + (slope(0.005) - slope(0.01)) / 3
+        held = tol * (size * v.abs()).sum().item() + 1e-6 * abs(want)
+        assert held <= 0.01 * abs(want)
+        assert abs((d * v).sum().item() - want) <= held
