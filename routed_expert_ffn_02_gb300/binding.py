@@ -665,8 +665,14 @@ class Fp8Experts:
     def _tensors(self):
         return (self.gate, self.gate_scales, self.up, self.up_scales, self.down, self.down_scales)
 
-    def __reduce__(self):      # copies and pickles are of the tensors
-        return Fp8Experts, self._tensors()
+    def __reduce__(self):
+        """Copies and pickles are of the tensors, as bytes (torch's pickle does
+        not read 8-bit floating point back)."""
+        return Fp8Experts._of_bytes, tuple(t.view(_U8) for t in self._tensors())
+
+    @staticmethod
+    def _of_bytes(*parts):
+        return Fp8Experts(*(t.view(_U8 if i % 2 else _E4M3) for i, t in enumerate(parts)))
 
     def ref(self, shape: Shape):
         """The C structure, for a layer of these sizes."""
