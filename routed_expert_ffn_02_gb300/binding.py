@@ -194,7 +194,8 @@ def _opt(t: torch.Tensor | None, dtype, shape):
 def _out(t: torch.Tensor | None, shape, dtype, like: torch.Tensor, stream):
     """The caller's output tensor, checked, or a new one, and its address."""
     if t is None:
-        t = _empty(shape, dtype, like.device, stream)
+        t = (torch.empty(shape, dtype=dtype, device=like.device) if stream is None
+             else _empty(shape, dtype, like.device, stream))
         return t, t.data_ptr()
     return t, _in(t, dtype, shape)
 
