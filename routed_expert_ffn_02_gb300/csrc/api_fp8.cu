@@ -167,10 +167,15 @@ moe_status check_experts(const moe_fp8_experts* w) {
 // Which kernels run, from sizes the host knows: `most` bounds any expert's
 // rows.  A single expert takes one kernel by its rows.  With several, small
 // experts cannot be ruled out, so the pair kernel is a launch more, and up to
-// kPairRows rows the one-CTA kernel takes the pair tiles as well (measured, us
-// with / without the pair kernel: 777 rows over 48 experts, N = 640, K = 1152:
-// 23.0 / 16.7; 4096 over 16, 4096 x 2048: 56.0 / 53.3; 8192 over 16: 67.6 /
-// 78.6; a layer of 512 tokens, 64 experts, 2048 x 1024: 162 / 134).
+// kPairRows rows the one-CTA kernel takes the pair tiles as well.  Measured, us
+// without / with the pair kernel, rows x (N, K) over E experts:
+//   777 x (640, 1152) over 48: 15.3 / 26.5      4096 x (4096, 2048) over 16: 53.5 / 56.6
+//   4000 x (2048, 2048) over 2: 26.8 / 28.4     4000 x (2048, 1024) over 4: 20.7 / 23.4
+//   4000 x (4096, 2048) over 8: 45.4 / 44.6     8192 x (4096, 2048) over 16: 78.6 / 67.6
+//   layer of 512 tokens, 64 experts, 2048 x 1024: 134 / 163
+// A few experts with many rows each and long K would gain from pairs below the
+// limit (2000 x (4096, 4096) over 2: 36.4 / 32.6, 4000 over 2: 68.5 / 60.1,
+// over 4: 69.3 / 61.7); the host does not know the rows of each expert.
 struct Kernels {
     bool pair, solo;
 };

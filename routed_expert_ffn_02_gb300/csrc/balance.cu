@@ -21,10 +21,10 @@
 // chunks in order, all fp32: no floating-point atomics, so repeated runs give
 // the same bits.  A chunk that several sequences share writes one partial row
 // per sequence: chunk c and sequence s meet in row c + s, which no other pair
-// of the staircase uses.  The last CTA to finish adds the chunks up; with more
-// than kFusedSequences sequences that would be one CTA's work for too many
-// rows, and a second kernel does it with a CTA per sequence (a second launch
-// for the usual one sequence cost 2 us of a 30 us host-bound call).
+// of the staircase uses.  A second kernel adds the chunks up, a CTA per 32
+// experts and sequence, and its last CTA the loss.  One sequence of at most
+// kFusedChunks chunks (128 tokens) does without it: the last CTA of the first
+// kernel adds up, which is one CTA's work for so few rows only.
 //
 // Backward: bound by HBM (4 T E read, 4 T E written).  A warp per token, as
 // many consecutive ones as fill the GPU once, so that the coefficients a_se of
