@@ -18,6 +18,7 @@
 // every real logit, including -inf.
 #pragma once
 
+#include "ld_dev.cuh"
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -48,9 +49,9 @@ __device__ __forceinline__ void route_row(const float* row, int E, int k,
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const int e = lane + 32 * j;
-        key[j] = (e < E) ? ((uint64_t)float_order(row[e]) << 32) |
-                               (uint64_t)(~(uint32_t)e)
-                         : 0ull;
+        // (loaded either way, so that the loads follow one another)
+        const uint32_t v = float_order(ld::f32(row + min(e, E - 1)));
+        key[j] = e < E ? ((uint64_t)v << 32) | (uint64_t)(~(uint32_t)e) : 0ull;
     }
 
     float sel_val = 0.f;   // lane r < k: the r-th selected logit and its expert

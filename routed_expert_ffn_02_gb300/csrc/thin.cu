@@ -48,12 +48,14 @@ thin_gate_up_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restri
     const uint32_t half = (uint32_t)R * H * 2;
     const uint32_t xrow = (uint32_t)H * 2;
 
+    bool ok = true;
+    Issued is{true, 0, 0};
     if (warp < kProducers) {
         if (lane == 0) {
             const uint64_t policy = policy_evict_first();
             const __nv_bfloat16* W = warp == 0 ? Wg : Wu;
             const uint32_t part = warp == 0 ? 0u : half;
-            const bool ok = produce(
+            is = produce(
                 m, warp, rg, warp == 0,
                 [&](int it, uint32_t dst, uint32_t bar) {
                     const ThinUnit un = U[it / ipe];
@@ -69,18 +71,18 @@ thin_gate_up_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restri
                         bulk_g2s(dst + t * xrow, x + (size_t)(order[un.row0 + t] / k) * H, xrow, bar);
                 },
                 wait_cycles);
-            if (!ok) set_status(hdr, MOE_ERR_TIMEOUT);
+            ok = is.ok;
         }
-        return;
+    } else {
+        ok = consume<16>(m, rg, ipe, U, warp - kProducers, nc, wait_cycles,
+                         [&]<int N>(int it, int slot, const Smem& mu) {
+            const ThinUnit un = U[it / ipe];
+            __nv_bfloat16* hcol = h + (int64_t)un.row0 * I + (it % ipe) * R;
+            gate_up_slot<N, VPL>(mu, slot, R, vec, un.n, hcol, I);
+        });
     }
-
-    const bool ok = consume<16>(m, rg, ipe, U, warp - kProducers, nc, wait_cycles,
-                                [&]<int N>(int it, int slot, const Smem& mu) {
-        const ThinUnit un = U[it / ipe];
-        __nv_bfloat16* hcol = h + (int64_t)un.row0 * I + (it % ipe) * R;
-        gate_up_slot<N, VPL>(mu, slot, R, vec, un.n, hcol, I);
-    });
     if (!ok) set_status(hdr, MOE_ERR_TIMEOUT);
+    if (__syncthreads_or(!ok)) drain_copies(m, warp, is);
 }
 
 template <int V>

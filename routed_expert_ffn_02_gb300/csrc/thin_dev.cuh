@@ -50,7 +50,8 @@
 // (small_plan.cuh).
 //
 // Waits are bounded; on expiry the kernel records MOE_ERR_TIMEOUT, the
-// producer waits (bounded) for its outstanding copies, and the CTA returns.
+// producers wait (bounded) for their outstanding copies, whichever role gave
+// up, and the CTA returns.
 #pragma once
 
 #include <algorithm>
@@ -269,14 +270,16 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, long lo
 // the consumers have released the unit that used that buffer before.  Items
 // [0, pre) (pre <= slots) were already issued into slots [0, pre).  While a
 // slot is still in use the lane sleeps in try_wait.  Each wait gives up after
-// `limit` cycles, and it returns false.  The copies it issued are waited for
-// (full bound) before it returns.
+// `limit` cycles; ok is then false.  What it returns goes to drain_copies once
+// the block knows whether any of its roles gave up.
+struct Issued {
+    bool ok;
+    int items, acts;   // item copies (in ring order) and staged units
+};
 template <int kBufs = 1, typename ItemFn, typename ActFn>
-__device__ bool produce(const Smem& m, int producer, const Range& rg, bool stager,
-                        ItemFn copy_item, ActFn copy_act, long long limit, int pre = 0) {
-    if (rg.cnt <= 0) return true;
-    int last_round[kMaxSlots];
-    for (int s = 0; s < kMaxSlots; ++s) last_round[s] = s < pre ? 0 : -1;
+__device__ Issued produce(const Smem& m, int producer, const Range& rg, bool stager,
+                          ItemFn copy_item, ActFn copy_act, long long limit, int pre = 0) {
+    if (rg.cnt <= 0) return {true, 0, 0};
     const int n_units = stager ? rg.u_last - rg.u_first + 1 : 0;
     int act_issued = 0;                       // units whose activations are staged
     for (; act_issued < kBufs && act_issued < n_units; ++act_issued)
@@ -295,7 +298,8 @@ __device__ bool produce(const Smem& m, int producer, const Range& rg, bool stage
     };
     bool ok = true;
     int slot = pre % m.slots, round = pre / m.slots;
-    for (int seq = pre; ok && seq < rg.cnt; ++seq) {
+    int seq = pre;
+    for (; seq < rg.cnt; ++seq) {
         if (round > 0) {
             const uint32_t par = (uint32_t)((round - 1) & 1);
             const long long start = clock64();
@@ -309,7 +313,6 @@ __device__ bool produce(const Smem& m, int producer, const Range& rg, bool stage
             if (!ok) break;
         }
         copy_item(rg.beg + seq, m.buf(slot), m.full_of(producer, slot));
-        last_round[slot] = round;
         try_stage();
         if (++slot == m.slots) {
             slot = 0;
@@ -323,16 +326,27 @@ __device__ bool produce(const Smem& m, int producer, const Range& rg, bool stage
         }
         stage_next();
     }
-    // Every copy has landed before the CTA exits.  Also where all of them could
-    // be issued: a consumer may have given up.
-    for (int s = 0; s < m.slots; ++s)
-        if (last_round[s] >= 0)
-            (void)mbar_wait(m.full_of(producer, s), (uint32_t)(last_round[s] & 1));
+    return {ok, seq, act_issued};
+}
+
+// Every copy that `producer` issued has landed (full bound); run behind a block
+// barrier once a role has given up (is: what produce() returned to this thread,
+// {true, 0, 0} for one that copied nothing).  It cannot be left to produce(): a
+// producer that issued all its items does not know of a consumer that gave up.
+// Called, not inlined: the one-launch decode layer feels its instructions (four
+// layers at batch 1 / 2: 276.6 / 407.6 us without, 281.4 / 407.8 with these
+// waits at the end of produce(), 280.7 / 409.2 inlined behind the barrier, 278.1
+// / 404.6 as it is).
+template <int kBufs = 1>
+__device__ __noinline__ void drain_copies(Smem m, int producer, Issued is) {
+    for (int s = 0; s < m.slots && s < is.items; ++s) {
+        const int rounds = (is.items - s + m.slots - 1) / m.slots;
+        (void)mbar_wait(m.full_of(producer, s), (uint32_t)((rounds - 1) & 1));
+    }
     for (int b = 0; b < kBufs; ++b) {
-        const int uses = (act_issued - b + kBufs - 1) / kBufs;   // units staged in b
+        const int uses = (is.acts - b + kBufs - 1) / kBufs;   // units staged in b
         if (uses > 0) (void)mbar_wait(m.act_full(b), (uint32_t)((uses - 1) & 1));
     }
-    return ok;
 }
 
 // Called by all lanes of a consumer warp once they are done reading a slot.

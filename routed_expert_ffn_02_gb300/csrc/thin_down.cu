@@ -47,6 +47,8 @@ thin_down_kernel(const __nv_bfloat16* __restrict__ h, int H, int I, int R,
     const uint32_t bytes = (uint32_t)R * I * 2;
     const uint32_t hrow = (uint32_t)I * 2;
 
+    bool ok = true;
+    Issued is{true, 0, 0};
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t policy = policy_evict_first();
@@ -61,7 +63,7 @@ thin_down_kernel(const __nv_bfloat16* __restrict__ h, int H, int I, int R,
             for (int i = 0; i < pre; ++i) copy_item(rg.beg + i, m.buf(i), m.full(i));
             grid_dep_wait();
             grid_dep_launch();
-            const bool ok = produce(
+            is = produce(
                 m, 0, rg, true, copy_item,
                 [&](int u, uint32_t dst, uint32_t bar) {
                     const ThinUnit un = U[u];
@@ -70,25 +72,26 @@ thin_down_kernel(const __nv_bfloat16* __restrict__ h, int H, int I, int R,
                     bulk_g2s(dst, h + (size_t)un.row0 * I, (uint32_t)un.n * hrow, bar);
                 },
                 wait_cycles, pre);
-            if (!ok) set_status(hdr, MOE_ERR_TIMEOUT);
+            ok = is.ok;
         }
     } else {
         grid_dep_wait();      // consumers write y
         grid_dep_launch();
         constexpr int kExact =
             (VPL > 0 && DownRegSlots<VPL>::value > 0) ? DownRegSlots<VPL>::value : 16;
-        const bool ok = consume<kExact>(m, rg, ipe, U, warp - kProducers, nc, wait_cycles,
-                                        [&]<int N>(int it, int slot, const Smem& mu) {
+        ok = consume<kExact>(m, rg, ipe, U, warp - kProducers, nc, wait_cycles,
+                             [&]<int N>(int it, int slot, const Smem& mu) {
             const ThinUnit un = U[it / ipe];
             __nv_bfloat16* ycol = y + (int64_t)un.row0 * H + (it % ipe) * R;
             down_slot<N, VPL>(mu, slot, R, vec, un.n, ycol, H);
         });
-        if (!ok) set_status(hdr, MOE_ERR_TIMEOUT);
     }
+    if (!ok) set_status(hdr, MOE_ERR_TIMEOUT);
     if (sr.out) {   // fused combine; every thread has waited for the gate/up kernel
         grid_dep_wait();
         combine_if_last(sr, sp, hdr, y, H);
     }
+    if (__syncthreads_or(!ok)) drain_copies(m, warp, is);
 }
 
 template <int V>

@@ -41,10 +41,13 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
     const int n_warps = blockDim.x >> 5;
 
     int failed;
+    Smem m;                     // the ring of the current phase, and what this
+    Issued is{true, 0, 0};      // thread (a producer's lane) copied into it
+    bool ok = true;
     {   // ---------------- gate/up ----------------
         constexpr int kProducers = 2;   // warp 0 issues the gate rows, warp 1 the up rows
         const int nc = min(n_warps - kProducers, slots_g - 1);
-        const Smem m = smem_setup(smem, stage_g, slots_g, act_g, kProducers, nc, kBufs);
+        m = smem_setup(smem, stage_g, slots_g, act_g, kProducers, nc, kBufs);
         grid_dep_wait();      // the logits may come from the previous kernel
         grid_dep_launch();
         build_small_plan(sr, sp);
@@ -52,13 +55,12 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
         const int vec = H / 8, ipe = I / Rg;
         const Range rg = cta_range(sp.units, sp.n_units, sp.weight, ipe);
         const uint32_t half = (uint32_t)Rg * H * 2, xrow = (uint32_t)H * 2;
-        bool ok = true;
         if (warp < kProducers) {
             if (lane == 0) {
                 const uint64_t policy = policy_evict_first();
                 const __nv_bfloat16* W = warp == 0 ? Wg : Wu;
                 const uint32_t part = warp == 0 ? 0u : half;
-                ok = produce<kBufs>(
+                is = produce<kBufs>(
                     m, warp, rg, warp == 0,
                     [&](int it, uint32_t dst, uint32_t bar) {
                         const ThinUnit un = sp.units[it / ipe];
@@ -75,6 +77,7 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
                                      xrow, bar);
                     },
                     wait_cycles);
+                ok = is.ok;
             }
         } else if (warp - kProducers < nc) {
             ok = consume<16, kBufs>(m, rg, ipe, sp.units, warp - kProducers, nc, wait_cycles,
@@ -99,12 +102,12 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
     }
     if (!failed) {   // ---------------- down ----------------
         constexpr int kProducers = 1;
+        is = {true, 0, 0};
         const int nc = min(n_warps - kProducers, slots_d - 1);
-        const Smem m = smem_setup(smem, stage_d, slots_d, act_d, kProducers, nc, kBufs);
+        m = smem_setup(smem, stage_d, slots_d, act_d, kProducers, nc, kBufs);
         const int vec = I / 8, ipe = H / Rd;
         const Range rg = cta_range(sp.units, sp.n_units, sp.weight, ipe);
         const uint32_t bytes = (uint32_t)Rd * I * 2, hrow = (uint32_t)I * 2;
-        bool ok = true;
         if (warp == 0) {
             if (lane == 0) {
                 const uint64_t policy = policy_evict_first();
@@ -133,7 +136,7 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
                     __nanosleep(32);
                 }
                 fence_proxy_async_global();
-                ok = produce<kBufs>(
+                is = produce<kBufs>(
                     m, 0, rg, true, copy_item,
                     [&](int u, uint32_t dst, uint32_t bar) {
                         const ThinUnit un = sp.units[u];
@@ -142,6 +145,7 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
                         bulk_g2s(dst, h + (size_t)un.row0 * I, (uint32_t)un.n * hrow, bar);
                     },
                     wait_cycles, pre);
+                ok = is.ok;
             }
         } else if (warp - kProducers < nc) {
             constexpr int kExact =
@@ -156,6 +160,7 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
         if (!ok) set_status(hdr, MOE_ERR_TIMEOUT);
     }
     combine_spread(sr, sp.inv_perm, sp.gates, hdr, y, H, wait_cycles);
+    if (__syncthreads_or(!ok)) drain_copies<kBufs>(m, warp, is);
 }
 
 template <int VG, int VD, int kBufs>
