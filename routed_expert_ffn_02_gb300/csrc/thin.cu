@@ -21,9 +21,10 @@ thin_gate_up_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restri
                     int act_bytes, SelfRoute sr, long long wait_cycles) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ SmallPlan sp;
+    __shared__ RingNotes notes;
     constexpr int kProducers = 2;   // warp 0 issues the gate rows, warp 1 the up rows
     const int nc = (blockDim.x >> 5) - kProducers;
-    const Smem m = smem_setup(smem, stage_bytes, slots, act_bytes, kProducers, nc);
+    const Smem m = smem_setup(smem, stage_bytes, slots, act_bytes, kProducers, nc, notes);
     grid_dep_wait();      // the plan (or the logits) may come from the previous kernel
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -49,13 +50,12 @@ thin_gate_up_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restri
     const uint32_t xrow = (uint32_t)H * 2;
 
     bool ok = true;
-    Issued is{true, 0, 0};
     if (warp < kProducers) {
         if (lane == 0) {
             const uint64_t policy = policy_evict_first();
             const __nv_bfloat16* W = warp == 0 ? Wg : Wu;
             const uint32_t part = warp == 0 ? 0u : half;
-            is = produce(
+            ok = produce(
                 m, warp, rg, warp == 0,
                 [&](int it, uint32_t dst, uint32_t bar) {
                     const ThinUnit un = U[it / ipe];
@@ -70,8 +70,7 @@ thin_gate_up_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restri
                     for (int t = 0; t < un.n; ++t)
                         bulk_g2s(dst + t * xrow, x + (size_t)(order[un.row0 + t] / k) * H, xrow, bar);
                 },
-                wait_cycles);
-            ok = is.ok;
+                wait_cycles, notes);
         }
     } else {
         ok = consume<16>(m, rg, ipe, U, warp - kProducers, nc, wait_cycles,
@@ -81,8 +80,12 @@ thin_gate_up_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restri
             gate_up_slot<N, VPL>(mu, slot, R, vec, un.n, hcol, I);
         });
     }
-    if (!ok) set_status(hdr, MOE_ERR_TIMEOUT);
-    if (__syncthreads_or(!ok)) drain_copies(m, warp, is);
+    if (!ok) {
+        notes.gave_up = 1;
+        set_status(hdr, MOE_ERR_TIMEOUT);
+    }
+    __syncthreads();
+    if (notes.gave_up) drain_copies(notes);
 }
 
 template <int V>

@@ -174,10 +174,21 @@ struct Smem {
     __device__ uint32_t full_of(int p, int s) const { return p == 0 ? full(s) : full2(s); }
 };
 
+// What the end of the kernel needs, in shared memory, if a role has given up:
+// the ring and what its producers copied into it.
+struct Issued {
+    int items, acts;   // item copies (in ring order) and staged units
+};
+struct RingNotes {
+    Smem ring;
+    Issued issued[2];   // by producer
+    int gave_up;        // a role's wait ran out
+};
+
 // act_bytes: one activation buffer; act_bufs: 1 or 2 buffers.
 __device__ __forceinline__ Smem smem_setup(uint8_t* smem, int stage_bytes, int slots,
                                            int act_bytes, int producers, int consumers,
-                                           int act_bufs = 1) {
+                                           RingNotes& notes, int act_bufs = 1) {
     Smem m;
     m.base = smem_u32(smem);
     m.stage_bytes = stage_bytes;
@@ -196,6 +207,7 @@ __device__ __forceinline__ Smem smem_setup(uint8_t* smem, int stage_bytes, int s
             mbar_init(m.act_full(b), 1);
             mbar_init(m.act_free(b), consumers);
         }
+        notes = RingNotes{m, {{0, 0}, {0, 0}}, 0};
         fence_mbar_init();
     }
     __syncthreads();
@@ -270,16 +282,13 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, long lo
 // the consumers have released the unit that used that buffer before.  Items
 // [0, pre) (pre <= slots) were already issued into slots [0, pre).  While a
 // slot is still in use the lane sleeps in try_wait.  Each wait gives up after
-// `limit` cycles; ok is then false.  What it returns goes to drain_copies once
-// the block knows whether any of its roles gave up.
-struct Issued {
-    bool ok;
-    int items, acts;   // item copies (in ring order) and staged units
-};
+// `limit` cycles; it then returns false.  What it copied is noted for
+// drain_copies.
 template <int kBufs = 1, typename ItemFn, typename ActFn>
-__device__ Issued produce(const Smem& m, int producer, const Range& rg, bool stager,
-                          ItemFn copy_item, ActFn copy_act, long long limit, int pre = 0) {
-    if (rg.cnt <= 0) return {true, 0, 0};
+__device__ bool produce(const Smem& m, int producer, const Range& rg, bool stager,
+                        ItemFn copy_item, ActFn copy_act, long long limit, RingNotes& notes,
+                        int pre = 0) {
+    if (rg.cnt <= 0) return true;
     const int n_units = stager ? rg.u_last - rg.u_first + 1 : 0;
     int act_issued = 0;                       // units whose activations are staged
     for (; act_issued < kBufs && act_issued < n_units; ++act_issued)
@@ -326,25 +335,30 @@ __device__ Issued produce(const Smem& m, int producer, const Range& rg, bool sta
         }
         stage_next();
     }
-    return {ok, seq, act_issued};
+    notes.issued[producer] = {seq, act_issued};
+    return ok;
 }
 
-// Every copy that `producer` issued has landed (full bound); run behind a block
-// barrier once a role has given up (is: what produce() returned to this thread,
-// {true, 0, 0} for one that copied nothing).  It cannot be left to produce(): a
-// producer that issued all its items does not know of a consumer that gave up.
-// Called, not inlined: the one-launch decode layer feels its instructions (four
-// layers at batch 1 / 2: 276.6 / 407.6 us without, 281.4 / 407.8 with these
-// waits at the end of produce(), 280.7 / 409.2 inlined behind the barrier, 278.1
-// / 404.6 as it is).
-template <int kBufs = 1>
-__device__ __noinline__ void drain_copies(Smem m, int producer, Issued is) {
+// Called by every thread behind a block barrier if notes.gave_up: every copy that
+// the ring's producers issued has landed (full bound).  It cannot be left to
+// produce(): a producer that issued all its items does not know of a consumer
+// that gave up.  Called, with everything in shared memory, because the one-launch
+// decode layer feels its instructions and registers: four layers at batch 1 / 2
+// take 275.3 / 404.0 us; with these waits at the end of produce() 281.4 / 407.8;
+// called with the ring in registers 278.5 / 407.1, and then the kernel needs more
+// than 216 of them, so that its CTA does not fit beside an expert copy's (cached
+// decode 1.40 -> 1.95 ms).
+__device__ __noinline__ void drain_copies(const RingNotes& notes) {
+    const Smem& m = notes.ring;
+    const int producer = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) != 0 || producer >= m.producers) return;
+    const Issued is = notes.issued[producer];
     for (int s = 0; s < m.slots && s < is.items; ++s) {
         const int rounds = (is.items - s + m.slots - 1) / m.slots;
         (void)mbar_wait(m.full_of(producer, s), (uint32_t)((rounds - 1) & 1));
     }
-    for (int b = 0; b < kBufs; ++b) {
-        const int uses = (is.acts - b + kBufs - 1) / kBufs;   // units staged in b
+    for (int b = 0; b < m.act_bufs; ++b) {
+        const int uses = (is.acts - b + m.act_bufs - 1) / m.act_bufs;   // units staged in b
         if (uses > 0) (void)mbar_wait(m.act_full(b), (uint32_t)((uses - 1) & 1));
     }
 }

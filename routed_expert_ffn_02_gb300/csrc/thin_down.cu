@@ -18,9 +18,10 @@ thin_down_kernel(const __nv_bfloat16* __restrict__ h, int H, int I, int R,
                  SelfRoute sr, long long wait_cycles) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ SmallPlan sp;
+    __shared__ RingNotes notes;
     constexpr int kProducers = 1;
     const int nc = (blockDim.x >> 5) - kProducers;
-    const Smem m = smem_setup(smem, stage_bytes, slots, act_bytes, kProducers, nc);
+    const Smem m = smem_setup(smem, stage_bytes, slots, act_bytes, kProducers, nc, notes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int vec = I / 8;
     const int ipe = H / R;
@@ -48,7 +49,6 @@ thin_down_kernel(const __nv_bfloat16* __restrict__ h, int H, int I, int R,
     const uint32_t hrow = (uint32_t)I * 2;
 
     bool ok = true;
-    Issued is{true, 0, 0};
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t policy = policy_evict_first();
@@ -63,7 +63,7 @@ thin_down_kernel(const __nv_bfloat16* __restrict__ h, int H, int I, int R,
             for (int i = 0; i < pre; ++i) copy_item(rg.beg + i, m.buf(i), m.full(i));
             grid_dep_wait();
             grid_dep_launch();
-            is = produce(
+            ok = produce(
                 m, 0, rg, true, copy_item,
                 [&](int u, uint32_t dst, uint32_t bar) {
                     const ThinUnit un = U[u];
@@ -71,8 +71,7 @@ thin_down_kernel(const __nv_bfloat16* __restrict__ h, int H, int I, int R,
                     mbar_expect_tx(bar, (uint32_t)un.n * hrow);
                     bulk_g2s(dst, h + (size_t)un.row0 * I, (uint32_t)un.n * hrow, bar);
                 },
-                wait_cycles, pre);
-            ok = is.ok;
+                wait_cycles, notes, pre);
         }
     } else {
         grid_dep_wait();      // consumers write y
@@ -86,12 +85,16 @@ thin_down_kernel(const __nv_bfloat16* __restrict__ h, int H, int I, int R,
             down_slot<N, VPL>(mu, slot, R, vec, un.n, ycol, H);
         });
     }
-    if (!ok) set_status(hdr, MOE_ERR_TIMEOUT);
+    if (!ok) {
+        notes.gave_up = 1;
+        set_status(hdr, MOE_ERR_TIMEOUT);
+    }
     if (sr.out) {   // fused combine; every thread has waited for the gate/up kernel
         grid_dep_wait();
         combine_if_last(sr, sp, hdr, y, H);
     }
-    if (__syncthreads_or(!ok)) drain_copies(m, warp, is);
+    __syncthreads();
+    if (notes.gave_up) drain_copies(notes);
 }
 
 template <int V>

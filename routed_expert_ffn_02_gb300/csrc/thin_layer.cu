@@ -37,17 +37,15 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ SmallPlan sp;
     __shared__ uint32_t s_target;
+    __shared__ RingNotes notes;   // of the current phase
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n_warps = blockDim.x >> 5;
 
     int failed;
-    Smem m;                     // the ring of the current phase, and what this
-    Issued is{true, 0, 0};      // thread (a producer's lane) copied into it
-    bool ok = true;
     {   // ---------------- gate/up ----------------
         constexpr int kProducers = 2;   // warp 0 issues the gate rows, warp 1 the up rows
         const int nc = min(n_warps - kProducers, slots_g - 1);
-        m = smem_setup(smem, stage_g, slots_g, act_g, kProducers, nc, kBufs);
+        const Smem m = smem_setup(smem, stage_g, slots_g, act_g, kProducers, nc, notes, kBufs);
         grid_dep_wait();      // the logits may come from the previous kernel
         grid_dep_launch();
         build_small_plan(sr, sp);
@@ -55,12 +53,13 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
         const int vec = H / 8, ipe = I / Rg;
         const Range rg = cta_range(sp.units, sp.n_units, sp.weight, ipe);
         const uint32_t half = (uint32_t)Rg * H * 2, xrow = (uint32_t)H * 2;
+        bool ok = true;
         if (warp < kProducers) {
             if (lane == 0) {
                 const uint64_t policy = policy_evict_first();
                 const __nv_bfloat16* W = warp == 0 ? Wg : Wu;
                 const uint32_t part = warp == 0 ? 0u : half;
-                is = produce<kBufs>(
+                ok = produce<kBufs>(
                     m, warp, rg, warp == 0,
                     [&](int it, uint32_t dst, uint32_t bar) {
                         const ThinUnit un = sp.units[it / ipe];
@@ -76,8 +75,7 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
                             bulk_g2s(dst + t * xrow, x + (size_t)(sp.perm[un.row0 + t] / k) * H,
                                      xrow, bar);
                     },
-                    wait_cycles);
-                ok = is.ok;
+                    wait_cycles, notes);
             }
         } else if (warp - kProducers < nc) {
             ok = consume<16, kBufs>(m, rg, ipe, sp.units, warp - kProducers, nc, wait_cycles,
@@ -87,7 +85,10 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
                 gate_up_slot<N, VG>(mu, slot, Rg, vec, un.n, hcol, I);
             });
         }
-        if (!ok) set_status(hdr, MOE_ERR_TIMEOUT);
+        if (!ok) {
+            notes.gave_up = 1;
+            set_status(hdr, MOE_ERR_TIMEOUT);
+        }
         // this CTA's h rows, for other CTAs' bulk copies
         fence_proxy_async_global();
         __threadfence();
@@ -102,9 +103,9 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
     }
     if (!failed) {   // ---------------- down ----------------
         constexpr int kProducers = 1;
-        is = {true, 0, 0};
+        bool ok = true;
         const int nc = min(n_warps - kProducers, slots_d - 1);
-        m = smem_setup(smem, stage_d, slots_d, act_d, kProducers, nc, kBufs);
+        const Smem m = smem_setup(smem, stage_d, slots_d, act_d, kProducers, nc, notes, kBufs);
         const int vec = I / 8, ipe = H / Rd;
         const Range rg = cta_range(sp.units, sp.n_units, sp.weight, ipe);
         const uint32_t bytes = (uint32_t)Rd * I * 2, hrow = (uint32_t)I * 2;
@@ -136,7 +137,7 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
                     __nanosleep(32);
                 }
                 fence_proxy_async_global();
-                is = produce<kBufs>(
+                ok = produce<kBufs>(
                     m, 0, rg, true, copy_item,
                     [&](int u, uint32_t dst, uint32_t bar) {
                         const ThinUnit un = sp.units[u];
@@ -144,8 +145,7 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
                         mbar_expect_tx(bar, (uint32_t)un.n * hrow);
                         bulk_g2s(dst, h + (size_t)un.row0 * I, (uint32_t)un.n * hrow, bar);
                     },
-                    wait_cycles, pre);
-                ok = is.ok;
+                    wait_cycles, notes, pre);
             }
         } else if (warp - kProducers < nc) {
             constexpr int kExact =
@@ -157,10 +157,14 @@ thin_layer_kernel(const __nv_bfloat16* __restrict__ x, int k, int H, int I, int 
                 down_slot<N, VD>(mu, slot, Rd, vec, un.n, ycol, H);
             });
         }
-        if (!ok) set_status(hdr, MOE_ERR_TIMEOUT);
+        if (!ok) {
+            notes.gave_up = 1;
+            set_status(hdr, MOE_ERR_TIMEOUT);
+        }
     }
     combine_spread(sr, sp.inv_perm, sp.gates, hdr, y, H, wait_cycles);
-    if (__syncthreads_or(!ok)) drain_copies<kBufs>(m, warp, is);
+    // (behind the combine's block barriers)
+    if (notes.gave_up) drain_copies(notes);
 }
 
 template <int VG, int VD, int kBufs>
