@@ -466,6 +466,111 @@ moe_status moe_balance_backward(const float* logits, const float* stats, const i
                                 const int32_t* topk_idx, const float* gates, const float* d_gates,
                                 float* d_logits, moe_stream_t stream);
 
+/* ---- training the experts ------------------------------------------------ */
+
+/* The experts' gated feed-forward block with what its backward pass needs, and
+ * that pass: the gradients of x, of the router's gates and of the three
+ * matrices.  The pages do not train their model.  Both calls work on the
+ * routed layer, or on a dense block (a shared expert): perm and offsets (and
+ * inv_perm) NULL with E = 1 and k = 1, whose sorted rows are the rows of x.
+ * The shape's fat_threshold and thin_mma_min do not apply.
+ *
+ * What the forward call keeps, and the backward call reads (P = T * k sorted
+ * rows).  fp8 == 0: gate, up [P, I] bf16 hold g = x W_gate^T and u = x W_up^T
+ * rounded once, and x is the call's own input, which the caller keeps.
+ * fp8 == 1 (8-bit checkpoints, about half the bytes): the same rows, and x
+ * [T, H] by token, in e4m3 with a scale byte per block of 128 along the row,
+ * in the format of the 8-bit experts; the scales are [P, I / 128] and
+ * [T, H / 128].  With fp8 == 0 the scales are NULL.  Device pointers. */
+typedef struct {
+    int32_t fp8;
+    void* x;             /* fp8: written by the forward call; else only read by the backward */
+    uint8_t* x_scales;
+    void* gate;
+    uint8_t* gate_scales;
+    void* up;
+    uint8_t* up_scales;
+} moe_saved;
+
+/* Forward: for sorted position p of expert e and token t
+ *   g = W_gate[e] . x[t],  u = W_up[e] . x[t],
+ *   y_sorted[p] = bf16( W_down[e] . bf16( silu(g) * u ) )
+ * with fp32 accumulation, g and u in `saved`.  perm, offsets as moe_permute
+ * wrote them.  Offsets that do not ascend from 0 to T*k set MOE_ERR_BAD_INDEX
+ * in the workspace status; rows of no expert are then not written.  ws:
+ * moe_expert_ffn_train_workspace_size() bytes, initialised once with
+ * moe_workspace_init(). */
+size_t moe_expert_ffn_train_workspace_size(const moe_shape* shape);
+moe_status moe_expert_ffn_train(const moe_shape* shape, const moe_bf16* x, const int32_t* perm,
+                                const int32_t* offsets, const moe_bf16* W_gate,
+                                const moe_bf16* W_up, const moe_bf16* W_down, moe_bf16* y_sorted,
+                                const moe_saved* saved, void* ws, size_t ws_bytes,
+                                moe_stream_t stream);
+
+/* Backward: from d_out [T, H], the gradient of out = moe_combine(y_sorted),
+ * with w the gate of row p's slot, d = d_out[t], s = sigmoid(g), h = g s u and
+ * q = W_down^T d:
+ *   d_gates[slot] = q . h,   dh = w q,   du = dh g s,
+ *   dg = dh u s (1 + g (1 - s)),
+ *   d_x[t] = sum over t's slots of W_gate^T dg + W_up^T du,
+ *   dW_down[e] = sum over e's rows of d (w h)^T,
+ *   dW_gate[e] = sum of dg x[t]^T,   dW_up[e] = sum of du x[t]^T.
+ * Sums are fp32 in a fixed order (repeated runs give the same bits); dg, du,
+ * w h and, with k > 1 or route lists, each slot's part of d_x are rounded to
+ * bf16 once.  Every element of the three dW is written, experts without rows
+ * get zeros.
+ *   gates [T, k] fp32 as moe_route wrote them, or NULL: all 1, and d_gates is
+ *   NULL too.  d_x [T, H] bf16, d_gates [T, k] fp32 and the dW (bf16, in the
+ *   matrices' layouts) written; d_x, d_gates, and the three dW together, may
+ *   be NULL.  inv_perm as moe_permute wrote it.  Where moe_permute skipped a
+ *   routed index, d_gates and d_x of its token are unspecified.  ws:
+ *   moe_expert_ffn_backward_workspace_size() bytes, initialised once with
+ *   moe_workspace_init(). */
+size_t moe_expert_ffn_backward_workspace_size(const moe_shape* shape);
+moe_status moe_expert_ffn_backward(const moe_shape* shape, const moe_bf16* d_out,
+                                   const float* gates, const moe_saved* saved,
+                                   const int32_t* perm, const int32_t* offsets,
+                                   const int32_t* inv_perm, const moe_bf16* W_gate,
+                                   const moe_bf16* W_up, const moe_bf16* W_down, moe_bf16* d_x,
+                                   float* d_gates, moe_bf16* dW_gate, moe_bf16* dW_up,
+                                   moe_bf16* dW_down, void* ws, size_t ws_bytes,
+                                   moe_stream_t stream);
+
+/* The values of rows in 8 bits (as moe_quantize_rows or an 8-bit checkpoint
+ * holds them): x [rows, K] bf16 = q times its block's scale, exact unless it
+ * leaves bf16's range.  K: a positive multiple of 128, at most 16384. */
+moe_status moe_dequantize_rows(const uint8_t* q, const uint8_t* scales, int32_t rows, int32_t K,
+                               moe_bf16* x, moe_stream_t stream);
+
+/* ---- product with an epilogue ---------------------------------------------- */
+
+typedef enum {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,
+    MOE_ACT_GELU = 2,   /* v times the normal distribution's mass below v (erf) */
+    MOE_ACT_SILU = 3
+} moe_activation;
+
+/* Grouped bf16 product with bias, activation and residual: for the rows
+ * offsets[e] <= p < offsets[e + 1] of group e
+ *   y[p, n] = act( sum_k x[p, k] W[e, n, k] + bias[e, n] ) + residual[p, n]
+ * in fp32, rounded once where y is bf16.  A router's logits are E = 1 with
+ * fp32 y; a shared expert's down product takes the routed output as residual.
+ *   x [rows, K] bf16; W [E, N, K] bf16; offsets [E + 1] ascending from 0 to
+ *   rows (groups may be empty), or NULL with E = 1; bias [E, N] fp32 or NULL;
+ *   residual [rows, N] bf16 or NULL; y [rows, N] bf16 (y_fp32 == 0) or fp32,
+ *   may be the residual itself when bf16.  K: a positive multiple of 8 and N:
+ *   positive, each at most 65536; E <= 1024, E * N < 2^31.  ws:
+ *   moe_grouped_gemm_workspace_size() bytes, initialised once with
+ *   moe_workspace_init().  Offsets that are not as stated set
+ *   MOE_ERR_BAD_INDEX in the workspace status; rows of no group are then not
+ *   written. */
+size_t moe_grouped_gemm_workspace_size(int32_t rows, int32_t E, int32_t N, int32_t K);
+moe_status moe_grouped_gemm(const moe_bf16* x, int32_t rows, const int32_t* offsets, int32_t E,
+                            int32_t N, int32_t K, const moe_bf16* W, const float* bias,
+                            int32_t activation, const moe_bf16* residual, void* y, int32_t y_fp32,
+                            void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* ---- activations in host memory --------------------------------------- */
 
 /* The layer on host-resident activations, as a serving process feeds it:

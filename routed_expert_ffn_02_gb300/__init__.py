@@ -16,4 +16,7 @@ from .binding import (  # noqa: F401
     grouped_gemm_fp8_workspace_size, Fp8Experts, quantize_experts, moe_expert_ffn_fp8,
     expert_ffn_fp8_workspace_size, moe_forward_fp8, fp8_workspace_size, moe_balance,
     moe_balance_backward, balance_workspace_size,
+    SavedFfn, moe_expert_ffn_train, expert_ffn_train_workspace_size, moe_expert_ffn_backward,
+    expert_ffn_backward_workspace_size, moe_dequantize_rows, moe_grouped_gemm,
+    grouped_gemm_workspace_size, ACTIVATIONS,
 )

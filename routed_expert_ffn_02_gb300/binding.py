@@ -44,7 +44,10 @@ EXPORTED = ("moe_route", "moe_permute_workspace_size", "moe_permute", "moe_permu
             "moe_quantize_rows", "moe_quantize_weights", "moe_grouped_gemm_fp8_workspace_size",
             "moe_grouped_gemm_fp8", "moe_expert_ffn_fp8_workspace_size", "moe_expert_ffn_fp8",
             "moe_fp8_workspace_size", "moe_forward_fp8", "moe_balance_workspace_size",
-            "moe_balance", "moe_balance_backward")
+            "moe_balance", "moe_balance_backward",
+            "moe_expert_ffn_train_workspace_size", "moe_expert_ffn_train",
+            "moe_expert_ffn_backward_workspace_size", "moe_expert_ffn_backward",
+            "moe_dequantize_rows", "moe_grouped_gemm_workspace_size", "moe_grouped_gemm")
 
 
 class MoeShape(ctypes.Structure):
@@ -57,6 +60,11 @@ class MoeShape(ctypes.Structure):
 class MoeFp8Experts(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "gate_scales", "up", "up_scales",
                                                "down", "down_scales")]
+
+
+class MoeSaved(ctypes.Structure):
+    _fields_ = [("fp8", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in (
+        "x", "x_scales", "gate", "gate_scales", "up", "up_scales")]
 
 
 @dataclass(frozen=True)
@@ -95,6 +103,7 @@ _sz = ctypes.c_size_t
 _SP = ctypes.POINTER(MoeShape)
 
 _WP = ctypes.POINTER(MoeFp8Experts)
+_VP = ctypes.POINTER(MoeSaved)
 _f32 = ctypes.c_float
 
 _sig = {
@@ -110,6 +119,15 @@ _sig = {
     "moe_balance": ([_P, _P, _i32, _i32, _i32, _P, _i32, _f32, _P, _P, _P, _P, _sz, _P], _i32),
     "moe_balance_backward": ([_P, _P, _P, _P, _i32, _i32, _i32, _i32, _f32, _P, _P, _P, _P, _P,
                               _P], _i32),
+    "moe_expert_ffn_train_workspace_size": ([_SP], _sz),
+    "moe_expert_ffn_train": ([_SP, _P, _P, _P, _P, _P, _P, _P, _VP, _P, _sz, _P], _i32),
+    "moe_expert_ffn_backward_workspace_size": ([_SP], _sz),
+    "moe_expert_ffn_backward": ([_SP, _P, _P, _VP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                 _sz, _P], _i32),
+    "moe_dequantize_rows": ([_P, _P, _i32, _i32, _P, _P], _i32),
+    "moe_grouped_gemm_workspace_size": ([_i32, _i32, _i32, _i32], _sz),
+    "moe_grouped_gemm": ([_P, _i32, _P, _i32, _i32, _i32, _P, _P, _i32, _P, _P, _i32, _P, _sz, _P],
+                         _i32),
     "moe_route": ([_P, _i32, _i32, _i32, _P, _P, _P], _i32),
     "moe_permute_workspace_size": ([_i32, _i32, _i32], _sz),
     "moe_permute": ([_P, _i32, _i32, _i32, _P, _P, _P, _P, _P, _sz, _P], _i32),
@@ -779,6 +797,156 @@ def moe_balance_backward(logits, stats, counts, k: int, seq_offsets=None, coef: 
     if st:
         raise MoeError(st, "moe_balance_backward")
     return d_logits
+
+
+@dataclass(frozen=True)
+class SavedFfn:
+    """What moe_expert_ffn_train keeps for moe_expert_ffn_backward, by sorted
+    row: the two projections gate, up [P, I], with x [T, H].  In bf16 (the
+    scales are None; x is the call's own input), or in 8 bits: float8_e4m3fn
+    with scales [P, I/128] and [T, H/128] uint8."""
+    x: torch.Tensor
+    gate: torch.Tensor
+    up: torch.Tensor
+    x_scales: torch.Tensor | None = None
+    gate_scales: torch.Tensor | None = None
+    up_scales: torch.Tensor | None = None
+
+    def ref(self, shape: Shape):
+        """The C structure, for a layer of these sizes."""
+        T, P, H, I = shape.T, shape.P, shape.H, shape.I
+        fp8 = self.gate_scales is not None
+        kind = _E4M3 if fp8 else _BF16
+        c = MoeSaved(int(fp8), _in(self.x, kind, (T, H)), None, _in(self.gate, kind, (P, I)), None,
+                     _in(self.up, kind, (P, I)), None)
+        if fp8:
+            c.x_scales = _in(self.x_scales, _U8, (T, H // 128))
+            c.gate_scales = _in(self.gate_scales, _U8, (P, I // 128))
+            c.up_scales = _in(self.up_scales, _U8, (P, I // 128))
+        return ctypes.byref(c)
+
+    @staticmethod
+    def empty(shape: Shape, x: torch.Tensor, checkpoint: str = "bf16", stream=None) -> "SavedFfn":
+        """Room for one forward call on x ("bf16" or "fp8" checkpoints)."""
+        assert checkpoint in ("bf16", "fp8"), f"checkpoint = {checkpoint!r}: 'bf16' or 'fp8'"
+        T, P, H, I, dev = shape.T, shape.P, shape.H, shape.I, x.device
+        if checkpoint == "bf16":
+            return SavedFfn(x, _empty((P, I), _BF16, dev, stream), _empty((P, I), _BF16, dev, stream))
+        return SavedFfn(*(_empty(s, _E4M3, dev, stream) for s in ((T, H), (P, I), (P, I))),
+                        *(_empty(s, _U8, dev, stream) for s in ((T, H // 128), (P, I // 128), (P, I // 128))))
+
+
+def expert_ffn_train_workspace_size(shape: Shape) -> int:
+    n = _lib.moe_expert_ffn_train_workspace_size(ctypes.byref(shape.c()))
+    if n == 0:
+        raise MoeError(1, "moe_expert_ffn_train_workspace_size")
+    return n
+
+
+def moe_expert_ffn_train(shape: Shape, x, perm, offsets, W_gate, W_up, W_down,
+                         checkpoint: str = "bf16", y_sorted=None, saved: SavedFfn | None = None,
+                         ws: Workspace | None = None, stream=None):
+    """moe_expert_ffn that keeps what the backward pass needs, in bf16 or
+    ("fp8") in 8 bits.  perm and offsets from moe_permute, or None with
+    E = k = 1: a dense block.  `saved`: room from an earlier call, whose kind
+    then counts.  Returns (y_sorted [P, H] bf16, SavedFfn)."""
+    T, E, P, H, I = shape.T, shape.E, shape.P, shape.H, shape.I
+    xp = _in(x, _BF16, (T, H))
+    y_sorted, yp = _out(y_sorted, (P, H), _BF16, x, stream)
+    if saved is None:
+        saved = SavedFfn.empty(shape, x, checkpoint, stream)
+    elif saved.gate_scales is None:      # the record of this call: its own x
+        saved = SavedFfn(x, saved.gate, saved.up)
+    ws = ws or Workspace(expert_ffn_train_workspace_size(shape), x.device, stream)
+    st = _lib.moe_expert_ffn_train(
+        ctypes.byref(shape.c()), xp, _opt(perm, _I32, (P,)), _opt(offsets, _I32, (E + 1,)),
+        _in(W_gate, _BF16, (E, I, H)), _in(W_up, _BF16, (E, I, H)), _in(W_down, _BF16, (E, H, I)),
+        yp, saved.ref(shape), ws.addr, ws.nbytes, _on(stream, x))
+    if st:
+        raise MoeError(st, "moe_expert_ffn_train")
+    return y_sorted, saved
+
+
+def expert_ffn_backward_workspace_size(shape: Shape) -> int:
+    n = _lib.moe_expert_ffn_backward_workspace_size(ctypes.byref(shape.c()))
+    if n == 0:
+        raise MoeError(1, "moe_expert_ffn_backward_workspace_size")
+    return n
+
+
+def moe_expert_ffn_backward(shape: Shape, d_out, saved: SavedFfn, perm, offsets, inv_perm, W_gate,
+                            W_up, W_down, gates=None, need_x: bool = True,
+                            need_weights: bool = True, d_x=None, d_gates=None, dW=None,
+                            ws: Workspace | None = None, stream=None):
+    """Gradients of the layer's experts and gates from d_out [T, H] bf16, the
+    gradient of moe_combine's output (gates None: all 1).  Returns (d_x [T, H]
+    bf16, d_gates [T, k] fp32, dW_gate, dW_up, dW_down bf16); None in the place
+    of what is not needed, and of d_gates without gates."""
+    T, E, k, P, H, I = shape.T, shape.E, shape.k, shape.P, shape.H, shape.I
+    dp = _in(d_out, _BF16, (T, H))
+    xp = gp = None
+    if need_x:
+        d_x, xp = _out(d_x, (T, H), _BF16, d_out, stream)
+    if gates is not None:
+        d_gates, gp = _out(d_gates, (T, k), _F32, d_out, stream)
+    dW, wp = (None,) * 3 if dW is None else dW, (None,) * 3
+    if need_weights:
+        dW, wp = zip(*(_out(w, s, _BF16, d_out, stream)
+                       for w, s in zip(dW, ((E, I, H), (E, I, H), (E, H, I)))))
+    ws = ws or Workspace(expert_ffn_backward_workspace_size(shape), d_out.device, stream)
+    st = _lib.moe_expert_ffn_backward(
+        ctypes.byref(shape.c()), dp, _opt(gates, _F32, (T, k)), saved.ref(shape),
+        _opt(perm, _I32, (P,)), _opt(offsets, _I32, (E + 1,)), _opt(inv_perm, _I32, (P,)),
+        _in(W_gate, _BF16, (E, I, H)), _in(W_up, _BF16, (E, I, H)), _in(W_down, _BF16, (E, H, I)),
+        xp, gp, *wp, ws.addr, ws.nbytes, _on(stream, d_out))
+    if st:
+        raise MoeError(st, "moe_expert_ffn_backward")
+    return (d_x if need_x else None, d_gates if gates is not None else None,
+            *(dW if need_weights else (None,) * 3))
+
+
+def moe_dequantize_rows(q, scales, x=None, stream=None):
+    """The values of 8-bit rows (q [rows, K] float8_e4m3fn, scales [rows, K/128]
+    uint8) as bf16 [rows, K]."""
+    rows, K = q.shape
+    x, xp = _out(x, (rows, K), _BF16, q, stream)
+    st = _lib.moe_dequantize_rows(_in(q, _E4M3, (rows, K)), _in(scales, _U8, (rows, K // 128)), rows, K,
+                                  xp, _on(stream, q))
+    if st:
+        raise MoeError(st, "moe_dequantize_rows")
+    return x
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+
+
+def grouped_gemm_workspace_size(rows: int, E: int, N: int, K: int) -> int:
+    n = _lib.moe_grouped_gemm_workspace_size(rows, E, N, K)
+    if n == 0:
+        raise MoeError(1, "moe_grouped_gemm_workspace_size")
+    return n
+
+
+def moe_grouped_gemm(x, W, offsets=None, bias=None, activation: str = "none", residual=None,
+                     out_dtype=torch.bfloat16, y=None, ws: Workspace | None = None, stream=None):
+    """y[p] = act(x[p] . W[e]^T + bias[e]) + residual[p] for the rows
+    offsets[e] <= p < offsets[e + 1] (None with E = 1: all); x [rows, K],
+    W [E, N, K] and residual [rows, N] bf16, bias [E, N] fp32; y [rows, N] of
+    out_dtype (bf16 or fp32).  activation: "none", "relu", "gelu" or "silu"."""
+    rows, K = x.shape
+    E, N, _ = W.shape
+    assert activation in ACTIVATIONS, f"activation = {activation!r}: one of {', '.join(ACTIVATIONS)}"
+    assert out_dtype in (_BF16, _F32), f"out_dtype = {out_dtype}: bfloat16 or float32"
+    y, yp = _out(y, (rows, N), out_dtype, x, stream)
+    ws = ws or Workspace(grouped_gemm_workspace_size(rows, E, N, K), x.device, stream)
+    st = _lib.moe_grouped_gemm(
+        _in(x, _BF16, (rows, K)), rows, _opt(offsets, _I32, (E + 1,)), E, N, K,
+        _in(W, _BF16, (E, N, K)), _opt(bias, _F32, (E, N)), ACTIVATIONS[activation],
+        _opt(residual, _BF16, (rows, N)), yp, int(out_dtype is _F32), ws.addr, ws.nbytes,
+        _on(stream, x))
+    if st:
+        raise MoeError(st, "moe_grouped_gemm")
+    return y
 
 
 def raw_lib():

@@ -1,0 +1,312 @@
+// api_train.cu -- the C ABI of the experts' training passes and of the product
+// with an epilogue (include/moe.h): argument validation, workspace layout and
+// the launch sequence of each entry point.  Nothing here allocates or throws.
+
+#include "api_common.cuh"
+#include "train.cuh"
+
+using namespace moe;
+
+namespace {
+
+// Rows of B per CTA of the tile kernel: the narrow build for groups that hold
+// at most a narrow chunk (32 rows) on average, else the wide one.
+int rows_per_cta(int64_t rows, int E) { return rows <= (int64_t)2 * kThinRows * E ? kThinRows : kWideRows; }
+
+struct Lists {
+    WsHeader* hdr;
+    RowLists l;
+};
+void take_lists(Carver* c, int64_t rows, int E, int most, Lists* l) {
+    l->hdr = c->take<WsHeader>(1);
+    l->l.n_chunks = c->take<int32_t>(1);
+    l->l.groups = c->take<RowChunk>((size_t)E);
+    l->l.chunks = c->take<RowChunk>((size_t)max_chunks(rows, E, most));
+}
+
+// The tile kernel's arguments over the lists, or (dense) over one group.
+TileArgs args_of(const Lists& l, bool dense, int64_t rows, int E, int most) {
+    TileArgs a = {};
+    a.hdr = l.hdr;
+    a.rows = (int)rows;
+    a.E = E;
+    if (dense) {
+        a.chunk_rows = chunk_size((int)rows, most);
+        a.dense_chunks = a.chunk_rows ? (int)((rows + a.chunk_rows - 1) / a.chunk_rows) : 0;
+    } else {
+        a.chunks = l.l.chunks;
+        a.groups = l.l.groups;
+        a.n_chunks = l.l.n_chunks;
+    }
+    a.wait_cycles = main_wait_cycles();
+    return a;
+}
+
+struct FwdBufs {
+    Lists l;
+    __nv_bfloat16 *xs, *h;
+};
+size_t carve_fwd(const moe_shape* sh, void* ws, FwdBufs* b) {
+    const int64_t P = (int64_t)sh->T * sh->k;
+    Carver c(ws);
+    take_lists(&c, P, sh->E, 2 * rows_per_cta(P, sh->E), &b->l);
+    b->xs = c.take<__nv_bfloat16>((size_t)(P * sh->H));
+    b->h = c.take<__nv_bfloat16>((size_t)(P * sh->I));
+    return align_up(c.off, 256);
+}
+
+struct BwdBufs {
+    Lists l;
+    __nv_bfloat16 *x, *d, *dx;     // padded rows of x and d_out; each slot's part of d_x
+    __nv_bfloat16 *h, *dg, *du;    // padded
+    float* parts;
+};
+size_t carve_bwd(const moe_shape* sh, void* ws, BwdBufs* b) {
+    const int64_t P = (int64_t)sh->T * sh->k, pad = padded_rows(P, sh->E);
+    Carver c(ws);
+    take_lists(&c, P, sh->E, 2 * rows_per_cta(P, sh->E), &b->l);
+    b->x = c.take<__nv_bfloat16>((size_t)(pad * sh->H));
+    b->d = c.take<__nv_bfloat16>((size_t)(pad * sh->H));
+    b->dx = c.take<__nv_bfloat16>((size_t)(P * sh->H));
+    b->h = c.take<__nv_bfloat16>((size_t)(pad * sh->I));
+    b->dg = c.take<__nv_bfloat16>((size_t)(pad * sh->I));
+    b->du = c.take<__nv_bfloat16>((size_t)(pad * sh->I));
+    b->parts = c.take<float>((size_t)(P * (sh->I / 32)));
+    return align_up(c.off, 256);
+}
+
+// Route lists given together, or a dense block.
+moe_status check_lists(const moe_shape* sh, const int32_t* perm, const int32_t* offsets, bool* dense) {
+    *dense = !perm && !offsets;
+    if (!*dense && (!perm || !offsets))
+        return fail(MOE_ERR_INVALID_ARG, "perm and offsets come together");
+    if (*dense && (sh->E != 1 || sh->k != 1))
+        return fail(MOE_ERR_INVALID_ARG, "no route lists with E = %d, k = %d (a dense block has 1, 1)",
+                    sh->E, sh->k);
+    return MOE_OK;
+}
+
+moe_status check_saved(const moe_saved* v, bool need_x) {
+    if (!v) return fail(MOE_ERR_INVALID_ARG, "saved is NULL");
+    CHECK_PTR(v->gate); CHECK_PTR(v->up);
+    if (v->fp8 || need_x) CHECK_PTR(v->x);
+    if (v->fp8 && (!v->x_scales || !v->gate_scales || !v->up_scales))
+        return fail(MOE_ERR_INVALID_ARG, "8-bit checkpoints without scales");
+    return MOE_OK;
+}
+
+moe_status check_product(int32_t rows, int32_t E, int32_t N, int32_t K) {
+    constexpr int kMost = 65536;
+    if (rows < 0 || rows > INT32_MAX - kTileM)
+        return fail(MOE_ERR_INVALID_ARG, "rows = %d out of range", rows);
+    if (E < 1 || E > kMaxE) return fail(MOE_ERR_INVALID_ARG, "E = %d outside [1, %d]", E, kMaxE);
+    if (N < 1) return fail(MOE_ERR_INVALID_ARG, "N = %d is not positive", N);
+    if (K < 8 || K % 8) return fail(MOE_ERR_INVALID_ARG, "K = %d is not a positive multiple of 8", K);
+    if (N > kMost || K > kMost) return fail(MOE_ERR_UNSUPPORTED, "N and K are limited to %d", kMost);
+    return MOE_OK;
+}
+size_t carve_product(int32_t rows, int32_t E, void* ws, Lists* l) {
+    Carver c(ws);
+    take_lists(&c, rows, E, 2 * rows_per_cta(rows, E), l);
+    return align_up(c.off, 256);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_expert_ffn_train_workspace_size(const moe_shape* shape) {
+    if (check_shape_status(shape) != MOE_OK) return 0;
+    FwdBufs b;
+    return carve_fwd(shape, nullptr, &b);
+}
+
+moe_status moe_expert_ffn_train(const moe_shape* shape, const moe_bf16* x, const int32_t* perm,
+                                const int32_t* offsets, const moe_bf16* W_gate,
+                                const moe_bf16* W_up, const moe_bf16* W_down, moe_bf16* y_sorted,
+                                const moe_saved* saved, void* ws, size_t ws_bytes,
+                                moe_stream_t stream) {
+    STATUS_TRY(check_shape_status(shape));
+    bool dense;
+    STATUS_TRY(check_lists(shape, perm, offsets, &dense));
+    if (shape->T == 0) return ok();
+    CHECK_PTR(x); CHECK_PTR(W_gate); CHECK_PTR(W_up); CHECK_PTR(W_down); CHECK_PTR(y_sorted);
+    STATUS_TRY(check_saved(saved, false));
+    FwdBufs b;
+    STATUS_TRY(check_ws(ws, ws_bytes, carve_fwd(shape, nullptr, &b)));
+    carve_fwd(shape, ws, &b);
+    int sms = 0;
+    STATUS_TRY(current_device(&sms));
+    cudaStream_t s = (cudaStream_t)stream;
+    const int T = shape->T, E = shape->E, k = shape->k, H = shape->H, I = shape->I;
+    const int64_t P = (int64_t)T * k;
+    const int nb = rows_per_cta(P, E), most = 2 * nb;
+    const PdlScope pdl(P <= kPermChunk);
+    const __nv_bfloat16* xs = (const __nv_bfloat16*)x;
+    if (saved->fp8)
+        CUDA_TRY(launch_quantize_rows(xs, T, H, nullptr, 1, 0, (uint8_t*)saved->x, saved->x_scales,
+                                      sms, s), "quantize rows");
+    if (!dense) {
+        CUDA_TRY(launch_plan_rows(offsets, (int)P, E, most, b.l.l, b.l.hdr, s), "plan");
+        const GatherJob g = {xs, nullptr, nullptr, b.xs, nullptr, perm, k, H, (int)P, 0};
+        CUDA_TRY(launch_gather_rows(g, b.l.l, max_chunks(P, E, most), most, sms, s), "gather");
+        xs = b.xs;
+    }
+    TileArgs a = args_of(b.l, dense, P, E, most);
+    a.out = b.h;
+    a.gate = saved->gate;
+    a.up = saved->up;
+    a.gate_scales = saved->gate_scales;
+    a.up_scales = saved->up_scales;
+    CUDA_TRY(launch_train_gate_up(xs, P, (const __nv_bfloat16*)W_gate, (const __nv_bfloat16*)W_up,
+                                  H, I, saved->fp8 != 0, nb, a, sms, s), "gate/up");
+    a.out = (__nv_bfloat16*)y_sorted;
+    CUDA_TRY(launch_train_down(b.h, P, (const __nv_bfloat16*)W_down, H, I, nb, a, sms, s), "down");
+    return ok();
+}
+
+size_t moe_expert_ffn_backward_workspace_size(const moe_shape* shape) {
+    if (check_shape_status(shape) != MOE_OK) return 0;
+    BwdBufs b;
+    return carve_bwd(shape, nullptr, &b);
+}
+
+moe_status moe_expert_ffn_backward(const moe_shape* shape, const moe_bf16* d_out,
+                                   const float* gates, const moe_saved* saved,
+                                   const int32_t* perm, const int32_t* offsets,
+                                   const int32_t* inv_perm, const moe_bf16* W_gate,
+                                   const moe_bf16* W_up, const moe_bf16* W_down, moe_bf16* d_x,
+                                   float* d_gates, moe_bf16* dW_gate, moe_bf16* dW_up,
+                                   moe_bf16* dW_down, void* ws, size_t ws_bytes,
+                                   moe_stream_t stream) {
+    STATUS_TRY(check_shape_status(shape));
+    bool dense;
+    STATUS_TRY(check_lists(shape, perm, offsets, &dense));
+    if (dense != !inv_perm) return fail(MOE_ERR_INVALID_ARG, "perm, offsets and inv_perm come together");
+    if (d_gates && !gates) return fail(MOE_ERR_INVALID_ARG, "d_gates without gates");
+    const bool weights = dW_gate || dW_up || dW_down;
+    if (weights) {
+        CHECK_PTR(dW_gate); CHECK_PTR(dW_up); CHECK_PTR(dW_down);
+    }
+    const int T = shape->T, E = shape->E, k = shape->k, H = shape->H, I = shape->I;
+    cudaStream_t s = (cudaStream_t)stream;
+    int sms = 0;
+    if (T == 0) {       // no row: the weights' gradients are zero
+        if (!weights) return ok();
+        STATUS_TRY(current_device(&sms));
+        for (moe_bf16* w : {dW_gate, dW_up, dW_down})
+            CUDA_TRY(cudaMemsetAsync(w, 0, (size_t)E * H * I * 2, s), "clear weight gradients");
+        return ok();
+    }
+    CHECK_PTR(d_out); CHECK_PTR(W_gate); CHECK_PTR(W_up); CHECK_PTR(W_down);
+    if (d_x) CHECK_PTR(d_x);
+    STATUS_TRY(check_saved(saved, true));
+    BwdBufs b;
+    STATUS_TRY(check_ws(ws, ws_bytes, carve_bwd(shape, nullptr, &b)));
+    carve_bwd(shape, ws, &b);
+    STATUS_TRY(current_device(&sms));
+    const int64_t P = (int64_t)T * k, pad = padded_rows(P, E);
+    const int nb = rows_per_cta(P, E), most = 2 * nb;
+    const PdlScope pdl(P <= kPermChunk);
+    // x and d_out by sorted row: the caller's own where the block is dense
+    const __nv_bfloat16 *x = (const __nv_bfloat16*)saved->x, *d = (const __nv_bfloat16*)d_out;
+    const int64_t xd_rows = dense ? T : pad;
+    if (!dense) {
+        CUDA_TRY(launch_plan_rows(offsets, (int)P, E, most, b.l.l, b.l.hdr, s), "plan");
+        const GatherJob g = {saved->x, saved->fp8 ? saved->x_scales : nullptr, d, b.x, b.d, perm, k, H,
+                             (int)P, 1};
+        CUDA_TRY(launch_gather_rows(g, b.l.l, max_chunks(P, E, most), most, sms, s), "gather");
+        x = b.x;
+        d = b.d;
+    } else if (saved->fp8) {
+        CUDA_TRY(launch_dequantize_rows((const uint8_t*)saved->x, saved->x_scales, T, H, b.x, sms, s),
+                 "dequantize rows");
+        x = b.x;
+    }
+    TileArgs a = args_of(b.l, dense, P, E, most);
+    a.padded = !dense;
+    a.gate = saved->gate;
+    a.up = saved->up;
+    a.gate_scales = saved->gate_scales;
+    a.up_scales = saved->up_scales;
+    a.gates = gates;
+    a.perm = perm;
+    a.out = b.h;
+    a.d_gate = b.dg;
+    a.d_up = b.du;
+    a.gate_parts = d_gates ? b.parts : nullptr;
+    CUDA_TRY(launch_hidden_grad(d, xd_rows, (const __nv_bfloat16*)W_down, H, I, saved->fp8 != 0, nb, a,
+                                sms, s), "gradient of the projections");
+    if (d_gates)
+        CUDA_TRY(launch_sum_gate_parts(b.parts, I / 32, (int)P, inv_perm, d_gates, s), "gradient of the gates");
+    if (d_x) {
+        a.out = dense ? (__nv_bfloat16*)d_x : b.dx;
+        CUDA_TRY(launch_input_grad(b.dg, b.du, pad, (const __nv_bfloat16*)W_gate,
+                                   (const __nv_bfloat16*)W_up, H, I, nb, a, sms, s), "gradient of x");
+        if (!dense)
+            CUDA_TRY(launch_sum_slots(b.dx, inv_perm, T, k, H, (__nv_bfloat16*)d_x, sms, s), "sum over slots");
+    }
+    if (weights) {
+        a.out = (__nv_bfloat16*)dW_down;
+        a.d_gate = (__nv_bfloat16*)dW_gate;
+        a.d_up = (__nv_bfloat16*)dW_up;
+        CUDA_TRY(launch_weight_grad(b.h, b.dg, b.du, pad, x, d, xd_rows, H, I, a, sms, s),
+                 "gradients of the weights");
+    }
+    return ok();
+}
+
+moe_status moe_dequantize_rows(const uint8_t* q, const uint8_t* scales, int32_t rows, int32_t K,
+                               moe_bf16* x, moe_stream_t stream) {
+    if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows = %d < 0", rows);
+    if (K < 128 || K % 128) return fail(MOE_ERR_INVALID_ARG, "K = %d is not a positive multiple of 128", K);
+    if (K > kMaxHidden) return fail(MOE_ERR_UNSUPPORTED, "K is limited to %d", kMaxHidden);
+    if (rows == 0) return ok();
+    CHECK_PTR(q); CHECK_PTR(x);
+    if (!scales) return fail(MOE_ERR_INVALID_ARG, "scales is NULL");
+    int sms = 0;
+    STATUS_TRY(current_device(&sms));
+    CUDA_TRY(launch_dequantize_rows(q, scales, rows, K, (__nv_bfloat16*)x, sms, (cudaStream_t)stream),
+             "dequantize rows");
+    return ok();
+}
+
+size_t moe_grouped_gemm_workspace_size(int32_t rows, int32_t E, int32_t N, int32_t K) {
+    if (check_product(rows, E, N, K) != MOE_OK) return 0;
+    Lists l;
+    return carve_product(rows, E, nullptr, &l);
+}
+
+moe_status moe_grouped_gemm(const moe_bf16* x, int32_t rows, const int32_t* offsets, int32_t E,
+                            int32_t N, int32_t K, const moe_bf16* W, const float* bias,
+                            int32_t activation, const moe_bf16* residual, void* y, int32_t y_fp32,
+                            void* ws, size_t ws_bytes, moe_stream_t stream) {
+    STATUS_TRY(check_product(rows, E, N, K));
+    if (activation < MOE_ACT_NONE || activation > MOE_ACT_SILU)
+        return fail(MOE_ERR_INVALID_ARG, "activation = %d is none of moe_activation", activation);
+    if (!offsets && E != 1) return fail(MOE_ERR_INVALID_ARG, "offsets is NULL with E = %d", E);
+    if (rows == 0) return ok();
+    CHECK_PTR(x); CHECK_PTR(W); CHECK_PTR(y);
+    if (!aligned(bias, 4)) return fail(MOE_ERR_INVALID_ARG, "bias is not 4-byte aligned");
+    if (!aligned(residual, 2)) return fail(MOE_ERR_INVALID_ARG, "residual is not 2-byte aligned");
+    Lists l;
+    STATUS_TRY(check_ws(ws, ws_bytes, carve_product(rows, E, nullptr, &l)));
+    carve_product(rows, E, ws, &l);
+    int sms = 0;
+    STATUS_TRY(current_device(&sms));
+    cudaStream_t s = (cudaStream_t)stream;
+    const int nb = rows_per_cta(rows, E), most = 2 * nb;
+    const PdlScope pdl(rows <= kPermChunk);
+    if (offsets) CUDA_TRY(launch_plan_rows(offsets, rows, E, most, l.l, l.hdr, s), "plan");
+    TileArgs a = args_of(l, !offsets, rows, E, most);
+    a.out = y_fp32 ? nullptr : (__nv_bfloat16*)y;
+    a.out32 = y_fp32 ? (float*)y : nullptr;
+    a.bias = bias;
+    a.residual = (const __nv_bfloat16*)residual;
+    a.act = activation;
+    CUDA_TRY(launch_product((const __nv_bfloat16*)x, rows, (const __nv_bfloat16*)W, N, K, nb, a, sms, s),
+             "product");
+    return ok();
+}
+
+}  // extern "C"

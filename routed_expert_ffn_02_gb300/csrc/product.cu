@@ -1,0 +1,23 @@
+// product.cu -- the grouped bf16 product with bias, activation and residual in
+// its epilogue, on the tile kernel.
+#include "tile_gemm.cuh"
+
+namespace moe {
+
+cudaError_t launch_product(const __nv_bfloat16* x, int64_t rows, const __nv_bfloat16* W, int N,
+                           int K, int nb, TileArgs a, int num_sms, cudaStream_t s) {
+    using C = tg::Cfg<tg::kProduct, kWideRows>;
+    tg::Maps m = {};
+    cudaError_t e;
+    if ((e = make_tma_map_bf16(&m.a0, W, (uint64_t)a.E * N, K, 128)) != cudaSuccess) return e;
+    if ((e = make_tma_map_bf16(&m.b0, x, rows, K, nb)) != cudaSuccess) return e;
+    a.n_mtiles = (N + 255) / 256;
+    a.m_total = N;
+    a.a_rows = N;
+    a.ld = N;
+    a.k_blocks = (K + C::BK - 1) / C::BK;
+    if (nb == kWideRows) return tg::launch<tg::kProduct, kWideRows>(m, a, num_sms, s);
+    return tg::launch<tg::kProduct, kThinRows>(m, a, num_sms, s);
+}
+
+}  // namespace moe

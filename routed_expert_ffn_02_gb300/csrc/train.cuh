@@ -1,0 +1,126 @@
+// train.cuh -- what the translation units of the training passes and of the
+// product with an epilogue share: the lists of their work, the arguments of
+// the tile kernel (tile_gemm.cuh), and the launchers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+// Rows [row0, row0 + rows) of the sorted rows, of one expert.  In the padded
+// buffers each expert's rows start at a multiple of 16 and are followed by
+// zero rows up to the next one, so that a product over an expert's rows can
+// run in whole MMA steps of 16.
+struct RowChunk {
+    int32_t expert;
+    int32_t row0;
+    int32_t rows;
+    int32_t row0_pad;
+};
+inline int64_t max_chunks(int64_t P, int E, int most) { return P / most + E; }
+inline int64_t padded_rows(int64_t P, int E) { return (int64_t)align_up((size_t)P, 16) + 16 * (int64_t)E; }
+
+// A group of c rows in chunks of at most `most` rows (a multiple of 16):
+// ceil(c / most) of them, of equal size up to the rounding to 16.
+__host__ __device__ inline int chunk_size(int c, int most) {
+    const int n = (c + most - 1) / most;
+    return n == 0 ? 0 : ((c + n - 1) / n + 15) & ~15;
+}
+
+struct TileArgs {
+    WsHeader* hdr;
+    const RowChunk* chunks;    // the chunks, or null: one group of `rows` rows
+    const int32_t* n_chunks;
+    const RowChunk* groups;    // weight gradients: each expert's rows, or null likewise
+    int dense_chunks;          // without lists: chunks, and the rows of each
+    int chunk_rows;
+    int rows;                  // sorted rows
+    int E;
+    int padded;                // B's rows are those of a padded buffer
+    int n_mtiles, n_ntiles;    // 256-wide tiles of the features (weights: of I and of H)
+    int m_total, n_total;      // product: features; weights: I and H
+    int a_rows;                // rows of A per expert
+    int k_blocks;
+    int seg_blocks;            // input gradient: blocks of the first product
+    int64_t ld;                // features of an output row
+    long long wait_cycles;
+    // Buffers by kind (see the epilogues).
+    __nv_bfloat16* out;
+    float* out32;
+    void *gate, *up;           // the kept projections
+    uint8_t *gate_scales, *up_scales;
+    __nv_bfloat16 *d_gate, *d_up;
+    const float* gates;        // gates and the slot of each sorted row
+    const int32_t* perm;
+    float* gate_parts;         // [I / 32, rows]
+    const float* bias;
+    const __nv_bfloat16* residual;
+    int act;
+};
+
+// Lists of the offsets' groups (chunks of at most `most` rows); the offsets
+// are forced to ascend inside [0, rows] (MOE_ERR_BAD_INDEX recorded where
+// they do not, or do not start at 0 and end at rows).
+struct RowLists {
+    RowChunk* chunks;      // [max_chunks]
+    RowChunk* groups;      // [E]
+    int32_t* n_chunks;
+};
+cudaError_t launch_plan_rows(const int32_t* offsets, int rows, int E, int most, const RowLists& l,
+                             WsHeader* hdr, cudaStream_t s);
+
+// dst[row0 + i] (padded: row0_pad + i, and zeros up to the multiple of 16) =
+// src[perm[row0 + i] / k] for every chunk; two sources at once where src1 is
+// given.  src0_scales: src0 holds e4m3 with a scale per 128 values.
+struct GatherJob {
+    const void* src0;
+    const uint8_t* src0_scales;
+    const __nv_bfloat16* src1;
+    __nv_bfloat16 *dst0, *dst1;
+    const int32_t* perm;
+    int k, H, P, padded;
+};
+// `most`: the chunks' rows at most; chunks_bound: how many chunks there may be.
+cudaError_t launch_gather_rows(const GatherJob& g, const RowLists& l, int64_t chunks_bound, int most,
+                               int num_sms, cudaStream_t s);
+
+// out[t] = sum_j y[inv[t * k + j]], fp32 in ascending j; positions outside
+// [0, P) count as zero rows.
+cudaError_t launch_sum_slots(const __nv_bfloat16* y, const int32_t* inv, int T, int k, int H,
+                             __nv_bfloat16* out, int num_sms, cudaStream_t s);
+
+// d_gates[s] = sum over parts [n, P] at position inv[s], in order.
+cudaError_t launch_sum_gate_parts(const float* parts, int n, int P, const int32_t* inv,
+                                  float* d_gates, cudaStream_t s);
+
+// bf16 values of rows of e4m3 with a scale per 128 of K (exact).
+cudaError_t launch_dequantize_rows(const uint8_t* q, const uint8_t* scales, int64_t rows, int K,
+                                   __nv_bfloat16* x, int num_sms, cudaStream_t s);
+
+// Products on CTA pairs.  `a` carries the lists, sizes and epilogue buffers;
+// the launchers add the operands.
+// Rows of B per CTA (half of the most rows of a chunk) that are built.
+constexpr int kWideRows = 128, kThinRows = 16;
+cudaError_t launch_train_gate_up(const __nv_bfloat16* x, int64_t x_rows, const __nv_bfloat16* Wg,
+                                 const __nv_bfloat16* Wu, int H, int I, bool fp8, int nb,
+                                 TileArgs a, int num_sms, cudaStream_t s);
+cudaError_t launch_train_down(const __nv_bfloat16* h, int64_t h_rows, const __nv_bfloat16* Wd,
+                              int H, int I, int nb, TileArgs a, int num_sms, cudaStream_t s);
+cudaError_t launch_hidden_grad(const __nv_bfloat16* d, int64_t d_rows, const __nv_bfloat16* Wd,
+                               int H, int I, bool fp8, int nb, TileArgs a, int num_sms,
+                               cudaStream_t s);
+cudaError_t launch_input_grad(const __nv_bfloat16* dg, const __nv_bfloat16* du, int64_t rows,
+                              const __nv_bfloat16* Wg, const __nv_bfloat16* Wu, int H, int I,
+                              int nb, TileArgs a, int num_sms, cudaStream_t s);
+cudaError_t launch_weight_grad(const __nv_bfloat16* h, const __nv_bfloat16* dg,
+                               const __nv_bfloat16* du, int64_t rows, const __nv_bfloat16* x,
+                               const __nv_bfloat16* d, int64_t xd_rows, int H, int I, TileArgs a,
+                               int num_sms, cudaStream_t s);
+cudaError_t launch_product(const __nv_bfloat16* x, int64_t rows, const __nv_bfloat16* W, int N,
+                           int K, int nb, TileArgs a, int num_sms, cudaStream_t s);
+
+}  // namespace moe

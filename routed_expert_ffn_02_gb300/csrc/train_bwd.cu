@@ -1,0 +1,67 @@
+// train_bwd.cu -- the experts' backward pass on the tile kernel, from the
+// gradient d of the layer's output at each row's token and the row's gate w:
+//   hidden   q = d Wd; dg, du, w h and the parts of d_gate in its epilogue;
+//   input    dx = dg Wg + du Wu, one accumulation over both products;
+//   weights  dWd = d^T (w h), dWg = dg^T x, dWu = du^T x over each expert's rows.
+#include "tile_gemm.cuh"
+
+namespace moe {
+
+cudaError_t launch_hidden_grad(const __nv_bfloat16* d, int64_t d_rows, const __nv_bfloat16* Wd,
+                               int H, int I, bool fp8, int nb, TileArgs a, int num_sms,
+                               cudaStream_t s) {
+    using C = tg::Cfg<tg::kHidden, kWideRows>;
+    tg::Maps m = {};
+    cudaError_t e;
+    if ((e = make_tma_map_bf16(&m.a0, Wd, (uint64_t)a.E * H, I, C::BK)) != cudaSuccess) return e;
+    if ((e = make_tma_map_bf16(&m.b0, d, d_rows, H, nb)) != cudaSuccess) return e;
+    a.n_mtiles = I / 256;
+    a.a_rows = H;
+    a.ld = I;
+    a.k_blocks = H / C::BK;
+    if (nb == kWideRows)
+        return fp8 ? tg::launch<tg::kHiddenFp8, kWideRows>(m, a, num_sms, s)
+                   : tg::launch<tg::kHidden, kWideRows>(m, a, num_sms, s);
+    return fp8 ? tg::launch<tg::kHiddenFp8, kThinRows>(m, a, num_sms, s)
+               : tg::launch<tg::kHidden, kThinRows>(m, a, num_sms, s);
+}
+
+cudaError_t launch_input_grad(const __nv_bfloat16* dg, const __nv_bfloat16* du, int64_t rows,
+                              const __nv_bfloat16* Wg, const __nv_bfloat16* Wu, int H, int I,
+                              int nb, TileArgs a, int num_sms, cudaStream_t s) {
+    using C = tg::Cfg<tg::kInput, kWideRows>;
+    tg::Maps m = {};
+    cudaError_t e;
+    if ((e = make_tma_map_bf16(&m.a0, Wg, (uint64_t)a.E * I, H, C::BK)) != cudaSuccess) return e;
+    if ((e = make_tma_map_bf16(&m.a1, Wu, (uint64_t)a.E * I, H, C::BK)) != cudaSuccess) return e;
+    if ((e = make_tma_map_bf16(&m.b0, dg, rows, I, nb)) != cudaSuccess) return e;
+    if ((e = make_tma_map_bf16(&m.b1, du, rows, I, nb)) != cudaSuccess) return e;
+    a.n_mtiles = H / 256;
+    a.a_rows = I;
+    a.ld = H;
+    a.seg_blocks = I / C::BK;
+    a.k_blocks = 2 * a.seg_blocks;
+    if (nb == kWideRows) return tg::launch<tg::kInput, kWideRows>(m, a, num_sms, s);
+    return tg::launch<tg::kInput, kThinRows>(m, a, num_sms, s);
+}
+
+cudaError_t launch_weight_grad(const __nv_bfloat16* h, const __nv_bfloat16* dg,
+                               const __nv_bfloat16* du, int64_t rows, const __nv_bfloat16* x,
+                               const __nv_bfloat16* d, int64_t xd_rows, int H, int I, TileArgs a,
+                               int num_sms, cudaStream_t s) {
+    using C = tg::Cfg<tg::kWeights, kWideRows>;
+    tg::Maps m = {};
+    cudaError_t e;
+    if ((e = make_tma_map_bf16(&m.a0, h, rows, I, C::BK)) != cudaSuccess) return e;
+    if ((e = make_tma_map_bf16(&m.a1, x, xd_rows, H, C::BK)) != cudaSuccess) return e;
+    if ((e = make_tma_map_bf16(&m.b0, d, xd_rows, H, C::BK)) != cudaSuccess) return e;
+    if ((e = make_tma_map_bf16(&m.b1, dg, rows, I, C::BK)) != cudaSuccess) return e;
+    if ((e = make_tma_map_bf16(&m.b2, du, rows, I, C::BK)) != cudaSuccess) return e;
+    a.n_mtiles = I / 256;
+    a.n_ntiles = H / 256;
+    a.m_total = I;
+    a.n_total = H;
+    return tg::launch<tg::kWeights, kWideRows>(m, a, num_sms, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,41 @@
+// train_fwd.cu -- the training forward pass of the experts on the tile kernel:
+//   gate/up  h = bf16(silu(g) * u), g = x Wg^T and u = x Wu^T kept in bf16 or 8 bits;
+//   down     y = h Wd^T.
+#include "tile_gemm.cuh"
+
+namespace moe {
+
+cudaError_t launch_train_gate_up(const __nv_bfloat16* x, int64_t x_rows, const __nv_bfloat16* Wg,
+                                 const __nv_bfloat16* Wu, int H, int I, bool fp8, int nb,
+                                 TileArgs a, int num_sms, cudaStream_t s) {
+    tg::Maps m = {};
+    cudaError_t e;
+    if ((e = make_tma_map_bf16(&m.a0, Wg, (uint64_t)a.E * I, H, 128)) != cudaSuccess) return e;
+    if ((e = make_tma_map_bf16(&m.a1, Wu, (uint64_t)a.E * I, H, 128)) != cudaSuccess) return e;
+    if ((e = make_tma_map_bf16(&m.b0, x, x_rows, H, nb)) != cudaSuccess) return e;
+    a.n_mtiles = I / 256;
+    a.a_rows = I;
+    a.ld = I;
+    a.k_blocks = H / tg::Cfg<tg::kGated, kWideRows>::BK;
+    if (nb == kWideRows)
+        return fp8 ? tg::launch<tg::kGatedFp8, kWideRows>(m, a, num_sms, s)
+                   : tg::launch<tg::kGated, kWideRows>(m, a, num_sms, s);
+    return fp8 ? tg::launch<tg::kGatedFp8, kThinRows>(m, a, num_sms, s)
+               : tg::launch<tg::kGated, kThinRows>(m, a, num_sms, s);
+}
+
+cudaError_t launch_train_down(const __nv_bfloat16* h, int64_t h_rows, const __nv_bfloat16* Wd,
+                              int H, int I, int nb, TileArgs a, int num_sms, cudaStream_t s) {
+    tg::Maps m = {};
+    cudaError_t e;
+    if ((e = make_tma_map_bf16(&m.a0, Wd, (uint64_t)a.E * H, I, 128)) != cudaSuccess) return e;
+    if ((e = make_tma_map_bf16(&m.b0, h, h_rows, I, nb)) != cudaSuccess) return e;
+    a.n_mtiles = H / 256;
+    a.a_rows = H;
+    a.ld = H;
+    a.k_blocks = I / tg::Cfg<tg::kRows, kWideRows>::BK;
+    if (nb == kWideRows) return tg::launch<tg::kRows, kWideRows>(m, a, num_sms, s);
+    return tg::launch<tg::kRows, kThinRows>(m, a, num_sms, s);
+}
+
+}  // namespace moe
