@@ -515,9 +515,8 @@ moe_status moe_expert_ffn_train(const moe_shape* shape, const moe_bf16* x, const
  *   d_x[t] = sum over t's slots of W_gate^T dg + W_up^T du,
  *   dW_down[e] = sum over e's rows of d (w h)^T,
  *   dW_gate[e] = sum of dg x[t]^T,   dW_up[e] = sum of du x[t]^T.
- * Sums are fp32 in a fixed order (repeated runs give the same bits); dg, du,
- * w h and, with k > 1 or route lists, each slot's part of d_x are rounded to
- * bf16 once.  Every element of the three dW is written, experts without rows
+ * Sums are fp32 in a fixed order (repeated runs give the same bits); dg, du
+ * and w h are rounded to bf16 once, and so is each result but d_gates.  Every element of the three dW is written, experts without rows
  * get zeros.
  *   gates [T, k] fp32 as moe_route wrote them, or NULL: all 1, and d_gates is
  *   NULL too.  d_x [T, H] bf16, d_gates [T, k] fp32 and the dW (bf16, in the

@@ -25,15 +25,12 @@ void take_lists(Carver* c, int64_t rows, int E, int most, Lists* l) {
 }
 
 // The tile kernel's arguments over the lists, or (dense) over one group.
-TileArgs args_of(const Lists& l, bool dense, int64_t rows, int E, int most) {
+TileArgs args_of(const Lists& l, bool dense, int64_t rows, int E) {
     TileArgs a = {};
     a.hdr = l.hdr;
     a.rows = (int)rows;
     a.E = E;
-    if (dense) {
-        a.chunk_rows = chunk_size((int)rows, most);
-        a.dense_chunks = a.chunk_rows ? (int)((rows + a.chunk_rows - 1) / a.chunk_rows) : 0;
-    } else {
+    if (!dense) {
         a.chunks = l.l.chunks;
         a.groups = l.l.groups;
         a.n_chunks = l.l.n_chunks;
@@ -57,7 +54,8 @@ size_t carve_fwd(const moe_shape* sh, void* ws, FwdBufs* b) {
 
 struct BwdBufs {
     Lists l;
-    __nv_bfloat16 *x, *d, *dx;     // padded rows of x and d_out; each slot's part of d_x
+    __nv_bfloat16 *x, *d;          // padded rows of x and d_out
+    float* dx;                     // each slot's part of d_x
     __nv_bfloat16 *h, *dg, *du;    // padded
     float* parts;
 };
@@ -67,7 +65,7 @@ size_t carve_bwd(const moe_shape* sh, void* ws, BwdBufs* b) {
     take_lists(&c, P, sh->E, 2 * rows_per_cta(P, sh->E), &b->l);
     b->x = c.take<__nv_bfloat16>((size_t)(pad * sh->H));
     b->d = c.take<__nv_bfloat16>((size_t)(pad * sh->H));
-    b->dx = c.take<__nv_bfloat16>((size_t)(P * sh->H));
+    b->dx = c.take<float>((size_t)(P * sh->H));
     b->h = c.take<__nv_bfloat16>((size_t)(pad * sh->I));
     b->dg = c.take<__nv_bfloat16>((size_t)(pad * sh->I));
     b->du = c.take<__nv_bfloat16>((size_t)(pad * sh->I));
@@ -152,7 +150,7 @@ moe_status moe_expert_ffn_train(const moe_shape* shape, const moe_bf16* x, const
         CUDA_TRY(launch_gather_rows(g, b.l.l, max_chunks(P, E, most), most, sms, s), "gather");
         xs = b.xs;
     }
-    TileArgs a = args_of(b.l, dense, P, E, most);
+    TileArgs a = args_of(b.l, dense, P, E);
     a.out = b.h;
     a.gate = saved->gate;
     a.up = saved->up;
@@ -223,7 +221,7 @@ moe_status moe_expert_ffn_backward(const moe_shape* shape, const moe_bf16* d_out
                  "dequantize rows");
         x = b.x;
     }
-    TileArgs a = args_of(b.l, dense, P, E, most);
+    TileArgs a = args_of(b.l, dense, P, E);
     a.padded = !dense;
     a.gate = saved->gate;
     a.up = saved->up;
@@ -240,7 +238,8 @@ moe_status moe_expert_ffn_backward(const moe_shape* shape, const moe_bf16* d_out
     if (d_gates)
         CUDA_TRY(launch_sum_gate_parts(b.parts, I / 32, (int)P, inv_perm, d_gates, s), "gradient of the gates");
     if (d_x) {
-        a.out = dense ? (__nv_bfloat16*)d_x : b.dx;
+        a.out = dense ? (__nv_bfloat16*)d_x : nullptr;
+        a.out32 = dense ? nullptr : b.dx;
         CUDA_TRY(launch_input_grad(b.dg, b.du, pad, (const __nv_bfloat16*)W_gate,
                                    (const __nv_bfloat16*)W_up, H, I, nb, a, sms, s), "gradient of x");
         if (!dense)
@@ -298,12 +297,13 @@ moe_status moe_grouped_gemm(const moe_bf16* x, int32_t rows, const int32_t* offs
     const int nb = rows_per_cta(rows, E), most = 2 * nb;
     const PdlScope pdl(rows <= kPermChunk);
     if (offsets) CUDA_TRY(launch_plan_rows(offsets, rows, E, most, l.l, l.hdr, s), "plan");
-    TileArgs a = args_of(l, !offsets, rows, E, most);
+    TileArgs a = args_of(l, !offsets, rows, E);
     a.out = y_fp32 ? nullptr : (__nv_bfloat16*)y;
     a.out32 = y_fp32 ? (float*)y : nullptr;
     a.bias = bias;
     a.residual = (const __nv_bfloat16*)residual;
     a.act = activation;
+    a.vec = N % 8 == 0 && aligned(residual, 16);
     CUDA_TRY(launch_product((const __nv_bfloat16*)x, rows, (const __nv_bfloat16*)W, N, K, nb, a, sms, s),
              "product");
     return ok();

@@ -47,6 +47,7 @@ using namespace tc;
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kTileFeatures = 256;   // features per item (both CTAs)
+constexpr int kTileBytes = 32 * 64;  // a staging tile
 
 // What an item computes, and what its epilogue does with it.
 enum Kind {
@@ -76,13 +77,17 @@ struct Cfg {
     static constexpr int A_BYTES = MT * A_SUB;
     static constexpr int B_BYTES = NB * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = (200 * 1024) / STAGE_BYTES < 8 ? (200 * 1024) / STAGE_BYTES : 8;
+    static constexpr int STAGES = (192 * 1024) / STAGE_BYTES < 8 ? (192 * 1024) / STAGE_BYTES : 8;
     static constexpr int ACC_COLS = MT * BN;          // TMEM columns of one accumulator set
     static constexpr int BUFS = 2 * ACC_COLS <= 512 ? 2 : 1;
     static constexpr int TMEM_COLS = BUFS * ACC_COLS;
+    // staging tiles of an epilogue warp (32 rows x 32 features, bf16)
+    static constexpr int TILES = kKind == kGated || hidden(kKind) ? 2 : 1;
+    static constexpr int STAGING_BYTES = kEpiWarps * TILES * kTileBytes;
     // block maxima of the 8-bit epilogue: [half][parity][gate, up][4 warps][32 rows]
     static constexpr int AMAX_BYTES = kKind == kGatedFp8 ? 2 * 2 * 2 * 4 * 32 * 4 : 0;
-    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + AMAX_BYTES + 1024 /*align*/ + 512 /*barriers*/;
+    static constexpr int SMEM_BYTES =
+        STAGES * STAGE_BYTES + STAGING_BYTES + AMAX_BYTES + 1024 /*align*/ + 512 /*barriers*/;
     static_assert(STAGES >= 2 && SMEM_BYTES <= 227 * 1024);
     static_assert(TMEM_COLS >= 32 && (TMEM_COLS & (TMEM_COLS - 1)) == 0);
 };
@@ -169,111 +174,341 @@ __device__ __forceinline__ Item item_of(const TileArgs& a, int w) {
     return it;
 }
 
-// Sums of 32 values per lane over the lanes: lane l gets the sum of v[l].
-__device__ __forceinline__ float lane_sums(float (&v)[32], int lane) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int i = 0; i < o; ++i) {
-            const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-        }
-    }
-    return v[0];
-}
-
-// e4m3 byte -> fp32 (exact).
-__device__ __forceinline__ float from_e4m3(uint32_t b) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)b));
-    return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
-}
 // 2^(b - 127); byte 255 stands for NaN.
 __device__ __forceinline__ float scale_value(uint32_t b) {
     return __uint_as_float(b == 0 ? 1u << 22 : b == 255 ? 0x7fc00000u : b << 23);
 }
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+__device__ __forceinline__ float2 unpack(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
+// ---- fragments and staging tiles --------------------------------------------
+//
+// An epilogue warp takes 32 features x 32 rows at a time.  It reads them from
+// TMEM in the layout of 8 x 8 matrix fragments: lane t holds, for feature
+// 8 i + t / 4 and row 8 j + 2 (t mod 4) + s, value [i][j][s].  Rounded to bf16
+// and packed by s, a fragment is what stmatrix/ldmatrix with .trans exchange
+// with a shared tile of 32 rows x 32 features: 4 instructions instead of 32
+// two-byte accesses.  From the tile, four lanes copy a row's 64 bytes to or
+// from global memory in 16-byte vectors.  16-byte chunk c of row r lies at
+// chunk c ^ (r / 2 mod 4) of the row, so that neither side meets bank
+// conflicts.  (Loading the residual of a 16384 x 4096 x 4096 product two bytes
+// per lane, 64 bytes per instruction, took 280 us more than its 295.)
+struct Frag {
+    float v[4][4][2];
+};
+struct Packed {
+    uint32_t v[4][4];
+};
 
-// ---- epilogues: one 32-column block of one warp ----------------------------
-// f: this lane's feature; c0: first column; the columns are rows row0 + c.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&r)[2][4][2]) {
+    uint32_t v[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) r[q >> 1][j][q & 1] = __uint_as_float(v[4 * j + q]);
+}
+// 32 lanes x 32 columns at taddr; complete after tmem_ld_wait().
+__device__ __forceinline__ void load_frag(uint32_t taddr, Frag& f) {
+    tmem_ld_frag(taddr, *reinterpret_cast<float(*)[2][4][2]>(&f.v[0]));
+    tmem_ld_frag(taddr + (16u << 16), *reinterpret_cast<float(*)[2][4][2]>(&f.v[2]));
+}
 
+__device__ __forceinline__ Packed pack(const Frag& f) {
+    Packed p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p.v[i][j] = pack_bf16(f.v[i][j][0], f.v[i][j][1]);
+    return p;
+}
+
+__device__ __forceinline__ uint32_t tile_at(uint32_t tile, int row, int chunk) {
+    return tile + (uint32_t)row * 64u + (uint32_t)((chunk ^ (row >> 1)) & 3) * 16u;
+}
+__device__ __forceinline__ void frag_to_tile(uint32_t tile, const Packed& p, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                         tile_at(tile, 8 * j + (lane & 7), lane >> 3)),
+                     "r"(p.v[0][j]), "r"(p.v[1][j]), "r"(p.v[2][j]), "r"(p.v[3][j])
+                     : "memory");
+}
+__device__ __forceinline__ void tile_to_frag(uint32_t tile, Packed& p, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(p.v[0][j]), "=r"(p.v[1][j]), "=r"(p.v[2][j]), "=r"(p.v[3][j])
+                     : "r"(tile_at(tile, 8 * j + (lane & 7), lane >> 3))
+                     : "memory");
+}
+__device__ __forceinline__ uint4 tile_vec(uint32_t tile, int row, int chunk) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(tile_at(tile, row, chunk))
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void tile_put(uint32_t tile, int row, int chunk, const uint4& v) {
+    st_shared_v4(tile_at(tile, row, chunk), v.x, v.y, v.z, v.w);
+}
+
+// The tile's first `left` rows to out (feature 0 of row 0; 16-byte aligned
+// rows of ld values), by the whole warp.
+__device__ __forceinline__ void tile_to_rows(uint32_t tile, __nv_bfloat16* out, int64_t ld, int left,
+                                             int lane) {
+    __nv_bfloat16* o = out + (int64_t)(lane >> 2) * ld + (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 8 * i + (lane >> 2);
+        const uint4 v = tile_vec(tile, row, lane & 3);
+        if (row < left) *reinterpret_cast<uint4*>(o) = v;
+        o += 8 * ld;
+    }
+}
+// Packed fragment -> rows, through the tile.
+__device__ __forceinline__ void store_packed(uint32_t tile, const Packed& p, __nv_bfloat16* out,
+                                             int64_t ld, int left, int lane) {
+    __syncwarp();                       // what the tile held before has been read
+    frag_to_tile(tile, p, lane);
+    __syncwarp();
+    tile_to_rows(tile, out, ld, left, lane);
+}
+
+// Rows of a bf16 tensor on their way into a tile: loaded ahead, put later.
+struct RowVecs {
+    uint4 v[4];
+};
+__device__ __forceinline__ void load_rows(RowVecs& r, const __nv_bfloat16* in, int64_t ld, int left,
+                                          int lane) {
+    const __nv_bfloat16* p = in + (int64_t)(lane >> 2) * ld + (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r.v[i] = make_uint4(0, 0, 0, 0);
+        if (8 * i + (lane >> 2) < left) r.v[i] = *reinterpret_cast<const uint4*>(p);
+        p += 8 * ld;
+    }
+}
+__device__ __forceinline__ void put_rows(uint32_t tile, const RowVecs& r, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tile_put(tile, 8 * i + (lane >> 2), lane & 3, r.v[i]);
+}
+// The same for rows of e4m3 with a scale per 128 features (two lanes a row).
+struct RowBytes {
+    uint4 v[2];
+    uint32_t scale;      // of rows lane / 2 and 16 + lane / 2, a byte each
+};
+__device__ __forceinline__ void load_rows(RowBytes& r, const uint8_t* in, const uint8_t* scales,
+                                          int64_t ld, int left, int lane) {
+    r.scale = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = 16 * i + (lane >> 1);
+        r.v[i] = make_uint4(0, 0, 0, 0);
+        if (row < left) {
+            r.v[i] = *reinterpret_cast<const uint4*>(in + (int64_t)row * ld + (lane & 1) * 16);
+            r.scale |= (uint32_t)scales[(int64_t)row * (ld / 128)] << (8 * i);
+        }
+    }
+}
+__device__ __forceinline__ void put_rows(uint32_t tile, const RowBytes& r, int lane) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float s = scale_value((r.scale >> (8 * i)) & 0xffu);
+        const uint32_t w[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            uint32_t h;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[q >> 1] >> (16 * (q & 1)))));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            o[q] = pack_bf16(f.x * s, f.y * s);
+        }
+        const int row = 16 * i + (lane >> 1), c = (lane & 1) * 2;
+        tile_put(tile, row, c, make_uint4(o[0], o[1], o[2], o[3]));
+        tile_put(tile, row, c + 1, make_uint4(o[4], o[5], o[6], o[7]));
+    }
+}
+
+// Sums over the 32 features of one value per row: v[j][s] are this lane's
+// sums of row 8 j + 2 (t mod 4) + s.  Each lane gets the sum of one row, whose
+// number is returned in *row.
+__device__ __forceinline__ float feature_sums(float (&v)[4][2], int lane, int* row) {
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = v[i >> 1][i & 1];
+#pragma unroll
+    for (int o = 16, n = 4; o >= 4; o >>= 1, n >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float keep = up ? w[i + n] : w[i], send = up ? w[i] : w[i + n];
+            w[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    // lane bit 4 chose the upper half of j, bit 3 the lower bit of j, bit 2 s
+    *row = ((lane >> 4) & 1) * 16 + ((lane >> 3) & 1) * 8 + (lane & 3) * 2 + ((lane >> 2) & 1);
+    return w[0];
+}
+
+// ---- epilogues: one warp's 32 features from f0, 32 rows from c0 ---------------
+
+struct Warp {
+    int lane, quad;
+    uint32_t tile;        // staging tiles
+    uint32_t* amax;       // 8-bit epilogue: this block's maxima [gate, up][4 warps][32 rows]
+    int bar_id;
+};
+
+// h = silu(g) u, with g and u kept.
 template <int kKind>
-__device__ __forceinline__ void store_gated(const TileArgs& a, const Item& it, int f, int c0,
-                                            int lane, const uint32_t (&g)[32],
-                                            const uint32_t (&u)[32], uint32_t* amax, int quad,
-                                            int bar_id) {
-    const int left = it.rows - c0;                        // valid columns of the block
-    const int64_t at = (int64_t)(it.row0 + c0) * a.ld + f;
-    __nv_bfloat16* h = a.out + at;
+__device__ __forceinline__ void store_gated(const TileArgs& a, const Item& it, int f0, int c0,
+                                            const Frag& g, const Frag& u, const Warp& w) {
+    const int left = it.rows - c0, lane = w.lane;
+    const int64_t at = (int64_t)(it.row0 + c0) * a.ld + f0;
+    Packed h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            h.v[i][j] = pack_bf16(g.v[i][j][0] * sigmoid(g.v[i][j][0]) * u.v[i][j][0],
+                                  g.v[i][j][1] * sigmoid(g.v[i][j][1]) * u.v[i][j][1]);
     if constexpr (kKind == kGated) {
-        __nv_bfloat16 *kg = static_cast<__nv_bfloat16*>(a.gate) + at,
-                      *ku = static_cast<__nv_bfloat16*>(a.up) + at;
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-            if (c < left) {
-                const float gv = __uint_as_float(g[c]), uv = __uint_as_float(u[c]);
-                const int64_t o = (int64_t)c * a.ld;
-                h[o] = __float2bfloat16_rn(swiglu(gv, uv));
-                kg[o] = __float2bfloat16_rn(gv);
-                ku[o] = __float2bfloat16_rn(uv);
-            }
-        }
+        store_packed(w.tile, h, a.out + at, a.ld, left, lane);
+        store_packed(w.tile + kTileBytes, pack(g), static_cast<__nv_bfloat16*>(a.gate) + at, a.ld, left, lane);
+        store_packed(w.tile, pack(u), static_cast<__nv_bfloat16*>(a.up) + at, a.ld, left, lane);
     } else {
-        // The block's scale covers 128 features: the four warps of the CTA's
-        // 128 lanes exchange their maxima through shared memory.
-        uint32_t mg = 0, mu = 0;                          // of column `lane`
+        // The block's scale covers 128 features: each lane takes the maxima of
+        // its features, the eight lanes of a row then theirs, and the four
+        // warps of the CTA's 128 lanes exchange them through shared memory.
+        uint32_t m[2][8];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-            const uint32_t bg = __float_as_uint(fp8::finite_abs(__uint_as_float(g[c]))),
-                           bu = __float_as_uint(fp8::finite_abs(__uint_as_float(u[c])));
-            const uint32_t wg = __reduce_max_sync(0xffffffffu, bg),
-                           wu = __reduce_max_sync(0xffffffffu, bu);
-            if (lane == c) {
-                mg = wg;
-                mu = wu;
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                float mg = 0.f, mu = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mg = fmaxf(mg, fp8::finite_abs(g.v[i][j][s]));
+                    mu = fmaxf(mu, fp8::finite_abs(u.v[i][j][s]));
+                }
+                m[0][2 * j + s] = __float_as_uint(mg);      // magnitudes: ordered as integers
+                m[1][2 * j + s] = __float_as_uint(mu);
             }
+#pragma unroll
+        for (int o = 16, n = 4; o >= 4; o >>= 1, n >>= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const uint32_t keep = up ? m[z][i + n] : m[z][i], send = up ? m[z][i] : m[z][i + n];
+                    m[z][i] = max(keep, __shfl_xor_sync(0xffffffffu, send, o));
+                }
         }
-        amax[quad * 32 + lane] = mg;
-        amax[128 + quad * 32 + lane] = mu;
-        asm volatile("bar.sync %0, 128;" ::"r"(bar_id) : "memory");
+        const int row = ((lane >> 4) & 1) * 16 + ((lane >> 3) & 1) * 8 + (lane & 3) * 2 + ((lane >> 2) & 1);
+        w.amax[w.quad * 32 + row] = m[0][0];
+        w.amax[128 + w.quad * 32 + row] = m[1][0];
+        asm volatile("bar.sync %0, 128;" ::"r"(w.bar_id) : "memory");
+        uint32_t mg = 0, mu = 0;                          // of row c0 + lane
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            mg = max(mg, amax[q * 32 + lane]);
-            mu = max(mu, amax[128 + q * 32 + lane]);
+            mg = max(mg, w.amax[q * 32 + lane]);
+            mu = max(mu, w.amax[128 + q * 32 + lane]);
         }
         const uint32_t sg = fp8::scale_byte(__uint_as_float(mg)),
                        su = fp8::scale_byte(__uint_as_float(mu));
-        if (quad == 0 && lane < left) {
-            const int64_t s = (int64_t)(it.row0 + c0 + lane) * (a.ld / 128) + (f >> 7);
+        if (w.quad == 0 && lane < left) {
+            const int64_t s = (int64_t)(it.row0 + c0 + lane) * (a.ld / 128) + (f0 >> 7);
             a.gate_scales[s] = (uint8_t)sg;
             a.up_scales[s] = (uint8_t)su;
         }
         const float ig = fp8::inverse_scale(sg), iu = fp8::inverse_scale(su);
-        uint8_t *kg = static_cast<uint8_t*>(a.gate) + at, *ku = static_cast<uint8_t*>(a.up) + at;
+        Packed q;      // per value a byte of the gate and one of the up projection
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-            const float gv = __uint_as_float(g[c]), uv = __uint_as_float(u[c]);
-            const float xg = __shfl_sync(0xffffffffu, ig, c), xu = __shfl_sync(0xffffffffu, iu, c);
-            if (c < left) {
-                const uint32_t p = fp8::pack_e4m3x2(fp8::scaled(gv, xg), fp8::scaled(uv, xu));
-                const int64_t o = (int64_t)c * a.ld;
-                h[o] = __float2bfloat16_rn(swiglu(gv, uv));
-                kg[o] = (uint8_t)(p & 0xffu);
-                ku[o] = (uint8_t)(p >> 8);
+        for (int j = 0; j < 4; ++j) {
+            uint32_t b[2][4];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int r = 8 * j + 2 * (lane & 3) + s;
+                const float xg = __shfl_sync(0xffffffffu, ig, r), xu = __shfl_sync(0xffffffffu, iu, r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    b[s][i] = fp8::pack_e4m3x2(fp8::scaled(g.v[i][j][s], xg), fp8::scaled(u.v[i][j][s], xu));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q.v[i][j] = b[0][i] | b[1][i] << 16;
+        }
+        store_packed(w.tile, h, a.out + at, a.ld, left, lane);
+        __syncwarp();
+        frag_to_tile(w.tile, q, lane);
+        __syncwarp();
+        // two lanes a row, 16 features each: the gate's bytes and the up's
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 16 * i + (lane >> 1), c = (lane & 1) * 2;
+            const uint4 lo = tile_vec(w.tile, r, c), hi = tile_vec(w.tile, r, c + 1);
+            if (r < left) {
+                const int64_t to = at + (int64_t)r * a.ld + c * 8;
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.gate) + to) =
+                    make_uint4(__byte_perm(lo.x, lo.y, 0x6420), __byte_perm(lo.z, lo.w, 0x6420),
+                               __byte_perm(hi.x, hi.y, 0x6420), __byte_perm(hi.z, hi.w, 0x6420));
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.up) + to) =
+                    make_uint4(__byte_perm(lo.x, lo.y, 0x7531), __byte_perm(lo.z, lo.w, 0x7531),
+                               __byte_perm(hi.x, hi.y, 0x7531), __byte_perm(hi.z, hi.w, 0x7531));
             }
         }
     }
 }
 
-__device__ __forceinline__ void store_rows(const TileArgs& a, const Item& it, int f, int c0,
-                                           const uint32_t (&v)[32]) {
-    const int left = it.rows - c0;
-    __nv_bfloat16* y = a.out + (int64_t)(it.row0 + c0) * a.ld + f;
+// fp32 rows straight from the fragment: eight lanes store 32 bytes of a row.
+__device__ __forceinline__ void store_f32(float* out, int64_t ld, const Frag& f, int left, int feats,
+                                          int lane) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c)
-        if (c < left) y[(int64_t)c * a.ld] = __float2bfloat16_rn(__uint_as_float(v[c]));
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int r = 8 * j + 2 * (lane & 3) + s;
+            float* o = out + (int64_t)r * ld + (lane >> 2);
+            if (r < left) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (8 * i + (lane >> 2) < feats) o[8 * i] = f.v[i][j][s];
+            }
+        }
+}
+
+// What a hidden block reads, loaded a block ahead.
+template <int kKind>
+struct KeptRows {
+    RowVecs g, u;
+};
+template <>
+struct KeptRows<kHiddenFp8> {
+    RowBytes g, u;
+};
+template <int kKind>
+__device__ __forceinline__ void load_kept(KeptRows<kKind>& k, const TileArgs& a, const Item& it, int f0,
+                                          int c0, int lane) {
+    const int left = it.rows - c0;
+    const int64_t at = (int64_t)(it.row0 + c0) * a.ld + f0;
+    if constexpr (kKind == kHidden) {
+        load_rows(k.g, static_cast<const __nv_bfloat16*>(a.gate) + at, a.ld, left, lane);
+        load_rows(k.u, static_cast<const __nv_bfloat16*>(a.up) + at, a.ld, left, lane);
+    } else if constexpr (kKind == kHiddenFp8) {
+        const int64_t s = (int64_t)(it.row0 + c0) * (a.ld / 128) + (f0 >> 7);
+        load_rows(k.g, static_cast<const uint8_t*>(a.gate) + at, a.gate_scales + s, a.ld, left, lane);
+        load_rows(k.u, static_cast<const uint8_t*>(a.up) + at, a.up_scales + s, a.ld, left, lane);
+    }
 }
 
 // With q = d Wd (this accumulator), s = sigmoid(g), w the row's gate:
@@ -281,104 +516,144 @@ __device__ __forceinline__ void store_rows(const TileArgs& a, const Item& it, in
 //   d_gate = sum_i q_i h_i  (a part of it here: this warp's 32 features).
 // dg, du and w h are rounded to bf16, the operands of the next products.
 template <int kKind>
-__device__ __forceinline__ void store_hidden(const TileArgs& a, const Item& it, int f, int c0,
-                                             int lane, const uint32_t (&v)[32]) {
-    const int left = it.rows - c0, pad = it.n - c0;
-    const int64_t at = (int64_t)(it.row0 + c0) * a.ld + f;
-    float g[32], u[32];
-    if constexpr (kKind == kHidden) {
-        const __nv_bfloat16 *kg = static_cast<const __nv_bfloat16*>(a.gate) + at,
-                            *ku = static_cast<const __nv_bfloat16*>(a.up) + at;
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-            g[c] = c < left ? __bfloat162float(kg[(int64_t)c * a.ld]) : 0.f;
-            u[c] = c < left ? __bfloat162float(ku[(int64_t)c * a.ld]) : 0.f;
-        }
-    } else {
-        const uint8_t *kg = static_cast<const uint8_t*>(a.gate) + at,
-                      *ku = static_cast<const uint8_t*>(a.up) + at;
-        float sg = 0.f, su = 0.f;
-        if (lane < left) {
-            const int64_t s = (int64_t)(it.row0 + c0 + lane) * (a.ld / 128) + (f >> 7);
-            sg = scale_value(a.gate_scales[s]);
-            su = scale_value(a.up_scales[s]);
-        }
-        uint32_t bg[32], bu[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-            bg[c] = c < left ? kg[(int64_t)c * a.ld] : 0u;
-            bu[c] = c < left ? ku[(int64_t)c * a.ld] : 0u;
-        }
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-            g[c] = from_e4m3(bg[c]) * __shfl_sync(0xffffffffu, sg, c);
-            u[c] = from_e4m3(bu[c]) * __shfl_sync(0xffffffffu, su, c);
-        }
-    }
+__device__ __forceinline__ void store_hidden(const TileArgs& a, const Item& it, int f0, int c0,
+                                             const Frag& q, const Packed& kg, const Packed& ku,
+                                             const Warp& wp) {
+    const int left = it.rows - c0, pad = it.n - c0, lane = wp.lane;
     float w = 1.f;
     if (a.gates && lane < left) {
         const int r = it.row0 + c0 + lane, slot = a.perm ? a.perm[r] : r;
         w = slot >= 0 && slot < a.rows ? a.gates[slot] : 0.f;
     }
-    const int64_t to = (int64_t)(it.row0_pad + c0) * a.ld + f;
-    __nv_bfloat16 *dg = a.d_gate + to, *du = a.d_up + to, *ho = a.out + to;
-    float part[32];
+    Packed dg, du, ho;
+    float part[4][2] = {};
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-        const float wc = __shfl_sync(0xffffffffu, w, c);
-        const float q = __uint_as_float(v[c]), s = sigmoid(g[c]);
-        const float gs = g[c] * s, h = gs * u[c], dh = wc * q;
-        part[c] = c < left ? q * h : 0.f;
-        if (c < pad) {
-            const int64_t o = (int64_t)c * a.ld;
-            const bool in = c < left;          // rows up to the next multiple of 16 are zero
-            dg[o] = __float2bfloat16_rn(in ? dh * u[c] * s * (1.f + g[c] * (1.f - s)) : 0.f);
-            du[o] = __float2bfloat16_rn(in ? dh * gs : 0.f);
-            ho[o] = __float2bfloat16_rn(in ? wc * h : 0.f);
+    for (int j = 0; j < 4; ++j) {
+        float wr[2];
+        bool in[2];      // rows up to the next multiple of 16 are zero
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int r = 8 * j + 2 * (lane & 3) + s;
+            wr[s] = __shfl_sync(0xffffffffu, w, r);
+            in[s] = r < left;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 g2 = unpack(kg.v[i][j]), u2 = unpack(ku.v[i][j]);
+            float og[2], ou[2], oh[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const float g = s ? g2.y : g2.x, u = s ? u2.y : u2.x, qv = q.v[i][j][s];
+                const float sg = sigmoid(g), gs = g * sg, h = gs * u, dh = wr[s] * qv;
+                if (in[s]) part[j][s] = fmaf(qv, h, part[j][s]);
+                og[s] = in[s] ? dh * u * sg * fmaf(g, 1.f - sg, 1.f) : 0.f;
+                ou[s] = in[s] ? dh * gs : 0.f;
+                oh[s] = in[s] ? wr[s] * h : 0.f;
+            }
+            dg.v[i][j] = pack_bf16(og[0], og[1]);
+            du.v[i][j] = pack_bf16(ou[0], ou[1]);
+            ho.v[i][j] = pack_bf16(oh[0], oh[1]);
         }
     }
+    const int64_t to = (int64_t)(it.row0_pad + c0) * a.ld + f0;
+    store_packed(wp.tile, dg, a.d_gate + to, a.ld, pad, lane);
+    store_packed(wp.tile + kTileBytes, du, a.d_up + to, a.ld, pad, lane);
+    store_packed(wp.tile, ho, a.out + to, a.ld, pad, lane);
     if (a.gate_parts) {
-        const float sum = lane_sums(part, lane);
-        if (lane < left)
-            a.gate_parts[(int64_t)(f >> 5) * a.rows + it.row0 + c0 + lane] = sum;
+        int r;
+        const float sum = feature_sums(part, lane, &r);
+        if (r < left) a.gate_parts[(int64_t)(f0 >> 5) * a.rows + it.row0 + c0 + r] = sum;
     }
 }
 
-__device__ __forceinline__ void store_weights(const TileArgs& a, const Item& it, int f, int c0,
-                                              const uint32_t (&v)[32]) {
+__device__ __forceinline__ void store_weights(const TileArgs& a, const Item& it, int f0, int c0,
+                                              const Frag& v, const Warp& w) {
     const int64_t ld = it.mat == 0 ? a.m_total : a.n_total;      // I, H
     const int64_t rows = it.mat == 0 ? a.n_total : a.m_total;    // H, I
     __nv_bfloat16* W = it.mat == 0 ? a.out : it.mat == 1 ? a.d_gate : a.d_up;
-    W += ((int64_t)it.expert * rows + it.n0 + c0) * ld + f;
-#pragma unroll
-    for (int c = 0; c < 32; ++c) W[(int64_t)c * ld] = __float2bfloat16_rn(__uint_as_float(v[c]));
+    store_packed(w.tile, pack(v), W + ((int64_t)it.expert * rows + it.n0 + c0) * ld + f0, ld, 32, w.lane);
 }
 
-__device__ __forceinline__ float activate(float v, int act) {
-    switch (act) {
-        case MOE_ACT_RELU: return v < 0.f ? 0.f : v;       // NaN stays
-        case MOE_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-        case MOE_ACT_SILU: return v * sigmoid(v);
-        default: return v;
+__device__ __forceinline__ void activate(Frag& f, int act) {
+    float* v = &f.v[0][0][0];
+    if (act == MOE_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];       // NaN stays
+    } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.5f * v[i] * (1.f + erff(v[i] * 0.70710678118654752f));
+    } else if (act == MOE_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= sigmoid(v[i]);
     }
 }
 
-__device__ __forceinline__ void store_product(const TileArgs& a, const Item& it, int f, int c0,
-                                              const uint32_t (&v)[32]) {
-    const int left = it.rows - c0;
-    if (f >= a.m_total) return;
-    const float bias = a.bias ? a.bias[(int64_t)it.expert * a.m_total + f] : 0.f;
-    const int64_t at = (int64_t)(it.row0 + c0) * a.ld + f;
-    float r[32];
+// What a product block adds: its residual, loaded a block ahead where rows
+// are 16-byte aligned (a.vec).
+__device__ __forceinline__ void load_residual(RowVecs& r, const TileArgs& a, const Item& it, int f0,
+                                              int c0, int lane) {
+    const int left = f0 + (lane & 3) * 8 < a.m_total ? it.rows - c0 : 0;
+    load_rows(r, a.residual + (int64_t)(it.row0 + c0) * a.ld + f0, a.ld, left, lane);
+}
+__device__ __forceinline__ void store_product(const TileArgs& a, const Item& it, int f0, int c0, Frag& v,
+                                              const RowVecs& res, const Warp& w) {
+    const int left = it.rows - c0, lane = w.lane, feats = a.m_total - f0;
+    const int64_t at = (int64_t)(it.row0 + c0) * a.ld + f0;
+    if (a.bias) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c)
-        r[c] = a.residual && c < left ? __bfloat162float(a.residual[at + (int64_t)c * a.ld]) : 0.f;
+        for (int i = 0; i < 4; ++i) {
+            const int f = 8 * i + (lane >> 2);
+            const float b = f < feats ? a.bias[(int64_t)it.expert * a.m_total + f0 + f] : 0.f;
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-        if (c < left) {
-            const float y = activate(__uint_as_float(v[c]) + bias, a.act) + r[c];
-            if (a.out32) a.out32[at + (int64_t)c * a.ld] = y;
-            else a.out[at + (int64_t)c * a.ld] = __float2bfloat16_rn(y);
+            for (int j = 0; j < 4; ++j) {
+                v.v[i][j][0] += b;
+                v.v[i][j][1] += b;
+            }
+        }
+    }
+    activate(v, a.act);
+    if (a.residual) {
+        __syncwarp();
+        if (a.vec) {
+            put_rows(w.tile, res, lane);
+        } else if (lane < feats) {
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r) {
+                uint16_t x = 0;
+                if (r < left) x = *reinterpret_cast<const uint16_t*>(a.residual + at + (int64_t)r * a.ld + lane);
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile_at(w.tile, r, lane >> 3) + (lane & 7) * 2), "h"(x)
+                             : "memory");
+            }
+        }
+        __syncwarp();
+        Packed p;
+        tile_to_frag(w.tile, p, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = unpack(p.v[i][j]);
+                v.v[i][j][0] += x.x;
+                v.v[i][j][1] += x.y;
+            }
+    }
+    if (a.out32) {
+        store_f32(a.out32 + at, a.ld, v, left, feats, lane);
+        return;
+    }
+    if (a.vec) {
+        store_packed(w.tile, pack(v), a.out + at, a.ld, (lane & 3) * 8 < feats ? left : 0, lane);
+        return;
+    }
+    __syncwarp();
+    frag_to_tile(w.tile, pack(v), lane);
+    __syncwarp();
+    if (lane < feats) {
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r) {
+            uint16_t x;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(tile_at(w.tile, r, lane >> 3) + (lane & 7) * 2) : "memory");
+            if (r < left) *reinterpret_cast<uint16_t*>(a.out + at + (int64_t)r * a.ld + lane) = x;
         }
     }
 }
@@ -400,15 +675,15 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* base_ptr = smem_raw + (base - raw);
-    uint32_t* amax_all = reinterpret_cast<uint32_t*>(base_ptr + C::STAGES * C::STAGE_BYTES);
-    const uint32_t bars = base + C::STAGES * C::STAGE_BYTES + C::AMAX_BYTES;
+    constexpr int kStagingAt = C::STAGES * C::STAGE_BYTES, kAmaxAt = kStagingAt + C::STAGING_BYTES,
+                  kBarsAt = kAmaxAt + C::AMAX_BYTES;
+    const uint32_t bars = base + kBarsAt;
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
     auto tfull_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + b); };
     auto tempty_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + 2 + b); };
     const uint32_t done_bar = bars + 8u * (2 * C::STAGES + 4);
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(
-        base_ptr + C::STAGES * C::STAGE_BYTES + C::AMAX_BYTES + 8 * (2 * C::STAGES + 5));
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + kBarsAt + 8 * (2 * C::STAGES + 5));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     int* fills_out = reinterpret_cast<int*>(tmem_holder + 2);
 
@@ -584,13 +859,23 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
     } else if (warp >= 4) {
         // ---------------- epilogue (both CTAs) ----------------
         const int quad = warp & 3;            // TMEM lanes 32*quad .. 32*quad+31
-        const int half = (warp - 4) >> 2;     // which 32-column blocks
+        const int half = (warp - 4) >> 2;     // which 32-row blocks
+        uint32_t* amax = reinterpret_cast<uint32_t*>(base_ptr + kAmaxAt) + half * 512;
+        Warp wp = {lane, quad, base + kStagingAt + (uint32_t)(warp - 4) * C::TILES * kTileBytes, amax, 1 + half};
         const uint32_t tempty0 = mapa_shared(tempty_bar(0), 0);
         int i = 0;
         for (int w = cluster; w < total; w += n_clusters, ++i) {
             const Item it = item_of<kKind, C>(args, w);
             const int acc = i % C::BUFS;
             const uint32_t acc_phase = (uint32_t)((i / C::BUFS) & 1);
+            const int f0 = it.m0 + (int)rank * 128 + quad * 32;
+            const bool live = kKind != kProduct || f0 < args.m_total;
+            // what the first block reads does not wait for the products
+            [[maybe_unused]] KeptRows<kKind> kept;
+            [[maybe_unused]] RowVecs res;
+            if constexpr (hidden(kKind)) load_kept<kKind>(kept, args, it, f0, 32 * half, lane);
+            if constexpr (kKind == kProduct)
+                if (live && args.residual && args.vec) load_residual(res, args, it, f0, 32 * half, lane);
             bool ok = __all_sync(0xffffffffu, mbar_wait_for(tfull_bar(acc), acc_phase, args.wait_cycles, abort_flag));
             if constexpr (kKind == kGatedFp8) {
                 // the four warps that exchange maxima go on together or not at all
@@ -601,7 +886,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                     "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
                     "selp.u32 %0, 1, 0, q;\n\t}"
                     : "=r"(all)
-                    : "r"((uint32_t)ok), "r"(1 + half)
+                    : "r"((uint32_t)ok), "r"(wp.bar_id)
                     : "memory");
                 ok = all != 0;
             }
@@ -610,30 +895,49 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                 break;
             }
             fence_after();
-            const int f = it.m0 + (int)rank * 128 + quad * 32 + lane;
             const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * C::ACC_COLS);
+            const int n = live ? it.n : 0;
 #pragma unroll 1
-            for (int c0 = 32 * half; c0 < it.n; c0 += 64) {
-                uint32_t v[32];
+            for (int c0 = 32 * half; c0 < n; c0 += 64) {
+                Frag v;
                 if constexpr (gated(kKind)) {
-                    uint32_t u[32];
-                    tmem_ld32(taddr + c0, v);
-                    tmem_ld32(taddr + C::BN + c0, u);
+                    Frag u;
+                    load_frag(taddr + c0, v);
+                    load_frag(taddr + C::BN + c0, u);
                     tmem_ld_wait();
-                    store_gated<kKind>(args, it, f, c0, lane, v, u,
-                                       amax_all + half * 512 + ((c0 >> 6) & 1) * 256, quad, 1 + half);
+                    wp.amax = amax + ((c0 >> 6) & 1) * 256;
+                    store_gated<kKind>(args, it, f0, c0, v, u, wp);
+                } else if constexpr (hidden(kKind)) {
+                    load_frag(taddr + c0, v);
+                    Packed g, u;
+                    __syncwarp();
+                    put_rows(wp.tile, kept.g, lane);
+                    put_rows(wp.tile + kTileBytes, kept.u, lane);
+                    __syncwarp();
+                    tile_to_frag(wp.tile, g, lane);
+                    tile_to_frag(wp.tile + kTileBytes, u, lane);
+                    if (c0 + 64 < n) load_kept<kKind>(kept, args, it, f0, c0 + 64, lane);
+                    tmem_ld_wait();
+                    store_hidden<kKind>(args, it, f0, c0, v, g, u, wp);
                 } else {
                     if (kKind == kWeights && it.rows == 0) {      // a group without rows: zeros
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) v[c] = 0;
+                        v = Frag{};
                     } else {
-                        tmem_ld32(taddr + c0, v);
+                        load_frag(taddr + c0, v);
                         tmem_ld_wait();
                     }
-                    if constexpr (kKind == kRows || kKind == kInput) store_rows(args, it, f, c0, v);
-                    else if constexpr (hidden(kKind)) store_hidden<kKind>(args, it, f, c0, lane, v);
-                    else if constexpr (kKind == kWeights) store_weights(args, it, f, c0, v);
-                    else store_product(args, it, f, c0, v);
+                    if constexpr (kKind == kWeights) {
+                        store_weights(args, it, f0, c0, v, wp);
+                    } else if constexpr (kKind == kProduct) {
+                        const RowVecs now = res;
+                        if (args.residual && args.vec && c0 + 64 < n) load_residual(res, args, it, f0, c0 + 64, lane);
+                        store_product(args, it, f0, c0, v, now, wp);
+                    } else if (kKind == kInput && args.out32) {   // a slot's part of the sum
+                        store_f32(args.out32 + (int64_t)(it.row0 + c0) * args.ld + f0, args.ld, v, it.rows - c0, 32, lane);
+                    } else {
+                        store_packed(wp.tile, pack(v), args.out + (int64_t)(it.row0 + c0) * args.ld + f0, args.ld,
+                                     it.rows - c0, lane);
+                    }
                 }
             }
             fence_before();
@@ -661,7 +965,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
 }
 
 template <int kKind, int kNB>
-cudaError_t launch(const Maps& maps, const TileArgs& args, int num_sms, cudaStream_t s) {
+cudaError_t launch(const Maps& maps, TileArgs args, int num_sms, cudaStream_t s) {
     using C = Cfg<kKind, kNB>;
     static std::atomic<int> done[kMaxDevices];
     cudaError_t e = smem_limit_once(tile_gemm_kernel<kKind, kNB>, C::SMEM_BYTES, done);
@@ -669,6 +973,10 @@ cudaError_t launch(const Maps& maps, const TileArgs& args, int num_sms, cudaStre
     int grid = 0;
     e = pair_grid<tile_gemm_kernel<kKind, kNB>, C::SMEM_BYTES, kThreads>(num_sms, &grid);
     if (e != cudaSuccess) return e;
+    if (kKind != kWeights && !args.chunks) {
+        args.chunk_rows = dense_chunk(args.rows, C::BN, args.n_mtiles, grid / 2);
+        args.dense_chunks = (int)(((int64_t)args.rows + args.chunk_rows - 1) / args.chunk_rows);
+    }
     return launch_pdl(tile_gemm_kernel<kKind, kNB>, dim3(grid), dim3(kThreads), C::SMEM_BYTES, s, maps, args);
 }
 

@@ -31,12 +31,31 @@ __host__ __device__ inline int chunk_size(int c, int most) {
     return n == 0 ? 0 : ((c + n - 1) / n + 15) & ~15;
 }
 
+// Rows of one group's chunks, for n_mtiles feature tiles on `pairs` CTA pairs.
+// An item costs about its rows, but no less than 128 (below that the features'
+// operand, whose bytes do not shrink, bounds it), and 16 for its ends; the
+// grid takes whole rounds of items.  8192 x 2048 over K = 4096 in chunks of 256
+// is 256 items on 76 pairs, four rounds for 3.4; in chunks of 224 it is 3.9.
+inline int dense_chunk(int rows, int most, int n_mtiles, int pairs) {
+    int best = most;
+    int64_t least = INT64_MAX;
+    for (int size = most; size >= 16; size -= 16) {
+        const int64_t items = ((int64_t)rows + size - 1) / size * n_mtiles;
+        const int64_t cost = (items + pairs - 1) / pairs * ((size < 128 && most > 128 ? 128 : size) + 16);
+        if (cost < least) {
+            least = cost;
+            best = size;
+        }
+    }
+    return best;
+}
+
 struct TileArgs {
     WsHeader* hdr;
     const RowChunk* chunks;    // the chunks, or null: one group of `rows` rows
     const int32_t* n_chunks;
     const RowChunk* groups;    // weight gradients: each expert's rows, or null likewise
-    int dense_chunks;          // without lists: chunks, and the rows of each
+    int dense_chunks;          // without lists: chunks, and the rows of each; set by the launchers
     int chunk_rows;
     int rows;                  // sorted rows
     int E;
@@ -60,6 +79,7 @@ struct TileArgs {
     const float* bias;
     const __nv_bfloat16* residual;
     int act;
+    int vec;                   // product: rows of y and of the residual are 16-byte aligned
 };
 
 // Lists of the offsets' groups (chunks of at most `most` rows); the offsets
@@ -90,7 +110,7 @@ cudaError_t launch_gather_rows(const GatherJob& g, const RowLists& l, int64_t ch
 
 // out[t] = sum_j y[inv[t * k + j]], fp32 in ascending j; positions outside
 // [0, P) count as zero rows.
-cudaError_t launch_sum_slots(const __nv_bfloat16* y, const int32_t* inv, int T, int k, int H,
+cudaError_t launch_sum_slots(const float* y, const int32_t* inv, int T, int k, int H,
                              __nv_bfloat16* out, int num_sms, cudaStream_t s);
 
 // d_gates[s] = sum over parts [n, P] at position inv[s], in order.

@@ -113,7 +113,7 @@ def check_backward(case, out, saved, moe):
     for n, v in (("d_x", d_x), ("d_gates", d_gates), *zip(("dWg", "dWu", "dWd"), dW)):
         if v is None:
             continue
-        roundings = {"d_gates": 0, "d_x": 2}.get(n, 1)       # d_x: the operands', and each slot's part's
+        roundings = 0 if n == "d_gates" else 1
         tol = (roundings * plain.U * (1 + plain.U) + 2.0 ** -16 + (terms[n] + 1) * plain.ADD) * mag[n]
         tol = tol + (H + 1) * plain.ADD * mag_q[n]           # q's own sum
         if n != "d_gates":
