@@ -145,9 +145,8 @@ moe_status moe_expert_ffn_train(const moe_shape* shape, const moe_bf16* x, const
         CUDA_TRY(launch_quantize_rows(xs, T, H, nullptr, 1, 0, (uint8_t*)saved->x, saved->x_scales,
                                       sms, s), "quantize rows");
     if (!dense) {
-        CUDA_TRY(launch_plan_rows(offsets, (int)P, E, most, b.l.l, b.l.hdr, s), "plan");
-        const GatherJob g = {xs, nullptr, nullptr, b.xs, nullptr, perm, k, H, (int)P, 0};
-        CUDA_TRY(launch_gather_rows(g, b.l.l, max_chunks(P, E, most), most, sms, s), "gather");
+        CUDA_TRY(launch_forward_rows(xs, perm, k, H, offsets, (int)P, E, most, b.xs, b.l.l, b.l.hdr, sms, s),
+                 "sorted rows");
         xs = b.xs;
     }
     TileArgs a = args_of(b.l, dense, P, E);
@@ -210,10 +209,9 @@ moe_status moe_expert_ffn_backward(const moe_shape* shape, const moe_bf16* d_out
     const __nv_bfloat16 *x = (const __nv_bfloat16*)saved->x, *d = (const __nv_bfloat16*)d_out;
     const int64_t xd_rows = dense ? T : pad;
     if (!dense) {
-        CUDA_TRY(launch_plan_rows(offsets, (int)P, E, most, b.l.l, b.l.hdr, s), "plan");
-        const GatherJob g = {saved->x, saved->fp8 ? saved->x_scales : nullptr, d, b.x, b.d, perm, k, H,
-                             (int)P, 1};
-        CUDA_TRY(launch_gather_rows(g, b.l.l, max_chunks(P, E, most), most, sms, s), "gather");
+        const BackwardRows q = {saved->x, saved->fp8 ? saved->x_scales : nullptr, d, perm, inv_perm, offsets,
+                                b.x, b.d, b.l.l, b.l.hdr, T, k, H, E, most};
+        CUDA_TRY(launch_backward_rows(q, sms, s), "sorted rows");
         x = b.x;
         d = b.d;
     } else if (saved->fp8) {
@@ -233,18 +231,17 @@ moe_status moe_expert_ffn_backward(const moe_shape* shape, const moe_bf16* d_out
     a.d_gate = b.dg;
     a.d_up = b.du;
     a.gate_parts = d_gates ? b.parts : nullptr;
-    CUDA_TRY(launch_hidden_grad(d, xd_rows, (const __nv_bfloat16*)W_down, H, I, saved->fp8 != 0, nb, a,
-                                sms, s), "gradient of the projections");
-    if (d_gates)
-        CUDA_TRY(launch_sum_gate_parts(b.parts, I / 32, (int)P, inv_perm, d_gates, s), "gradient of the gates");
+    CUDA_TRY(launch_hidden_grad(d, xd_rows, (const __nv_bfloat16*)W_down, H, I, saved->fp8 != 0, nb,
+                                pad, a, sms, s), "gradient of the projections");
     if (d_x) {
         a.out = dense ? (__nv_bfloat16*)d_x : nullptr;
         a.out32 = dense ? nullptr : b.dx;
         CUDA_TRY(launch_input_grad(b.dg, b.du, pad, (const __nv_bfloat16*)W_gate,
                                    (const __nv_bfloat16*)W_up, H, I, nb, a, sms, s), "gradient of x");
-        if (!dense)
-            CUDA_TRY(launch_sum_slots(b.dx, inv_perm, T, k, H, (__nv_bfloat16*)d_x, sms, s), "sum over slots");
     }
+    __nv_bfloat16* sums = d_x && !dense ? (__nv_bfloat16*)d_x : nullptr;
+    if (sums || d_gates)
+        CUDA_TRY(launch_finish(b.dx, sums, b.parts, I / 32, d_gates, inv_perm, T, k, H, sms, s), "sums over slots");
     if (weights) {
         a.out = (__nv_bfloat16*)dW_down;
         a.d_gate = (__nv_bfloat16*)dW_gate;

@@ -10,7 +10,12 @@ cudaError_t launch_product(const __nv_bfloat16* x, int64_t rows, const __nv_bflo
     tg::Maps m = {};
     cudaError_t e;
     if ((e = make_tma_map_bf16(&m.a0, W, (uint64_t)a.E * N, K, 128)) != cudaSuccess) return e;
-    if ((e = make_tma_map_bf16(&m.b0, x, rows, K, nb)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(&m.b0, &m.tail_b0, x, rows, K, nb)) != cudaSuccess) return e;
+    a.map_out = N % (a.out32 ? 4 : 8) == 0;
+    if (a.map_out) {
+        e = a.out32 ? make_tma_map_tile(&m.o0, a.out32, true, rows, N) : make_tma_map_tile(&m.o0, a.out, false, rows, N);
+        if (e != cudaSuccess) return e;
+    }
     a.n_mtiles = (N + 255) / 256;
     a.m_total = N;
     a.a_rows = N;

@@ -145,5 +145,8 @@ cudaError_t make_tma_map_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, ui
 // Same over 8-bit values: box = 128 columns (128 bytes) x box_rows.
 cudaError_t make_tma_map_u8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
                             uint32_t box_rows);
+// Map for storing 32 x 32 tiles (box = 32 columns x 32 rows) of bf16 (64-byte
+// swizzle) or fp32 (128-byte swizzle).
+cudaError_t make_tma_map_tile(CUtensorMap* m, const void* ptr, bool f32, uint64_t rows, uint64_t cols);
 
 }  // namespace moe

@@ -45,7 +45,7 @@ using namespace ptx;
 using namespace tc;
 
 constexpr int kThreads = 384;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 8;         // 16 took 15% longer: shared memory and stores bound them
 constexpr int kTileFeatures = 256;   // features per item (both CTAs)
 constexpr int kTileBytes = 32 * 64;  // a staging tile
 
@@ -77,12 +77,15 @@ struct Cfg {
     static constexpr int A_BYTES = MT * A_SUB;
     static constexpr int B_BYTES = NB * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    // rows of a box of B, and of the K rows of a weight gradient's last block
+    static constexpr int BOX = NB < 32 ? NB : 32;
     static constexpr int STAGES = (192 * 1024) / STAGE_BYTES < 8 ? (192 * 1024) / STAGE_BYTES : 8;
     static constexpr int ACC_COLS = MT * BN;          // TMEM columns of one accumulator set
     static constexpr int BUFS = 2 * ACC_COLS <= 512 ? 2 : 1;
     static constexpr int TMEM_COLS = BUFS * ACC_COLS;
-    // staging tiles of an epilogue warp (32 rows x 32 features, bf16)
-    static constexpr int TILES = kKind == kGated || hidden(kKind) ? 2 : 1;
+    // staging tiles of an epilogue warp (32 rows x 32 features, bf16; two hold
+    // a tile of fp32)
+    static constexpr int TILES = kKind == kGatedFp8 ? 1 : 2;
     static constexpr int STAGING_BYTES = kEpiWarps * TILES * kTileBytes;
     // block maxima of the 8-bit epilogue: [half][parity][gate, up][4 warps][32 rows]
     static constexpr int AMAX_BYTES = kKind == kGatedFp8 ? 2 * 2 * 2 * 4 * 32 * 4 : 0;
@@ -124,6 +127,7 @@ struct Item {
     int row0_pad;  // the same in the padded buffers
     int k_blocks;
     int k16_last;  // 16-deep steps of the last block
+    int boxes;     // boxes of B's rows that hold the chunk's (of one CTA)
 };
 
 template <int kKind, typename C>
@@ -170,9 +174,24 @@ __device__ __forceinline__ Item item_of(const TileArgs& a, int w) {
         it.n = (it.rows + 15) & ~15;
         it.k_blocks = a.k_blocks;
         it.k16_last = C::BK / 16;
+        it.boxes = (it.n / 2 + C::BOX - 1) / C::BOX;
     }
     return it;
 }
+
+// Tensor maps, by kind:
+//   gated     a0 = Wg, a1 = Wu, b0 = x; o0 = h, o1 = gate, o2 = up
+//   hidden    a0 = Wd, b0 = d; o0 = w h, o1 = dg, o2 = du
+//   input     a0 = Wg, a1 = Wu, b0 = dg, b1 = du; o0 = d_x
+//   weights   a0 = w h, a1 = x, b0 = d, b1 = dg, b2 = du; o0 = dWd, o1 = dWg, o2 = dWu
+//   others    a0 = W, b0 = x; o0 = y
+// The tail maps have boxes of at most 32 rows, for chunks and groups that do
+// not fill the whole box; the o maps store 32 x 32 tiles.
+struct Maps {
+    CUtensorMap a0, a1, b0, b1, b2;
+    CUtensorMap tail_a0, tail_a1, tail_b0, tail_b1, tail_b2;
+    CUtensorMap o0, o1, o2;
+};
 
 // 2^(b - 127); byte 255 stands for NaN.
 __device__ __forceinline__ float scale_value(uint32_t b) {
@@ -262,26 +281,55 @@ __device__ __forceinline__ void tile_put(uint32_t tile, int row, int chunk, cons
     st_shared_v4(tile_at(tile, row, chunk), v.x, v.y, v.z, v.w);
 }
 
-// The tile's first `left` rows to out (feature 0 of row 0; 16-byte aligned
-// rows of ld values), by the whole warp.
-__device__ __forceinline__ void tile_to_rows(uint32_t tile, __nv_bfloat16* out, int64_t ld, int left,
-                                             int lane) {
-    __nv_bfloat16* o = out + (int64_t)(lane >> 2) * ld + (lane & 3) * 8;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = 8 * i + (lane >> 2);
-        const uint4 v = tile_vec(tile, row, lane & 3);
-        if (row < left) *reinterpret_cast<uint4*>(o) = v;
-        o += 8 * ld;
-    }
-}
-// Packed fragment -> rows, through the tile.
-__device__ __forceinline__ void store_packed(uint32_t tile, const Packed& p, __nv_bfloat16* out,
-                                             int64_t ld, int left, int lane) {
-    __syncwarp();                       // what the tile held before has been read
-    frag_to_tile(tile, p, lane);
+// An epilogue warp's place and its ring of staging tiles.
+struct Warp {
+    int lane, quad;
+    uint32_t tiles;       // its staging tiles
+    int used;             // tiles handed out
+    uint32_t* amax;       // 8-bit epilogue: this block's maxima [gate, up][4 warps][32 rows]
+    int bar_id;
+};
+// The next tile of the ring, no longer read by the store that used it before.
+// Every use ends with a commit, so the groups in flight count the tiles in use.
+template <int kTiles>
+__device__ __forceinline__ uint32_t next_tile(Warp& w) {
+    if (w.lane == 0) bulk_wait_read<kTiles - 1>();
     __syncwarp();
-    tile_to_rows(tile, out, ld, left, lane);
+    return w.tiles + (uint32_t)(w.used++ % kTiles) * kTileBytes;
+}
+
+// Where 32 x 32 blocks of an output go: a map for whole blocks, which the copy
+// engine stores from the tile (the LSU's part of it, 64 bytes of each of 8 rows
+// an instruction, was what bound the epilogues: 10 cycles of the data pipe
+// each), and the address for a group's last rows.
+struct OutBlock {
+    const CUtensorMap* map;
+    int x, y;                  // column and row of the block
+    __nv_bfloat16* p;          // the same as an address, rows of ld values
+    int64_t ld;
+    int rows;                  // rows of the block that are there
+};
+// Packed fragment -> output.
+template <int kTiles>
+__device__ __forceinline__ void store_packed(Warp& w, const Packed& p, const OutBlock& o) {
+    const uint32_t tile = next_tile<kTiles>(w);
+    frag_to_tile(tile, p, w.lane);
+    if (o.rows >= 32) {
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (w.lane == 0) tma_store_2d(o.map, tile, o.x, o.y);
+    } else {
+        __syncwarp();
+        __nv_bfloat16* to = o.p + (int64_t)(w.lane >> 2) * o.ld + (w.lane & 3) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 8 * i + (w.lane >> 2);
+            const uint4 v = tile_vec(tile, row, w.lane & 3);
+            if (row < o.rows) *reinterpret_cast<uint4*>(to) = v;
+            to += 8 * o.ld;
+        }
+    }
+    if (w.lane == 0) bulk_commit();
 }
 
 // Rows of a bf16 tensor on their way into a tile: loaded ahead, put later.
@@ -362,19 +410,16 @@ __device__ __forceinline__ float feature_sums(float (&v)[4][2], int lane, int* r
 
 // ---- epilogues: one warp's 32 features from f0, 32 rows from c0 ---------------
 
-struct Warp {
-    int lane, quad;
-    uint32_t tile;        // staging tiles
-    uint32_t* amax;       // 8-bit epilogue: this block's maxima [gate, up][4 warps][32 rows]
-    int bar_id;
-};
-
 // h = silu(g) u, with g and u kept.
 template <int kKind>
 __device__ __forceinline__ void store_gated(const TileArgs& a, const Item& it, int f0, int c0,
-                                            const Frag& g, const Frag& u, const Warp& w) {
+                                            const Frag& g, const Frag& u, const Maps& maps, Warp& w) {
     const int left = it.rows - c0, lane = w.lane;
     const int64_t at = (int64_t)(it.row0 + c0) * a.ld + f0;
+    constexpr int kTiles = kKind == kGated ? 2 : 1;
+    const auto out = [&](const CUtensorMap& m, void* p) {
+        return OutBlock{&m, f0, it.row0 + c0, static_cast<__nv_bfloat16*>(p) + at, a.ld, left};
+    };
     Packed h;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -383,9 +428,9 @@ __device__ __forceinline__ void store_gated(const TileArgs& a, const Item& it, i
             h.v[i][j] = pack_bf16(g.v[i][j][0] * sigmoid(g.v[i][j][0]) * u.v[i][j][0],
                                   g.v[i][j][1] * sigmoid(g.v[i][j][1]) * u.v[i][j][1]);
     if constexpr (kKind == kGated) {
-        store_packed(w.tile, h, a.out + at, a.ld, left, lane);
-        store_packed(w.tile + kTileBytes, pack(g), static_cast<__nv_bfloat16*>(a.gate) + at, a.ld, left, lane);
-        store_packed(w.tile, pack(u), static_cast<__nv_bfloat16*>(a.up) + at, a.ld, left, lane);
+        store_packed<kTiles>(w, h, out(maps.o0, a.out));
+        store_packed<kTiles>(w, pack(g), out(maps.o1, a.gate));
+        store_packed<kTiles>(w, pack(u), out(maps.o2, a.up));
     } else {
         // The block's scale covers 128 features: each lane takes the maxima of
         // its features, the eight lanes of a row then theirs, and the four
@@ -448,15 +493,15 @@ __device__ __forceinline__ void store_gated(const TileArgs& a, const Item& it, i
 #pragma unroll
             for (int i = 0; i < 4; ++i) q.v[i][j] = b[0][i] | b[1][i] << 16;
         }
-        store_packed(w.tile, h, a.out + at, a.ld, left, lane);
-        __syncwarp();
-        frag_to_tile(w.tile, q, lane);
+        store_packed<kTiles>(w, h, out(maps.o0, a.out));
+        const uint32_t tile = next_tile<kTiles>(w);
+        frag_to_tile(tile, q, lane);
         __syncwarp();
         // two lanes a row, 16 features each: the gate's bytes and the up's
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = 16 * i + (lane >> 1), c = (lane & 1) * 2;
-            const uint4 lo = tile_vec(w.tile, r, c), hi = tile_vec(w.tile, r, c + 1);
+            const uint4 lo = tile_vec(tile, r, c), hi = tile_vec(tile, r, c + 1);
             if (r < left) {
                 const int64_t to = at + (int64_t)r * a.ld + c * 8;
                 *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.gate) + to) =
@@ -467,12 +512,39 @@ __device__ __forceinline__ void store_gated(const TileArgs& a, const Item& it, i
                                __byte_perm(hi.x, hi.y, 0x7531), __byte_perm(hi.z, hi.w, 0x7531));
             }
         }
+        if (lane == 0) bulk_commit();
     }
 }
 
-// fp32 rows straight from the fragment: eight lanes store 32 bytes of a row.
-__device__ __forceinline__ void store_f32(float* out, int64_t ld, const Frag& f, int left, int feats,
-                                          int lane) {
+// fp32 block: through a tile of 128-byte rows (16-byte chunk c of row r at
+// chunk c ^ (r mod 8)) where whole rows can be stored by the copy engine, else
+// straight from the fragment, eight lanes storing 32 bytes of a row.
+__device__ __forceinline__ void store_f32(Warp& w, const Frag& f, const CUtensorMap* map, int x, int y, float* out,
+                                          int64_t ld, int left, int feats) {
+    const int lane = w.lane;
+    if (map && left >= 32) {
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int r = 8 * j + 2 * (lane & 3) + s, c = 2 * i + (lane >> 4);
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(w.tiles + r * 128 + ((c ^ r) & 7) * 16 + ((lane >> 2) & 3) * 4),
+                                 "f"(f.v[i][j][s])
+                                 : "memory");
+                }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(map, w.tiles, x, y);
+            bulk_commit();
+            bulk_commit();      // two tiles of the ring
+        }
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -518,7 +590,7 @@ __device__ __forceinline__ void load_kept(KeptRows<kKind>& k, const TileArgs& a,
 template <int kKind>
 __device__ __forceinline__ void store_hidden(const TileArgs& a, const Item& it, int f0, int c0,
                                              const Frag& q, const Packed& kg, const Packed& ku,
-                                             const Warp& wp) {
+                                             const Maps& maps, Warp& wp) {
     const int left = it.rows - c0, pad = it.n - c0, lane = wp.lane;
     float w = 1.f;
     if (a.gates && lane < left) {
@@ -556,9 +628,12 @@ __device__ __forceinline__ void store_hidden(const TileArgs& a, const Item& it, 
         }
     }
     const int64_t to = (int64_t)(it.row0_pad + c0) * a.ld + f0;
-    store_packed(wp.tile, dg, a.d_gate + to, a.ld, pad, lane);
-    store_packed(wp.tile + kTileBytes, du, a.d_up + to, a.ld, pad, lane);
-    store_packed(wp.tile, ho, a.out + to, a.ld, pad, lane);
+    const auto out = [&](const CUtensorMap& m, __nv_bfloat16* p) {
+        return OutBlock{&m, f0, it.row0_pad + c0, p + to, a.ld, pad};
+    };
+    store_packed<2>(wp, dg, out(maps.o1, a.d_gate));
+    store_packed<2>(wp, du, out(maps.o2, a.d_up));
+    store_packed<2>(wp, ho, out(maps.o0, a.out));
     if (a.gate_parts) {
         int r;
         const float sum = feature_sums(part, lane, &r);
@@ -567,11 +642,13 @@ __device__ __forceinline__ void store_hidden(const TileArgs& a, const Item& it, 
 }
 
 __device__ __forceinline__ void store_weights(const TileArgs& a, const Item& it, int f0, int c0,
-                                              const Frag& v, const Warp& w) {
+                                              const Frag& v, const Maps& maps, Warp& w) {
     const int64_t ld = it.mat == 0 ? a.m_total : a.n_total;      // I, H
     const int64_t rows = it.mat == 0 ? a.n_total : a.m_total;    // H, I
     __nv_bfloat16* W = it.mat == 0 ? a.out : it.mat == 1 ? a.d_gate : a.d_up;
-    store_packed(w.tile, pack(v), W + ((int64_t)it.expert * rows + it.n0 + c0) * ld + f0, ld, 32, w.lane);
+    const int64_t row = it.expert * rows + it.n0 + c0;
+    store_packed<2>(w, pack(v), OutBlock{it.mat == 0 ? &maps.o0 : it.mat == 1 ? &maps.o1 : &maps.o2, f0, (int)row,
+                                         W + row * ld + f0, ld, 32});
 }
 
 __device__ __forceinline__ void activate(Frag& f, int act) {
@@ -596,7 +673,7 @@ __device__ __forceinline__ void load_residual(RowVecs& r, const TileArgs& a, con
     load_rows(r, a.residual + (int64_t)(it.row0 + c0) * a.ld + f0, a.ld, left, lane);
 }
 __device__ __forceinline__ void store_product(const TileArgs& a, const Item& it, int f0, int c0, Frag& v,
-                                              const RowVecs& res, const Warp& w) {
+                                              const RowVecs& res, const Maps& maps, Warp& w) {
     const int left = it.rows - c0, lane = w.lane, feats = a.m_total - f0;
     const int64_t at = (int64_t)(it.row0 + c0) * a.ld + f0;
     if (a.bias) {
@@ -613,21 +690,22 @@ __device__ __forceinline__ void store_product(const TileArgs& a, const Item& it,
     }
     activate(v, a.act);
     if (a.residual) {
-        __syncwarp();
+        const uint32_t tile = next_tile<2>(w);
         if (a.vec) {
-            put_rows(w.tile, res, lane);
+            put_rows(tile, res, lane);
         } else if (lane < feats) {
 #pragma unroll 8
             for (int r = 0; r < 32; ++r) {
                 uint16_t x = 0;
                 if (r < left) x = *reinterpret_cast<const uint16_t*>(a.residual + at + (int64_t)r * a.ld + lane);
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile_at(w.tile, r, lane >> 3) + (lane & 7) * 2), "h"(x)
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile_at(tile, r, lane >> 3) + (lane & 7) * 2), "h"(x)
                              : "memory");
             }
         }
         __syncwarp();
         Packed p;
-        tile_to_frag(w.tile, p, lane);
+        tile_to_frag(tile, p, lane);
+        if (lane == 0) bulk_commit();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -638,34 +716,51 @@ __device__ __forceinline__ void store_product(const TileArgs& a, const Item& it,
             }
     }
     if (a.out32) {
-        store_f32(a.out32 + at, a.ld, v, left, feats, lane);
+        store_f32(w, v, a.map_out ? &maps.o0 : nullptr, f0, it.row0 + c0, a.out32 + at, a.ld, left, feats);
         return;
     }
-    if (a.vec) {
-        store_packed(w.tile, pack(v), a.out + at, a.ld, (lane & 3) * 8 < feats ? left : 0, lane);
+    if (a.map_out) {
+        const int rows = left >= 32 ? 32 : (lane & 3) * 8 < feats ? left : 0;
+        store_packed<2>(w, pack(v), OutBlock{&maps.o0, f0, it.row0 + c0, a.out + at, a.ld, rows});
         return;
     }
-    __syncwarp();
-    frag_to_tile(w.tile, pack(v), lane);
+    const uint32_t tile = next_tile<2>(w);
+    frag_to_tile(tile, pack(v), lane);
     __syncwarp();
     if (lane < feats) {
 #pragma unroll 8
         for (int r = 0; r < 32; ++r) {
             uint16_t x;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(tile_at(w.tile, r, lane >> 3) + (lane & 7) * 2) : "memory");
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(tile_at(tile, r, lane >> 3) + (lane & 7) * 2) : "memory");
             if (r < left) *reinterpret_cast<uint16_t*>(a.out + at + (int64_t)r * a.ld + lane) = x;
         }
     }
+    if (lane == 0) bulk_commit();
 }
 
 // ---- the kernel ------------------------------------------------------------
 
-// Maps: tmA[0..1] / tmB[0..1], meaning by kind:
-//   gated     A0 = Wg, A1 = Wu, B0 = x          input    A0 = Wg, A1 = Wu, B0 = dg, B1 = du
-//   weights   A0 = w h, A1 = x, B0 = d, B1 = dg, B2 = du        others   A0, B0
-struct Maps {
-    CUtensorMap a0, a1, b0, b1, b2;
-};
+// Waits for what is in flight after an abort, as drain_pair does; here a
+// stage's bytes differ from item to item: bytes(cta, s) of CTA 0 or 1's last
+// fill of stage s.
+template <int kStages, typename Bytes>
+__device__ __forceinline__ void drain_stages(uint32_t full0, int fills_even, int fills_odd, Bytes bytes) {
+    for (int s = 0; s < kStages; ++s) {
+        const uint32_t bar = full0 + 8u * s;
+        const int re = rounds_filled<kStages>(fills_even, s) - 1, ro = rounds_filled<kStages>(fills_odd, s) - 1;
+        if (re < 0 && ro < 0) continue;
+        if (ro == re + 1) {
+            if (re >= 0) (void)mbar_wait(bar, (uint32_t)(re & 1));
+            mbar_expect_tx(bar, bytes(1, s));
+            (void)mbar_wait(bar, (uint32_t)(ro & 1));
+        } else if (re == ro + 1) {
+            mbar_complete_tx(bar, bytes(0, s));
+            (void)mbar_wait(bar, (uint32_t)(re & 1));
+        } else {
+            (void)mbar_wait(bar, (uint32_t)(re & 1));
+        }
+    }
+}
 
 template <int kKind, int kNB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -686,6 +781,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + kBarsAt + 8 * (2 * C::STAGES + 5));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     int* fills_out = reinterpret_cast<int*>(tmem_holder + 2);
+    uint32_t* stage_bytes = tmem_holder + 3;     // of each stage's last fill
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -742,6 +838,11 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
         for (int w = cluster; ok && w < total; w += n_clusters) {
             const Item it = item_of<kKind, C>(args, w);
             const int m = it.m0 + (int)rank * 128;
+            const CUtensorMap *ma = &maps.a0, *mb = &maps.b0;
+            if constexpr (kKind == kWeights) {
+                if (it.mat > 0) ma = &maps.a1;
+                mb = it.mat == 0 ? &maps.b0 : it.mat == 1 ? &maps.b1 : &maps.b2;
+            }
             for (int kb = 0; kb < it.k_blocks; ++kb) {
                 if (!mbar_wait_for(empty_bar(stage), phase ^ 1u, args.wait_cycles, abort_flag)) {
                     ok = false;
@@ -749,47 +850,72 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                 }
                 const uint32_t sa = base + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
                 const uint32_t fb = full0 + 8u * stage;
-                if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * C::STAGE_BYTES);
                 int k = kb * C::BK;
-                const CUtensorMap *ma = &maps.a0, *mb = &maps.b0;
-                if constexpr (kKind == kInput) {
-                    if (kb >= args.seg_blocks) {      // the second product of the sum
-                        k -= args.seg_blocks * C::BK;
-                        ma = &maps.a1;
-                        mb = &maps.b1;
-                    }
-                }
                 if constexpr (kKind == kWeights) {
-                    if (it.mat > 0) ma = &maps.a1;
-                    mb = it.mat == 0 ? &maps.b0 : it.mat == 1 ? &maps.b1 : &maps.b2;
-                }
+                    // K runs over the group's rows: the last block loads the boxes that hold some
+                    const int krow = it.row0_pad + k, n = it.n0 + (int)rank * C::NB;
+                    const bool tail = kb == it.k_blocks - 1 && it.k16_last <= (C::BK - 32) / 16;
+                    const int boxes = tail ? (it.k16_last + 1) / 2 : 1;
+                    const uint32_t bytes = tail ? (uint32_t)boxes * (32 * 128 * 4) : (uint32_t)C::STAGE_BYTES;
+                    stage_bytes[stage] = bytes;
+                    if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * bytes);
+                    if (!tail) {
 #pragma unroll
-                for (int mt = 0; mt < C::MT; ++mt) {
-                    const CUtensorMap* mam = gated(kKind) && mt == 1 ? &maps.a1 : ma;
-                    if constexpr (C::kAMN) {
-                        const int krow = kKind == kWeights ? it.row0_pad + k
-                                                           : it.expert * args.a_rows + k;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            tma_load_2d_pair(sa + mt * C::A_SUB + j * C::BK * 128, mam, fb, m + 64 * j, krow);
+                        for (int j = 0; j < 2; ++j) {
+                            tma_load_2d_pair(sa + j * C::BK * 128, ma, fb, m + 64 * j, krow);
+                            tma_load_2d_pair(sb + j * C::BK * 128, mb, fb, n + 64 * j, krow);
+                        }
                     } else {
+                        const CUtensorMap *ta = it.mat ? &maps.tail_a1 : &maps.tail_a0,
+                                          *tb = it.mat == 0 ? &maps.tail_b0 : it.mat == 1 ? &maps.tail_b1 : &maps.tail_b2;
+                        for (int q = 0; q < boxes; ++q)
 #pragma unroll
-                        for (int j = 0; j < C::KSUB; ++j)
-                            tma_load_2d_pair(sa + mt * C::A_SUB + j * 128 * 128, mam, fb, k + 64 * j,
-                                             it.expert * args.a_rows + m);
+                            for (int j = 0; j < 2; ++j) {
+                                tma_load_2d_pair(sa + j * C::BK * 128 + q * 32 * 128, ta, fb, m + 64 * j, krow + 32 * q);
+                                tma_load_2d_pair(sb + j * C::BK * 128 + q * 32 * 128, tb, fb, n + 64 * j, krow + 32 * q);
+                            }
                     }
-                }
-                if constexpr (C::kBMN) {
-#pragma unroll
-                    for (int j = 0; j < C::NB / 64; ++j)
-                        tma_load_2d_pair(sb + j * C::BK * 128, mb, fb, it.n0 + (int)rank * C::NB + 64 * j,
-                                         it.row0_pad + k);
                 } else {
+                    // B: the boxes that hold the chunk's rows, no more
+                    const bool whole = it.boxes * C::BOX == C::NB;
+                    const uint32_t bytes = (uint32_t)(C::A_BYTES + it.boxes * C::BOX * C::BK * 2);
+                    stage_bytes[stage] = bytes;
+                    if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * bytes);
+                    if constexpr (kKind == kInput) {
+                        if (kb >= args.seg_blocks) {      // the second product of the sum
+                            k -= args.seg_blocks * C::BK;
+                            ma = &maps.a1;
+                            mb = &maps.b1;
+                        }
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < C::MT; ++mt) {
+                        const CUtensorMap* mam = gated(kKind) && mt == 1 ? &maps.a1 : ma;
+                        if constexpr (C::kAMN) {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                tma_load_2d_pair(sa + mt * C::A_SUB + j * C::BK * 128, mam, fb, m + 64 * j,
+                                                 it.expert * args.a_rows + k);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < C::KSUB; ++j)
+                                tma_load_2d_pair(sa + mt * C::A_SUB + j * 128 * 128, mam, fb, k + 64 * j,
+                                                 it.expert * args.a_rows + m);
+                        }
+                    }
                     // the odd CTA holds the upper half of the N rows
                     const int brow = (args.padded ? it.row0_pad : it.row0) + (int)rank * (it.n >> 1);
+                    if (whole) {
 #pragma unroll
-                    for (int j = 0; j < C::KSUB; ++j)
-                        tma_load_2d_pair(sb + j * C::NB * 128, mb, fb, k + 64 * j, brow);
+                        for (int j = 0; j < C::KSUB; ++j)
+                            tma_load_2d_pair(sb + j * C::NB * 128, mb, fb, k + 64 * j, brow);
+                    } else {
+                        const CUtensorMap* tb = mb == &maps.b0 ? &maps.tail_b0 : &maps.tail_b1;
+                        for (int q = 0; q < it.boxes; ++q)
+#pragma unroll
+                            for (int j = 0; j < C::KSUB; ++j)
+                                tma_load_2d_pair(sb + j * C::NB * 128 + q * C::BOX * 128, tb, fb, k + 64 * j, brow + q * C::BOX);
+                    }
                 }
                 ++fills;
                 if (++stage == C::STAGES) {
@@ -859,9 +985,9 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
     } else if (warp >= 4) {
         // ---------------- epilogue (both CTAs) ----------------
         const int quad = warp & 3;            // TMEM lanes 32*quad .. 32*quad+31
-        const int half = (warp - 4) >> 2;     // which 32-row blocks
+        const int half = (warp - 4) >> 2;     // which 32-row blocks: every other
         uint32_t* amax = reinterpret_cast<uint32_t*>(base_ptr + kAmaxAt) + half * 512;
-        Warp wp = {lane, quad, base + kStagingAt + (uint32_t)(warp - 4) * C::TILES * kTileBytes, amax, 1 + half};
+        Warp wp = {lane, quad, base + kStagingAt + (uint32_t)(warp - 4) * C::TILES * kTileBytes, 0, amax, 1 + half};
         const uint32_t tempty0 = mapa_shared(tempty_bar(0), 0);
         int i = 0;
         for (int w = cluster; w < total; w += n_clusters, ++i) {
@@ -906,19 +1032,20 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                     load_frag(taddr + C::BN + c0, u);
                     tmem_ld_wait();
                     wp.amax = amax + ((c0 >> 6) & 1) * 256;
-                    store_gated<kKind>(args, it, f0, c0, v, u, wp);
+                    store_gated<kKind>(args, it, f0, c0, v, u, maps, wp);
                 } else if constexpr (hidden(kKind)) {
                     load_frag(taddr + c0, v);
                     Packed g, u;
+                    if (lane == 0) bulk_wait_read<0>();
                     __syncwarp();
-                    put_rows(wp.tile, kept.g, lane);
-                    put_rows(wp.tile + kTileBytes, kept.u, lane);
+                    put_rows(wp.tiles, kept.g, lane);
+                    put_rows(wp.tiles + kTileBytes, kept.u, lane);
                     __syncwarp();
-                    tile_to_frag(wp.tile, g, lane);
-                    tile_to_frag(wp.tile + kTileBytes, u, lane);
+                    tile_to_frag(wp.tiles, g, lane);
+                    tile_to_frag(wp.tiles + kTileBytes, u, lane);
                     if (c0 + 64 < n) load_kept<kKind>(kept, args, it, f0, c0 + 64, lane);
                     tmem_ld_wait();
-                    store_hidden<kKind>(args, it, f0, c0, v, g, u, wp);
+                    store_hidden<kKind>(args, it, f0, c0, v, g, u, maps, wp);
                 } else {
                     if (kKind == kWeights && it.rows == 0) {      // a group without rows: zeros
                         v = Frag{};
@@ -927,16 +1054,18 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                         tmem_ld_wait();
                     }
                     if constexpr (kKind == kWeights) {
-                        store_weights(args, it, f0, c0, v, wp);
+                        store_weights(args, it, f0, c0, v, maps, wp);
                     } else if constexpr (kKind == kProduct) {
                         const RowVecs now = res;
-                        if (args.residual && args.vec && c0 + 64 < n) load_residual(res, args, it, f0, c0 + 64, lane);
-                        store_product(args, it, f0, c0, v, now, wp);
-                    } else if (kKind == kInput && args.out32) {   // a slot's part of the sum
-                        store_f32(args.out32 + (int64_t)(it.row0 + c0) * args.ld + f0, args.ld, v, it.rows - c0, 32, lane);
+                        if (args.residual && args.vec && c0 + 64 < n)
+                            load_residual(res, args, it, f0, c0 + 64, lane);
+                        store_product(args, it, f0, c0, v, now, maps, wp);
                     } else {
-                        store_packed(wp.tile, pack(v), args.out + (int64_t)(it.row0 + c0) * args.ld + f0, args.ld,
-                                     it.rows - c0, lane);
+                        const int64_t at = (int64_t)(it.row0 + c0) * args.ld + f0;
+                        if (kKind == kInput && args.out32)        // a slot's part of the sum
+                            store_f32(wp, v, &maps.o0, f0, it.row0 + c0, args.out32 + at, args.ld, it.rows - c0, 32);
+                        else
+                            store_packed<2>(wp, pack(v), OutBlock{&maps.o0, f0, it.row0 + c0, args.out + at, args.ld, it.rows - c0});
                     }
                 }
             }
@@ -944,6 +1073,8 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_tmem(tempty0 + 8u * acc);
         }
+        if (lane == 0) bulk_wait_all();   // the stores have completed before the CTA leaves
+        __syncwarp();
     }
 
     fence_before();
@@ -953,15 +1084,25 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
     cluster_sync();
     if (aborted) {
         if (rank == 0 && threadIdx.x == 0)
-            drain_pair<C::STAGES>(full_bar(0), *fills_out,
-                                  (int)ld_shared_cluster(mapa_shared(smem_u32(fills_out), 1)),
-                                  (uint32_t)C::STAGE_BYTES);
+            drain_stages<C::STAGES>(full_bar(0), *fills_out,
+                                    (int)ld_shared_cluster(mapa_shared(smem_u32(fills_out), 1)),
+                                    [&](uint32_t cta, int s) {
+                                        return ld_shared_cluster(mapa_shared(smem_u32(stage_bytes + s), cta));
+                                    });
         cluster_sync();
     }
     if (warp == 2) {
         fence_after();
         tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
     }
+}
+
+// The whole-box and tail maps of an operand whose rows are the groups'.
+inline cudaError_t row_maps(CUtensorMap* whole, CUtensorMap* tail, const __nv_bfloat16* p, int64_t rows, int cols,
+                            int box) {
+    const cudaError_t e = make_tma_map_bf16(whole, p, (uint64_t)rows, (uint64_t)cols, (uint32_t)box);
+    if (e != cudaSuccess) return e;
+    return make_tma_map_bf16(tail, p, (uint64_t)rows, (uint64_t)cols, (uint32_t)(box < 32 ? box : 32));
 }
 
 template <int kKind, int kNB>

@@ -80,6 +80,7 @@ struct TileArgs {
     const __nv_bfloat16* residual;
     int act;
     int vec;                   // product: rows of y and of the residual are 16-byte aligned
+    int map_out;               // product: rows of y can be stored by the copy engine; set by the launcher
 };
 
 // Lists of the offsets' groups (chunks of at most `most` rows); the offsets
@@ -93,29 +94,30 @@ struct RowLists {
 cudaError_t launch_plan_rows(const int32_t* offsets, int rows, int E, int most, const RowLists& l,
                              WsHeader* hdr, cudaStream_t s);
 
-// dst[row0 + i] (padded: row0_pad + i, and zeros up to the multiple of 16) =
-// src[perm[row0 + i] / k] for every chunk; two sources at once where src1 is
-// given.  src0_scales: src0 holds e4m3 with a scale per 128 values.
-struct GatherJob {
-    const void* src0;
-    const uint8_t* src0_scales;
-    const __nv_bfloat16* src1;
-    __nv_bfloat16 *dst0, *dst1;
-    const int32_t* perm;
-    int k, H, P, padded;
+// Forward: the lists, and xs[p] = x[perm[p] / k] for the sorted rows.
+cudaError_t launch_forward_rows(const __nv_bfloat16* x, const int32_t* perm, int k, int H,
+                                const int32_t* offsets, int P, int E, int most, __nv_bfloat16* xs,
+                                const RowLists& l, WsHeader* hdr, int num_sms, cudaStream_t s);
+
+// Backward: the lists, and the padded rows of x (its values, where x_scales
+// says that it holds e4m3) and of d.
+struct BackwardRows {
+    const void* x;
+    const uint8_t* x_scales;
+    const __nv_bfloat16* d;
+    const int32_t *perm, *inv_perm, *offsets;
+    __nv_bfloat16 *x_rows, *d_rows;
+    RowLists lists;
+    WsHeader* hdr;
+    int T, k, H, E, most;
 };
-// `most`: the chunks' rows at most; chunks_bound: how many chunks there may be.
-cudaError_t launch_gather_rows(const GatherJob& g, const RowLists& l, int64_t chunks_bound, int most,
-                               int num_sms, cudaStream_t s);
+cudaError_t launch_backward_rows(const BackwardRows& q, int num_sms, cudaStream_t s);
 
-// out[t] = sum_j y[inv[t * k + j]], fp32 in ascending j; positions outside
-// [0, P) count as zero rows.
-cudaError_t launch_sum_slots(const float* y, const int32_t* inv, int T, int k, int H,
-                             __nv_bfloat16* out, int num_sms, cudaStream_t s);
-
-// d_gates[s] = sum over parts [n, P] at position inv[s], in order.
-cudaError_t launch_sum_gate_parts(const float* parts, int n, int P, const int32_t* inv,
-                                  float* d_gates, cudaStream_t s);
+// d_x[t] = sum_j y[inv[t * k + j]] (y fp32 [P, H]; d_x null: left out), and
+// d_gates[s] = sum over parts [n_parts, P] at position inv[s] (null: left out;
+// inv null: position s).  Positions outside [0, P) count as zeros.
+cudaError_t launch_finish(const float* y, __nv_bfloat16* d_x, const float* parts, int n_parts, float* d_gates,
+                          const int32_t* inv, int T, int k, int H, int num_sms, cudaStream_t s);
 
 // bf16 values of rows of e4m3 with a scale per 128 of K (exact).
 cudaError_t launch_dequantize_rows(const uint8_t* q, const uint8_t* scales, int64_t rows, int K,
@@ -131,8 +133,8 @@ cudaError_t launch_train_gate_up(const __nv_bfloat16* x, int64_t x_rows, const _
 cudaError_t launch_train_down(const __nv_bfloat16* h, int64_t h_rows, const __nv_bfloat16* Wd,
                               int H, int I, int nb, TileArgs a, int num_sms, cudaStream_t s);
 cudaError_t launch_hidden_grad(const __nv_bfloat16* d, int64_t d_rows, const __nv_bfloat16* Wd,
-                               int H, int I, bool fp8, int nb, TileArgs a, int num_sms,
-                               cudaStream_t s);
+                               int H, int I, bool fp8, int nb, int64_t out_rows, TileArgs a,
+                               int num_sms, cudaStream_t s);
 cudaError_t launch_input_grad(const __nv_bfloat16* dg, const __nv_bfloat16* du, int64_t rows,
                               const __nv_bfloat16* Wg, const __nv_bfloat16* Wu, int H, int I,
                               int nb, TileArgs a, int num_sms, cudaStream_t s);

@@ -8,13 +8,16 @@
 namespace moe {
 
 cudaError_t launch_hidden_grad(const __nv_bfloat16* d, int64_t d_rows, const __nv_bfloat16* Wd,
-                               int H, int I, bool fp8, int nb, TileArgs a, int num_sms,
-                               cudaStream_t s) {
+                               int H, int I, bool fp8, int nb, int64_t out_rows, TileArgs a,
+                               int num_sms, cudaStream_t s) {
     using C = tg::Cfg<tg::kHidden, kWideRows>;
     tg::Maps m = {};
     cudaError_t e;
     if ((e = make_tma_map_bf16(&m.a0, Wd, (uint64_t)a.E * H, I, C::BK)) != cudaSuccess) return e;
-    if ((e = make_tma_map_bf16(&m.b0, d, d_rows, H, nb)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(&m.b0, &m.tail_b0, d, d_rows, H, nb)) != cudaSuccess) return e;
+    if ((e = make_tma_map_tile(&m.o0, a.out, false, out_rows, I)) != cudaSuccess) return e;
+    if ((e = make_tma_map_tile(&m.o1, a.d_gate, false, out_rows, I)) != cudaSuccess) return e;
+    if ((e = make_tma_map_tile(&m.o2, a.d_up, false, out_rows, I)) != cudaSuccess) return e;
     a.n_mtiles = I / 256;
     a.a_rows = H;
     a.ld = I;
@@ -34,8 +37,10 @@ cudaError_t launch_input_grad(const __nv_bfloat16* dg, const __nv_bfloat16* du, 
     cudaError_t e;
     if ((e = make_tma_map_bf16(&m.a0, Wg, (uint64_t)a.E * I, H, C::BK)) != cudaSuccess) return e;
     if ((e = make_tma_map_bf16(&m.a1, Wu, (uint64_t)a.E * I, H, C::BK)) != cudaSuccess) return e;
-    if ((e = make_tma_map_bf16(&m.b0, dg, rows, I, nb)) != cudaSuccess) return e;
-    if ((e = make_tma_map_bf16(&m.b1, du, rows, I, nb)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(&m.b0, &m.tail_b0, dg, rows, I, nb)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(&m.b1, &m.tail_b1, du, rows, I, nb)) != cudaSuccess) return e;
+    e = a.out32 ? make_tma_map_tile(&m.o0, a.out32, true, a.rows, H) : make_tma_map_tile(&m.o0, a.out, false, a.rows, H);
+    if (e != cudaSuccess) return e;
     a.n_mtiles = H / 256;
     a.a_rows = I;
     a.ld = H;
@@ -52,11 +57,14 @@ cudaError_t launch_weight_grad(const __nv_bfloat16* h, const __nv_bfloat16* dg,
     using C = tg::Cfg<tg::kWeights, kWideRows>;
     tg::Maps m = {};
     cudaError_t e;
-    if ((e = make_tma_map_bf16(&m.a0, h, rows, I, C::BK)) != cudaSuccess) return e;
-    if ((e = make_tma_map_bf16(&m.a1, x, xd_rows, H, C::BK)) != cudaSuccess) return e;
-    if ((e = make_tma_map_bf16(&m.b0, d, xd_rows, H, C::BK)) != cudaSuccess) return e;
-    if ((e = make_tma_map_bf16(&m.b1, dg, rows, I, C::BK)) != cudaSuccess) return e;
-    if ((e = make_tma_map_bf16(&m.b2, du, rows, I, C::BK)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(&m.a0, &m.tail_a0, h, rows, I, C::BK)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(&m.a1, &m.tail_a1, x, xd_rows, H, C::BK)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(&m.b0, &m.tail_b0, d, xd_rows, H, C::BK)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(&m.b1, &m.tail_b1, dg, rows, I, C::BK)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(&m.b2, &m.tail_b2, du, rows, I, C::BK)) != cudaSuccess) return e;
+    if ((e = make_tma_map_tile(&m.o0, a.out, false, (uint64_t)a.E * H, I)) != cudaSuccess) return e;
+    if ((e = make_tma_map_tile(&m.o1, a.d_gate, false, (uint64_t)a.E * I, H)) != cudaSuccess) return e;
+    if ((e = make_tma_map_tile(&m.o2, a.d_up, false, (uint64_t)a.E * I, H)) != cudaSuccess) return e;
     a.n_mtiles = I / 256;
     a.n_ntiles = H / 256;
     a.m_total = I;

@@ -12,7 +12,12 @@ cudaError_t launch_train_gate_up(const __nv_bfloat16* x, int64_t x_rows, const _
     cudaError_t e;
     if ((e = make_tma_map_bf16(&m.a0, Wg, (uint64_t)a.E * I, H, 128)) != cudaSuccess) return e;
     if ((e = make_tma_map_bf16(&m.a1, Wu, (uint64_t)a.E * I, H, 128)) != cudaSuccess) return e;
-    if ((e = make_tma_map_bf16(&m.b0, x, x_rows, H, nb)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(&m.b0, &m.tail_b0, x, x_rows, H, nb)) != cudaSuccess) return e;
+    if ((e = make_tma_map_tile(&m.o0, a.out, false, x_rows, I)) != cudaSuccess) return e;
+    if (!fp8) {
+        if ((e = make_tma_map_tile(&m.o1, a.gate, false, x_rows, I)) != cudaSuccess) return e;
+        if ((e = make_tma_map_tile(&m.o2, a.up, false, x_rows, I)) != cudaSuccess) return e;
+    }
     a.n_mtiles = I / 256;
     a.a_rows = I;
     a.ld = I;
@@ -29,7 +34,8 @@ cudaError_t launch_train_down(const __nv_bfloat16* h, int64_t h_rows, const __nv
     tg::Maps m = {};
     cudaError_t e;
     if ((e = make_tma_map_bf16(&m.a0, Wd, (uint64_t)a.E * H, I, 128)) != cudaSuccess) return e;
-    if ((e = make_tma_map_bf16(&m.b0, h, h_rows, I, nb)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(&m.b0, &m.tail_b0, h, h_rows, I, nb)) != cudaSuccess) return e;
+    if ((e = make_tma_map_tile(&m.o0, a.out, false, h_rows, H)) != cudaSuccess) return e;
     a.n_mtiles = H / 256;
     a.a_rows = H;
     a.ld = H;

@@ -8,55 +8,104 @@
 namespace moe {
 namespace {
 
-// Inclusive scan over the block's threads (blockDim.x <= 1024), with op + or max.
+constexpr int kThreads = 256;
+constexpr int kPerThread = kMaxE / kThreads;      // groups per thread
+
+// Exclusive scan over the block's threads, + or max (from 0).
 template <bool kMax>
-__device__ int block_scan(int v, int* warp_vals) {
+__device__ int scan_before(int v, int* warp_vals) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v = kMax ? max(v, u) : v + u;
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl = kMax ? max(incl, u) : incl + u;
     }
     __syncthreads();       // the values of a scan before have been read
-    if (lane == 31) warp_vals[w] = v;
+    if (lane == 31) warp_vals[w] = incl;
     __syncthreads();
-    for (int i = 0; i < w; ++i) v = kMax ? max(v, warp_vals[i]) : v + warp_vals[i];
-    return v;
+    int before = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane == 0) before = 0;
+    for (int i = 0; i < w; ++i) before = kMax ? max(before, warp_vals[i]) : before + warp_vals[i];
+    return before;
 }
 
-// A thread per group: offsets forced to ascend, then scans of the chunk
-// counts and of the padded row counts.
-__global__ void __launch_bounds__(1024)
+// The groups of offsets [E + 1], the same in every block that asks: first row
+// off[e] (forced to ascend inside [0, rows]) and first padded row pad[e].
+struct Groups {
+    int off[kMaxE + 1], pad[kMaxE + 1];
+    int warp_vals[kThreads / 32];
+};
+__device__ void scan_groups(Groups& g, const int32_t* offsets, int rows, int E, WsHeader* hdr) {
+    const int e0 = threadIdx.x * kPerThread;
+    int given[kPerThread], v[kPerThread];
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) given[i] = e0 + i < E ? ld::i32(offsets + e0 + i) : 0;
+    const int end = ld::i32(offsets + E);
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        v[i] = min(max(given[i], 0), rows);
+        if (i) v[i] = max(v[i], v[i - 1]);
+    }
+    const int before = scan_before<true>(v[kPerThread - 1], g.warp_vals);
+    bool bad = threadIdx.x == 0 && (given[0] != 0 || end != rows);
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        v[i] = max(v[i], before);
+        if (e0 + i < E) {
+            g.off[e0 + i] = v[i];
+            bad |= v[i] != given[i];
+            if (e0 + i == E - 1) g.off[E] = max(v[i], min(max(end, 0), rows));
+        }
+    }
+    if (bad && hdr) set_status(hdr, MOE_ERR_BAD_INDEX);
+    __syncthreads();
+    int p[kPerThread], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        p[i] = sum;
+        if (e0 + i < E) sum += (g.off[e0 + i + 1] - g.off[e0 + i] + 15) & ~15;
+    }
+    const int pad_before = scan_before<false>(sum, g.warp_vals);
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i)
+        if (e0 + i <= E) g.pad[e0 + i] = pad_before + p[i];
+    if (threadIdx.x == kThreads - 1 && E == kMaxE) g.pad[E] = pad_before + sum;
+    __syncthreads();
+}
+
+// The lists of the groups, by one block.
+__device__ void write_lists(Groups& g, int E, int most, const RowLists& l) {
+    const int e0 = threadIdx.x * kPerThread;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i)
+        if (e0 + i < E) {
+            const int c = g.off[e0 + i + 1] - g.off[e0 + i], size = chunk_size(c, most);
+            n += size ? (c + size - 1) / size : 0;
+        }
+    int at = scan_before<false>(n, g.warp_vals);
+    for (int e = e0; e < e0 + kPerThread && e < E; ++e) {
+        const int v = g.off[e], c = g.off[e + 1] - v, size = chunk_size(c, most);
+        RowChunk ch = {e, v, c, g.pad[e]};
+        l.groups[e] = ch;
+        for (int r = 0; r < c; r += size) {
+            ch.row0 = v + r;
+            ch.rows = min(size, c - r);
+            ch.row0_pad = g.pad[e] + r;
+            l.chunks[at++] = ch;
+        }
+    }
+    if (threadIdx.x == kThreads - 1) *l.n_chunks = at;     // no group behind it
+}
+
+__global__ void __launch_bounds__(kThreads)
 plan_rows_kernel(const int32_t* offsets, int rows, int E, int most, RowLists l, WsHeader* hdr) {
+    __shared__ Groups g;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    __shared__ int off[kMaxE + 1];
-    __shared__ int warp_vals[32];
-    const int e = threadIdx.x;
-    const int given = e < E ? ld::i32(offsets + e) : 0, end = ld::i32(offsets + E);
-    const int v = block_scan<true>(min(max(given, 0), rows), warp_vals);
-    if (e < E) off[e] = v;
-    if (e == E - 1) off[E] = max(v, min(max(end, 0), rows));
-    if ((e < E && v != given) || (e == 0 && (given != 0 || end != rows)))
-        set_status(hdr, MOE_ERR_BAD_INDEX);
-    __syncthreads();
-    const int c = e < E ? off[e + 1] - off[e] : 0;
-    const int size = chunk_size(c, most);
-    const int n = size ? (c + size - 1) / size : 0;
-    const int pad = (c + 15) & ~15;
-    const int n_incl = block_scan<false>(n, warp_vals);
-    const int pad_incl = block_scan<false>(pad, warp_vals);
-    if (e < E) {
-        RowChunk ch = {e, v, c, pad_incl - pad};
-        if (l.groups) l.groups[e] = ch;
-        for (int i = 0; i < n; ++i) {
-            ch.row0 = v + i * size;
-            ch.rows = min(size, c - i * size);
-            ch.row0_pad = pad_incl - pad + i * size;
-            l.chunks[n_incl - n + i] = ch;
-        }
-        if (e == E - 1) *l.n_chunks = n_incl;
-    }
+    scan_groups(g, offsets, rows, E, hdr);
+    write_lists(g, E, most, l);
 }
 
 // Eight e4m3 values (one 8-byte word) of one scale as bf16: exact.
@@ -77,74 +126,132 @@ __device__ __forceinline__ float scale_of(uint32_t b) {
     return __uint_as_float(b == 0 ? 1u << 22 : b == 255 ? 0x7fc00000u : b << 23);
 }
 
-// Warps take parts of 16 rows of the chunks in turn; a row is copied in
-// 16-byte vectors, eight per lane in flight.
-constexpr int kPartRows = 16;
-__global__ void __launch_bounds__(256)
-gather_rows_kernel(GatherJob g, RowLists l, int most) {
+// Forward: xs[p] = x[perm[p] / k] for the groups' rows, a warp per row, eight
+// 16-byte vectors per lane in flight; block 0 writes the lists.
+__global__ void __launch_bounds__(kThreads)
+forward_rows_kernel(const uint4* x, const int32_t* perm, int k, int vec, const int32_t* offsets, int P, int E,
+                    int most, uint4* xs, RowLists l, WsHeader* hdr) {
+    __shared__ Groups g;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
+    if (blockIdx.x == 0) {
+        scan_groups(g, offsets, P, E, hdr);
+        write_lists(g, E, most, l);
+    }
     const int lane = threadIdx.x & 31;
-    const int vec = g.H / 8;
-    const int per_chunk = most / kPartRows;
-    const int64_t parts = (int64_t)ld::i32(l.n_chunks) * per_chunk;
-    // a warp per row: the rows of a part are spread over the block's warps
-    for (int64_t part = blockIdx.x; part < parts; part += gridDim.x) {
-        const int4 c = *reinterpret_cast<const int4*>(l.chunks + part / per_chunk);
-        const int r0 = (int)(part % per_chunk) * kPartRows;
-        const int r1 = min(r0 + kPartRows, g.padded ? (c.z + 15) & ~15 : c.z);
-        for (int r = r0 + (int)(threadIdx.x >> 5); r < r1; r += (int)(blockDim.x >> 5)) {
-            const bool in = r < c.z;
-            const int64_t to = (int64_t)((g.padded ? c.w : c.y) + r) * vec;
-            const int slot = in ? ld::i32(g.perm + c.y + r) : 0;
-            const bool ok = in && slot >= 0 && slot < g.P;
-            const int64_t t = slot / g.k;
-            uint4* d0 = reinterpret_cast<uint4*>(g.dst0) + to;
-            uint4* d1 = reinterpret_cast<uint4*>(g.dst1) + to;
-            for (int i0 = lane; i0 < vec; i0 += 32 * 8) {
-                uint4 a[8], b[8];
+    for (int64_t p = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); p < P; p += (int64_t)gridDim.x * (kThreads / 32)) {
+        const int slot = ld::i32(perm + p);
+        if (slot < 0 || slot >= P) continue;
+        const uint4* from = x + (int64_t)(slot / k) * vec;
+        uint4* to = xs + p * vec;
+        for (int i0 = lane; i0 < vec; i0 += 32 * 8) {
+            uint4 a[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int i = i0 + 32 * j;
-                    a[j] = b[j] = make_uint4(0, 0, 0, 0);
-                    if (i < vec && ok) {
-                        if (g.src0_scales) {
-                            const uint2 q = reinterpret_cast<const uint2*>(g.src0)[t * vec + i];
-                            a[j] = widen8(q, scale_of(g.src0_scales[t * (g.H / 128) + (i >> 4)]));
-                        } else {
-                            a[j] = reinterpret_cast<const uint4*>(g.src0)[t * vec + i];
-                        }
-                        if (g.src1) b[j] = reinterpret_cast<const uint4*>(g.src1)[t * vec + i];
-                    }
+            for (int j = 0; j < 8; ++j)
+                if (i0 + 32 * j < vec) a[j] = from[i0 + 32 * j];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (i0 + 32 * j < vec) to[i0 + 32 * j] = a[j];
+        }
+    }
+}
+
+// Backward: each token's rows of x and d_out to the padded rows of its slots,
+// and zeros to the padding.  A warp takes a token, so that a row is read once
+// however many slots it has (by sorted row, x and d of 16384 tokens do not fit
+// L2 together and were read from memory k times: 631 us at 16384 x 4096, k = 8).
+__global__ void __launch_bounds__(kThreads)
+backward_rows_kernel(BackwardRows q) {
+    __shared__ Groups g;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    scan_groups(g, q.offsets, q.T * q.k, q.E, blockIdx.x == 0 ? q.hdr : nullptr);
+    if (blockIdx.x == 0) write_lists(g, q.E, q.most, q.lists);
+    const int lane = threadIdx.x & 31, vec = q.H / 8;
+    const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5),
+                  warps = (int64_t)gridDim.x * (kThreads / 32);
+    for (int64_t t = warp; t < q.T; t += warps) {
+        // lane j < k: the padded row of the token's slot j, -1 where it has none
+        int64_t mine = -1;
+        if (lane < q.k) {
+            const int slot = (int)(t * q.k) + lane, p = ld::i32(q.inv_perm + slot);
+            if (p >= 0 && p < g.off[q.E] && ld::i32(q.perm + p) == slot) {
+                int lo = 0, hi = q.E;          // the last group whose first row is not above p
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (g.off[mid] <= p) lo = mid;
+                    else hi = mid;
                 }
+                mine = ((int64_t)g.pad[lo] + (p - g.off[lo])) * vec;
+            }
+        }
+        for (int i0 = lane; i0 - lane < vec; i0 += 32 * 4) {
+            uint4 a[4], b[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 4; ++j) {
+                const int i = i0 + 32 * j;
+                if (i < vec) {
+                    if (q.x_scales)
+                        a[j] = widen8(reinterpret_cast<const uint2*>(q.x)[t * vec + i],
+                                      scale_of(q.x_scales[t * (q.H / 128) + (i >> 4)]));
+                    else
+                        a[j] = reinterpret_cast<const uint4*>(q.x)[t * vec + i];
+                    b[j] = reinterpret_cast<const uint4*>(q.d)[t * vec + i];
+                }
+            }
+            for (int s = 0; s < q.k; ++s) {
+                const int64_t to = __shfl_sync(0xffffffffu, mine, s);
+                if (to < 0) continue;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
                     const int i = i0 + 32 * j;
                     if (i < vec) {
-                        d0[i] = a[j];
-                        if (g.src1) d1[i] = b[j];
+                        reinterpret_cast<uint4*>(q.x_rows)[to + i] = a[j];
+                        reinterpret_cast<uint4*>(q.d_rows)[to + i] = b[j];
                     }
                 }
             }
         }
     }
+    for (int64_t e = warp; e < q.E; e += warps) {
+        const int c = g.off[e + 1] - g.off[e];
+        const int64_t from = ((int64_t)g.pad[e] + c) * vec, to = (int64_t)g.pad[e + 1] * vec;
+        for (int64_t i = from + lane; i < to; i += 32)
+            reinterpret_cast<uint4*>(q.x_rows)[i] = reinterpret_cast<uint4*>(q.d_rows)[i] = make_uint4(0, 0, 0, 0);
+    }
 }
 
-// The parts are fp32: rounding each slot's part to bf16 as well would make the
-// rounding error of d_x 1.22 times as large (relative RMS 2.9e-3 for 2.4e-3).
-__global__ void __launch_bounds__(256)
-sum_slots_kernel(const float4* y, const int32_t* inv, int T, int k, int vec, uint2* out) {
+// Per token: d_x = the sum of its slots' parts, in order of j, and each slot's
+// d_gate = the sum of its parts over the features (a warp per slot: lanes in
+// order, then a fixed tree).  The parts of d_x are fp32: rounding them to bf16
+// as well would make the rounding error of d_x 1.22 times as large (relative
+// RMS 2.9e-3 for 2.4e-3).
+__global__ void __launch_bounds__(kThreads)
+finish_kernel(const float4* y, uint2* d_x, const float* parts, int n_parts, float* d_gates, const int32_t* inv, int T,
+              int k, int vec) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int64_t P = (int64_t)T * k;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+        if (d_gates && warp < k) {
+            const int64_t s = t * k + warp;
+            const int64_t p = inv ? ld::i32(inv + s) : s;
+            float sum = 0.f;
+            if (p >= 0 && p < P)
+                for (int i = lane; i < n_parts; i += 32) sum += parts[(int64_t)i * P + p];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) d_gates[s] = sum;
+        }
+        if (!d_x) continue;
         int64_t src[kMaxK];
 #pragma unroll
         for (int j = 0; j < kMaxK; ++j) {
             const int p = j < k ? ld::i32(inv + t * k + j) : -1;
             src[j] = p >= 0 && p < P ? (int64_t)p * vec : -1;
         }
-        for (int v = threadIdx.x; v < vec; v += blockDim.x) {
+        for (int v = threadIdx.x; v < vec; v += kThreads) {
             float4 r[kMaxK];
 #pragma unroll
             for (int j = 0; j < kMaxK; ++j)
@@ -158,23 +265,10 @@ sum_slots_kernel(const float4* y, const int32_t* inv, int T, int k, int vec, uin
                 s.w += r[j].w;
             }
             const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
-            out[t * vec + v] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+            d_x[t * vec + v] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
                                           *reinterpret_cast<const uint32_t*>(&hi));
         }
     }
-}
-
-__global__ void __launch_bounds__(256)
-sum_gate_parts_kernel(const float* parts, int n, int P, const int32_t* inv, float* d_gates) {
-    ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
-    const int64_t s = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (s >= P) return;
-    const int p = inv ? ld::i32(inv + s) : (int)s;
-    float sum = 0.f;
-    if (p >= 0 && p < P)
-        for (int i = 0; i < n; ++i) sum += parts[(int64_t)i * P + p];
-    d_gates[s] = sum;
 }
 
 __global__ void __launch_bounds__(256)
@@ -191,28 +285,29 @@ dequantize_rows_kernel(const uint2* q, const uint8_t* scales, int64_t n, uint4* 
 
 cudaError_t launch_plan_rows(const int32_t* offsets, int rows, int E, int most, const RowLists& l,
                              WsHeader* hdr, cudaStream_t s) {
-    return launch_pdl(plan_rows_kernel, dim3(1), dim3((E + 31) / 32 * 32), 0, s, offsets, rows, E,
-                      most, l, hdr);
+    return launch_pdl(plan_rows_kernel, dim3(1), dim3(kThreads), 0, s, offsets, rows, E, most, l, hdr);
 }
 
-cudaError_t launch_gather_rows(const GatherJob& g, const RowLists& l, int64_t parts_bound, int most,
-                               int num_sms, cudaStream_t s) {
-    const int blocks = (int)(parts_bound < 8 * num_sms ? (parts_bound > 0 ? parts_bound : 1) : 8 * num_sms);
-    return launch_pdl(gather_rows_kernel, dim3(blocks), dim3(256), 0, s, g, l, most);
+cudaError_t launch_forward_rows(const __nv_bfloat16* x, const int32_t* perm, int k, int H,
+                                const int32_t* offsets, int P, int E, int most, __nv_bfloat16* xs,
+                                const RowLists& l, WsHeader* hdr, int num_sms, cudaStream_t s) {
+    const int64_t want = ((int64_t)P + 7) / 8;
+    return launch_pdl(forward_rows_kernel, dim3((unsigned)(want < 8 * num_sms ? want : 8 * num_sms)), dim3(kThreads), 0, s,
+                      reinterpret_cast<const uint4*>(x), perm, k, H / 8, offsets, P, E, most,
+                      reinterpret_cast<uint4*>(xs), l, hdr);
 }
 
-cudaError_t launch_sum_slots(const float* y, const int32_t* inv, int T, int k, int H,
-                             __nv_bfloat16* out, int num_sms, cudaStream_t s) {
+cudaError_t launch_backward_rows(const BackwardRows& q, int num_sms, cudaStream_t s) {
+    // a block per few tokens: few tokens are spread over blocks of their own
+    const int64_t want = q.T < num_sms ? q.T : ((int64_t)q.T + 7) / 8 < num_sms ? num_sms : ((int64_t)q.T + 7) / 8;
+    return launch_pdl(backward_rows_kernel, dim3((unsigned)(want < 8 * num_sms ? want : 8 * num_sms)), dim3(kThreads), 0, s, q);
+}
+
+cudaError_t launch_finish(const float* y, __nv_bfloat16* d_x, const float* parts, int n_parts, float* d_gates,
+                          const int32_t* inv, int T, int k, int H, int num_sms, cudaStream_t s) {
     const int blocks = T < 8 * num_sms ? T : 8 * num_sms;
-    return launch_pdl(sum_slots_kernel, dim3(blocks), dim3(256), 0, s,
-                      reinterpret_cast<const float4*>(y), inv, T, k, H / 4,
-                      reinterpret_cast<uint2*>(out));
-}
-
-cudaError_t launch_sum_gate_parts(const float* parts, int n, int P, const int32_t* inv,
-                                  float* d_gates, cudaStream_t s) {
-    return launch_pdl(sum_gate_parts_kernel, dim3((unsigned)(((int64_t)P + 255) / 256)), dim3(256), 0, s, parts, n, P,
-                      inv, d_gates);
+    return launch_pdl(finish_kernel, dim3(blocks), dim3(kThreads), 0, s, reinterpret_cast<const float4*>(y),
+                      reinterpret_cast<uint2*>(d_x), parts, n_parts, d_gates, inv, T, k, H / 4);
 }
 
 cudaError_t launch_dequantize_rows(const uint8_t* q, const uint8_t* scales, int64_t rows, int K,
