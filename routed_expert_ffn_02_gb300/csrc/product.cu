@@ -9,8 +9,16 @@ cudaError_t launch_product(const __nv_bfloat16* x, int64_t rows, const __nv_bflo
     using C = tg::Cfg<tg::kProduct, kWideRows>;
     tg::Maps m = {};
     cudaError_t e;
-    if ((e = make_tma_map_bf16(&m.a0, W, (uint64_t)a.E * N, K, 128)) != cudaSuccess) return e;
-    if ((e = tg::row_maps(&m.b0, &m.tail_b0, x, rows, K, nb)) != cudaSuccess) return e;
+    a.k_blocks = (K + C::BK - 1) / C::BK;
+    a.flat_from = K / C::BK;           // the block that K does not fill, if there is one
+    if (a.flat_from > 0) {
+        if ((e = make_tma_map_strips(&m.a0, W, (uint64_t)a.E * N, K, 128, C::KSUB)) != cudaSuccess) return e;
+        if ((e = tg::row_maps(m.b[0], x, rows, K, nb, C::KSUB)) != cudaSuccess) return e;
+    }
+    if (K % C::BK) {
+        if ((e = make_tma_map_bf16(&m.flat_a, W, (uint64_t)a.E * N, K, 128)) != cudaSuccess) return e;
+        if ((e = make_tma_map_bf16(&m.flat_b, x, rows, K, nb < 32 ? nb : 32)) != cudaSuccess) return e;
+    }
     a.map_out = N % (a.out32 ? 4 : 8) == 0;
     if (a.map_out) {
         e = a.out32 ? make_tma_map_tile(&m.o0, a.out32, true, rows, N) : make_tma_map_tile(&m.o0, a.out, false, rows, N);
@@ -20,7 +28,6 @@ cudaError_t launch_product(const __nv_bfloat16* x, int64_t rows, const __nv_bflo
     a.m_total = N;
     a.a_rows = N;
     a.ld = N;
-    a.k_blocks = (K + C::BK - 1) / C::BK;
     if (nb == kWideRows) return tg::launch<tg::kProduct, kWideRows>(m, a, num_sms, s);
     return tg::launch<tg::kProduct, kThinRows>(m, a, num_sms, s);
 }

@@ -77,7 +77,7 @@ struct Cfg {
     static constexpr int A_BYTES = MT * A_SUB;
     static constexpr int B_BYTES = NB * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    // rows of a box of B, and of the K rows of a weight gradient's last block
+    // what B's rows, and the K rows of a weight gradient's last block, are rounded up to
     static constexpr int BOX = NB < 32 ? NB : 32;
     static constexpr int STAGES = (192 * 1024) / STAGE_BYTES < 8 ? (192 * 1024) / STAGE_BYTES : 8;
     static constexpr int ACC_COLS = MT * BN;          // TMEM columns of one accumulator set
@@ -127,7 +127,7 @@ struct Item {
     int row0_pad;  // the same in the padded buffers
     int k_blocks;
     int k16_last;  // 16-deep steps of the last block
-    int boxes;     // boxes of B's rows that hold the chunk's (of one CTA)
+    int boxes;     // B's rows of one CTA, in boxes of BOX
 };
 
 template <int kKind, typename C>
@@ -180,16 +180,23 @@ __device__ __forceinline__ Item item_of(const TileArgs& a, int w) {
 }
 
 // Tensor maps, by kind:
-//   gated     a0 = Wg, a1 = Wu, b0 = x; o0 = h, o1 = gate, o2 = up
-//   hidden    a0 = Wd, b0 = d; o0 = w h, o1 = dg, o2 = du
-//   input     a0 = Wg, a1 = Wu, b0 = dg, b1 = du; o0 = d_x
-//   weights   a0 = w h, a1 = x, b0 = d, b1 = dg, b2 = du; o0 = dWd, o1 = dWg, o2 = dWu
-//   others    a0 = W, b0 = x; o0 = y
-// The tail maps have boxes of at most 32 rows, for chunks and groups that do
-// not fill the whole box; the o maps store 32 x 32 tiles.
+//   gated     a0 = Wg, a1 = Wu, b[0] = x; o0 = h, o1 = gate, o2 = up
+//   hidden    a0 = Wd, b[0] = d; o0 = w h, o1 = dg, o2 = du
+//   input     a0 = Wg, a1 = Wu, b[0] = dg, b[1] = du; o0 = d_x
+//   weights   a0 = w h, a1 = x, b = d, dg, du; o0 = dWd, o1 = dWg, o2 = dWu
+//   others    a0 = W, b[0] = x; o0 = y
+// Operands are seen as strips of 64 columns (make_tma_map_strips), so that one
+// copy loads a stage's tile of A or of B: the producer's copies, about 110
+// cycles each to issue, bounded every item with fewer than 256 rows when a
+// stage took 8 (K = 4096: 17.6 us for any N from 96 to 192).  b[..][i] holds
+// boxes of 32 (i + 1) rows, for chunks of so many rows (a CTA's half, rounded
+// up); weights: [0] 32 and [3] 128 rows of K, of a and b.  flat: 64-column
+// boxes, zero beyond the last column, for a product's K behind its last whole
+// strip.
 struct Maps {
-    CUtensorMap a0, a1, b0, b1, b2;
-    CUtensorMap tail_a0, tail_a1, tail_b0, tail_b1, tail_b2;
+    CUtensorMap a0, a1, tail_a0, tail_a1;
+    CUtensorMap b[3][4];
+    CUtensorMap flat_a, flat_b;
     CUtensorMap o0, o1, o2;
 };
 
@@ -811,10 +818,10 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
     }
     if (warp == 0 && lane == 0) {
         prefetch_map(&maps.a0);
-        prefetch_map(&maps.b0);
+        prefetch_map(&maps.b[0][C::NB / C::BOX - 1]);
         if (gated(kKind) || kKind == kInput || kKind == kWeights) prefetch_map(&maps.a1);
-        if (kKind == kInput || kKind == kWeights) prefetch_map(&maps.b1);
-        if (kKind == kWeights) prefetch_map(&maps.b2);
+        if (kKind == kInput || kKind == kWeights) prefetch_map(&maps.b[1][C::NB / C::BOX - 1]);
+        if (kKind == kWeights) prefetch_map(&maps.b[2][C::NB / C::BOX - 1]);
     }
     if (warp == 2) tmem_alloc_pair(smem_u32(tmem_holder), C::TMEM_COLS);
     fence_before();
@@ -838,11 +845,6 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
         for (int w = cluster; ok && w < total; w += n_clusters) {
             const Item it = item_of<kKind, C>(args, w);
             const int m = it.m0 + (int)rank * 128;
-            const CUtensorMap *ma = &maps.a0, *mb = &maps.b0;
-            if constexpr (kKind == kWeights) {
-                if (it.mat > 0) ma = &maps.a1;
-                mb = it.mat == 0 ? &maps.b0 : it.mat == 1 ? &maps.b1 : &maps.b2;
-            }
             for (int kb = 0; kb < it.k_blocks; ++kb) {
                 if (!mbar_wait_for(empty_bar(stage), phase ^ 1u, args.wait_cycles, abort_flag)) {
                     ok = false;
@@ -860,61 +862,50 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                     stage_bytes[stage] = bytes;
                     if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * bytes);
                     if (!tail) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            tma_load_2d_pair(sa + j * C::BK * 128, ma, fb, m + 64 * j, krow);
-                            tma_load_2d_pair(sb + j * C::BK * 128, mb, fb, n + 64 * j, krow);
-                        }
+                        tma_load_3d_pair(sa, it.mat ? &maps.a1 : &maps.a0, fb, 0, krow, m / 64);
+                        tma_load_3d_pair(sb, &maps.b[it.mat][3], fb, 0, krow, n / 64);
                     } else {
-                        const CUtensorMap *ta = it.mat ? &maps.tail_a1 : &maps.tail_a0,
-                                          *tb = it.mat == 0 ? &maps.tail_b0 : it.mat == 1 ? &maps.tail_b1 : &maps.tail_b2;
+                        // (in 64-wide strips of 32 rows each, where the whole block's are)
                         for (int q = 0; q < boxes; ++q)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                tma_load_2d_pair(sa + j * C::BK * 128 + q * 32 * 128, ta, fb, m + 64 * j, krow + 32 * q);
-                                tma_load_2d_pair(sb + j * C::BK * 128 + q * 32 * 128, tb, fb, n + 64 * j, krow + 32 * q);
+                                const uint32_t to = j * C::BK * 128 + q * 32 * 128;
+                                tma_load_3d_pair(sa + to, it.mat ? &maps.tail_a1 : &maps.tail_a0, fb, 0, krow + 32 * q, m / 64 + j);
+                                tma_load_3d_pair(sb + to, &maps.b[it.mat][0], fb, 0, krow + 32 * q, n / 64 + j);
                             }
                     }
                 } else {
-                    // B: the boxes that hold the chunk's rows, no more
-                    const bool whole = it.boxes * C::BOX == C::NB;
+                    // B: the rows of the chunk, rounded up to a box, no more
                     const uint32_t bytes = (uint32_t)(C::A_BYTES + it.boxes * C::BOX * C::BK * 2);
                     stage_bytes[stage] = bytes;
                     if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * bytes);
+                    const CUtensorMap *ma = &maps.a0, *mb = &maps.b[0][it.boxes - 1];
                     if constexpr (kKind == kInput) {
                         if (kb >= args.seg_blocks) {      // the second product of the sum
                             k -= args.seg_blocks * C::BK;
                             ma = &maps.a1;
-                            mb = &maps.b1;
-                        }
-                    }
-#pragma unroll
-                    for (int mt = 0; mt < C::MT; ++mt) {
-                        const CUtensorMap* mam = gated(kKind) && mt == 1 ? &maps.a1 : ma;
-                        if constexpr (C::kAMN) {
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                tma_load_2d_pair(sa + mt * C::A_SUB + j * C::BK * 128, mam, fb, m + 64 * j,
-                                                 it.expert * args.a_rows + k);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < C::KSUB; ++j)
-                                tma_load_2d_pair(sa + mt * C::A_SUB + j * 128 * 128, mam, fb, k + 64 * j,
-                                                 it.expert * args.a_rows + m);
+                            mb = &maps.b[1][it.boxes - 1];
                         }
                     }
                     // the odd CTA holds the upper half of the N rows
                     const int brow = (args.padded ? it.row0_pad : it.row0) + (int)rank * (it.n >> 1);
-                    if (whole) {
-#pragma unroll
-                        for (int j = 0; j < C::KSUB; ++j)
-                            tma_load_2d_pair(sb + j * C::NB * 128, mb, fb, k + 64 * j, brow);
+                    if (kKind == kProduct && kb >= args.flat_from) {
+                        for (int j = 0; j < C::KSUB; ++j) {
+                            tma_load_2d_pair(sa + j * 128 * 128, &maps.flat_a, fb, k + 64 * j, it.expert * args.a_rows + m);
+                            for (int q = 0; q < it.boxes; ++q)
+                                tma_load_2d_pair(sb + (j * it.boxes + q) * C::BOX * 128, &maps.flat_b, fb, k + 64 * j,
+                                                 brow + q * C::BOX);
+                        }
                     } else {
-                        const CUtensorMap* tb = mb == &maps.b0 ? &maps.tail_b0 : &maps.tail_b1;
-                        for (int q = 0; q < it.boxes; ++q)
 #pragma unroll
-                            for (int j = 0; j < C::KSUB; ++j)
-                                tma_load_2d_pair(sb + j * C::NB * 128 + q * C::BOX * 128, tb, fb, k + 64 * j, brow + q * C::BOX);
+                        for (int mt = 0; mt < C::MT; ++mt) {
+                            const CUtensorMap* mam = gated(kKind) && mt == 1 ? &maps.a1 : ma;
+                            if constexpr (C::kAMN)
+                                tma_load_3d_pair(sa + mt * C::A_SUB, mam, fb, 0, it.expert * args.a_rows + k, m / 64);
+                            else
+                                tma_load_3d_pair(sa + mt * C::A_SUB, mam, fb, 0, it.expert * args.a_rows + m, k / 64);
+                        }
+                        tma_load_3d_pair(sb, mb, fb, 0, brow, k / 64);
                     }
                 }
                 ++fills;
@@ -944,6 +935,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
             fence_after();
             const uint32_t d_tmem = tmem_base + (uint32_t)(acc * C::ACC_COLS);
             const uint32_t idesc = idesc_for<C::kAMN, C::kBMN>(it.n);
+            [[maybe_unused]] const uint32_t b_strip = (uint32_t)(it.boxes * C::BOX * 128);
             for (int kb = 0; kb < it.k_blocks; ++kb) {
                 if (!mbar_wait_for(full_bar(stage), phase, args.wait_cycles, abort_flag)) {
                     ok = false;
@@ -957,7 +949,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                     if (kKind == kWeights && kk >= steps) break;
                     uint64_t bd;
                     if constexpr (C::kBMN) bd = mn_desc(sb + kk * 2048, C::BK * 128);
-                    else bd = sw128_desc(sb + (kk / 4) * C::NB * 128) + (uint64_t)((kk % 4) * 2);
+                    else bd = sw128_desc(sb + (kk / 4) * b_strip) + (uint64_t)((kk % 4) * 2);
 #pragma unroll
                     for (int mt = 0; mt < C::MT; ++mt) {
                         uint64_t ad;
@@ -1097,12 +1089,14 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
     }
 }
 
-// The whole-box and tail maps of an operand whose rows are the groups'.
-inline cudaError_t row_maps(CUtensorMap* whole, CUtensorMap* tail, const __nv_bfloat16* p, int64_t rows, int cols,
-                            int box) {
-    const cudaError_t e = make_tma_map_bf16(whole, p, (uint64_t)rows, (uint64_t)cols, (uint32_t)box);
-    if (e != cudaSuccess) return e;
-    return make_tma_map_bf16(tail, p, (uint64_t)rows, (uint64_t)cols, (uint32_t)(box < 32 ? box : 32));
+// Maps of the rows operand b (chunks of at most 2 * nb rows), ksub strips of K per stage.
+inline cudaError_t row_maps(CUtensorMap (&b)[4], const __nv_bfloat16* p, int64_t rows, int cols, int nb, int ksub) {
+    if (nb < 32) return make_tma_map_strips(&b[0], p, (uint64_t)rows, (uint64_t)cols, (uint32_t)nb, (uint32_t)ksub);
+    for (int i = 0; i < nb / 32; ++i) {
+        const cudaError_t e = make_tma_map_strips(&b[i], p, (uint64_t)rows, (uint64_t)cols, 32u * (i + 1), (uint32_t)ksub);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 template <int kKind, int kNB>

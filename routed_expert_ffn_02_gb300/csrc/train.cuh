@@ -65,6 +65,7 @@ struct TileArgs {
     int a_rows;                // rows of A per expert
     int k_blocks;
     int seg_blocks;            // input gradient: blocks of the first product
+    int flat_from;             // product: first block of K with a partial strip
     int64_t ld;                // features of an output row
     long long wait_cycles;
     // Buffers by kind (see the epilogues).

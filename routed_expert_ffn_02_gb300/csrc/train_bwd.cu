@@ -13,8 +13,8 @@ cudaError_t launch_hidden_grad(const __nv_bfloat16* d, int64_t d_rows, const __n
     using C = tg::Cfg<tg::kHidden, kWideRows>;
     tg::Maps m = {};
     cudaError_t e;
-    if ((e = make_tma_map_bf16(&m.a0, Wd, (uint64_t)a.E * H, I, C::BK)) != cudaSuccess) return e;
-    if ((e = tg::row_maps(&m.b0, &m.tail_b0, d, d_rows, H, nb)) != cudaSuccess) return e;
+    if ((e = make_tma_map_strips(&m.a0, Wd, (uint64_t)a.E * H, I, C::BK, 2)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(m.b[0], d, d_rows, H, nb, C::KSUB)) != cudaSuccess) return e;
     if ((e = make_tma_map_tile(&m.o0, a.out, false, out_rows, I)) != cudaSuccess) return e;
     if ((e = make_tma_map_tile(&m.o1, a.d_gate, false, out_rows, I)) != cudaSuccess) return e;
     if ((e = make_tma_map_tile(&m.o2, a.d_up, false, out_rows, I)) != cudaSuccess) return e;
@@ -35,10 +35,10 @@ cudaError_t launch_input_grad(const __nv_bfloat16* dg, const __nv_bfloat16* du, 
     using C = tg::Cfg<tg::kInput, kWideRows>;
     tg::Maps m = {};
     cudaError_t e;
-    if ((e = make_tma_map_bf16(&m.a0, Wg, (uint64_t)a.E * I, H, C::BK)) != cudaSuccess) return e;
-    if ((e = make_tma_map_bf16(&m.a1, Wu, (uint64_t)a.E * I, H, C::BK)) != cudaSuccess) return e;
-    if ((e = tg::row_maps(&m.b0, &m.tail_b0, dg, rows, I, nb)) != cudaSuccess) return e;
-    if ((e = tg::row_maps(&m.b1, &m.tail_b1, du, rows, I, nb)) != cudaSuccess) return e;
+    if ((e = make_tma_map_strips(&m.a0, Wg, (uint64_t)a.E * I, H, C::BK, 2)) != cudaSuccess) return e;
+    if ((e = make_tma_map_strips(&m.a1, Wu, (uint64_t)a.E * I, H, C::BK, 2)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(m.b[0], dg, rows, I, nb, C::KSUB)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(m.b[1], du, rows, I, nb, C::KSUB)) != cudaSuccess) return e;
     e = a.out32 ? make_tma_map_tile(&m.o0, a.out32, true, a.rows, H) : make_tma_map_tile(&m.o0, a.out, false, a.rows, H);
     if (e != cudaSuccess) return e;
     a.n_mtiles = H / 256;
@@ -57,11 +57,20 @@ cudaError_t launch_weight_grad(const __nv_bfloat16* h, const __nv_bfloat16* dg,
     using C = tg::Cfg<tg::kWeights, kWideRows>;
     tg::Maps m = {};
     cudaError_t e;
-    if ((e = tg::row_maps(&m.a0, &m.tail_a0, h, rows, I, C::BK)) != cudaSuccess) return e;
-    if ((e = tg::row_maps(&m.a1, &m.tail_a1, x, xd_rows, H, C::BK)) != cudaSuccess) return e;
-    if ((e = tg::row_maps(&m.b0, &m.tail_b0, d, xd_rows, H, C::BK)) != cudaSuccess) return e;
-    if ((e = tg::row_maps(&m.b1, &m.tail_b1, dg, rows, I, C::BK)) != cudaSuccess) return e;
-    if ((e = tg::row_maps(&m.b2, &m.tail_b2, du, rows, I, C::BK)) != cudaSuccess) return e;
+    const struct {
+        CUtensorMap *whole, *tail;      // 128 and 32 rows of K
+        const __nv_bfloat16* p;
+        int64_t rows;
+        int cols;
+    } operands[] = {{&m.a0, &m.tail_a0, h, rows, I},
+                    {&m.a1, &m.tail_a1, x, xd_rows, H},
+                    {&m.b[0][3], &m.b[0][0], d, xd_rows, H},
+                    {&m.b[1][3], &m.b[1][0], dg, rows, I},
+                    {&m.b[2][3], &m.b[2][0], du, rows, I}};
+    for (const auto& q : operands) {
+        if ((e = make_tma_map_strips(q.whole, q.p, q.rows, q.cols, C::BK, 2)) != cudaSuccess) return e;
+        if ((e = make_tma_map_strips(q.tail, q.p, q.rows, q.cols, 32, 1)) != cudaSuccess) return e;
+    }
     if ((e = make_tma_map_tile(&m.o0, a.out, false, (uint64_t)a.E * H, I)) != cudaSuccess) return e;
     if ((e = make_tma_map_tile(&m.o1, a.d_gate, false, (uint64_t)a.E * I, H)) != cudaSuccess) return e;
     if ((e = make_tma_map_tile(&m.o2, a.d_up, false, (uint64_t)a.E * I, H)) != cudaSuccess) return e;

@@ -10,9 +10,10 @@ cudaError_t launch_train_gate_up(const __nv_bfloat16* x, int64_t x_rows, const _
                                  TileArgs a, int num_sms, cudaStream_t s) {
     tg::Maps m = {};
     cudaError_t e;
-    if ((e = make_tma_map_bf16(&m.a0, Wg, (uint64_t)a.E * I, H, 128)) != cudaSuccess) return e;
-    if ((e = make_tma_map_bf16(&m.a1, Wu, (uint64_t)a.E * I, H, 128)) != cudaSuccess) return e;
-    if ((e = tg::row_maps(&m.b0, &m.tail_b0, x, x_rows, H, nb)) != cudaSuccess) return e;
+    using C = tg::Cfg<tg::kGated, kWideRows>;
+    if ((e = make_tma_map_strips(&m.a0, Wg, (uint64_t)a.E * I, H, 128, C::KSUB)) != cudaSuccess) return e;
+    if ((e = make_tma_map_strips(&m.a1, Wu, (uint64_t)a.E * I, H, 128, C::KSUB)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(m.b[0], x, x_rows, H, nb, C::KSUB)) != cudaSuccess) return e;
     if ((e = make_tma_map_tile(&m.o0, a.out, false, x_rows, I)) != cudaSuccess) return e;
     if (!fp8) {
         if ((e = make_tma_map_tile(&m.o1, a.gate, false, x_rows, I)) != cudaSuccess) return e;
@@ -21,7 +22,7 @@ cudaError_t launch_train_gate_up(const __nv_bfloat16* x, int64_t x_rows, const _
     a.n_mtiles = I / 256;
     a.a_rows = I;
     a.ld = I;
-    a.k_blocks = H / tg::Cfg<tg::kGated, kWideRows>::BK;
+    a.k_blocks = H / C::BK;
     if (nb == kWideRows)
         return fp8 ? tg::launch<tg::kGatedFp8, kWideRows>(m, a, num_sms, s)
                    : tg::launch<tg::kGated, kWideRows>(m, a, num_sms, s);
@@ -33,13 +34,14 @@ cudaError_t launch_train_down(const __nv_bfloat16* h, int64_t h_rows, const __nv
                               int H, int I, int nb, TileArgs a, int num_sms, cudaStream_t s) {
     tg::Maps m = {};
     cudaError_t e;
-    if ((e = make_tma_map_bf16(&m.a0, Wd, (uint64_t)a.E * H, I, 128)) != cudaSuccess) return e;
-    if ((e = tg::row_maps(&m.b0, &m.tail_b0, h, h_rows, I, nb)) != cudaSuccess) return e;
+    using C = tg::Cfg<tg::kRows, kWideRows>;
+    if ((e = make_tma_map_strips(&m.a0, Wd, (uint64_t)a.E * H, I, 128, C::KSUB)) != cudaSuccess) return e;
+    if ((e = tg::row_maps(m.b[0], h, h_rows, I, nb, C::KSUB)) != cudaSuccess) return e;
     if ((e = make_tma_map_tile(&m.o0, a.out, false, h_rows, H)) != cudaSuccess) return e;
     a.n_mtiles = H / 256;
     a.a_rows = H;
     a.ld = H;
-    a.k_blocks = I / tg::Cfg<tg::kRows, kWideRows>::BK;
+    a.k_blocks = I / C::BK;
     if (nb == kWideRows) return tg::launch<tg::kRows, kWideRows>(m, a, num_sms, s);
     return tg::launch<tg::kRows, kThinRows>(m, a, num_sms, s);
 }
