@@ -204,7 +204,16 @@ struct Maps {
 __device__ __forceinline__ float scale_value(uint32_t b) {
     return __uint_as_float(b == 0 ? 1u << 22 : b == 255 ? 0x7fc00000u : b << 23);
 }
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// 1 / (1 + exp(-g)) by the hardware's 2^x and reciprocal (2^-22 and one unit in
+// the last place), subnormals flushed: the library's __expf and __fdividef take
+// twice the instructions for them, and the epilogues are bound by those
+// (a block of store_hidden: 5000 cycles of which 2/3 were this).
+__device__ __forceinline__ float sigmoid(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
 __device__ __forceinline__ float2 unpack(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
@@ -417,6 +426,52 @@ __device__ __forceinline__ float feature_sums(float (&v)[4][2], int lane, int* r
 
 // ---- epilogues: one warp's 32 features from f0, 32 rows from c0 ---------------
 
+// Largest magnitudes (as integers, which order them alike) of row c0 + lane of
+// the two projections over the CTA's 128 features: each lane takes its
+// features', the eight lanes of a row theirs, and the four warps exchange
+// theirs through shared memory.  NaN does not count, nor, with kFinite, do
+// infinities.
+template <bool kFinite>
+__device__ __forceinline__ void block_maxima(const Frag& g, const Frag& u, const Warp& w, uint32_t* mg, uint32_t* mu) {
+    const int lane = w.lane;
+    uint32_t m[2][8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float a = 0.f, b = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a = fmaxf(a, kFinite ? fp8::finite_abs(g.v[i][j][s]) : fabsf(g.v[i][j][s]));
+                b = fmaxf(b, kFinite ? fp8::finite_abs(u.v[i][j][s]) : fabsf(u.v[i][j][s]));
+            }
+            m[0][2 * j + s] = __float_as_uint(a);
+            m[1][2 * j + s] = __float_as_uint(b);
+        }
+#pragma unroll
+    for (int o = 16, n = 4; o >= 4; o >>= 1, n >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const uint32_t keep = up ? m[z][i + n] : m[z][i], send = up ? m[z][i] : m[z][i + n];
+                m[z][i] = max(keep, __shfl_xor_sync(0xffffffffu, send, o));
+            }
+    }
+    const int row = ((lane >> 4) & 1) * 16 + ((lane >> 3) & 1) * 8 + (lane & 3) * 2 + ((lane >> 2) & 1);
+    if (kFinite) asm volatile("bar.sync %0, 128;" ::"r"(w.bar_id) : "memory");   // the first exchange has been read
+    w.amax[w.quad * 32 + row] = m[0][0];
+    w.amax[128 + w.quad * 32 + row] = m[1][0];
+    asm volatile("bar.sync %0, 128;" ::"r"(w.bar_id) : "memory");
+    *mg = *mu = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        *mg = max(*mg, w.amax[q * 32 + lane]);
+        *mu = max(*mu, w.amax[128 + q * 32 + lane]);
+    }
+}
+
 // h = silu(g) u, with g and u kept.
 template <int kKind>
 __device__ __forceinline__ void store_gated(const TileArgs& a, const Item& it, int f0, int c0,
@@ -439,44 +494,13 @@ __device__ __forceinline__ void store_gated(const TileArgs& a, const Item& it, i
         store_packed<kTiles>(w, pack(g), out(maps.o1, a.gate));
         store_packed<kTiles>(w, pack(u), out(maps.o2, a.up));
     } else {
-        // The block's scale covers 128 features: each lane takes the maxima of
-        // its features, the eight lanes of a row then theirs, and the four
-        // warps of the CTA's 128 lanes exchange them through shared memory.
-        uint32_t m[2][8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                float mg = 0.f, mu = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    mg = fmaxf(mg, fp8::finite_abs(g.v[i][j][s]));
-                    mu = fmaxf(mu, fp8::finite_abs(u.v[i][j][s]));
-                }
-                m[0][2 * j + s] = __float_as_uint(mg);      // magnitudes: ordered as integers
-                m[1][2 * j + s] = __float_as_uint(mu);
-            }
-#pragma unroll
-        for (int o = 16, n = 4; o >= 4; o >>= 1, n >>= 1) {
-            const bool up = lane & o;
-#pragma unroll
-            for (int z = 0; z < 2; ++z)
-#pragma unroll
-                for (int i = 0; i < n; ++i) {
-                    const uint32_t keep = up ? m[z][i + n] : m[z][i], send = up ? m[z][i] : m[z][i + n];
-                    m[z][i] = max(keep, __shfl_xor_sync(0xffffffffu, send, o));
-                }
-        }
-        const int row = ((lane >> 4) & 1) * 16 + ((lane >> 3) & 1) * 8 + (lane & 3) * 2 + ((lane >> 2) & 1);
-        w.amax[w.quad * 32 + row] = m[0][0];
-        w.amax[128 + w.quad * 32 + row] = m[1][0];
-        asm volatile("bar.sync %0, 128;" ::"r"(w.bar_id) : "memory");
-        uint32_t mg = 0, mu = 0;                          // of row c0 + lane
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            mg = max(mg, w.amax[q * 32 + lane]);
-            mu = max(mu, w.amax[128 + q * 32 + lane]);
-        }
+        // a block's scale covers 128 features
+        uint32_t mg, mu;                                  // of row c0 + lane
+        block_maxima<false>(g, u, w, &mg, &mu);
+        // an infinity among them: the maxima of the finite values (rare; the
+        // four warps see the same maxima, so they go this way together)
+        const bool infinite = __any_sync(0xffffffffu, max(mg, mu) == 0x7f800000u);
+        if (infinite) block_maxima<true>(g, u, w, &mg, &mu);
         const uint32_t sg = fp8::scale_byte(__uint_as_float(mg)),
                        su = fp8::scale_byte(__uint_as_float(mu));
         if (w.quad == 0 && lane < left) {
@@ -493,9 +517,11 @@ __device__ __forceinline__ void store_gated(const TileArgs& a, const Item& it, i
             for (int s = 0; s < 2; ++s) {
                 const int r = 8 * j + 2 * (lane & 3) + s;
                 const float xg = __shfl_sync(0xffffffffu, ig, r), xu = __shfl_sync(0xffffffffu, iu, r);
+                // (the conversion keeps NaN and would saturate infinities)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    b[s][i] = fp8::pack_e4m3x2(fp8::scaled(g.v[i][j][s], xg), fp8::scaled(u.v[i][j][s], xu));
+                    b[s][i] = infinite ? fp8::pack_e4m3x2(fp8::scaled(g.v[i][j][s], xg), fp8::scaled(u.v[i][j][s], xu))
+                                       : fp8::pack_e4m3x2(g.v[i][j][s] * xg, u.v[i][j][s] * xu);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) q.v[i][j] = b[0][i] | b[1][i] << 16;
@@ -570,16 +596,23 @@ __device__ __forceinline__ void store_f32(Warp& w, const Frag& f, const CUtensor
 template <int kKind>
 struct KeptRows {
     RowVecs g, u;
+    float w;            // the gate of row c0 + lane
 };
 template <>
 struct KeptRows<kHiddenFp8> {
     RowBytes g, u;
+    float w;
 };
 template <int kKind>
 __device__ __forceinline__ void load_kept(KeptRows<kKind>& k, const TileArgs& a, const Item& it, int f0,
                                           int c0, int lane) {
     const int left = it.rows - c0;
     const int64_t at = (int64_t)(it.row0 + c0) * a.ld + f0;
+    k.w = 1.f;
+    if (a.gates && lane < left) {
+        const int r = it.row0 + c0 + lane, slot = a.perm ? a.perm[r] : r;
+        k.w = slot >= 0 && slot < a.rows ? a.gates[slot] : 0.f;
+    }
     if constexpr (kKind == kHidden) {
         load_rows(k.g, static_cast<const __nv_bfloat16*>(a.gate) + at, a.ld, left, lane);
         load_rows(k.u, static_cast<const __nv_bfloat16*>(a.up) + at, a.ld, left, lane);
@@ -591,31 +624,30 @@ __device__ __forceinline__ void load_kept(KeptRows<kKind>& k, const TileArgs& a,
 }
 
 // With q = d Wd (this accumulator), s = sigmoid(g), w the row's gate:
-//   h = g s u,  dh = w q,  du = dh g s,  dg = dh u s (1 + g (1 - s)),
+//   h = g s u,  dh = w q,  du = dh g s,  dg = dh u (s + g s (1 - s)),
 //   d_gate = sum_i q_i h_i  (a part of it here: this warp's 32 features).
 // dg, du and w h are rounded to bf16, the operands of the next products.
 template <int kKind>
 __device__ __forceinline__ void store_hidden(const TileArgs& a, const Item& it, int f0, int c0,
-                                             const Frag& q, const Packed& kg, const Packed& ku,
+                                             Frag& q, const Packed& kg, const Packed& ku, float w,
                                              const Maps& maps, Warp& wp) {
     const int left = it.rows - c0, pad = it.n - c0, lane = wp.lane;
-    float w = 1.f;
-    if (a.gates && lane < left) {
-        const int r = it.row0 + c0 + lane, slot = a.perm ? a.perm[r] : r;
-        w = slot >= 0 && slot < a.rows ? a.gates[slot] : 0.f;
+    if (left < 32) {       // rows up to the next multiple of 16 become zero (g and u are already)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (8 * j + 2 * (lane & 3) + s >= left)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) q.v[i][j][s] = 0.f;
     }
     Packed dg, du, ho;
     float part[4][2] = {};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         float wr[2];
-        bool in[2];      // rows up to the next multiple of 16 are zero
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int r = 8 * j + 2 * (lane & 3) + s;
-            wr[s] = __shfl_sync(0xffffffffu, w, r);
-            in[s] = r < left;
-        }
+        for (int s = 0; s < 2; ++s) wr[s] = __shfl_sync(0xffffffffu, w, 8 * j + 2 * (lane & 3) + s);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 g2 = unpack(kg.v[i][j]), u2 = unpack(ku.v[i][j]);
@@ -624,10 +656,10 @@ __device__ __forceinline__ void store_hidden(const TileArgs& a, const Item& it, 
             for (int s = 0; s < 2; ++s) {
                 const float g = s ? g2.y : g2.x, u = s ? u2.y : u2.x, qv = q.v[i][j][s];
                 const float sg = sigmoid(g), gs = g * sg, h = gs * u, dh = wr[s] * qv;
-                if (in[s]) part[j][s] = fmaf(qv, h, part[j][s]);
-                og[s] = in[s] ? dh * u * sg * fmaf(g, 1.f - sg, 1.f) : 0.f;
-                ou[s] = in[s] ? dh * gs : 0.f;
-                oh[s] = in[s] ? wr[s] * h : 0.f;
+                part[j][s] = fmaf(qv, h, part[j][s]);
+                og[s] = dh * u * fmaf(gs, 1.f - sg, sg);
+                ou[s] = dh * gs;
+                oh[s] = wr[s] * h;
             }
             dg.v[i][j] = pack_bf16(og[0], og[1]);
             du.v[i][j] = pack_bf16(ou[0], ou[1]);
@@ -1035,9 +1067,10 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                     __syncwarp();
                     tile_to_frag(wp.tiles, g, lane);
                     tile_to_frag(wp.tiles + kTileBytes, u, lane);
+                    const float gate = kept.w;
                     if (c0 + 64 < n) load_kept<kKind>(kept, args, it, f0, c0 + 64, lane);
                     tmem_ld_wait();
-                    store_hidden<kKind>(args, it, f0, c0, v, g, u, maps, wp);
+                    store_hidden<kKind>(args, it, f0, c0, v, g, u, gate, maps, wp);
                 } else {
                     if (kKind == kWeights && it.rows == 0) {      // a group without rows: zeros
                         v = Frag{};
