@@ -466,12 +466,13 @@ cudaError_t make_tma_map_strips(CUtensorMap* m, const void* ptr, uint64_t rows, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_tma_map_tile(CUtensorMap* m, const void* ptr, bool f32, uint64_t rows, uint64_t cols) {
+cudaError_t make_tma_map_tile(CUtensorMap* m, const void* ptr, bool f32, uint64_t rows, uint64_t cols,
+                              uint32_t box_rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return cudaErrorNotSupported;
     cuuint64_t dims[2] = {cols, rows};
     cuuint64_t strides[1] = {cols * (f32 ? 4 : 2)};
-    cuuint32_t box[2] = {32u, 32u};
+    cuuint32_t box[2] = {32u, box_rows};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                     const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -150,8 +150,9 @@ cudaError_t make_tma_map_u8(CUtensorMap* m, const void* ptr, uint64_t rows, uint
 // that one copy loads several of the 128-byte-wide tiles the MMA reads.
 cudaError_t make_tma_map_strips(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
                                 uint32_t box_strips);
-// Map for storing 32 x 32 tiles (box = 32 columns x 32 rows) of bf16 (64-byte
+// Map for storing tiles (box = 32 columns x box_rows) of bf16 (64-byte
 // swizzle) or fp32 (128-byte swizzle).
-cudaError_t make_tma_map_tile(CUtensorMap* m, const void* ptr, bool f32, uint64_t rows, uint64_t cols);
+cudaError_t make_tma_map_tile(CUtensorMap* m, const void* ptr, bool f32, uint64_t rows, uint64_t cols,
+                              uint32_t box_rows = 32);
 
 }  // namespace moe

@@ -680,14 +680,22 @@ __device__ __forceinline__ void store_hidden(const TileArgs& a, const Item& it, 
     }
 }
 
+// 64 rows of a weight gradient from c0 (always whole), in one copy out of both
+// staging tiles: half the fences, barriers and copies of 32-row blocks.
 __device__ __forceinline__ void store_weights(const TileArgs& a, const Item& it, int f0, int c0,
-                                              const Frag& v, const Maps& maps, Warp& w) {
-    const int64_t ld = it.mat == 0 ? a.m_total : a.n_total;      // I, H
-    const int64_t rows = it.mat == 0 ? a.n_total : a.m_total;    // H, I
-    __nv_bfloat16* W = it.mat == 0 ? a.out : it.mat == 1 ? a.d_gate : a.d_up;
-    const int64_t row = it.expert * rows + it.n0 + c0;
-    store_packed<2>(w, pack(v), OutBlock{it.mat == 0 ? &maps.o0 : it.mat == 1 ? &maps.o1 : &maps.o2, f0, (int)row,
-                                         W + row * ld + f0, ld, 32});
+                                              const Packed& lo, const Packed& hi, const Maps& maps, Warp& w) {
+    if (w.lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+    frag_to_tile(w.tiles, lo, w.lane);
+    frag_to_tile(w.tiles + kTileBytes, hi, w.lane);
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (w.lane == 0) {
+        const int rows = it.mat == 0 ? a.n_total : a.m_total;    // of an expert's matrix: H, I
+        tma_store_2d(it.mat == 0 ? &maps.o0 : it.mat == 1 ? &maps.o1 : &maps.o2, w.tiles, f0,
+                     it.expert * rows + it.n0 + c0);
+        bulk_commit();
+    }
 }
 
 __device__ __forceinline__ void activate(Frag& f, int act) {
@@ -1047,6 +1055,21 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
             fence_after();
             const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * C::ACC_COLS);
             const int n = live ? it.n : 0;
+            if constexpr (kKind == kWeights) {
+#pragma unroll 1
+                for (int c0 = 64 * half; c0 < n; c0 += 128) {
+                    Packed lo = {}, hi = {};
+                    if (it.rows > 0) {                 // a group without rows: zeros
+                        Frag v, u;
+                        load_frag(taddr + c0, v);
+                        load_frag(taddr + c0 + 32, u);
+                        tmem_ld_wait();
+                        lo = pack(v);
+                        hi = pack(u);
+                    }
+                    store_weights(args, it, f0, c0, lo, hi, maps, wp);
+                }
+            } else
 #pragma unroll 1
             for (int c0 = 32 * half; c0 < n; c0 += 64) {
                 Frag v;
@@ -1072,15 +1095,9 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                     tmem_ld_wait();
                     store_hidden<kKind>(args, it, f0, c0, v, g, u, gate, maps, wp);
                 } else {
-                    if (kKind == kWeights && it.rows == 0) {      // a group without rows: zeros
-                        v = Frag{};
-                    } else {
-                        load_frag(taddr + c0, v);
-                        tmem_ld_wait();
-                    }
-                    if constexpr (kKind == kWeights) {
-                        store_weights(args, it, f0, c0, v, maps, wp);
-                    } else if constexpr (kKind == kProduct) {
+                    load_frag(taddr + c0, v);
+                    tmem_ld_wait();
+                    if constexpr (kKind == kProduct) {
                         const RowVecs now = res;
                         if (args.residual && args.vec && c0 + 64 < n)
                             load_residual(res, args, it, f0, c0 + 64, lane);

@@ -71,9 +71,9 @@ cudaError_t launch_weight_grad(const __nv_bfloat16* h, const __nv_bfloat16* dg,
         if ((e = make_tma_map_strips(q.whole, q.p, q.rows, q.cols, C::BK, 2)) != cudaSuccess) return e;
         if ((e = make_tma_map_strips(q.tail, q.p, q.rows, q.cols, 32, 1)) != cudaSuccess) return e;
     }
-    if ((e = make_tma_map_tile(&m.o0, a.out, false, (uint64_t)a.E * H, I)) != cudaSuccess) return e;
-    if ((e = make_tma_map_tile(&m.o1, a.d_gate, false, (uint64_t)a.E * I, H)) != cudaSuccess) return e;
-    if ((e = make_tma_map_tile(&m.o2, a.d_up, false, (uint64_t)a.E * I, H)) != cudaSuccess) return e;
+    if ((e = make_tma_map_tile(&m.o0, a.out, false, (uint64_t)a.E * H, I, 64)) != cudaSuccess) return e;
+    if ((e = make_tma_map_tile(&m.o1, a.d_gate, false, (uint64_t)a.E * I, H, 64)) != cudaSuccess) return e;
+    if ((e = make_tma_map_tile(&m.o2, a.d_up, false, (uint64_t)a.E * I, H, 64)) != cudaSuccess) return e;
     a.n_mtiles = I / 256;
     a.n_ntiles = H / 256;
     a.m_total = I;
