@@ -29,6 +29,16 @@ cudaError_t launch_product(const __nv_bfloat16* x, int64_t rows, const __nv_bflo
     a.a_rows = N;
     a.ld = N;
     if (nb == kWideRows) return tg::launch<tg::kProduct, kWideRows>(m, a, num_sms, s);
+    // Few rows, few feature tiles: K is split so that more SMs stream weights.
+    // One row times 4096 x 4096 took 17.4 us on 16 pairs, 32 blocks of K at
+    // 0.41 us (a pair's MMAs of few rows take about 100 cycles each).
+    if (!a.chunks && a.rows <= 2 * kThinRows && a.k_blocks >= 8) {
+        bool fits = false;
+        e = tg::launch_split<tg::kProduct, kThinRows, 4>(m, a, num_sms, s, &fits);
+        if (fits || e != cudaSuccess) return e;
+        e = tg::launch_split<tg::kProduct, kThinRows, 2>(m, a, num_sms, s, &fits);
+        if (fits || e != cudaSuccess) return e;
+    }
     return tg::launch<tg::kProduct, kThinRows>(m, a, num_sms, s);
 }
 

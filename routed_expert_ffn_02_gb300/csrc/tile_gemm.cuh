@@ -25,11 +25,12 @@
 //   warps 4-11  epilogue, two warps per 32 lanes of the accumulator, taking
 //               its 32-column blocks in turn.
 // Every mbarrier wait is bounded and drained as in gemm_tc.cu: on expiry a
-// role records MOE_ERR_TIMEOUT, both CTAs stop, and copies and MMAs in flight
+// role records MOE_ERR_TIMEOUT, the cluster's CTAs stop, and copies and MMAs in flight
 // are waited for before TMEM is freed.
 #pragma once
 
 #include <cuda.h>
+#include <algorithm>
 
 #include "fp8.cuh"
 #include "moe_internal.cuh"
@@ -64,8 +65,15 @@ enum Kind {
 constexpr bool gated(int kind) { return kind == kGated || kind == kGatedFp8; }
 constexpr bool hidden(int kind) { return kind == kHidden || kind == kHiddenFp8; }
 
-template <int kKind, int kNB>
+// kSplit pairs of a cluster share an item: each takes a part of K, and the
+// first adds the others' accumulators, which they store into its shared memory.
+template <int kKind, int kNB, int kSplit = 1>
 struct Cfg {
+    static_assert(kSplit == 1 || (kKind == kProduct && kNB == 16));
+    static constexpr int SPLIT = kSplit;
+    static constexpr int CTAS = 2 * kSplit;           // of a cluster
+    // the other pairs' parts: [pair - 1][4 warps][32 values][32 lanes]
+    static constexpr int PARTS_BYTES = (kSplit - 1) * 4 * 32 * 32 * 4;
     static constexpr bool kAMN = hidden(kKind) || kKind == kInput || kKind == kWeights;
     static constexpr bool kBMN = kKind == kWeights;
     static constexpr int MT = gated(kKind) ? 2 : 1;   // accumulators (A tiles) per item
@@ -79,7 +87,8 @@ struct Cfg {
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     // what B's rows, and the K rows of a weight gradient's last block, are rounded up to
     static constexpr int BOX = NB < 32 ? NB : 32;
-    static constexpr int STAGES = (192 * 1024) / STAGE_BYTES < 8 ? (192 * 1024) / STAGE_BYTES : 8;
+    static constexpr int STAGES =
+        (192 * 1024 - PARTS_BYTES) / STAGE_BYTES < 8 ? (192 * 1024 - PARTS_BYTES) / STAGE_BYTES : 8;
     static constexpr int ACC_COLS = MT * BN;          // TMEM columns of one accumulator set
     static constexpr int BUFS = 2 * ACC_COLS <= 512 ? 2 : 1;
     static constexpr int TMEM_COLS = BUFS * ACC_COLS;
@@ -90,7 +99,7 @@ struct Cfg {
     // block maxima of the 8-bit epilogue: [half][parity][gate, up][4 warps][32 rows]
     static constexpr int AMAX_BYTES = kKind == kGatedFp8 ? 2 * 2 * 2 * 4 * 32 * 4 : 0;
     static constexpr int SMEM_BYTES =
-        STAGES * STAGE_BYTES + STAGING_BYTES + AMAX_BYTES + 1024 /*align*/ + 512 /*barriers*/;
+        STAGES * STAGE_BYTES + STAGING_BYTES + AMAX_BYTES + PARTS_BYTES + 1024 /*align*/ + 512 /*barriers*/;
     static_assert(STAGES >= 2 && SMEM_BYTES <= 227 * 1024);
     static_assert(TMEM_COLS >= 32 && (TMEM_COLS & (TMEM_COLS - 1)) == 0);
 };
@@ -712,12 +721,28 @@ __device__ __forceinline__ void activate(Frag& f, int act) {
     }
 }
 
-// What a product block adds: its residual, loaded a block ahead where rows
-// are 16-byte aligned (a.vec).
+// What a product block adds, loaded a block ahead: its residual in vectors
+// where rows are 16-byte aligned (a.vec), else a feature per lane, rows 2 i and
+// 2 i + 1 in word i.
 __device__ __forceinline__ void load_residual(RowVecs& r, const TileArgs& a, const Item& it, int f0,
                                               int c0, int lane) {
-    const int left = f0 + (lane & 3) * 8 < a.m_total ? it.rows - c0 : 0;
-    load_rows(r, a.residual + (int64_t)(it.row0 + c0) * a.ld + f0, a.ld, left, lane);
+    const int64_t at = (int64_t)(it.row0 + c0) * a.ld + f0;
+    if (a.vec) {
+        load_rows(r, a.residual + at, a.ld, f0 + (lane & 3) * 8 < a.m_total ? it.rows - c0 : 0, lane);
+        return;
+    }
+    const int left = f0 + lane < a.m_total ? it.rows - c0 : 0;
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(a.residual + at) + lane;
+    uint16_t x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        x[i] = 0;
+        if (i < left) x[i] = *p;
+        p += a.ld;
+    }
+    uint32_t* w = &r.v[0].x;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = (uint32_t)x[2 * i] | (uint32_t)x[2 * i + 1] << 16;
 }
 __device__ __forceinline__ void store_product(const TileArgs& a, const Item& it, int f0, int c0, Frag& v,
                                               const RowVecs& res, const Maps& maps, Warp& w) {
@@ -740,14 +765,13 @@ __device__ __forceinline__ void store_product(const TileArgs& a, const Item& it,
         const uint32_t tile = next_tile<2>(w);
         if (a.vec) {
             put_rows(tile, res, lane);
-        } else if (lane < feats) {
-#pragma unroll 8
-            for (int r = 0; r < 32; ++r) {
-                uint16_t x = 0;
-                if (r < left) x = *reinterpret_cast<const uint16_t*>(a.residual + at + (int64_t)r * a.ld + lane);
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile_at(tile, r, lane >> 3) + (lane & 7) * 2), "h"(x)
+        } else {
+            const uint32_t* x = &res.v[0].x;
+#pragma unroll
+            for (int r = 0; r < 32; ++r)
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile_at(tile, r, lane >> 3) + (lane & 7) * 2),
+                             "h"((uint16_t)(x[r >> 1] >> (16 * (r & 1))))
                              : "memory");
-            }
         }
         __syncwarp();
         Packed p;
@@ -809,16 +833,16 @@ __device__ __forceinline__ void drain_stages(uint32_t full0, int fills_even, int
     }
 }
 
-template <int kKind, int kNB>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <int kKind, int kNB, int kSplit>
+__global__ void __cluster_dims__(2 * kSplit, 1, 1) __launch_bounds__(kThreads, 1)
 tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ TileArgs args) {
-    using C = Cfg<kKind, kNB>;
+    using C = Cfg<kKind, kNB, kSplit>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* base_ptr = smem_raw + (base - raw);
     constexpr int kStagingAt = C::STAGES * C::STAGE_BYTES, kAmaxAt = kStagingAt + C::STAGING_BYTES,
-                  kBarsAt = kAmaxAt + C::AMAX_BYTES;
+                  kPartsAt = kAmaxAt + C::AMAX_BYTES, kBarsAt = kPartsAt + C::PARTS_BYTES;
     const uint32_t bars = base + kBarsAt;
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
@@ -832,15 +856,17 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
-    const uint32_t peer_abort = mapa_shared(smem_u32(tmem_holder + 1), rank ^ 1u);
+    const uint32_t cta = cluster_ctarank();
+    const uint32_t rank = cta & 1u, even = cta & ~1u;      // the CTA's place in its pair; the pair's even CTA
+    const int part = (int)(cta >> 1);                      // the pair's part of K
     auto give_up = [&]() {
+        for (uint32_t c = 0; c < C::CTAS; ++c) st_shared_cluster(mapa_shared(smem_u32(tmem_holder + 1), c), 1u);
         *abort_flag = 1;
-        st_shared_cluster(peer_abort, 1u);
         set_status(args.hdr, MOE_ERR_TIMEOUT);
     };
-    const int cluster = (int)blockIdx.x >> 1;
-    const int n_clusters = (int)gridDim.x >> 1;
+    const int cluster = (int)blockIdx.x / C::CTAS;
+    const int n_clusters = (int)gridDim.x / C::CTAS;
+    const uint16_t pair_mask = (uint16_t)(0x3u << even);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -875,9 +901,12 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
     if constexpr (kKind == kWeights) total = args.E * 3 * args.n_mtiles * args.n_ntiles;
     else total = (args.chunks ? *args.n_chunks : args.dense_chunks) * args.n_mtiles;
 
+    [[maybe_unused]] Frag mine;          // split items: this warp's accumulator
+    [[maybe_unused]] bool have = false;
+
     if (warp == 0 && lane == 0) {
         // ---------------- TMA producer (both CTAs) ----------------
-        const uint32_t full0 = mapa_shared(full_bar(0), 0);
+        const uint32_t full0 = mapa_shared(full_bar(0), even);
         int stage = 0;
         uint32_t phase = 0;
         int fills = 0;
@@ -885,7 +914,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
         for (int w = cluster; ok && w < total; w += n_clusters) {
             const Item it = item_of<kKind, C>(args, w);
             const int m = it.m0 + (int)rank * 128;
-            for (int kb = 0; kb < it.k_blocks; ++kb) {
+            for (int kb = part * it.k_blocks / kSplit; kb < (part + 1) * it.k_blocks / kSplit; ++kb) {
                 if (!mbar_wait_for(empty_bar(stage), phase ^ 1u, args.wait_cycles, abort_flag)) {
                     ok = false;
                     break;
@@ -976,7 +1005,8 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
             const uint32_t d_tmem = tmem_base + (uint32_t)(acc * C::ACC_COLS);
             const uint32_t idesc = idesc_for<C::kAMN, C::kBMN>(it.n);
             [[maybe_unused]] const uint32_t b_strip = (uint32_t)(it.boxes * C::BOX * 128);
-            for (int kb = 0; kb < it.k_blocks; ++kb) {
+            const int kb0 = part * it.k_blocks / kSplit;
+            for (int kb = kb0; kb < (part + 1) * it.k_blocks / kSplit; ++kb) {
                 if (!mbar_wait_for(full_bar(stage), phase, args.wait_cycles, abort_flag)) {
                     ok = false;
                     break;
@@ -995,23 +1025,23 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                         uint64_t ad;
                         if constexpr (C::kAMN) ad = mn_desc(sa + mt * C::A_SUB + kk * 2048, C::BK * 128);
                         else ad = sw128_desc(sa + mt * C::A_SUB + (kk / 4) * 128 * 128) + (uint64_t)((kk % 4) * 2);
-                        mma_bf16_pair(d_tmem + (uint32_t)(mt * C::BN), ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                        mma_bf16_pair(d_tmem + (uint32_t)(mt * C::BN), ad, bd, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
                     }
                 }
                 issued = true;
-                commit_pair_multicast(empty_bar(stage), 0x3);
+                commit_pair_multicast(empty_bar(stage), pair_mask);
                 if (++stage == C::STAGES) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
             if (!ok) break;
-            commit_pair_multicast(tfull_bar(acc), 0x3);
+            commit_pair_multicast(tfull_bar(acc), pair_mask);
         }
         if (!ok && !*abort_flag) give_up();
         // Every MMA has completed before TMEM is freed.
         if (issued) {
-            commit_pair_multicast(done_bar, 0x1);
+            commit_pair_multicast(done_bar, (uint16_t)(1u << cta));
             (void)mbar_wait(done_bar, 0);
         }
     } else if (warp >= 4) {
@@ -1020,7 +1050,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
         const int half = (warp - 4) >> 2;     // which 32-row blocks: every other
         uint32_t* amax = reinterpret_cast<uint32_t*>(base_ptr + kAmaxAt) + half * 512;
         Warp wp = {lane, quad, base + kStagingAt + (uint32_t)(warp - 4) * C::TILES * kTileBytes, 0, amax, 1 + half};
-        const uint32_t tempty0 = mapa_shared(tempty_bar(0), 0);
+        const uint32_t tempty0 = mapa_shared(tempty_bar(0), even);
         int i = 0;
         for (int w = cluster; w < total; w += n_clusters, ++i) {
             const Item it = item_of<kKind, C>(args, w);
@@ -1033,7 +1063,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
             [[maybe_unused]] RowVecs res;
             if constexpr (hidden(kKind)) load_kept<kKind>(kept, args, it, f0, 32 * half, lane);
             if constexpr (kKind == kProduct)
-                if (live && args.residual && args.vec) load_residual(res, args, it, f0, 32 * half, lane);
+                if (kSplit == 1 && live && args.residual) load_residual(res, args, it, f0, 32 * half, lane);
             bool ok = __all_sync(0xffffffffu, mbar_wait_for(tfull_bar(acc), acc_phase, args.wait_cycles, abort_flag));
             if constexpr (kKind == kGatedFp8) {
                 // the four warps that exchange maxima go on together or not at all
@@ -1055,7 +1085,20 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
             fence_after();
             const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * C::ACC_COLS);
             const int n = live ? it.n : 0;
-            if constexpr (kKind == kWeights) {
+            if constexpr (kSplit > 1) {
+                // at most 32 rows and one item: the first pair waits for the others' parts below
+                if (half == 0) {
+                    load_frag(taddr, mine);
+                    tmem_ld_wait();
+                    have = true;
+                    if (part > 0) {
+                        const uint32_t to = mapa_shared(base + kPartsAt + (uint32_t)((part - 1) * 4 + quad) * 4096u, rank);
+#pragma unroll
+                        for (int q = 0; q < 32; ++q)
+                            st_shared_cluster(to + (uint32_t)(q * 32 + lane) * 4u, __float_as_uint((&mine.v[0][0][0])[q]));
+                    }
+                }
+            } else if constexpr (kKind == kWeights) {
 #pragma unroll 1
                 for (int c0 = 64 * half; c0 < n; c0 += 128) {
                     Packed lo = {}, hi = {};
@@ -1099,7 +1142,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                     tmem_ld_wait();
                     if constexpr (kKind == kProduct) {
                         const RowVecs now = res;
-                        if (args.residual && args.vec && c0 + 64 < n)
+                        if (args.residual && c0 + 64 < n)
                             load_residual(res, args, it, f0, c0 + 64, lane);
                         store_product(args, it, f0, c0, v, now, maps, wp);
                     } else {
@@ -1121,17 +1164,39 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
 
     fence_before();
     __syncthreads();
-    cluster_sync();   // both CTAs' roles have stopped
-    const bool aborted = *abort_flag || ld_shared_cluster(peer_abort) != 0;
+    cluster_sync();   // all CTAs' roles have stopped, and the parts of a split item are in place
+    bool aborted = *abort_flag != 0;
+    for (uint32_t c = 0; c < C::CTAS; ++c)
+        aborted |= ld_shared_cluster(mapa_shared(smem_u32(tmem_holder + 1), c)) != 0;
     cluster_sync();
     if (aborted) {
         if (rank == 0 && threadIdx.x == 0)
             drain_stages<C::STAGES>(full_bar(0), *fills_out,
-                                    (int)ld_shared_cluster(mapa_shared(smem_u32(fills_out), 1)),
-                                    [&](uint32_t cta, int s) {
-                                        return ld_shared_cluster(mapa_shared(smem_u32(stage_bytes + s), cta));
+                                    (int)ld_shared_cluster(mapa_shared(smem_u32(fills_out), even + 1)),
+                                    [&](uint32_t c, int s) {
+                                        return ld_shared_cluster(mapa_shared(smem_u32(stage_bytes + s), even + c));
                                     });
         cluster_sync();
+    }
+    if constexpr (kSplit > 1) {
+        if (!aborted && part == 0 && have) {
+            const int quad = warp & 3;
+            const Item it = item_of<kKind, C>(args, cluster);
+            const int f0 = it.m0 + (int)rank * 128 + quad * 32;
+            if (f0 < args.m_total) {
+                const float* parts = reinterpret_cast<const float*>(base_ptr + kPartsAt) + quad * 1024 + lane;
+#pragma unroll
+                for (int p = 0; p < kSplit - 1; ++p)
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) (&mine.v[0][0][0])[q] += parts[p * 4096 + q * 32];
+                Warp wp = {lane, quad, base + kStagingAt + (uint32_t)(warp - 4) * C::TILES * kTileBytes, 0, nullptr, 0};
+                RowVecs res;
+                if (args.residual) load_residual(res, args, it, f0, 0, lane);
+                store_product(args, it, f0, 0, mine, res, maps, wp);
+                if (lane == 0) bulk_wait_all();
+                __syncwarp();
+            }
+        }
     }
     if (warp == 2) {
         fence_after();
@@ -1149,20 +1214,49 @@ inline cudaError_t row_maps(CUtensorMap (&b)[4], const __nv_bfloat16* p, int64_t
     return cudaSuccess;
 }
 
+// No more CTAs than there can be items: a small launch leaves SMs to the next
+// one, whose prologue then overlaps it.
 template <int kKind, int kNB>
 cudaError_t launch(const Maps& maps, TileArgs args, int num_sms, cudaStream_t s) {
     using C = Cfg<kKind, kNB>;
     static std::atomic<int> done[kMaxDevices];
-    cudaError_t e = smem_limit_once(tile_gemm_kernel<kKind, kNB>, C::SMEM_BYTES, done);
+    cudaError_t e = smem_limit_once(tile_gemm_kernel<kKind, kNB, 1>, C::SMEM_BYTES, done);
     if (e != cudaSuccess) return e;
     int grid = 0;
-    e = pair_grid<tile_gemm_kernel<kKind, kNB>, C::SMEM_BYTES, kThreads>(num_sms, &grid);
+    e = pair_grid<tile_gemm_kernel<kKind, kNB, 1>, C::SMEM_BYTES, kThreads>(num_sms, &grid);
     if (e != cudaSuccess) return e;
-    if (kKind != kWeights && !args.chunks) {
+    int64_t items;
+    if (kKind == kWeights) {
+        items = (int64_t)args.E * 3 * args.n_mtiles * args.n_ntiles;
+    } else if (args.chunks) {
+        items = max_chunks(args.rows, args.E, C::BN) * args.n_mtiles;
+    } else {
         args.chunk_rows = dense_chunk(args.rows, C::BN, args.n_mtiles, grid / 2);
         args.dense_chunks = (int)(((int64_t)args.rows + args.chunk_rows - 1) / args.chunk_rows);
+        items = (int64_t)args.dense_chunks * args.n_mtiles;
     }
-    return launch_pdl(tile_gemm_kernel<kKind, kNB>, dim3(grid), dim3(kThreads), C::SMEM_BYTES, s, maps, args);
+    grid = (int)std::min<int64_t>(grid, 2 * items);
+    return launch_pdl(tile_gemm_kernel<kKind, kNB, 1>, dim3(grid), dim3(kThreads), C::SMEM_BYTES, s, maps, args);
+}
+
+// One dense product of at most 2 * kNB rows, each item split over kSplit pairs.
+// *fits: every item's cluster can be resident at once (nothing is launched if
+// not).
+template <int kKind, int kNB, int kSplit>
+cudaError_t launch_split(const Maps& maps, TileArgs args, int num_sms, cudaStream_t s, bool* fits) {
+    using C = Cfg<kKind, kNB, kSplit>;
+    static std::atomic<int> done[kMaxDevices];
+    cudaError_t e = smem_limit_once(tile_gemm_kernel<kKind, kNB, kSplit>, C::SMEM_BYTES, done);
+    if (e != cudaSuccess) return e;
+    int twice = 0;       // two for each resident cluster
+    e = pair_grid<tile_gemm_kernel<kKind, kNB, kSplit>, C::SMEM_BYTES, kThreads>(num_sms / C::CTAS * C::CTAS, &twice);
+    if (e != cudaSuccess) return e;
+    *fits = 2 * args.n_mtiles <= twice;
+    if (!*fits) return cudaSuccess;
+    args.chunk_rows = C::BN;
+    args.dense_chunks = 1;
+    return launch_pdl(tile_gemm_kernel<kKind, kNB, kSplit>, dim3(C::CTAS * args.n_mtiles), dim3(kThreads),
+                      C::SMEM_BYTES, s, maps, args);
 }
 
 }  // namespace tg

@@ -9,7 +9,8 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPerThread = kMaxE / kThreads;      // groups per thread
+// Groups per thread in the scans of E groups: 1, or enough for kMaxE.
+constexpr int kMostPerThread = kMaxE / kThreads;
 
 // Exclusive scan over the block's threads, + or max (from 0).
 template <bool kMax>
@@ -36,6 +37,7 @@ struct Groups {
     int off[kMaxE + 1], pad[kMaxE + 1];
     int warp_vals[kThreads / 32];
 };
+template <int kPerThread>
 __device__ void scan_groups(Groups& g, const int32_t* offsets, int rows, int E, WsHeader* hdr) {
     const int e0 = threadIdx.x * kPerThread;
     int given[kPerThread], v[kPerThread];
@@ -70,11 +72,12 @@ __device__ void scan_groups(Groups& g, const int32_t* offsets, int rows, int E, 
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i)
         if (e0 + i <= E) g.pad[e0 + i] = pad_before + p[i];
-    if (threadIdx.x == kThreads - 1 && E == kMaxE) g.pad[E] = pad_before + sum;
+    if (threadIdx.x == kThreads - 1 && E == kThreads * kPerThread) g.pad[E] = pad_before + sum;
     __syncthreads();
 }
 
 // The lists of the groups, by one block.
+template <int kPerThread>
 __device__ void write_lists(Groups& g, int E, int most, const RowLists& l) {
     const int e0 = threadIdx.x * kPerThread;
     int n = 0;
@@ -99,13 +102,14 @@ __device__ void write_lists(Groups& g, int E, int most, const RowLists& l) {
     if (threadIdx.x == kThreads - 1) *l.n_chunks = at;     // no group behind it
 }
 
+template <int kPerThread>
 __global__ void __launch_bounds__(kThreads)
 plan_rows_kernel(const int32_t* offsets, int rows, int E, int most, RowLists l, WsHeader* hdr) {
     __shared__ Groups g;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    scan_groups(g, offsets, rows, E, hdr);
-    write_lists(g, E, most, l);
+    scan_groups<kPerThread>(g, offsets, rows, E, hdr);
+    write_lists<kPerThread>(g, E, most, l);
 }
 
 // Eight e4m3 values (one 8-byte word) of one scale as bf16: exact.
@@ -128,6 +132,7 @@ __device__ __forceinline__ float scale_of(uint32_t b) {
 
 // Forward: xs[p] = x[perm[p] / k] for the groups' rows, a warp per row, eight
 // 16-byte vectors per lane in flight; block 0 writes the lists.
+template <int kPerThread>
 __global__ void __launch_bounds__(kThreads)
 forward_rows_kernel(const uint4* x, const int32_t* perm, int k, int vec, const int32_t* offsets, int P, int E,
                     int most, uint4* xs, RowLists l, WsHeader* hdr) {
@@ -135,8 +140,8 @@ forward_rows_kernel(const uint4* x, const int32_t* perm, int k, int vec, const i
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     if (blockIdx.x == 0) {
-        scan_groups(g, offsets, P, E, hdr);
-        write_lists(g, E, most, l);
+        scan_groups<kPerThread>(g, offsets, P, E, hdr);
+        write_lists<kPerThread>(g, E, most, l);
     }
     const int lane = threadIdx.x & 31;
     for (int64_t p = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); p < P; p += (int64_t)gridDim.x * (kThreads / 32)) {
@@ -160,13 +165,14 @@ forward_rows_kernel(const uint4* x, const int32_t* perm, int k, int vec, const i
 // and zeros to the padding.  A warp takes a token, so that a row is read once
 // however many slots it has (by sorted row, x and d of 16384 tokens do not fit
 // L2 together and were read from memory k times: 631 us at 16384 x 4096, k = 8).
+template <int kPerThread>
 __global__ void __launch_bounds__(kThreads)
 backward_rows_kernel(BackwardRows q) {
     __shared__ Groups g;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    scan_groups(g, q.offsets, q.T * q.k, q.E, blockIdx.x == 0 ? q.hdr : nullptr);
-    if (blockIdx.x == 0) write_lists(g, q.E, q.most, q.lists);
+    scan_groups<kPerThread>(g, q.offsets, q.T * q.k, q.E, blockIdx.x == 0 ? q.hdr : nullptr);
+    if (blockIdx.x == 0) write_lists<kPerThread>(g, q.E, q.most, q.lists);
     const int lane = threadIdx.x & 31, vec = q.H / 8;
     const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5),
                   warps = (int64_t)gridDim.x * (kThreads / 32);
@@ -285,14 +291,14 @@ dequantize_rows_kernel(const uint2* q, const uint8_t* scales, int64_t n, uint4* 
 
 cudaError_t launch_plan_rows(const int32_t* offsets, int rows, int E, int most, const RowLists& l,
                              WsHeader* hdr, cudaStream_t s) {
-    return launch_pdl(plan_rows_kernel, dim3(1), dim3(kThreads), 0, s, offsets, rows, E, most, l, hdr);
+    return launch_pdl(E <= kThreads ? plan_rows_kernel<1> : plan_rows_kernel<kMostPerThread>, dim3(1), dim3(kThreads), 0, s, offsets, rows, E, most, l, hdr);
 }
 
 cudaError_t launch_forward_rows(const __nv_bfloat16* x, const int32_t* perm, int k, int H,
                                 const int32_t* offsets, int P, int E, int most, __nv_bfloat16* xs,
                                 const RowLists& l, WsHeader* hdr, int num_sms, cudaStream_t s) {
     const int64_t want = ((int64_t)P + 7) / 8;
-    return launch_pdl(forward_rows_kernel, dim3((unsigned)(want < 8 * num_sms ? want : 8 * num_sms)), dim3(kThreads), 0, s,
+    return launch_pdl(E <= kThreads ? forward_rows_kernel<1> : forward_rows_kernel<kMostPerThread>, dim3((unsigned)(want < 8 * num_sms ? want : 8 * num_sms)), dim3(kThreads), 0, s,
                       reinterpret_cast<const uint4*>(x), perm, k, H / 8, offsets, P, E, most,
                       reinterpret_cast<uint4*>(xs), l, hdr);
 }
@@ -300,7 +306,7 @@ cudaError_t launch_forward_rows(const __nv_bfloat16* x, const int32_t* perm, int
 cudaError_t launch_backward_rows(const BackwardRows& q, int num_sms, cudaStream_t s) {
     // a block per few tokens: few tokens are spread over blocks of their own
     const int64_t want = q.T < num_sms ? q.T : ((int64_t)q.T + 7) / 8 < num_sms ? num_sms : ((int64_t)q.T + 7) / 8;
-    return launch_pdl(backward_rows_kernel, dim3((unsigned)(want < 8 * num_sms ? want : 8 * num_sms)), dim3(kThreads), 0, s, q);
+    return launch_pdl(q.E <= kThreads ? backward_rows_kernel<1> : backward_rows_kernel<kMostPerThread>, dim3((unsigned)(want < 8 * num_sms ? want : 8 * num_sms)), dim3(kThreads), 0, s, q);
 }
 
 cudaError_t launch_finish(const float* y, __nv_bfloat16* d_x, const float* parts, int n_parts, float* d_gates,
