@@ -799,7 +799,7 @@ def moe_balance_backward(logits, stats, counts, k: int, seq_offsets=None, coef: 
     return d_logits
 
 
-@dataclass(frozen=True)
+@dataclass(eq=False)
 class SavedFfn:
     """What moe_expert_ffn_train keeps for moe_expert_ffn_backward, by sorted
     row: the two projections gate, up [P, I], with x [T, H].  In bf16 (the
@@ -814,16 +814,15 @@ class SavedFfn:
 
     def ref(self, shape: Shape):
         """The C structure, for a layer of these sizes."""
-        T, P, H, I = shape.T, shape.P, shape.H, shape.I
-        fp8 = self.gate_scales is not None
-        kind = _E4M3 if fp8 else _BF16
-        c = MoeSaved(int(fp8), _in(self.x, kind, (T, H)), None, _in(self.gate, kind, (P, I)), None,
-                     _in(self.up, kind, (P, I)), None)
-        if fp8:
-            c.x_scales = _in(self.x_scales, _U8, (T, H // 128))
-            c.gate_scales = _in(self.gate_scales, _U8, (P, I // 128))
-            c.up_scales = _in(self.up_scales, _U8, (P, I // 128))
-        return ctypes.byref(c)
+        T, H, I = shape.T, shape.H, shape.I
+        P = T * shape.k
+        if self.gate_scales is None:
+            return ctypes.byref(MoeSaved(0, _in(self.x, _BF16, (T, H)), None, _in(self.gate, _BF16, (P, I)), None,
+                                         _in(self.up, _BF16, (P, I)), None))
+        rows = (P, I // 128)
+        return ctypes.byref(MoeSaved(
+            1, _in(self.x, _E4M3, (T, H)), _in(self.x_scales, _U8, (T, H // 128)), _in(self.gate, _E4M3, (P, I)),
+            _in(self.gate_scales, _U8, rows), _in(self.up, _E4M3, (P, I)), _in(self.up_scales, _U8, rows)))
 
     @staticmethod
     def empty(shape: Shape, x: torch.Tensor, checkpoint: str = "bf16", stream=None) -> "SavedFfn":
@@ -850,17 +849,19 @@ def moe_expert_ffn_train(shape: Shape, x, perm, offsets, W_gate, W_up, W_down,
     ("fp8") in 8 bits.  perm and offsets from moe_permute, or None with
     E = k = 1: a dense block.  `saved`: room from an earlier call, whose kind
     then counts.  Returns (y_sorted [P, H] bf16, SavedFfn)."""
-    T, E, P, H, I = shape.T, shape.E, shape.P, shape.H, shape.I
+    T, E, H, I = shape.T, shape.E, shape.H, shape.I
+    P = T * shape.k
     xp = _in(x, _BF16, (T, H))
     y_sorted, yp = _out(y_sorted, (P, H), _BF16, x, stream)
     if saved is None:
         saved = SavedFfn.empty(shape, x, checkpoint, stream)
     elif saved.gate_scales is None:      # the record of this call: its own x
         saved = SavedFfn(x, saved.gate, saved.up)
+    up = (E, I, H)
     ws = ws or Workspace(expert_ffn_train_workspace_size(shape), x.device, stream)
     st = _lib.moe_expert_ffn_train(
         ctypes.byref(shape.c()), xp, _opt(perm, _I32, (P,)), _opt(offsets, _I32, (E + 1,)),
-        _in(W_gate, _BF16, (E, I, H)), _in(W_up, _BF16, (E, I, H)), _in(W_down, _BF16, (E, H, I)),
+        _in(W_gate, _BF16, up), _in(W_up, _BF16, up), _in(W_down, _BF16, (E, H, I)),
         yp, saved.ref(shape), ws.addr, ws.nbytes, _on(stream, x))
     if st:
         raise MoeError(st, "moe_expert_ffn_train")
@@ -882,27 +883,29 @@ def moe_expert_ffn_backward(shape: Shape, d_out, saved: SavedFfn, perm, offsets,
     gradient of moe_combine's output (gates None: all 1).  Returns (d_x [T, H]
     bf16, d_gates [T, k] fp32, dW_gate, dW_up, dW_down bf16); None in the place
     of what is not needed, and of d_gates without gates."""
-    T, E, k, P, H, I = shape.T, shape.E, shape.k, shape.P, shape.H, shape.I
+    T, E, k, H, I = shape.T, shape.E, shape.k, shape.H, shape.I
+    P, up, down = T * k, (E, I, H), (E, H, I)
     dp = _in(d_out, _BF16, (T, H))
-    xp = gp = None
+    xp = gp = wg = wu = wd = None
     if need_x:
         d_x, xp = _out(d_x, (T, H), _BF16, d_out, stream)
     if gates is not None:
         d_gates, gp = _out(d_gates, (T, k), _F32, d_out, stream)
-    dW, wp = (None,) * 3 if dW is None else dW, (None,) * 3
     if need_weights:
-        dW, wp = zip(*(_out(w, s, _BF16, d_out, stream)
-                       for w, s in zip(dW, ((E, I, H), (E, I, H), (E, H, I)))))
+        given = dW if dW is not None else (None, None, None)
+        dWg, wg = _out(given[0], up, _BF16, d_out, stream)
+        dWu, wu = _out(given[1], up, _BF16, d_out, stream)
+        dWd, wd = _out(given[2], down, _BF16, d_out, stream)
     ws = ws or Workspace(expert_ffn_backward_workspace_size(shape), d_out.device, stream)
     st = _lib.moe_expert_ffn_backward(
         ctypes.byref(shape.c()), dp, _opt(gates, _F32, (T, k)), saved.ref(shape),
         _opt(perm, _I32, (P,)), _opt(offsets, _I32, (E + 1,)), _opt(inv_perm, _I32, (P,)),
-        _in(W_gate, _BF16, (E, I, H)), _in(W_up, _BF16, (E, I, H)), _in(W_down, _BF16, (E, H, I)),
-        xp, gp, *wp, ws.addr, ws.nbytes, _on(stream, d_out))
+        _in(W_gate, _BF16, up), _in(W_up, _BF16, up), _in(W_down, _BF16, down),
+        xp, gp, wg, wu, wd, ws.addr, ws.nbytes, _on(stream, d_out))
     if st:
         raise MoeError(st, "moe_expert_ffn_backward")
     return (d_x if need_x else None, d_gates if gates is not None else None,
-            *(dW if need_weights else (None,) * 3))
+            *((dWg, dWu, dWd) if need_weights else (None, None, None)))
 
 
 def moe_dequantize_rows(q, scales, x=None, stream=None):

@@ -125,9 +125,9 @@ moe_status moe_expert_ffn_train(const moe_shape* shape, const moe_bf16* x, const
                                 const moe_saved* saved, void* ws, size_t ws_bytes,
                                 moe_stream_t stream) {
     STATUS_TRY(check_shape_status(shape));
+    if (shape->T == 0) return ok();
     bool dense;
     STATUS_TRY(check_lists(shape, perm, offsets, &dense));
-    if (shape->T == 0) return ok();
     CHECK_PTR(x); CHECK_PTR(W_gate); CHECK_PTR(W_up); CHECK_PTR(W_down); CHECK_PTR(y_sorted);
     STATUS_TRY(check_saved(saved, false));
     FwdBufs b;
@@ -177,10 +177,6 @@ moe_status moe_expert_ffn_backward(const moe_shape* shape, const moe_bf16* d_out
                                    moe_bf16* dW_down, void* ws, size_t ws_bytes,
                                    moe_stream_t stream) {
     STATUS_TRY(check_shape_status(shape));
-    bool dense;
-    STATUS_TRY(check_lists(shape, perm, offsets, &dense));
-    if (dense != !inv_perm) return fail(MOE_ERR_INVALID_ARG, "perm, offsets and inv_perm come together");
-    if (d_gates && !gates) return fail(MOE_ERR_INVALID_ARG, "d_gates without gates");
     const bool weights = dW_gate || dW_up || dW_down;
     if (weights) {
         CHECK_PTR(dW_gate); CHECK_PTR(dW_up); CHECK_PTR(dW_down);
@@ -195,6 +191,10 @@ moe_status moe_expert_ffn_backward(const moe_shape* shape, const moe_bf16* d_out
             CUDA_TRY(cudaMemsetAsync(w, 0, (size_t)E * H * I * 2, s), "clear weight gradients");
         return ok();
     }
+    bool dense;
+    STATUS_TRY(check_lists(shape, perm, offsets, &dense));
+    if (dense != !inv_perm) return fail(MOE_ERR_INVALID_ARG, "perm, offsets and inv_perm come together");
+    if (d_gates && !gates) return fail(MOE_ERR_INVALID_ARG, "d_gates without gates");
     CHECK_PTR(d_out); CHECK_PTR(W_gate); CHECK_PTR(W_up); CHECK_PTR(W_down);
     if (d_x) CHECK_PTR(d_x);
     STATUS_TRY(check_saved(saved, true));

@@ -145,15 +145,18 @@ forward_rows_kernel(const uint4* x, const int32_t* perm, int k, int vec, const i
     }
     const int lane = threadIdx.x & 31;
     for (int64_t p = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); p < P; p += (int64_t)gridDim.x * (kThreads / 32)) {
+        // a position without a slot (a routed index was skipped) is a zero row
         const int slot = ld::i32(perm + p);
-        if (slot < 0 || slot >= P) continue;
-        const uint4* from = x + (int64_t)(slot / k) * vec;
+        const bool in = slot >= 0 && slot < P;
+        const uint4* from = x + (int64_t)(in ? slot / k : 0) * vec;
         uint4* to = xs + p * vec;
         for (int i0 = lane; i0 < vec; i0 += 32 * 8) {
             uint4 a[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (i0 + 32 * j < vec) a[j] = from[i0 + 32 * j];
+            for (int j = 0; j < 8; ++j) {
+                a[j] = make_uint4(0, 0, 0, 0);
+                if (in && i0 + 32 * j < vec) a[j] = from[i0 + 32 * j];
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (i0 + 32 * j < vec) to[i0 + 32 * j] = a[j];
@@ -165,6 +168,16 @@ forward_rows_kernel(const uint4* x, const int32_t* perm, int k, int vec, const i
 // and zeros to the padding.  A warp takes a token, so that a row is read once
 // however many slots it has (by sorted row, x and d of 16384 tokens do not fit
 // L2 together and were read from memory k times: 631 us at 16384 x 4096, k = 8).
+__device__ __forceinline__ int64_t padded_row(const Groups& g, int E, int p) {
+    int lo = 0, hi = E;          // the last group whose first row is not above p
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (g.off[mid] <= p) lo = mid;
+        else hi = mid;
+    }
+    return (int64_t)g.pad[lo] + (p - g.off[lo]);
+}
+
 template <int kPerThread>
 __global__ void __launch_bounds__(kThreads)
 backward_rows_kernel(BackwardRows q) {
@@ -182,13 +195,7 @@ backward_rows_kernel(BackwardRows q) {
         if (lane < q.k) {
             const int slot = (int)(t * q.k) + lane, p = ld::i32(q.inv_perm + slot);
             if (p >= 0 && p < g.off[q.E] && ld::i32(q.perm + p) == slot) {
-                int lo = 0, hi = q.E;          // the last group whose first row is not above p
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (g.off[mid] <= p) lo = mid;
-                    else hi = mid;
-                }
-                mine = ((int64_t)g.pad[lo] + (p - g.off[lo])) * vec;
+                mine = padded_row(g, q.E, p) * vec;
             }
         }
         for (int i0 = lane; i0 - lane < vec; i0 += 32 * 4) {
@@ -217,6 +224,22 @@ backward_rows_kernel(BackwardRows q) {
                     }
                 }
             }
+        }
+    }
+    // Positions that no slot holds (a routed index was skipped): zeros, lest what
+    // the buffers held reach the weights' gradients of the last group.
+    for (int64_t p0 = warp * 32; p0 < g.off[q.E]; p0 += warps * 32) {
+        const int p = (int)p0 + lane;
+        bool none = false;
+        if (p < g.off[q.E]) {
+            const int slot = ld::i32(q.perm + p);
+            none = slot < 0 || slot >= q.T * q.k || ld::i32(q.inv_perm + slot) != p;
+        }
+        for (unsigned left = __ballot_sync(0xffffffffu, none); left; left &= left - 1) {
+            const int64_t to = padded_row(g, q.E, (int)p0 + __ffs(left) - 1) * vec;
+            for (int i = lane; i < vec; i += 32)
+                reinterpret_cast<uint4*>(q.x_rows)[to + i] = reinterpret_cast<uint4*>(q.d_rows)[to + i] =
+                    make_uint4(0, 0, 0, 0);
         }
     }
     for (int64_t e = warp; e < q.E; e += warps) {
