@@ -9,9 +9,9 @@ using namespace moe;
 
 namespace {
 
-// Rows of B per CTA of the tile kernel: the narrow build for groups that hold
-// at most a narrow chunk (32 rows) on average, else the wide one.
-int rows_per_cta(int64_t rows, int E) { return rows <= (int64_t)2 * kThinRows * E ? kThinRows : kWideRows; }
+// Rows of B per CTA of the tile kernel: the narrow build where the groups hold
+// at most 3/4 of a narrow chunk (128 rows) on average, else the wide one.
+int rows_per_cta(int64_t rows, int E) { return rows <= (int64_t)96 * E ? kThinRows : kWideRows; }
 
 struct Lists {
     WsHeader* hdr;

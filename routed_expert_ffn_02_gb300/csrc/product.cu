@@ -11,6 +11,12 @@ cudaError_t launch_product(const __nv_bfloat16* x, int64_t rows, const __nv_bflo
     cudaError_t e;
     a.k_blocks = (K + C::BK - 1) / C::BK;
     a.flat_from = K / C::BK;           // the block that K does not fill, if there is one
+    // Few rows, few feature tiles: K is split so that more SMs stream weights.
+    // One row times 4096 x 4096 took 17.4 us on 16 pairs, 32 blocks of K at
+    // 0.41 us (a pair's MMAs of few rows take about 100 cycles each); split in
+    // two, 11.0.
+    const bool split = !a.chunks && a.rows <= 2 * kSplitRows && a.k_blocks >= 8;
+    if (split) nb = kSplitRows;
     if (a.flat_from > 0) {
         if ((e = make_tma_map_strips(&m.a0, W, (uint64_t)a.E * N, K, 128, C::KSUB)) != cudaSuccess) return e;
         if ((e = tg::row_maps(m.b[0], x, rows, K, nb, C::KSUB)) != cudaSuccess) return e;
@@ -29,15 +35,13 @@ cudaError_t launch_product(const __nv_bfloat16* x, int64_t rows, const __nv_bflo
     a.a_rows = N;
     a.ld = N;
     if (nb == kWideRows) return tg::launch<tg::kProduct, kWideRows>(m, a, num_sms, s);
-    // Few rows, few feature tiles: K is split so that more SMs stream weights.
-    // One row times 4096 x 4096 took 17.4 us on 16 pairs, 32 blocks of K at
-    // 0.41 us (a pair's MMAs of few rows take about 100 cycles each).
-    if (!a.chunks && a.rows <= 2 * kThinRows && a.k_blocks >= 8) {
+    if (split) {
         bool fits = false;
-        e = tg::launch_split<tg::kProduct, kThinRows, 4>(m, a, num_sms, s, &fits);
+        e = tg::launch_split<tg::kProduct, kSplitRows, 4>(m, a, num_sms, s, &fits);
         if (fits || e != cudaSuccess) return e;
-        e = tg::launch_split<tg::kProduct, kThinRows, 2>(m, a, num_sms, s, &fits);
+        e = tg::launch_split<tg::kProduct, kSplitRows, 2>(m, a, num_sms, s, &fits);
         if (fits || e != cudaSuccess) return e;
+        return tg::launch<tg::kProduct, kSplitRows>(m, a, num_sms, s);
     }
     return tg::launch<tg::kProduct, kThinRows>(m, a, num_sms, s);
 }

@@ -32,8 +32,8 @@ __host__ __device__ inline int chunk_size(int c, int most) {
 }
 
 // Rows of one group's chunks, for n_mtiles feature tiles on `pairs` CTA pairs.
-// An item costs about its rows, but no less than 128 (below that the features'
-// operand, whose bytes do not shrink, bounds it), and 16 for its ends; the
+// An item costs about its rows, but no less than 128 (see kThinRows), and 16
+// for its ends; the
 // grid takes whole rounds of items.  8192 x 2048 over K = 4096 in chunks of 256
 // is 256 items on 76 pairs, four rounds for 3.4; in chunks of 224 it is 3.9.
 inline int dense_chunk(int rows, int most, int n_mtiles, int pairs) {
@@ -41,7 +41,7 @@ inline int dense_chunk(int rows, int most, int n_mtiles, int pairs) {
     int64_t least = INT64_MAX;
     for (int size = most; size >= 16; size -= 16) {
         const int64_t items = ((int64_t)rows + size - 1) / size * n_mtiles;
-        const int64_t cost = (items + pairs - 1) / pairs * ((size < 128 && most > 128 ? 128 : size) + 16);
+        const int64_t cost = (items + pairs - 1) / pairs * ((size < 128 ? 128 : size) + 16);
         if (cost < least) {
             least = cost;
             best = size;
@@ -126,8 +126,11 @@ cudaError_t launch_dequantize_rows(const uint8_t* q, const uint8_t* scales, int6
 
 // Products on CTA pairs.  `a` carries the lists, sizes and epilogue buffers;
 // the launchers add the operands.
-// Rows of B per CTA (half of the most rows of a chunk) that are built.
-constexpr int kWideRows = 128, kThinRows = 16;
+// Rows of B per CTA (half of the most rows of a chunk) that are built: a pair's
+// MMA takes about 100 cycles for any N up to 128 and 134 for 256, so chunks of
+// up to 128 rows are the narrowest of use (they leave room for a fourth stage
+// and for two pairs of accumulators in TMEM); 16 where K is split instead.
+constexpr int kWideRows = 128, kThinRows = 64, kSplitRows = 16;
 cudaError_t launch_train_gate_up(const __nv_bfloat16* x, int64_t x_rows, const __nv_bfloat16* Wg,
                                  const __nv_bfloat16* Wu, int H, int I, bool fp8, int nb,
                                  TileArgs a, int num_sms, cudaStream_t s);
