@@ -13,6 +13,14 @@ namespace {
 // at most 3/4 of a narrow chunk (128 rows) on average, else the wide one.
 int rows_per_cta(int64_t rows, int E) { return rows <= (int64_t)96 * E ? kThinRows : kWideRows; }
 
+// Whether a kernel may start while the one before it finishes.  It gains at the
+// ends of short launches and costs long ones (E, H, I, tokens; backward, us
+// with / without): 1, 4096, 2048, 8192: 482 / 506; 32, 2048, 1024, 1999: 267 /
+// 282; 384, 4096, 2048, 16384: 13300 / 12750.  Counted in weight tiles per SM.
+bool overlap(const moe_shape* sh, int num_sms) {
+    return (int64_t)sh->E * 3 * (sh->H / 256) * (sh->I / 256) <= (int64_t)64 * num_sms;
+}
+
 struct Lists {
     WsHeader* hdr;
     RowLists l;
@@ -139,7 +147,7 @@ moe_status moe_expert_ffn_train(const moe_shape* shape, const moe_bf16* x, const
     const int T = shape->T, E = shape->E, k = shape->k, H = shape->H, I = shape->I;
     const int64_t P = (int64_t)T * k;
     const int nb = rows_per_cta(P, E), most = 2 * nb;
-    const PdlScope pdl(P <= kPermChunk);
+    const PdlScope pdl(overlap(shape, sms));
     const __nv_bfloat16* xs = (const __nv_bfloat16*)x;
     if (saved->fp8)
         CUDA_TRY(launch_quantize_rows(xs, T, H, nullptr, 1, 0, (uint8_t*)saved->x, saved->x_scales,
@@ -204,7 +212,7 @@ moe_status moe_expert_ffn_backward(const moe_shape* shape, const moe_bf16* d_out
     STATUS_TRY(current_device(&sms));
     const int64_t P = (int64_t)T * k, pad = padded_rows(P, E);
     const int nb = rows_per_cta(P, E), most = 2 * nb;
-    const PdlScope pdl(P <= kPermChunk);
+    const PdlScope pdl(overlap(shape, sms));
     // x and d_out by sorted row: the caller's own where the block is dense
     const __nv_bfloat16 *x = (const __nv_bfloat16*)saved->x, *d = (const __nv_bfloat16*)d_out;
     const int64_t xd_rows = dense ? T : pad;
@@ -233,22 +241,27 @@ moe_status moe_expert_ffn_backward(const moe_shape* shape, const moe_bf16* d_out
     a.gate_parts = d_gates ? b.parts : nullptr;
     CUDA_TRY(launch_hidden_grad(d, xd_rows, (const __nv_bfloat16*)W_down, H, I, saved->fp8 != 0, nb,
                                 pad, a, sms, s), "gradient of the projections");
+    // The weights' gradients and that of x need nothing of one another: the
+    // second starts as the first one's CTAs run out of items (the first waits
+    // for the hidden gradients, so they are complete when the second starts).
+    if (weights) {
+        TileArgs w = a;
+        w.out = (__nv_bfloat16*)dW_down;
+        w.d_gate = (__nv_bfloat16*)dW_gate;
+        w.d_up = (__nv_bfloat16*)dW_up;
+        CUDA_TRY(launch_weight_grad(b.h, b.dg, b.du, pad, x, d, xd_rows, H, I, w, sms, s),
+                 "gradients of the weights");
+    }
     if (d_x) {
         a.out = dense ? (__nv_bfloat16*)d_x : nullptr;
         a.out32 = dense ? nullptr : b.dx;
+        a.early = weights && overlap(shape, sms);
         CUDA_TRY(launch_input_grad(b.dg, b.du, pad, (const __nv_bfloat16*)W_gate,
                                    (const __nv_bfloat16*)W_up, H, I, nb, a, sms, s), "gradient of x");
     }
     __nv_bfloat16* sums = d_x && !dense ? (__nv_bfloat16*)d_x : nullptr;
     if (sums || d_gates)
         CUDA_TRY(launch_finish(b.dx, sums, b.parts, I / 32, d_gates, inv_perm, T, k, H, sms, s), "sums over slots");
-    if (weights) {
-        a.out = (__nv_bfloat16*)dW_down;
-        a.d_gate = (__nv_bfloat16*)dW_gate;
-        a.d_up = (__nv_bfloat16*)dW_up;
-        CUDA_TRY(launch_weight_grad(b.h, b.dg, b.du, pad, x, d, xd_rows, H, I, a, sms, s),
-                 "gradients of the weights");
-    }
     return ok();
 }
 

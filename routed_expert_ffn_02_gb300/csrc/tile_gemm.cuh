@@ -894,7 +894,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
     cluster_sync();
     fence_after();
     const uint32_t tmem_base = *tmem_holder;
-    grid_dep_wait();
+    if (!args.early) grid_dep_wait();
     grid_dep_launch();
 
     int total;
@@ -1202,6 +1202,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
         fence_after();
         tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
     }
+    if (args.early) grid_dep_wait();   // complete only after the kernel before
 }
 
 // Maps of the rows operand b (chunks of at most 2 * nb rows), ksub strips of K per stage.

@@ -21,7 +21,7 @@ struct RowChunk {
     int32_t rows;
     int32_t row0_pad;
 };
-inline int64_t max_chunks(int64_t P, int E, int most) { return P / most + E; }
+__host__ __device__ inline int64_t max_chunks(int64_t P, int E, int most) { return P / most + E; }
 inline int64_t padded_rows(int64_t P, int E) { return (int64_t)align_up((size_t)P, 16) + 16 * (int64_t)E; }
 
 // A group of c rows in chunks of at most `most` rows (a multiple of 16):
@@ -59,6 +59,7 @@ struct TileArgs {
     int chunk_rows;
     int rows;                  // sorted rows
     int E;
+    int early;                 // reads nothing of the kernel before: starts as that one's CTAs leave
     int padded;                // B's rows are those of a padded buffer
     int n_mtiles, n_ntiles;    // 256-wide tiles of the features (weights: of I and of H)
     int m_total, n_total;      // product: features; weights: I and H

@@ -1,5 +1,7 @@
 // train_rows.cu -- the training passes' row work: lists of the groups' rows,
 // the gathers, the sums over a token's slots, and the 8-bit rows' values.
+#include <climits>
+
 #include "fp8.cuh"
 #include "ld_dev.cuh"
 #include "ptx.cuh"
@@ -76,30 +78,50 @@ __device__ void scan_groups(Groups& g, const int32_t* offsets, int rows, int E, 
     __syncthreads();
 }
 
-// The lists of the groups, by one block.
+// The lists of the groups, by one block.  Few chunks (kSorted at most: a few
+// rounds of the grid) are listed from large to small (in classes of 16 rows; a
+// group's stay together, they read the same weights), so that the items of one
+// round cost about the same and the last round has the smallest: backward of
+// 1999 tokens over 32 experts 267 us, unsorted 276; of many rounds it gains
+// nothing (8192 tokens over 64 experts, forward: 2275 us, unsorted 2255).  The
+// order inside a class is left to the atomics: it decides when an item runs, not
+// what it computes.
+constexpr int kSorted = 256;
 template <int kPerThread>
-__device__ void write_lists(Groups& g, int E, int most, const RowLists& l) {
+__device__ void write_lists(Groups& g, int rows, int E, int most, const RowLists& l) {
+    const int per_class = max_chunks(rows, E, most) <= kSorted ? 16 : INT_MAX;   // one class for all
+    __shared__ int at[17];              // chunks in larger classes, then the class's next place
     const int e0 = threadIdx.x * kPerThread;
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i)
-        if (e0 + i < E) {
-            const int c = g.off[e0 + i + 1] - g.off[e0 + i], size = chunk_size(c, most);
-            n += size ? (c + size - 1) / size : 0;
+    if (threadIdx.x < 17) at[threadIdx.x] = 0;
+    __syncthreads();
+    for (int e = e0; e < e0 + kPerThread && e < E; ++e) {
+        const int c = g.off[e + 1] - g.off[e], size = chunk_size(c, most);
+        if (size) atomicAdd(&at[size / per_class], (c + size - 1) / size);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int before = 0;
+        for (int i = 16; i >= 0; --i) {
+            const int n = at[i];
+            at[i] = before;
+            before += n;
         }
-    int at = scan_before<false>(n, g.warp_vals);
+        *l.n_chunks = before;
+    }
+    __syncthreads();
     for (int e = e0; e < e0 + kPerThread && e < E; ++e) {
         const int v = g.off[e], c = g.off[e + 1] - v, size = chunk_size(c, most);
         RowChunk ch = {e, v, c, g.pad[e]};
         l.groups[e] = ch;
+        if (!size) continue;
+        int to = atomicAdd(&at[size / per_class], (c + size - 1) / size);
         for (int r = 0; r < c; r += size) {
             ch.row0 = v + r;
             ch.rows = min(size, c - r);
             ch.row0_pad = g.pad[e] + r;
-            l.chunks[at++] = ch;
+            l.chunks[to++] = ch;
         }
     }
-    if (threadIdx.x == kThreads - 1) *l.n_chunks = at;     // no group behind it
 }
 
 template <int kPerThread>
@@ -109,7 +131,7 @@ plan_rows_kernel(const int32_t* offsets, int rows, int E, int most, RowLists l, 
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     scan_groups<kPerThread>(g, offsets, rows, E, hdr);
-    write_lists<kPerThread>(g, E, most, l);
+    write_lists<kPerThread>(g, rows, E, most, l);
 }
 
 // Eight e4m3 values (one 8-byte word) of one scale as bf16: exact.
@@ -141,7 +163,7 @@ forward_rows_kernel(const uint4* x, const int32_t* perm, int k, int vec, const i
     ptx::grid_dep_launch();
     if (blockIdx.x == 0) {
         scan_groups<kPerThread>(g, offsets, P, E, hdr);
-        write_lists<kPerThread>(g, E, most, l);
+        write_lists<kPerThread>(g, P, E, most, l);
     }
     const int lane = threadIdx.x & 31;
     for (int64_t p = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); p < P; p += (int64_t)gridDim.x * (kThreads / 32)) {
@@ -185,7 +207,7 @@ backward_rows_kernel(BackwardRows q) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     scan_groups<kPerThread>(g, q.offsets, q.T * q.k, q.E, blockIdx.x == 0 ? q.hdr : nullptr);
-    if (blockIdx.x == 0) write_lists<kPerThread>(g, q.E, q.most, q.lists);
+    if (blockIdx.x == 0) write_lists<kPerThread>(g, q.T * q.k, q.E, q.most, q.lists);
     const int lane = threadIdx.x & 31, vec = q.H / 8;
     const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5),
                   warps = (int64_t)gridDim.x * (kThreads / 32);
@@ -242,11 +264,14 @@ backward_rows_kernel(BackwardRows q) {
                     make_uint4(0, 0, 0, 0);
         }
     }
-    for (int64_t e = warp; e < q.E; e += warps) {
-        const int c = g.off[e + 1] - g.off[e];
-        const int64_t from = ((int64_t)g.pad[e] + c) * vec, to = (int64_t)g.pad[e + 1] * vec;
-        for (int64_t i = from + lane; i < to; i += 32)
-            reinterpret_cast<uint4*>(q.x_rows)[i] = reinterpret_cast<uint4*>(q.d_rows)[i] = make_uint4(0, 0, 0, 0);
+    // The padding, a row per warp.
+    for (int64_t i = warp; i < (int64_t)q.E * 15; i += warps) {
+        const int e = (int)(i / 15), c = g.off[e + 1] - g.off[e];
+        const int64_t row = (int64_t)g.pad[e] + c + i % 15;
+        if (row >= g.pad[e + 1]) continue;
+        for (int v = lane; v < vec; v += 32)
+            reinterpret_cast<uint4*>(q.x_rows)[row * vec + v] = reinterpret_cast<uint4*>(q.d_rows)[row * vec + v] =
+                make_uint4(0, 0, 0, 0);
     }
 }
 
