@@ -883,8 +883,10 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        prefetch_map(&maps.a0);
-        prefetch_map(&maps.b[0][C::NB / C::BOX - 1]);
+        if (kKind != kProduct || args.flat_from > 0) {     // else there are only flat maps
+            prefetch_map(&maps.a0);
+            prefetch_map(&maps.b[0][C::NB / C::BOX - 1]);
+        }
         if (gated(kKind) || kKind == kInput || kKind == kWeights) prefetch_map(&maps.a1);
         if (kKind == kInput || kKind == kWeights) prefetch_map(&maps.b[1][C::NB / C::BOX - 1]);
         if (kKind == kWeights) prefetch_map(&maps.b[2][C::NB / C::BOX - 1]);

@@ -75,6 +75,19 @@ def test_row_counts_at_the_tiles_edges(moe, rows, listed):
     check(y, x, W, None, b, "none", r)
 
 
+@pytest.mark.parametrize("rows,N,K", [(1, 4096, 4096), (24, 384, 4096), (32, 1001, 1032), (2, 8, 65536), (17, 16640, 1024),
+                                      (32, 9000, 2056), (5, 300, 1024)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_few_rows_of_long_k(moe, rows, N, K, out):
+    """K split over the pairs of a cluster, or too many columns for that."""
+    x, W, _, b, r = make(rows, 1, N, K, rows + N)
+    ws = moe.Workspace(moe.grouped_gemm_workspace_size(rows, 1, N, K))
+    y = torch.full((rows + 2, N), 7.0, dtype=out, device="cuda")
+    moe.moe_grouped_gemm(x, W, bias=b, activation="gelu", residual=r, out_dtype=out, y=y[:rows], ws=ws)
+    assert ws.status() == 0 and (y[rows:] == 7).all()
+    check(y[:rows], x, W, None, b, "gelu", r)
+
+
 def test_no_rows(moe):
     x, W, off, b, _ = make(0, 3, 64, 64, 1, residual=False, skew=0.0)
     assert moe.moe_grouped_gemm(x, W, off, bias=b).shape == (0, 64)
@@ -149,7 +162,7 @@ def test_another_stream_and_a_graph(moe):
     assert ws.status() == 0
 
 
-@pytest.mark.parametrize("rows,E", [(20, 1), (2000, 3), (40, 30)])
+@pytest.mark.parametrize("rows,E", [(20, 1), (300, 1), (2000, 3), (40, 30)])
 def test_waits_that_expire_leave_nothing_behind(moe, rows, E):
     x, W, off, b, r = make(rows, E, 1024, 2048, 9)
     ws = moe.Workspace(moe.grouped_gemm_workspace_size(rows, E, 1024, 2048))

@@ -179,6 +179,57 @@ def test_experts_without_rows(moe, sizes, checkpoint):
         assert all((w[e] == 0).all() for w in dW)
 
 
+def test_an_expert_twice_for_a_token(moe):
+    """Two slots of one token at the same expert: both count."""
+    case = Case(50, 4, 2, 256, 256, seed=19)
+    idx = torch.stack([torch.arange(50, device="cuda") % 4] * 2, 1).to(torch.int32).contiguous()
+    _, case.offsets, case.perm, case.inv = moe.moe_permute(idx, 4)
+    case.tokens = case.perm.long() // 2
+    y, saved = case.forward(moe)
+    check_forward(case, y, saved, moe)
+    check_backward(case, case.backward(moe, saved), saved, moe)
+
+
+def test_two_calls_at_once(moe):
+    """Two steps on two streams, each with its own workspaces."""
+    cases = [Case(600, 8, 2, 512, 256, seed=20), Case(50, 8, 2, 512, 256, seed=21)]
+    want = []
+    for c in cases:
+        y, saved = c.forward(moe)
+        want.append((y, *c.backward(moe, saved)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        got = []
+        for c, s in zip(cases, streams):
+            y, saved = c.forward(moe, stream=s)
+            got.append((y, *c.backward(moe, saved, stream=s)))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
+
+
+def test_calls_that_follow_one_another_on_one_workspace(moe):
+    """Kernels may start while the one before finishes: calls of different
+    sizes in a row, without a pause, give the bits of calls alone."""
+    cases = [Case(700, 1, 1, 512, 256, seed=22, dense=True), Case(33, 1, 1, 512, 256, seed=23, dense=True),
+             Case(300, 6, 2, 512, 256, seed=24), Case(40, 6, 2, 512, 256, seed=25)]
+    wf = moe.Workspace(max(moe.expert_ffn_train_workspace_size(moe.Shape(*c.sizes)) for c in cases))
+    wb = moe.Workspace(max(moe.expert_ffn_backward_workspace_size(moe.Shape(*c.sizes)) for c in cases))
+    want = []
+    for c in cases:
+        y, saved = c.forward(moe, "fp8", ws=wf)
+        want.append((y, *(v for v in c.backward(moe, saved, ws=wb))))
+        torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for c in cases:
+            y, saved = c.forward(moe, "fp8", ws=wf)
+            got.append((y, *c.backward(moe, saved, ws=wb)))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
+    assert wf.status() == 0 and wb.status() == 0
+
+
 def test_no_token(moe):
     case = Case(0, 4, 2, 256, 256)
     y, saved = case.forward(moe)
