@@ -178,16 +178,6 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
-// The same for a 3-D map.
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map,
-                                                 uint32_t bar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
-
 // Shared -> global tensor store of one box at (x, y) in the bulk async-group
 // of the issuing thread; x * element size must be a multiple of 16 bytes.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {

@@ -145,14 +145,5 @@ cudaError_t make_tma_map_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, ui
 // Same over 8-bit values: box = 128 columns (128 bytes) x box_rows.
 cudaError_t make_tma_map_u8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
                             uint32_t box_rows);
-// The same matrix as strips of 64 columns, [cols / 64][rows][64] (columns behind
-// the last whole strip left out): box = box_strips strips x box_rows rows, so
-// that one copy loads several of the 128-byte-wide tiles the MMA reads.
-cudaError_t make_tma_map_strips(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
-                                uint32_t box_strips);
-// Map for storing tiles (box = 32 columns x box_rows) of bf16 (64-byte
-// swizzle) or fp32 (128-byte swizzle).
-cudaError_t make_tma_map_tile(CUtensorMap* m, const void* ptr, bool f32, uint64_t rows, uint64_t cols,
-                              uint32_t box_rows = 32);
 
 }  // namespace moe

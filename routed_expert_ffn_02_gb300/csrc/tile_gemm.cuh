@@ -14,9 +14,23 @@
 //   gradient  dh = dy Wd          A = Wd[k, f]       B = dy[row, k]
 //   weights   dWd = dy^T h        A = h[k = row, i]  B = dy[k = row, h']
 // without a transposed copy of anything.  The accumulator has a feature per
-// lane and a row per column, so 32 lanes store 32 consecutive features of a
-// row: 64-byte segments straight from registers, for any row stride and any
-// row count.
+// lane and a row per column; an epilogue warp turns 32 x 32 values around
+// through shared memory (see "fragments and staging tiles").
+//
+// Three stages of 128 of K (64 KB per CTA), two accumulators in TMEM.  The gated
+// products of the forward pass have two accumulators per item (gate and up share
+// the rows' tile): with chunks of 256 rows these fill TMEM, and the epilogue is
+// not hidden under the next item.
+//
+// What bounds it (GB300, 1.9 GHz unless the power cap is reached): an item of
+// K = 4096 takes 19.3 us at N = 256 with its operands in L2 (17.9 for the MMAs
+// alone, 13.8 for the copies alone), 15.8 at N = 176 and 13.2 at any N up to 128
+// (the MMA's floor of about 100 cycles).  Shared memory carries 128 bytes a
+// cycle then: half of it the MMA's operands, half the copies that bring them.
+// Long runs of N = 256 reach 1.36 kW, the power cap, at 1.55-1.75 GHz: 1.6-1.7
+// PFLOP/s, as the library's products do (measured 1.69 sustained).  Halving the
+// copies of B (an experiment; multicast between pairs would save as much) gained
+// 2-5%, fetching weights into L2 ahead cost 2-30%.
 //
 // Roles per CTA (persistent, one cluster per SM pair):
 //   warp 0      TMA producer (one lane);
@@ -25,8 +39,8 @@
 //   warps 4-11  epilogue, two warps per 32 lanes of the accumulator, taking
 //               its 32-column blocks in turn.
 // Every mbarrier wait is bounded and drained as in gemm_tc.cu: on expiry a
-// role records MOE_ERR_TIMEOUT, the cluster's CTAs stop, and copies and MMAs in flight
-// are waited for before TMEM is freed.
+// role records MOE_ERR_TIMEOUT, the cluster's CTAs stop, and copies and MMAs in
+// flight are waited for before TMEM is freed.
 #pragma once
 
 #include <cuda.h>
@@ -225,6 +239,16 @@ __device__ __forceinline__ float sigmoid(float g) {
 }
 __device__ __forceinline__ float2 unpack(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+// tma_load_2d_pair for a 3-D map.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map,
+                                                 uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
 }
 
 // ---- fragments and staging tiles --------------------------------------------

@@ -3,6 +3,7 @@
 // the tile kernel (tile_gemm.cuh), and the launchers.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -124,6 +125,17 @@ cudaError_t launch_finish(const float* y, __nv_bfloat16* d_x, const float* parts
 // bf16 values of rows of e4m3 with a scale per 128 of K (exact).
 cudaError_t launch_dequantize_rows(const uint8_t* q, const uint8_t* scales, int64_t rows, int K,
                                    __nv_bfloat16* x, int num_sms, cudaStream_t s);
+
+// 3-D bf16 tensor map over a row-major [rows, cols] matrix seen as strips of 64
+// columns, [cols / 64][rows][64], 128-byte swizzle, zero fill outside (columns behind
+// the last whole strip left out): box = box_strips strips x box_rows rows, so
+// that one copy loads several of the 128-byte-wide tiles the MMA reads.
+cudaError_t make_tma_map_strips(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
+                                uint32_t box_strips);
+// Map for storing tiles (box = 32 columns x box_rows) of bf16 (64-byte
+// swizzle) or fp32 (128-byte swizzle).
+cudaError_t make_tma_map_tile(CUtensorMap* m, const void* ptr, bool f32, uint64_t rows, uint64_t cols,
+                              uint32_t box_rows = 32);
 
 // Products on CTA pairs.  `a` carries the lists, sizes and epilogue buffers;
 // the launchers add the operands.

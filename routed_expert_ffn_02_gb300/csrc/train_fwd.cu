@@ -1,6 +1,10 @@
 // train_fwd.cu -- the training forward pass of the experts on the tile kernel:
 //   gate/up  h = bf16(silu(g) * u), g = x Wg^T and u = x Wu^T kept in bf16 or 8 bits;
 //   down     y = h Wd^T.
+// Both are bound by the tensor cores at the power cap.  8192 rows, H = 4096, I =
+// 2048, one expert: gate/up 152 us (1.81 PFLOP/s; the items' epilogues, 6 of 38
+// us, are not hidden), down 75 us (1.83); 65536 rows of 64 experts, 8-bit
+// checkpoints: 1290 us (1.70) and 623 us (1.76).
 #include "tile_gemm.cuh"
 
 namespace moe {

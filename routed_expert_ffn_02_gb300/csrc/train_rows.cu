@@ -153,7 +153,8 @@ __device__ __forceinline__ float scale_of(uint32_t b) {
 }
 
 // Forward: xs[p] = x[perm[p] / k] for the groups' rows, a warp per row, eight
-// 16-byte vectors per lane in flight; block 0 writes the lists.
+// 16-byte vectors per lane in flight; block 0 writes the lists.  65536 x 4096
+// rows of 8192 tokens: 132 us, 4.1 TB/s written.
 template <int kPerThread>
 __global__ void __launch_bounds__(kThreads)
 forward_rows_kernel(const uint4* x, const int32_t* perm, int k, int vec, const int32_t* offsets, int P, int E,
@@ -189,7 +190,8 @@ forward_rows_kernel(const uint4* x, const int32_t* perm, int k, int vec, const i
 // Backward: each token's rows of x and d_out to the padded rows of its slots,
 // and zeros to the padding.  A warp takes a token, so that a row is read once
 // however many slots it has (by sorted row, x and d of 16384 tokens do not fit
-// L2 together and were read from memory k times: 631 us at 16384 x 4096, k = 8).
+// L2 together and were read from memory k times: 631 us at 16384 x 4096, k = 8;
+// 392 this way, 6.2 TB/s).
 __device__ __forceinline__ int64_t padded_row(const Groups& g, int E, int p) {
     int lo = 0, hi = E;          // the last group whose first row is not above p
     while (hi - lo > 1) {
@@ -279,7 +281,7 @@ backward_rows_kernel(BackwardRows q) {
 // d_gate = the sum of its parts over the features (a warp per slot: lanes in
 // order, then a fixed tree).  The parts of d_x are fp32: rounding them to bf16
 // as well would make the rounding error of d_x 1.22 times as large (relative
-// RMS 2.9e-3 for 2.4e-3).
+// RMS 2.9e-3 for 2.4e-3).  16384 x 4096, k = 8: 398 us, 5.7 TB/s.
 __global__ void __launch_bounds__(kThreads)
 finish_kernel(const float4* y, uint2* d_x, const float* parts, int n_parts, float* d_gates, const int32_t* inv, int T,
               int k, int vec) {
@@ -325,6 +327,7 @@ finish_kernel(const float4* y, uint2* d_x, const float* parts, int n_parts, floa
     }
 }
 
+// 65536 x 2048: 63 us, 6.4 TB/s.
 __global__ void __launch_bounds__(256)
 dequantize_rows_kernel(const uint2* q, const uint8_t* scales, int64_t n, uint4* x) {
     ptx::grid_dep_wait();
