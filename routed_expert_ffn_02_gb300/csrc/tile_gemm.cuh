@@ -60,7 +60,7 @@ using namespace ptx;
 using namespace tc;
 
 constexpr int kThreads = 384;
-constexpr int kEpiWarps = 8;         // 16 took 15% longer: shared memory and stores bound them
+constexpr int kEpiWarps = 8;         // 16 took 15% longer (16384 x 4096 results of K = 128)
 constexpr int kTileFeatures = 256;   // features per item (both CTAs)
 constexpr int kTileBytes = 32 * 64;  // a staging tile
 
@@ -84,7 +84,6 @@ constexpr bool hidden(int kind) { return kind == kHidden || kind == kHiddenFp8; 
 template <int kKind, int kNB, int kSplit = 1>
 struct Cfg {
     static_assert(kSplit == 1 || (kKind == kProduct && kNB == 16));
-    static constexpr int SPLIT = kSplit;
     static constexpr int CTAS = 2 * kSplit;           // of a cluster
     // the other pairs' parts: [pair - 1][4 warps][32 values][32 lanes]
     static constexpr int PARTS_BYTES = (kSplit - 1) * 4 * 32 * 32 * 4;
@@ -228,9 +227,10 @@ __device__ __forceinline__ float scale_value(uint32_t b) {
     return __uint_as_float(b == 0 ? 1u << 22 : b == 255 ? 0x7fc00000u : b << 23);
 }
 // 1 / (1 + exp(-g)) by the hardware's 2^x and reciprocal (2^-22 and one unit in
-// the last place), subnormals flushed: the library's __expf and __fdividef take
-// twice the instructions for them, and the epilogues are bound by those
-// (a block of store_hidden: 5000 cycles of which 2/3 were this).
+// the last place), subnormals flushed: __expf and __fdividef take twice the
+// instructions for them, which the epilogues feel (with fewer tests per value:
+// gradient of the projections at 1999 tokens 67.7 -> 62.0 us, 8-bit gate/up of
+// 65536 rows 1382 -> 1293).
 __device__ __forceinline__ float sigmoid(float g) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
@@ -348,9 +348,9 @@ __device__ __forceinline__ uint32_t next_tile(Warp& w) {
 }
 
 // Where 32 x 32 blocks of an output go: a map for whole blocks, which the copy
-// engine stores from the tile (the LSU's part of it, 64 bytes of each of 8 rows
-// an instruction, was what bound the epilogues: 10 cycles of the data pipe
-// each), and the address for a group's last rows.
+// engine stores from the tile, and the address for a group's last rows, stored
+// in 16-byte vectors by the warp (whole blocks stored that way take the same
+// time with four loads and stores more each).
 struct OutBlock {
     const CUtensorMap* map;
     int x, y;                  // column and row of the block
