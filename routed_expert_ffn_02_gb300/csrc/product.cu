@@ -25,9 +25,13 @@ cudaError_t launch_product(const __nv_bfloat16* x, int64_t rows, const __nv_bflo
         if ((e = make_tma_map_strips(&m.a0, W, (uint64_t)a.E * N, K, 128, C::KSUB)) != cudaSuccess) return e;
         if ((e = tg::row_maps(m.b[0], x, rows, K, nb, C::KSUB)) != cudaSuccess) return e;
     }
-    if (K % C::BK) {
+    const int rest = K - a.flat_from * C::BK;
+    a.flat_strips = (rest + 63) / 64;
+    a.k16_last = rest ? (rest + 15) / 16 : C::BK / 16;
+    if (rest) {
         if ((e = make_tma_map_bf16(&m.flat_a, W, (uint64_t)a.E * N, K, 128)) != cudaSuccess) return e;
-        if ((e = make_tma_map_bf16(&m.flat_b, x, rows, K, nb < 32 ? nb : 32)) != cudaSuccess) return e;
+        for (int i = 0; i < (nb < 32 ? 1 : nb / 32); ++i)
+            if ((e = make_tma_map_bf16(&m.b[1][i], x, rows, K, nb < 32 ? nb : 32 * (i + 1))) != cudaSuccess) return e;
     }
     a.map_out = N % (a.out32 ? 4 : 8) == 0;
     if (a.map_out) {

@@ -148,7 +148,7 @@ struct Item {
     int row0;      // first row among the sorted rows
     int row0_pad;  // the same in the padded buffers
     int k_blocks;
-    int k16_last;  // 16-deep steps of the last block
+    int k16_last;  // 16-deep steps of the last block (of whole K)
     int boxes;     // B's rows of one CTA, in boxes of BOX
 };
 
@@ -195,7 +195,7 @@ __device__ __forceinline__ Item item_of(const TileArgs& a, int w) {
         }
         it.n = (it.rows + 15) & ~15;
         it.k_blocks = a.k_blocks;
-        it.k16_last = C::BK / 16;
+        it.k16_last = kKind == kProduct ? a.k16_last : C::BK / 16;
         it.boxes = (it.n / 2 + C::BOX - 1) / C::BOX;
     }
     return it;
@@ -212,13 +212,13 @@ __device__ __forceinline__ Item item_of(const TileArgs& a, int w) {
 // cycles each to issue, bounded every item with fewer than 256 rows when a
 // stage took 8 (K = 4096: 17.6 us for any N from 96 to 192).  b[..][i] holds
 // boxes of 32 (i + 1) rows, for chunks of so many rows (a CTA's half, rounded
-// up); weights: [0] 32 and [3] 128 rows of K, of a and b.  flat: 64-column
-// boxes, zero beyond the last column, for a product's K behind its last whole
-// strip.
+// up); weights: [0] 32 and [3] 128 rows of K, of a and b.  flat_a and, as b[0],
+// b[1]: 64-column boxes, zero beyond the last column, for a product's last block
+// where K does not fill it (two copies a strip).
 struct Maps {
     CUtensorMap a0, a1, tail_a0, tail_a1;
     CUtensorMap b[3][4];
-    CUtensorMap flat_a, flat_b;
+    CUtensorMap flat_a;
     CUtensorMap o0, o1, o2;
 };
 
@@ -746,30 +746,30 @@ __device__ __forceinline__ void activate(Frag& f, int act) {
 }
 
 // What a product block adds, loaded a block ahead: its residual in vectors
-// where rows are 16-byte aligned (a.vec), else a feature per lane, rows 2 i and
-// 2 i + 1 in word i.
-__device__ __forceinline__ void load_residual(RowVecs& r, const TileArgs& a, const Item& it, int f0,
+// where rows are 16-byte aligned (a.vec), else a feature per lane and a row per
+// word (packing them here would wait for the loads).
+union Residual {
+    RowVecs vecs;
+    uint32_t words[32];
+};
+__device__ __forceinline__ void load_residual(Residual& r, const TileArgs& a, const Item& it, int f0,
                                               int c0, int lane) {
     const int64_t at = (int64_t)(it.row0 + c0) * a.ld + f0;
     if (a.vec) {
-        load_rows(r, a.residual + at, a.ld, f0 + (lane & 3) * 8 < a.m_total ? it.rows - c0 : 0, lane);
+        load_rows(r.vecs, a.residual + at, a.ld, f0 + (lane & 3) * 8 < a.m_total ? it.rows - c0 : 0, lane);
         return;
     }
     const int left = f0 + lane < a.m_total ? it.rows - c0 : 0;
     const uint16_t* p = reinterpret_cast<const uint16_t*>(a.residual + at) + lane;
-    uint16_t x[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-        x[i] = 0;
-        if (i < left) x[i] = *p;
+        r.words[i] = 0;
+        if (i < left) r.words[i] = *p;
         p += a.ld;
     }
-    uint32_t* w = &r.v[0].x;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = (uint32_t)x[2 * i] | (uint32_t)x[2 * i + 1] << 16;
 }
 __device__ __forceinline__ void store_product(const TileArgs& a, const Item& it, int f0, int c0, Frag& v,
-                                              const RowVecs& res, const Maps& maps, Warp& w) {
+                                              const Residual& res, const Maps& maps, Warp& w) {
     const int left = it.rows - c0, lane = w.lane, feats = a.m_total - f0;
     const int64_t at = (int64_t)(it.row0 + c0) * a.ld + f0;
     if (a.bias) {
@@ -788,13 +788,12 @@ __device__ __forceinline__ void store_product(const TileArgs& a, const Item& it,
     if (a.residual) {
         const uint32_t tile = next_tile<2>(w);
         if (a.vec) {
-            put_rows(tile, res, lane);
+            put_rows(tile, res.vecs, lane);
         } else {
-            const uint32_t* x = &res.v[0].x;
 #pragma unroll
             for (int r = 0; r < 32; ++r)
                 asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile_at(tile, r, lane >> 3) + (lane & 7) * 2),
-                             "h"((uint16_t)(x[r >> 1] >> (16 * (r & 1))))
+                             "h"((uint16_t)res.words[r])
                              : "memory");
         }
         __syncwarp();
@@ -822,13 +821,16 @@ __device__ __forceinline__ void store_product(const TileArgs& a, const Item& it,
     const uint32_t tile = next_tile<2>(w);
     frag_to_tile(tile, pack(v), lane);
     __syncwarp();
-    if (lane < feats) {
-#pragma unroll 8
-        for (int r = 0; r < 32; ++r) {
-            uint16_t x;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(tile_at(tile, r, lane >> 3) + (lane & 7) * 2) : "memory");
-            if (r < left) *reinterpret_cast<uint16_t*>(a.out + at + (int64_t)r * a.ld + lane) = x;
-        }
+    uint16_t x[32];      // all loads before the first store
+#pragma unroll
+    for (int r = 0; r < 32; ++r)
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x[r]) : "r"(tile_at(tile, r, lane >> 3) + (lane & 7) * 2) : "memory");
+    uint16_t* to = reinterpret_cast<uint16_t*>(a.out + at) + lane;
+    const int rows = lane < feats ? left : 0;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+        if (r < rows) *to = x[r];
+        to += a.ld;
     }
     if (lane == 0) bulk_commit();
 }
@@ -970,8 +972,11 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                             }
                     }
                 } else {
-                    // B: the rows of the chunk, rounded up to a box, no more
-                    const uint32_t bytes = (uint32_t)(C::A_BYTES + it.boxes * C::BOX * C::BK * 2);
+                    // B: the rows of the chunk, rounded up to a box, no more; of a product's
+                    // last block, the strips of K that there are
+                    const bool flat = kKind == kProduct && kb >= args.flat_from;
+                    const int strips = flat ? args.flat_strips : C::KSUB;
+                    const uint32_t bytes = (uint32_t)((C::A_BYTES / C::KSUB + it.boxes * C::BOX * 128) * strips);
                     stage_bytes[stage] = bytes;
                     if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * bytes);
                     const CUtensorMap *ma = &maps.a0, *mb = &maps.b[0][it.boxes - 1];
@@ -984,12 +989,10 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                     }
                     // the odd CTA holds the upper half of the N rows
                     const int brow = (args.padded ? it.row0_pad : it.row0) + (int)rank * (it.n >> 1);
-                    if (kKind == kProduct && kb >= args.flat_from) {
-                        for (int j = 0; j < C::KSUB; ++j) {
+                    if (flat) {
+                        for (int j = 0; j < strips; ++j) {
                             tma_load_2d_pair(sa + j * 128 * 128, &maps.flat_a, fb, k + 64 * j, it.expert * args.a_rows + m);
-                            for (int q = 0; q < it.boxes; ++q)
-                                tma_load_2d_pair(sb + (j * it.boxes + q) * C::BOX * 128, &maps.flat_b, fb, k + 64 * j,
-                                                 brow + q * C::BOX);
+                            tma_load_2d_pair(sb + j * it.boxes * C::BOX * 128, &maps.b[1][it.boxes - 1], fb, k + 64 * j, brow);
                         }
                     } else {
 #pragma unroll
@@ -1039,10 +1042,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                 }
                 fence_after();
                 const uint32_t sa = base + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
-                const int steps = kb == it.k_blocks - 1 ? it.k16_last : C::BK / 16;
-#pragma unroll
-                for (int kk = 0; kk < C::BK / 16; ++kk) {
-                    if (kKind == kWeights && kk >= steps) break;
+                const auto step = [&](int kk) {
                     uint64_t bd;
                     if constexpr (C::kBMN) bd = mn_desc(sb + kk * 2048, C::BK * 128);
                     else bd = sw128_desc(sb + (kk / 4) * b_strip) + (uint64_t)((kk % 4) * 2);
@@ -1053,6 +1053,13 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                         else ad = sw128_desc(sa + mt * C::A_SUB + (kk / 4) * 128 * 128) + (uint64_t)((kk % 4) * 2);
                         mma_bf16_pair(d_tmem + (uint32_t)(mt * C::BN), ad, bd, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
                     }
+                };
+                if ((kKind == kWeights || kKind == kProduct) && kb == it.k_blocks - 1 && it.k16_last < C::BK / 16) {
+#pragma unroll 1
+                    for (int kk = 0; kk < it.k16_last; ++kk) step(kk);
+                } else {
+#pragma unroll
+                    for (int kk = 0; kk < C::BK / 16; ++kk) step(kk);
                 }
                 issued = true;
                 commit_pair_multicast(empty_bar(stage), pair_mask);
@@ -1086,7 +1093,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
             const bool live = kKind != kProduct || f0 < args.m_total;
             // what the first block reads does not wait for the products
             [[maybe_unused]] KeptRows<kKind> kept;
-            [[maybe_unused]] RowVecs res;
+            [[maybe_unused]] Residual res;
             if constexpr (hidden(kKind)) load_kept<kKind>(kept, args, it, f0, 32 * half, lane);
             if constexpr (kKind == kProduct)
                 if (kSplit == 1 && live && args.residual) load_residual(res, args, it, f0, 32 * half, lane);
@@ -1167,7 +1174,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
                     load_frag(taddr + c0, v);
                     tmem_ld_wait();
                     if constexpr (kKind == kProduct) {
-                        const RowVecs now = res;
+                        const Residual now = res;
                         if (args.residual && c0 + 64 < n)
                             load_residual(res, args, it, f0, c0 + 64, lane);
                         store_product(args, it, f0, c0, v, now, maps, wp);
@@ -1216,7 +1223,7 @@ tile_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Tile
 #pragma unroll
                     for (int q = 0; q < 32; ++q) (&mine.v[0][0][0])[q] += parts[p * 4096 + q * 32];
                 Warp wp = {lane, quad, base + kStagingAt + (uint32_t)(warp - 4) * C::TILES * kTileBytes, 0, nullptr, 0};
-                RowVecs res;
+                Residual res;
                 if (args.residual) load_residual(res, args, it, f0, 0, lane);
                 store_product(args, it, f0, 0, mine, res, maps, wp);
                 if (lane == 0) bulk_wait_all();

@@ -67,7 +67,9 @@ struct TileArgs {
     int a_rows;                // rows of A per expert
     int k_blocks;
     int seg_blocks;            // input gradient: blocks of the first product
-    int flat_from;             // product: first block of K with a partial strip
+    int flat_from;             // product: the block that K does not fill, its strips of 64 and
+    int flat_strips;           // steps of 16
+    int k16_last;
     int64_t ld;                // features of an output row
     long long wait_cycles;
     // Buffers by kind (see the epilogues).
