@@ -306,6 +306,13 @@ moe_status moe_grouped_gemm(const moe_bf16* x, int32_t rows, const int32_t* offs
     cudaStream_t s = (cudaStream_t)stream;
     const int nb = rows_per_cta(rows, E), most = 2 * nb;
     const PdlScope pdl(rows <= kPermChunk);
+    if (!offsets && rows <= kFewRows) {
+        const ProductEpilogue e = {bias, (const __nv_bfloat16*)residual, y_fp32 ? nullptr : (__nv_bfloat16*)y,
+                                   y_fp32 ? (float*)y : nullptr, activation};
+        CUDA_TRY(launch_product_rows((const __nv_bfloat16*)x, rows, (const __nv_bfloat16*)W, N, K, e, s),
+                 "product of few rows");
+        return ok();
+    }
     if (offsets) CUDA_TRY(launch_plan_rows(offsets, rows, E, most, l.l, l.hdr, s), "plan");
     TileArgs a = args_of(l, !offsets, rows, E);
     a.out = y_fp32 ? nullptr : (__nv_bfloat16*)y;

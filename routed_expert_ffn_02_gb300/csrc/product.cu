@@ -16,9 +16,9 @@ cudaError_t launch_product(const __nv_bfloat16* x, int64_t rows, const __nv_bflo
     a.k_blocks = (K + C::BK - 1) / C::BK;
     a.flat_from = K / C::BK;           // the block that K does not fill, if there is one
     // Few rows, few feature tiles: K is split so that more SMs stream weights.
-    // One row times 4096 x 4096 took 17.4 us on 16 pairs, 32 blocks of K at
+    // Up to 32 rows times 4096 x 4096 took 17.4 us on 16 pairs, 32 blocks of K at
     // 0.41 us (a pair's MMAs of few rows take about 100 cycles each); split in
-    // two, 11.0.
+    // two, 11.0; 24 rows times 384 x 4096 16.8, split in four 7.6.
     const bool split = !a.chunks && a.rows <= 2 * kSplitRows && a.k_blocks >= 8;
     if (split) nb = kSplitRows;
     if (a.flat_from > 0) {

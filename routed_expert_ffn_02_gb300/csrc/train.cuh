@@ -164,4 +164,16 @@ cudaError_t launch_weight_grad(const __nv_bfloat16* h, const __nv_bfloat16* dg,
 cudaError_t launch_product(const __nv_bfloat16* x, int64_t rows, const __nv_bfloat16* W, int N,
                            int K, int nb, TileArgs a, int num_sms, cudaStream_t s);
 
+// The dense product of at most kFewRows rows by streaming the weights.
+constexpr int kFewRows = 3;
+struct ProductEpilogue {
+    const float* bias;
+    const __nv_bfloat16* residual;
+    __nv_bfloat16* out;        // or out32
+    float* out32;
+    int act;
+};
+cudaError_t launch_product_rows(const __nv_bfloat16* x, int rows, const __nv_bfloat16* W, int N, int K,
+                                const ProductEpilogue& e, cudaStream_t s);
+
 }  // namespace moe

@@ -75,7 +75,20 @@ def test_row_counts_at_the_tiles_edges(moe, rows, listed):
     check(y, x, W, None, b, "none", r)
 
 
-@pytest.mark.parametrize("rows,N,K", [(1, 4096, 4096), (24, 384, 4096), (32, 1001, 1032), (2, 8, 65536), (17, 16640, 1024),
+@pytest.mark.parametrize("rows", [1, 2, 3, 4])
+@pytest.mark.parametrize("N,K", [(1, 8), (5, 520), (384, 4096), (1001, 1000), (130, 16384), (7, 65536)])
+@pytest.mark.parametrize("act,out", [("silu", torch.bfloat16), ("relu", torch.float32)])
+def test_single_tokens(moe, rows, N, K, act, out):
+    """Up to three rows stream the weights on the CUDA cores."""
+    x, W, _, b, r = make(rows, 1, N, K, rows + N)
+    y = torch.full((rows + 2, N), 7.0, dtype=out, device="cuda")
+    moe.moe_grouped_gemm(x, W, bias=b, activation=act, residual=r, out_dtype=out, y=y[1:1 + rows] if N % 8 == 0 else y[:rows])
+    at = y[1:1 + rows] if N % 8 == 0 else y[:rows]
+    check(at, x, W, None, b, act, r)
+    assert (y[rows + 1:] == 7).all()
+
+
+@pytest.mark.parametrize("rows,N,K", [(1, 4096, 4096), (24, 384, 4096), (4, 4096, 4096), (32, 1001, 1032), (2, 8, 65536), (17, 16640, 1024),
                                       (32, 9000, 2056), (5, 300, 1024)])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 def test_few_rows_of_long_k(moe, rows, N, K, out):
