@@ -101,6 +101,16 @@ def test_few_rows_of_long_k(moe, rows, N, K, out):
     check(y[:rows], x, W, None, b, "gelu", r)
 
 
+@pytest.mark.parametrize("N,out", [(16400, torch.bfloat16), (16401, torch.float32)])
+def test_offsets_beyond_32_bits(moe, N, out):
+    rows = 140_000
+    x, W, _, b, _ = make(rows, 1, N, 64, 11, residual=False)
+    r = torch.ones((rows, N), dtype=torch.bfloat16, device="cuda")
+    y = moe.moe_grouped_gemm(x, W, bias=b, residual=r, out_dtype=out)
+    at = torch.cat([torch.arange(0, 3), torch.arange(130_900, 130_960), torch.arange(rows - 70, rows)]).cuda()
+    check(y[at], x[at], W, None, b, "none", r[at])
+
+
 def test_no_rows(moe):
     x, W, off, b, _ = make(0, 3, 64, 64, 1, residual=False, skew=0.0)
     assert moe.moe_grouped_gemm(x, W, off, bias=b).shape == (0, 64)

@@ -179,6 +179,31 @@ def test_experts_without_rows(moe, sizes, checkpoint):
         assert all((w[e] == 0).all() for w in dW)
 
 
+@pytest.mark.parametrize("checkpoint", ["bf16", "fp8"])
+@pytest.mark.parametrize("sizes", [(20, 2, 1, 16384, 256), (20, 2, 1, 256, 16384), (300, 2, 2, 256, 16384)], ids=str)
+def test_largest_sizes(moe, sizes, checkpoint):
+    case = Case(*sizes, seed=26)
+    y, saved = case.forward(moe, checkpoint)
+    check_forward(case, y, saved, moe)
+    check_backward(case, case.backward(moe, saved), saved, moe)
+
+
+def test_offsets_beyond_32_bits(moe):
+    """More than 2^31 values in each kept projection and in the products' results."""
+    T, H, I = 140_000, 256, 16384
+    case = Case(T, 1, 1, H, I, seed=27, dense=True)
+    y, saved = case.forward(moe)
+    d_x, d_gates, *_ = case.backward(moe, saved, need_weights=False)
+    rows = torch.cat([torch.arange(0, 3), torch.arange(131071, 131074), torch.arange(T - 40, T)]).cuda()
+    part = Case(len(rows), 1, 1, H, I, seed=27, dense=True)
+    part.W, part.x, part.d_out, part.gates = case.W, case.x[rows], case.d_out[rows], case.gates[rows]
+    kept = moe.SavedFfn(part.x, saved.gate[rows], saved.up[rows])
+    check_forward(part, y[rows], kept, moe)
+    want, _, _ = part.plain_backward(moe, kept)
+    assert plain.rel_rms(d_x[rows], want["d_x"]) <= REL_RMS_TOL
+    assert plain.rel_rms(d_gates[rows], want["d_gates"]) <= 2e-5
+
+
 def test_an_expert_twice_for_a_token(moe):
     """Two slots of one token at the same expert: both count."""
     case = Case(50, 4, 2, 256, 256, seed=19)
