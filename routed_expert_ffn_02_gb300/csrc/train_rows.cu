@@ -348,8 +348,9 @@ cudaError_t launch_plan_rows(const int32_t* offsets, int rows, int E, int most, 
 cudaError_t launch_forward_rows(const __nv_bfloat16* x, const int32_t* perm, int k, int H,
                                 const int32_t* offsets, int P, int E, int most, __nv_bfloat16* xs,
                                 const RowLists& l, WsHeader* hdr, int num_sms, cudaStream_t s) {
+    // (four times the resident blocks: 8192 tokens over 64 experts, forward, 2208 us; once, 2222)
     const int64_t want = ((int64_t)P + 7) / 8;
-    return launch_pdl(E <= kThreads ? forward_rows_kernel<1> : forward_rows_kernel<kMostPerThread>, dim3((unsigned)(want < 8 * num_sms ? want : 8 * num_sms)), dim3(kThreads), 0, s,
+    return launch_pdl(E <= kThreads ? forward_rows_kernel<1> : forward_rows_kernel<kMostPerThread>, dim3((unsigned)(want < 32 * num_sms ? want : 32 * num_sms)), dim3(kThreads), 0, s,
                       reinterpret_cast<const uint4*>(x), perm, k, H / 8, offsets, P, E, most,
                       reinterpret_cast<uint4*>(xs), l, hdr);
 }
