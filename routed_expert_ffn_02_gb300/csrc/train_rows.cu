@@ -192,6 +192,8 @@ forward_rows_kernel(const uint4* x, const int32_t* perm, int k, int vec, const i
 // however many slots it has (by sorted row, x and d of 16384 tokens do not fit
 // L2 together and were read from memory k times: 631 us at 16384 x 4096, k = 8;
 // 392 this way, 6.2 TB/s).
+// p: a position of the groups, off[0] <= p < off[E] (offsets that start above 0
+// leave positions before the first group, which have no padded row).
 __device__ __forceinline__ int64_t padded_row(const Groups& g, int E, int p) {
     int lo = 0, hi = E;          // the last group whose first row is not above p
     while (hi - lo > 1) {
@@ -218,9 +220,8 @@ backward_rows_kernel(BackwardRows q) {
         int64_t mine = -1;
         if (lane < q.k) {
             const int slot = (int)(t * q.k) + lane, p = ld::i32(q.inv_perm + slot);
-            if (p >= 0 && p < g.off[q.E] && ld::i32(q.perm + p) == slot) {
+            if (p >= g.off[0] && p < g.off[q.E] && ld::i32(q.perm + p) == slot)
                 mine = padded_row(g, q.E, p) * vec;
-            }
         }
         for (int i0 = lane; i0 - lane < vec; i0 += 32 * 4) {
             uint4 a[4], b[4];
@@ -252,7 +253,7 @@ backward_rows_kernel(BackwardRows q) {
     }
     // Positions that no slot holds (a routed index was skipped): zeros, lest what
     // the buffers held reach the weights' gradients of the last group.
-    for (int64_t p0 = warp * 32; p0 < g.off[q.E]; p0 += warps * 32) {
+    for (int64_t p0 = g.off[0] + warp * 32; p0 < g.off[q.E]; p0 += warps * 32) {
         const int p = (int)p0 + lane;
         bool none = false;
         if (p < g.off[q.E]) {
