@@ -96,7 +96,7 @@ __device__ void write_lists(Groups& g, int rows, int E, int most, const RowLists
     __syncthreads();
     for (int e = e0; e < e0 + kPerThread && e < E; ++e) {
         const int c = g.off[e + 1] - g.off[e], size = chunk_size(c, most);
-        if (size) atomicAdd(&at[size / per_class], (c + size - 1) / size);
+        if (size) atomicAdd(&at[size / per_class], chunk_count(c, size));
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -114,12 +114,13 @@ __device__ void write_lists(Groups& g, int rows, int E, int most, const RowLists
         RowChunk ch = {e, v, c, g.pad[e]};
         l.groups[e] = ch;
         if (!size) continue;
-        int to = atomicAdd(&at[size / per_class], (c + size - 1) / size);
-        for (int r = 0; r < c; r += size) {
+        const int n = chunk_count(c, size), to = atomicAdd(&at[size / per_class], n);
+        for (int i = 0; i < n; ++i) {
+            const int r = i * size;
             ch.row0 = v + r;
             ch.rows = min(size, c - r);
             ch.row0_pad = g.pad[e] + r;
-            l.chunks[to++] = ch;
+            l.chunks[to + i] = ch;
         }
     }
 }
