@@ -521,7 +521,9 @@ moe_status moe_expert_ffn_train(const moe_shape* shape, const moe_bf16* x, const
  *   gates [T, k] fp32 as moe_route wrote them, or NULL: all 1, and d_gates is
  *   NULL too.  d_x [T, H] bf16, d_gates [T, k] fp32 and the dW (bf16, in the
  *   matrices' layouts) written; d_x, d_gates, and the three dW together, may
- *   be NULL.  inv_perm as moe_permute wrote it.  Where moe_permute skipped a
+ *   be NULL.  inv_perm as moe_permute wrote it.  Offsets that do not ascend
+ *   from 0 to T*k set MOE_ERR_BAD_INDEX in the workspace status; rows of no
+ *   expert then add nothing to any gradient.  Where moe_permute skipped a
  *   routed index, d_gates and d_x of its token are unspecified.  ws:
  *   moe_expert_ffn_backward_workspace_size() bytes, initialised once with
  *   moe_workspace_init(). */

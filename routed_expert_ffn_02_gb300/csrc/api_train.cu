@@ -28,6 +28,7 @@ struct Lists {
 void take_lists(Carver* c, int64_t rows, int E, int most, Lists* l) {
     l->hdr = c->take<WsHeader>(1);
     l->l.n_chunks = c->take<int32_t>(1);
+    l->l.ends = c->take<int32_t>(2);
     l->l.groups = c->take<RowChunk>((size_t)E);
     l->l.chunks = c->take<RowChunk>((size_t)max_chunks(rows, E, most));
 }
@@ -261,7 +262,8 @@ moe_status moe_expert_ffn_backward(const moe_shape* shape, const moe_bf16* d_out
     }
     __nv_bfloat16* sums = d_x && !dense ? (__nv_bfloat16*)d_x : nullptr;
     if (sums || d_gates)
-        CUDA_TRY(launch_finish(b.dx, sums, b.parts, I / 32, d_gates, inv_perm, T, k, H, sms, s), "sums over slots");
+        CUDA_TRY(launch_finish(b.dx, sums, b.parts, I / 32, d_gates, inv_perm, dense ? nullptr : b.l.l.ends, T, k, H,
+                               sms, s), "sums over slots");
     return ok();
 }
 

@@ -98,6 +98,7 @@ struct RowLists {
     RowChunk* chunks;      // [max_chunks]
     RowChunk* groups;      // [E]
     int32_t* n_chunks;
+    int32_t* ends;         // [2]: the first group's first row, the last group's end
 };
 cudaError_t launch_plan_rows(const int32_t* offsets, int rows, int E, int most, const RowLists& l,
                              WsHeader* hdr, cudaStream_t s);
@@ -123,9 +124,10 @@ cudaError_t launch_backward_rows(const BackwardRows& q, int num_sms, cudaStream_
 
 // d_x[t] = sum_j y[inv[t * k + j]] (y fp32 [P, H]; d_x null: left out), and
 // d_gates[s] = sum over parts [n_parts, P] at position inv[s] (null: left out;
-// inv null: position s).  Positions outside [0, P) count as zeros.
+// inv null: position s).  Positions outside the groups (ends of the lists; null:
+// [0, P)) count as zeros.
 cudaError_t launch_finish(const float* y, __nv_bfloat16* d_x, const float* parts, int n_parts, float* d_gates,
-                          const int32_t* inv, int T, int k, int H, int num_sms, cudaStream_t s);
+                          const int32_t* inv, const int32_t* ends, int T, int k, int H, int num_sms, cudaStream_t s);
 
 // bf16 values of rows of e4m3 with a scale per 128 of K (exact).
 cudaError_t launch_dequantize_rows(const uint8_t* q, const uint8_t* scales, int64_t rows, int K,

@@ -107,6 +107,8 @@ __device__ void write_lists(Groups& g, int rows, int E, int most, const RowLists
             before += n;
         }
         *l.n_chunks = before;
+        l.ends[0] = g.off[0];
+        l.ends[1] = g.off[E];
     }
     __syncthreads();
     for (int e = e0; e < e0 + kPerThread && e < E; ++e) {
@@ -285,18 +287,21 @@ backward_rows_kernel(BackwardRows q) {
 // as well would make the rounding error of d_x 1.22 times as large (relative
 // RMS 2.9e-3 for 2.4e-3).  16384 x 4096, k = 8: 398 us, 5.7 TB/s.
 __global__ void __launch_bounds__(kThreads)
-finish_kernel(const float4* y, uint2* d_x, const float* parts, int n_parts, float* d_gates, const int32_t* inv, int T,
-              int k, int vec) {
+finish_kernel(const float4* y, uint2* d_x, const float* parts, int n_parts, float* d_gates, const int32_t* inv,
+              const int32_t* ends, int T, int k, int vec) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int64_t P = (int64_t)T * k;
+    // rows outside the groups (bad offsets) have no parts: what the workspace
+    // held of an earlier call stays out of the sums
+    const int64_t first = ends ? ld::i32(ends) : 0, end = ends ? ld::i32(ends + 1) : P;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
         if (d_gates && warp < k) {
             const int64_t s = t * k + warp;
             const int64_t p = inv ? ld::i32(inv + s) : s;
             float sum = 0.f;
-            if (p >= 0 && p < P)
+            if (p >= first && p < end)
                 for (int i = lane; i < n_parts; i += 32) sum += parts[(int64_t)i * P + p];
 #pragma unroll
             for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -306,8 +311,8 @@ finish_kernel(const float4* y, uint2* d_x, const float* parts, int n_parts, floa
         int64_t src[kMaxK];
 #pragma unroll
         for (int j = 0; j < kMaxK; ++j) {
-            const int p = j < k ? ld::i32(inv + t * k + j) : -1;
-            src[j] = p >= 0 && p < P ? (int64_t)p * vec : -1;
+            const int64_t p = j < k ? ld::i32(inv + t * k + j) : -1;
+            src[j] = p >= first && p < end ? p * vec : -1;
         }
         for (int v = threadIdx.x; v < vec; v += kThreads) {
             float4 r[kMaxK];
@@ -364,10 +369,10 @@ cudaError_t launch_backward_rows(const BackwardRows& q, int num_sms, cudaStream_
 }
 
 cudaError_t launch_finish(const float* y, __nv_bfloat16* d_x, const float* parts, int n_parts, float* d_gates,
-                          const int32_t* inv, int T, int k, int H, int num_sms, cudaStream_t s) {
+                          const int32_t* inv, const int32_t* ends, int T, int k, int H, int num_sms, cudaStream_t s) {
     const int blocks = T < 8 * num_sms ? T : 8 * num_sms;
     return launch_pdl(finish_kernel, dim3(blocks), dim3(kThreads), 0, s, reinterpret_cast<const float4*>(y),
-                      reinterpret_cast<uint2*>(d_x), parts, n_parts, d_gates, inv, T, k, H / 4);
+                      reinterpret_cast<uint2*>(d_x), parts, n_parts, d_gates, inv, ends, T, k, H / 4);
 }
 
 cudaError_t launch_dequantize_rows(const uint8_t* q, const uint8_t* scales, int64_t rows, int K,

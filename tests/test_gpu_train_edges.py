@@ -101,3 +101,21 @@ def test_offsets_that_are_no_offsets(moe, offsets, unmatched):  # noqa: F811
     if whole.any():
         assert plain.rel_rms(d_x[whole], want["d_x"][whole]) <= REL_RMS_TOL
         assert plain.rel_rms(d_gates[whole], want["d_gates"][whole]) <= 2e-5
+
+
+@pytest.mark.parametrize("unmatched", [False, True])
+@pytest.mark.parametrize("offsets", OFFSETS, ids=str)
+def test_rows_of_no_group_add_nothing(moe, offsets, unmatched):  # noqa: F811
+    """Gradients of tokens with slots outside the groups: those slots count as
+    zeros, whatever an earlier call left in the workspace."""
+    T, k = SIZES[0], SIZES[2]
+    _, saved = Case(*SIZES, seed=32).forward(moe)
+    case, ends, lost = lists_that_are_none(offsets, 32, unmatched)
+    ws, _ = guarded(moe, moe.expert_ffn_backward_workspace_size(moe.Shape(*SIZES)))
+    ws.tensor[256:].fill_(0xff)          # NaN, in bf16 and fp32
+    d_x, d_gates, *_ = case.backward(moe, saved, ws=ws)
+    assert ws.status() == MOE_ERR_BAD_INDEX
+    want, _, _ = plain_gradients(case, saved, ends, lost)
+    named = ~lost.view(T, k).any(1)
+    assert plain.rel_rms(d_x[named], want["d_x"][named]) <= REL_RMS_TOL
+    assert plain.rel_rms(d_gates[named], want["d_gates"][named]) <= 2e-5
