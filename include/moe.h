@@ -548,7 +548,7 @@ moe_status moe_dequantize_rows(const uint8_t* q, const uint8_t* scales, int32_t 
 typedef enum {
     MOE_ACT_NONE = 0,
     MOE_ACT_RELU = 1,
-    MOE_ACT_GELU = 2,   /* v times the normal distribution's mass below v (erf) */
+    MOE_ACT_GELU = 2,   /* v times the normal distribution's mass below v */
     MOE_ACT_SILU = 3
 } moe_activation;
 

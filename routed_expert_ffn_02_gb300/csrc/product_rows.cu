@@ -13,6 +13,7 @@
 // 7.6 (4.4 TB/s) / 11.0, two 7.3 / 11.0, three 8.3 / 11.1, four 13.5 / 11.1 (so
 // kFewRows is 3); one row: 16384 x 4096 21.5 (6.2 TB/s) / 23.8, 1024 x 16384
 // 10.0 / 16.6, 384 x 4096 2.7 / 7.2, 4096 x 512 2.5 / 5.3.
+#include "act_dev.cuh"
 #include "ld_dev.cuh"
 #include "ptx.cuh"
 #include "train.cuh"
@@ -34,7 +35,7 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
 __device__ __forceinline__ float activate(float v, int act) {
     switch (act) {
         case MOE_ACT_RELU: return v < 0.f ? 0.f : v;       // NaN stays
-        case MOE_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+        case MOE_ACT_GELU: return gelu(v);
         case MOE_ACT_SILU: return v / (1.f + __expf(-v));
         default: return v;
     }

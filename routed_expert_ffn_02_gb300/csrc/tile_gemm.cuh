@@ -46,6 +46,7 @@
 #include <cuda.h>
 #include <algorithm>
 
+#include "act_dev.cuh"
 #include "fp8.cuh"
 #include "moe_internal.cuh"
 #include "pair_dev.cuh"
@@ -738,7 +739,7 @@ __device__ __forceinline__ void activate(Frag& f, int act) {
         for (int i = 0; i < 32; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];       // NaN stays
     } else if (act == MOE_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.5f * v[i] * (1.f + erff(v[i] * 0.70710678118654752f));
+        for (int i = 0; i < 32; ++i) v[i] = gelu(v[i]);
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] *= sigmoid(v[i]);

@@ -1,5 +1,7 @@
 """GPU: the bf16 product at the ends of its ranges, against its plain 64-bit
 form with test_gpu_product's bounds."""
+import math
+
 import pytest
 import torch
 
@@ -30,3 +32,29 @@ def test_most_rows(moe, ends):  # noqa: F811
         part = slice(r, min(r + step, rows))
         inside = None if ends is None else torch.tensor(ends).clamp(r, part.stop) - r
         check(y[part], x[part], W, inside, b, "none", None)
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("by_bias", [False, True])
+@pytest.mark.parametrize("rows,K", [(1, 8), (3, 8), (4, 8), (24, 1024), (300, 72)])
+def test_gelu_keeps_its_digits(moe, rows, K, by_bias, out):  # noqa: F811
+    """Arguments that are exact (one term, or the bias alone), down to -12.5: the
+    relative error is that of the form in act_dev.cuh, at most 10.4 units of
+    2^-23 (its comment adds them up); a bf16 result is rounded once more."""
+    N = 1001
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows + K)
+    v = torch.rand((N, K), generator=g, device="cuda") * 12.49 - 12.5
+    v[::4] = v[::4] + 11                               # some of them positive
+    x = torch.zeros((rows, K), dtype=torch.bfloat16, device="cuda")
+    if by_bias:
+        W, b = torch.zeros((1, N, K), dtype=torch.bfloat16, device="cuda"), v[:, :1].t().contiguous()
+        at = v[:, :1].double().t().expand(rows, N)
+    else:
+        x[torch.arange(rows), torch.arange(rows) % K] = 1
+        W, b = v.to(torch.bfloat16)[None].contiguous(), None
+        at = W[0].double().t()[torch.arange(rows, device="cuda") % K]
+    y = moe.moe_grouped_gemm(x, W, bias=b, activation="gelu", out_dtype=out)
+    want = at * 0.5 * torch.special.erfc(-at * math.sqrt(0.5))      # (torch's ndtr cancels, in 64 bits too)
+    tol = 10.5 * 2.0 ** -23 + (2.0 ** -8 if out is torch.bfloat16 else 0.0)
+    assert ((y.double() - want).abs() <= tol * want.abs()).all(), ((y.double() - want) / want).abs().max()
