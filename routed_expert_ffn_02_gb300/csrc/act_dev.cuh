@@ -16,8 +16,10 @@ namespace moe {
 // Relative error in units of 2^-23: 2 for the hardware's 2^x; 3.5 for t (1 for
 // its reciprocal, half a unit for the argument, times the slope of ln R over
 // ln t, up to 2.3); 2.7 for p's coefficients and steps; half a unit each for
-// t p, 2^x's correction, Q and the result; 0.2 for the fit: at most 10.4.  A mass
-// below 2^-126 counts as none.
+// t p, 2^x's correction, Q and the result; 0.2 for the fit: at most 10.4 (3.4
+// measured).  A mass below 2^-126 (v < -12.9) keeps fewer digits, none from -13.2 on.
+// 16384 x 4096 x 4096 with gelu, bias and residual: 357 us; by erff 348, by
+// normcdff, as accurate, 385.  777 ragged rows of 650 x 1160: 19.9, 19.4 and 24.4.
 __device__ __forceinline__ float gelu(float v) {
     const float z = fminf(fabsf(v), 14.f);      // (2^x is 0 from 13.3 on)
     float t, e;
