@@ -5,6 +5,19 @@
 
 namespace moe {
 
+// 1 / (1 + exp(-g)) by the hardware's 2^x and reciprocal (2^-22 and one unit in
+// the last place), subnormals flushed (0 below -87.3); relative error at most
+// (3.5 + |g|) 2^-23, the argument's rounding included: __expf and __fdividef take twice the
+// instructions for them, which the epilogues feel (with fewer tests per value:
+// gradient of the projections at 1999 tokens 67.7 -> 62.0 us, 8-bit gate/up of
+// 65536 rows 1382 -> 1293).
+__device__ __forceinline__ float sigmoid(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
 // v Phi(v), Phi the normal distribution's mass below v.  (1 + erf(v / sqrt 2)) / 2
 // cancels for negative v (4% off at -5, zero from -5.6 on), so both sides use
 // the tail Q = Phi(-z), z = |v|: v Q below zero, v - v Q above.

@@ -36,7 +36,7 @@ __device__ __forceinline__ float activate(float v, int act) {
     switch (act) {
         case MOE_ACT_RELU: return v < 0.f ? 0.f : v;       // NaN stays
         case MOE_ACT_GELU: return gelu(v);
-        case MOE_ACT_SILU: return v / (1.f + __expf(-v));
+        case MOE_ACT_SILU: return v * sigmoid(v);
         default: return v;
     }
 }

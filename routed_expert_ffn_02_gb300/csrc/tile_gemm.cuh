@@ -227,17 +227,6 @@ struct Maps {
 __device__ __forceinline__ float scale_value(uint32_t b) {
     return __uint_as_float(b == 0 ? 1u << 22 : b == 255 ? 0x7fc00000u : b << 23);
 }
-// 1 / (1 + exp(-g)) by the hardware's 2^x and reciprocal (2^-22 and one unit in
-// the last place), subnormals flushed: __expf and __fdividef take twice the
-// instructions for them, which the epilogues feel (with fewer tests per value:
-// gradient of the projections at 1999 tokens 67.7 -> 62.0 us, 8-bit gate/up of
-// 65536 rows 1382 -> 1293).
-__device__ __forceinline__ float sigmoid(float g) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return r;
-}
 __device__ __forceinline__ float2 unpack(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }

@@ -58,3 +58,29 @@ def test_gelu_keeps_its_digits(moe, rows, K, by_bias, out):  # noqa: F811
     want = at * 0.5 * torch.special.erfc(-at * math.sqrt(0.5))      # (torch's ndtr cancels, in 64 bits too)
     tol = 10.5 * 2.0 ** -23 + (2.0 ** -8 if out is torch.bfloat16 else 0.0)
     assert ((y.double() - want).abs() <= tol * want.abs()).all(), ((y.double() - want) / want).abs().max()
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
+def test_an_activation_is_the_same_at_any_number_of_rows(moe, act):  # noqa: F811
+    """Arguments that are exact: the kernel of up to three rows, the split one
+    and the others give the same bits."""
+    N, K = 8192, 1024
+    v = torch.linspace(-90, 30, N, device="cuda")[None]
+    W = torch.zeros((1, N, K), dtype=torch.bfloat16, device="cuda")
+    out = [moe.moe_grouped_gemm(torch.zeros((rows, K), dtype=torch.bfloat16, device="cuda"), W, bias=v, activation=act,
+                                out_dtype=torch.float32) for rows in (1, 2, 3, 4, 40, 200)]
+    for y in out[1:]:
+        assert torch.equal(y, out[0][:1].expand_as(y))
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_silu_keeps_its_digits(moe, rows):  # noqa: F811
+    """Arguments that are exact, from -87 on: |v| 2^-23 for 2^x's argument (its
+    rounding and that of 1 / ln 2, half a unit each), 2^-22 for 2^x, 2^-24 for 1 + 2^x,
+    2^-23 for the reciprocal, 2^-24 for the product."""
+    v = torch.linspace(-87, 40, 8192, device="cuda")[None]
+    y = moe.moe_grouped_gemm(torch.zeros((rows, 64), dtype=torch.bfloat16, device="cuda"),
+                             torch.zeros((1, 8192, 64), dtype=torch.bfloat16, device="cuda"), bias=v, activation="silu",
+                             out_dtype=torch.float32)
+    want = v.double() * torch.sigmoid(v.double())
+    assert ((y.double() - want).abs() <= (4 + v.abs()) * 2.0 ** -23 * want.abs()).all()
