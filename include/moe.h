@@ -477,14 +477,17 @@ moe_status moe_balance_backward(const float* logits, const float* stats, const i
  *
  * What the forward call keeps, and the backward call reads (P = T * k sorted
  * rows).  fp8 == 0: gate, up [P, I] bf16 hold g = x W_gate^T and u = x W_up^T
- * rounded once, and x is the call's own input, which the caller keeps.
+ * rounded once, and x is the call's own input, which the caller keeps for the
+ * weights' gradients.
  * fp8 == 1 (8-bit checkpoints, about half the bytes): the same rows, and x
  * [T, H] by token, in e4m3 with a scale byte per block of 128 along the row,
  * in the format of the 8-bit experts; the scales are [P, I / 128] and
- * [T, H / 128].  With fp8 == 0 the scales are NULL.  Device pointers. */
+ * [T, H / 128].  With fp8 == 0 the scales are NULL.  A backward call without
+ * the weights' gradients (frozen experts) reads no x: x and x_scales may be NULL.
+ * Device pointers. */
 typedef struct {
     int32_t fp8;
-    void* x;             /* fp8: written by the forward call; else only read by the backward */
+    void* x;             /* fp8: written by the forward call; read by the backward for the dW */
     uint8_t* x_scales;
     void* gate;
     uint8_t* gate_scales;

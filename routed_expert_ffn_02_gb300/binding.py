@@ -804,25 +804,26 @@ class SavedFfn:
     """What moe_expert_ffn_train keeps for moe_expert_ffn_backward, by sorted
     row: the two projections gate, up [P, I], with x [T, H].  In bf16 (the
     scales are None; x is the call's own input), or in 8 bits: float8_e4m3fn
-    with scales [P, I/128] and [T, H/128] uint8."""
-    x: torch.Tensor
+    with scales [P, I/128] and [T, H/128] uint8.  A backward pass without the
+    weights' gradients does not read x: it may be None there."""
+    x: torch.Tensor | None
     gate: torch.Tensor
     up: torch.Tensor
     x_scales: torch.Tensor | None = None
     gate_scales: torch.Tensor | None = None
     up_scales: torch.Tensor | None = None
 
-    def ref(self, shape: Shape):
-        """The C structure, for a layer of these sizes."""
+    def ref(self, shape: Shape, need_x: bool = True):
+        """The C structure, for a layer of these sizes (need_x: with x)."""
         T, H, I = shape.T, shape.H, shape.I
         P = T * shape.k
         if self.gate_scales is None:
-            return ctypes.byref(MoeSaved(0, _in(self.x, _BF16, (T, H)), None, _in(self.gate, _BF16, (P, I)), None,
-                                         _in(self.up, _BF16, (P, I)), None))
+            x = _in(self.x, _BF16, (T, H)) if need_x else None
+            return ctypes.byref(MoeSaved(0, x, None, _in(self.gate, _BF16, (P, I)), None, _in(self.up, _BF16, (P, I)), None))
         rows = (P, I // 128)
-        return ctypes.byref(MoeSaved(
-            1, _in(self.x, _E4M3, (T, H)), _in(self.x_scales, _U8, (T, H // 128)), _in(self.gate, _E4M3, (P, I)),
-            _in(self.gate_scales, _U8, rows), _in(self.up, _E4M3, (P, I)), _in(self.up_scales, _U8, rows)))
+        x, x_scales = (_in(self.x, _E4M3, (T, H)), _in(self.x_scales, _U8, (T, H // 128))) if need_x else (None, None)
+        return ctypes.byref(MoeSaved(1, x, x_scales, _in(self.gate, _E4M3, (P, I)), _in(self.gate_scales, _U8, rows),
+                                     _in(self.up, _E4M3, (P, I)), _in(self.up_scales, _U8, rows)))
 
     @staticmethod
     def empty(shape: Shape, x: torch.Tensor, checkpoint: str = "bf16", stream=None) -> "SavedFfn":
@@ -880,7 +881,8 @@ def moe_expert_ffn_backward(shape: Shape, d_out, saved: SavedFfn, perm, offsets,
                             need_weights: bool = True, d_x=None, d_gates=None, dW=None,
                             ws: Workspace | None = None, stream=None):
     """Gradients of the layer's experts and gates from d_out [T, H] bf16, the
-    gradient of moe_combine's output (gates None: all 1).  Returns (d_x [T, H]
+    gradient of moe_combine's output (gates None: all 1); saved.x is read for the
+    weights' gradients only.  Returns (d_x [T, H]
     bf16, d_gates [T, k] fp32, dW_gate, dW_up, dW_down bf16); None in the place
     of what is not needed, and of d_gates without gates."""
     T, E, k, H, I = shape.T, shape.E, shape.k, shape.H, shape.I
@@ -898,7 +900,7 @@ def moe_expert_ffn_backward(shape: Shape, d_out, saved: SavedFfn, perm, offsets,
         dWd, wd = _out(given[2], down, _BF16, d_out, stream)
     ws = ws or Workspace(expert_ffn_backward_workspace_size(shape), d_out.device, stream)
     st = _lib.moe_expert_ffn_backward(
-        ctypes.byref(shape.c()), dp, _opt(gates, _F32, (T, k)), saved.ref(shape),
+        ctypes.byref(shape.c()), dp, _opt(gates, _F32, (T, k)), saved.ref(shape, need_weights),
         _opt(perm, _I32, (P,)), _opt(offsets, _I32, (E + 1,)), _opt(inv_perm, _I32, (P,)),
         _in(W_gate, _BF16, up), _in(W_up, _BF16, up), _in(W_down, _BF16, down),
         xp, gp, wg, wu, wd, ws.addr, ws.nbytes, _on(stream, d_out))

@@ -93,11 +93,12 @@ moe_status check_lists(const moe_shape* sh, const int32_t* perm, const int32_t* 
     return MOE_OK;
 }
 
+// need_x: the call reads or writes the record's x.
 moe_status check_saved(const moe_saved* v, bool need_x) {
     if (!v) return fail(MOE_ERR_INVALID_ARG, "saved is NULL");
     CHECK_PTR(v->gate); CHECK_PTR(v->up);
-    if (v->fp8 || need_x) CHECK_PTR(v->x);
-    if (v->fp8 && (!v->x_scales || !v->gate_scales || !v->up_scales))
+    if (need_x) CHECK_PTR(v->x);
+    if (v->fp8 && ((need_x && !v->x_scales) || !v->gate_scales || !v->up_scales))
         return fail(MOE_ERR_INVALID_ARG, "8-bit checkpoints without scales");
     return MOE_OK;
 }
@@ -138,7 +139,7 @@ moe_status moe_expert_ffn_train(const moe_shape* shape, const moe_bf16* x, const
     bool dense;
     STATUS_TRY(check_lists(shape, perm, offsets, &dense));
     CHECK_PTR(x); CHECK_PTR(W_gate); CHECK_PTR(W_up); CHECK_PTR(W_down); CHECK_PTR(y_sorted);
-    STATUS_TRY(check_saved(saved, false));
+    STATUS_TRY(check_saved(saved, saved && saved->fp8));
     FwdBufs b;
     STATUS_TRY(check_ws(ws, ws_bytes, carve_fwd(shape, nullptr, &b)));
     carve_fwd(shape, ws, &b);
@@ -206,7 +207,7 @@ moe_status moe_expert_ffn_backward(const moe_shape* shape, const moe_bf16* d_out
     if (d_gates && !gates) return fail(MOE_ERR_INVALID_ARG, "d_gates without gates");
     CHECK_PTR(d_out); CHECK_PTR(W_gate); CHECK_PTR(W_up); CHECK_PTR(W_down);
     if (d_x) CHECK_PTR(d_x);
-    STATUS_TRY(check_saved(saved, true));
+    STATUS_TRY(check_saved(saved, weights));
     BwdBufs b;
     STATUS_TRY(check_ws(ws, ws_bytes, carve_bwd(shape, nullptr, &b)));
     carve_bwd(shape, ws, &b);
@@ -214,16 +215,17 @@ moe_status moe_expert_ffn_backward(const moe_shape* shape, const moe_bf16* d_out
     const int64_t P = (int64_t)T * k, pad = padded_rows(P, E);
     const int nb = rows_per_cta(P, E), most = 2 * nb;
     const PdlScope pdl(overlap(shape, sms));
-    // x and d_out by sorted row: the caller's own where the block is dense
+    // x (for the weights' gradients alone) and d_out by sorted row: the caller's
+    // own where the block is dense
     const __nv_bfloat16 *x = (const __nv_bfloat16*)saved->x, *d = (const __nv_bfloat16*)d_out;
     const int64_t xd_rows = dense ? T : pad;
     if (!dense) {
         const BackwardRows q = {saved->x, saved->fp8 ? saved->x_scales : nullptr, d, perm, inv_perm, offsets,
-                                b.x, b.d, b.l.l, b.l.hdr, T, k, H, E, most};
+                                weights ? b.x : nullptr, b.d, b.l.l, b.l.hdr, T, k, H, E, most};
         CUDA_TRY(launch_backward_rows(q, sms, s), "sorted rows");
         x = b.x;
         d = b.d;
-    } else if (saved->fp8) {
+    } else if (saved->fp8 && weights) {
         CUDA_TRY(launch_dequantize_rows((const uint8_t*)saved->x, saved->x_scales, T, H, b.x, sms, s),
                  "dequantize rows");
         x = b.x;

@@ -109,7 +109,7 @@ cudaError_t launch_forward_rows(const __nv_bfloat16* x, const int32_t* perm, int
                                 const RowLists& l, WsHeader* hdr, int num_sms, cudaStream_t s);
 
 // Backward: the lists, and the padded rows of x (its values, where x_scales
-// says that it holds e4m3) and of d.
+// says that it holds e4m3; x_rows null: left out, x is not read) and of d.
 struct BackwardRows {
     const void* x;
     const uint8_t* x_scales;

@@ -207,7 +207,7 @@ __device__ __forceinline__ int64_t padded_row(const Groups& g, int E, int p) {
     return (int64_t)g.pad[lo] + (p - g.off[lo]);
 }
 
-template <int kPerThread>
+template <int kPerThread, bool kX>
 __global__ void __launch_bounds__(kThreads)
 backward_rows_kernel(BackwardRows q) {
     __shared__ Groups g;
@@ -218,6 +218,11 @@ backward_rows_kernel(BackwardRows q) {
     const int lane = threadIdx.x & 31, vec = q.H / 8;
     const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5),
                   warps = (int64_t)gridDim.x * (kThreads / 32);
+    const auto clear = [&](int64_t i) {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        if (kX) reinterpret_cast<uint4*>(q.x_rows)[i] = zero;
+        reinterpret_cast<uint4*>(q.d_rows)[i] = zero;
+    };
     for (int64_t t = warp; t < q.T; t += warps) {
         // lane j < k: the padded row of the token's slot j, -1 where it has none
         int64_t mine = -1;
@@ -232,10 +237,10 @@ backward_rows_kernel(BackwardRows q) {
             for (int j = 0; j < 4; ++j) {
                 const int i = i0 + 32 * j;
                 if (i < vec) {
-                    if (q.x_scales)
+                    if (kX && q.x_scales)
                         a[j] = widen8(reinterpret_cast<const uint2*>(q.x)[t * vec + i],
                                       scale_of(q.x_scales[t * (q.H / 128) + (i >> 4)]));
-                    else
+                    else if (kX)
                         a[j] = reinterpret_cast<const uint4*>(q.x)[t * vec + i];
                     b[j] = reinterpret_cast<const uint4*>(q.d)[t * vec + i];
                 }
@@ -247,7 +252,7 @@ backward_rows_kernel(BackwardRows q) {
                 for (int j = 0; j < 4; ++j) {
                     const int i = i0 + 32 * j;
                     if (i < vec) {
-                        reinterpret_cast<uint4*>(q.x_rows)[to + i] = a[j];
+                        if (kX) reinterpret_cast<uint4*>(q.x_rows)[to + i] = a[j];
                         reinterpret_cast<uint4*>(q.d_rows)[to + i] = b[j];
                     }
                 }
@@ -265,9 +270,7 @@ backward_rows_kernel(BackwardRows q) {
         }
         for (unsigned left = __ballot_sync(0xffffffffu, none); left; left &= left - 1) {
             const int64_t to = padded_row(g, q.E, (int)p0 + __ffs(left) - 1) * vec;
-            for (int i = lane; i < vec; i += 32)
-                reinterpret_cast<uint4*>(q.x_rows)[to + i] = reinterpret_cast<uint4*>(q.d_rows)[to + i] =
-                    make_uint4(0, 0, 0, 0);
+            for (int i = lane; i < vec; i += 32) clear(to + i);
         }
     }
     // The padding, a row per warp.
@@ -275,9 +278,7 @@ backward_rows_kernel(BackwardRows q) {
         const int e = (int)(i / 15), c = g.off[e + 1] - g.off[e];
         const int64_t row = (int64_t)g.pad[e] + c + i % 15;
         if (row >= g.pad[e + 1]) continue;
-        for (int v = lane; v < vec; v += 32)
-            reinterpret_cast<uint4*>(q.x_rows)[row * vec + v] = reinterpret_cast<uint4*>(q.d_rows)[row * vec + v] =
-                make_uint4(0, 0, 0, 0);
+        for (int v = lane; v < vec; v += 32) clear(row * vec + v);
     }
 }
 
@@ -365,7 +366,9 @@ cudaError_t launch_forward_rows(const __nv_bfloat16* x, const int32_t* perm, int
 cudaError_t launch_backward_rows(const BackwardRows& q, int num_sms, cudaStream_t s) {
     // a block per few tokens: few tokens are spread over blocks of their own
     const int64_t want = q.T < num_sms ? q.T : ((int64_t)q.T + 7) / 8 < num_sms ? num_sms : ((int64_t)q.T + 7) / 8;
-    return launch_pdl(q.E <= kThreads ? backward_rows_kernel<1> : backward_rows_kernel<kMostPerThread>, dim3((unsigned)(want < 8 * num_sms ? want : 8 * num_sms)), dim3(kThreads), 0, s, q);
+    const auto kernel = q.x_rows ? (q.E <= kThreads ? backward_rows_kernel<1, true> : backward_rows_kernel<kMostPerThread, true>)
+                                 : (q.E <= kThreads ? backward_rows_kernel<1, false> : backward_rows_kernel<kMostPerThread, false>);
+    return launch_pdl(kernel, dim3((unsigned)(want < 8 * num_sms ? want : 8 * num_sms)), dim3(kThreads), 0, s, q);
 }
 
 cudaError_t launch_finish(const float* y, __nv_bfloat16* d_x, const float* parts, int n_parts, float* d_gates,

@@ -119,3 +119,20 @@ def test_rows_of_no_group_add_nothing(moe, offsets, unmatched):  # noqa: F811
     named = ~lost.view(T, k).any(1)
     assert plain.rel_rms(d_x[named], want["d_x"][named]) <= REL_RMS_TOL
     assert plain.rel_rms(d_gates[named], want["d_gates"][named]) <= 2e-5
+
+
+@pytest.mark.parametrize("checkpoint", ["bf16", "fp8"])
+@pytest.mark.parametrize("sizes,dense", [((333, 6, 3, 256, 512), False), ((3, 300, 2, 256, 256), False), ((333, 1, 1, 512, 256), True)],
+                         ids=str)
+def test_frozen_experts_need_no_x(moe, sizes, dense, checkpoint):  # noqa: F811
+    """The gradients of x and of the gates do not depend on x: the same bits from
+    a record without it, over whatever the workspace held."""
+    case = Case(*sizes, seed=33, dense=dense)
+    _, saved = case.forward(moe, checkpoint)
+    want = case.backward(moe, saved)
+    saved.x = saved.x_scales = None
+    ws, sides = guarded(moe, moe.expert_ffn_backward_workspace_size(moe.Shape(*sizes)))
+    ws.tensor[256:].fill_(0xff)
+    got = case.backward(moe, saved, need_weights=False, ws=ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and got[2:] == (None,) * 3
+    assert ws.status() == 0 and all((v == 0x5a).all() for v in sides)

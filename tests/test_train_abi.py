@@ -85,6 +85,16 @@ def test_backward_reads_x_of_either_kind(moe):
     assert st == INVALID and "x is NULL" in said
 
 
+@pytest.mark.parametrize("kept", [dict(), dict(fp8=1, scales=GOOD, x_scales=None)])
+def test_backward_without_the_weights_gradients_needs_no_x(moe, kept):
+    st, said = backward(moe, kept=saved(moe, x=None, **kept), dW=(None,) * 3, ws=None)
+    assert st == WORKSPACE and "NULL" in said       # the next thing that is missing
+    st, said = backward(moe, kept=saved(moe, x=None, **kept), ws=None)
+    assert st == INVALID and "x is NULL" in said
+    st, said = backward(moe, kept=saved(moe, x=None, fp8=1, scales=GOOD, gate_scales=None), dW=(None,) * 3, ws=None)
+    assert st == INVALID and "without scales" in said
+
+
 def test_nothing_to_do(moe):
     """No token: no buffer is looked at (but the weights' gradients, which would be cleared)."""
     assert train(moe, shape=(0, 16, 2, 512, 256), x=None, y=None, kept=None, ws=None)[0] == 0
