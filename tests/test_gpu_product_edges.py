@@ -5,7 +5,8 @@ import math
 import pytest
 import torch
 
-from test_gpu_product import check, moe  # noqa: F401  (moe: the fixture)
+import train_plain as plain
+from test_gpu_product import check, make, moe  # noqa: F401  (moe: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,16 @@ def test_silu_keeps_its_digits(moe, rows):  # noqa: F811
                              out_dtype=torch.float32)
     want = v.double() * torch.sigmoid(v.double())
     assert ((y.double() - want).abs() <= (4 + v.abs()) * 2.0 ** -23 * want.abs()).all()
+
+
+@pytest.mark.parametrize("rows", [1, 3, 5, 40, 300])
+@pytest.mark.parametrize("K", [4096, 16392, 65536])
+def test_long_sums_lose_nothing(moe, rows, K):  # noqa: F811
+    """Beside the bound per element, which grows with K as the terms' magnitudes
+    do: over the whole result, K additions of at most 2^-23 of the sum so far (no
+    larger than the sum itself, in the mean over independent terms).  A block of
+    128 that is left out is sqrt(128 / K) of the result: six times the bound at
+    65536, more below."""
+    x, W, _, _, _ = make(rows, 1, 96, K, rows, False, False)
+    y = moe.moe_grouped_gemm(x, W, out_dtype=torch.float32)
+    assert plain.rel_rms(y, plain.product(x, W, None, None, "none", None)[0]) <= K * 2.0 ** -23
