@@ -26,14 +26,15 @@ __host__ __device__ inline int64_t max_chunks(int64_t P, int E, int most) { retu
 inline int64_t padded_rows(int64_t P, int E) { return (int64_t)align_up((size_t)P, 16) + 16 * (int64_t)E; }
 
 // A group of c rows in chunks of at most `most` rows (a multiple of 16):
-// ceil(c / most) of them, of equal size up to the rounding to 16.  Rounded up
-// from c - 1, so that nothing passes 32 bits at 2^31 - 129 rows.
+// ceil(c / most) of them, of equal size up to the rounding to 16.  Unsigned: a
+// group of 2^31 - 129 rows and its number of chunks add up to more than 2^31.
 __host__ __device__ inline int chunk_size(int c, int most) {
-    if (c <= 0) return 0;
-    const int n = (c - 1) / most + 1;
-    return ((c - 1) / n + 16) & ~15;
+    const uint32_t n = ((uint32_t)c + (uint32_t)most - 1) / (uint32_t)most;
+    return n == 0 ? 0 : (int)((((uint32_t)c + n - 1) / n + 15) & ~15u);
 }
-__host__ __device__ inline int chunk_count(int c, int size) { return c <= 0 ? 0 : (c - 1) / size + 1; }
+__host__ __device__ inline int chunk_count(int c, int size) {
+    return size == 0 ? 0 : (int)(((uint32_t)c + (uint32_t)size - 1) / (uint32_t)size);
+}
 
 // Rows of one group's chunks, for n_mtiles feature tiles on `pairs` CTA pairs.
 // An item costs about its rows, but no less than 128 (see kThinRows), and 16

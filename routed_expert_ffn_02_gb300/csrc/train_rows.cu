@@ -116,13 +116,12 @@ __device__ void write_lists(Groups& g, int rows, int E, int most, const RowLists
         RowChunk ch = {e, v, c, g.pad[e]};
         l.groups[e] = ch;
         if (!size) continue;
-        const int n = chunk_count(c, size), to = atomicAdd(&at[size / per_class], n);
-        for (int i = 0; i < n; ++i) {
-            const int r = i * size;
-            ch.row0 = v + r;
-            ch.rows = min(size, c - r);
-            ch.row0_pad = g.pad[e] + r;
-            l.chunks[to + i] = ch;
+        int to = atomicAdd(&at[size / per_class], chunk_count(c, size));
+        for (uint32_t r = 0; r < (uint32_t)c; r += (uint32_t)size) {
+            ch.row0 = v + (int)r;
+            ch.rows = min(size, c - (int)r);
+            ch.row0_pad = g.pad[e] + (int)r;
+            l.chunks[to++] = ch;
         }
     }
 }
@@ -295,12 +294,12 @@ finish_kernel(const float4* y, uint2* d_x, const float* parts, int n_parts, floa
     const int64_t P = (int64_t)T * k;
     // rows outside the groups (bad offsets) have no parts: what the workspace
     // held of an earlier call stays out of the sums
-    const int64_t first = ends ? ld::i32(ends) : 0, end = ends ? ld::i32(ends + 1) : P;
+    const int first = ends ? ld::i32(ends) : 0, end = ends ? ld::i32(ends + 1) : (int)P;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
         if (d_gates && warp < k) {
             const int64_t s = t * k + warp;
-            const int64_t p = inv ? ld::i32(inv + s) : s;
+            const int p = inv ? ld::i32(inv + s) : (int)s;
             float sum = 0.f;
             if (p >= first && p < end)
                 for (int i = lane; i < n_parts; i += 32) sum += parts[(int64_t)i * P + p];
@@ -312,8 +311,8 @@ finish_kernel(const float4* y, uint2* d_x, const float* parts, int n_parts, floa
         int64_t src[kMaxK];
 #pragma unroll
         for (int j = 0; j < kMaxK; ++j) {
-            const int64_t p = j < k ? ld::i32(inv + t * k + j) : -1;
-            src[j] = p >= first && p < end ? p * vec : -1;
+            const int p = j < k ? ld::i32(inv + t * k + j) : -1;
+            src[j] = p >= first && p < end ? (int64_t)p * vec : -1;
         }
         for (int v = threadIdx.x; v < vec; v += kThreads) {
             float4 r[kMaxK];
