@@ -728,7 +728,7 @@ __device__ __forceinline__ void activate(Frag& f, int act) {
         for (int i = 0; i < 32; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];       // NaN stays
     } else if (act == MOE_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = gelu(v[i]);
+        for (int i = 0; i < 32; i += 2) gelu2(v[i], v[i + 1]);
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] *= sigmoid(v[i]);
