@@ -82,6 +82,12 @@ size_t carve_bwd(const moe_shape* sh, void* ws, BwdBufs* b) {
     return align_up(c.off, 256);
 }
 
+// Lists and gates are read four bytes at a time (a slice of a longer list will do).
+#define CHECK_WORDS(p)                                                            \
+    do {                                                                          \
+        if (!aligned((p), 4)) return fail(MOE_ERR_INVALID_ARG, "%s is not 4-byte aligned", #p); \
+    } while (0)
+
 // Route lists given together, or a dense block.
 moe_status check_lists(const moe_shape* sh, const int32_t* perm, const int32_t* offsets, bool* dense) {
     *dense = !perm && !offsets;
@@ -90,6 +96,7 @@ moe_status check_lists(const moe_shape* sh, const int32_t* perm, const int32_t* 
     if (*dense && (sh->E != 1 || sh->k != 1))
         return fail(MOE_ERR_INVALID_ARG, "no route lists with E = %d, k = %d (a dense block has 1, 1)",
                     sh->E, sh->k);
+    CHECK_WORDS(perm); CHECK_WORDS(offsets);
     return MOE_OK;
 }
 
@@ -205,6 +212,7 @@ moe_status moe_expert_ffn_backward(const moe_shape* shape, const moe_bf16* d_out
     STATUS_TRY(check_lists(shape, perm, offsets, &dense));
     if (dense != !inv_perm) return fail(MOE_ERR_INVALID_ARG, "perm, offsets and inv_perm come together");
     if (d_gates && !gates) return fail(MOE_ERR_INVALID_ARG, "d_gates without gates");
+    CHECK_WORDS(inv_perm); CHECK_WORDS(gates); CHECK_WORDS(d_gates);
     CHECK_PTR(d_out); CHECK_PTR(W_gate); CHECK_PTR(W_up); CHECK_PTR(W_down);
     if (d_x) CHECK_PTR(d_x);
     STATUS_TRY(check_saved(saved, weights));
@@ -300,7 +308,7 @@ moe_status moe_grouped_gemm(const moe_bf16* x, int32_t rows, const int32_t* offs
     if (!offsets && E != 1) return fail(MOE_ERR_INVALID_ARG, "offsets is NULL with E = %d", E);
     if (rows == 0) return ok();
     CHECK_PTR(x); CHECK_PTR(W); CHECK_PTR(y);
-    if (!aligned(bias, 4)) return fail(MOE_ERR_INVALID_ARG, "bias is not 4-byte aligned");
+    CHECK_WORDS(offsets); CHECK_WORDS(bias);
     if (!aligned(residual, 2)) return fail(MOE_ERR_INVALID_ARG, "residual is not 2-byte aligned");
     Lists l;
     STATUS_TRY(check_ws(ws, ws_bytes, carve_product(rows, E, nullptr, &l)));

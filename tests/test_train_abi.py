@@ -95,6 +95,24 @@ def test_backward_without_the_weights_gradients_needs_no_x(moe, kept):
     assert st == INVALID and "without scales" in said
 
 
+@pytest.mark.parametrize("name", ["perm", "offsets"])
+def test_train_refuses_misaligned_lists(moe, name):
+    st, said = train(moe, **{name: ctypes.c_void_p(0x10002)}, ws=None)
+    assert st == INVALID and f"{name} is not 4-byte aligned" in said
+
+
+@pytest.mark.parametrize("name", ["perm", "offsets", "inv", "gates", "d_gates"])
+def test_backward_refuses_misaligned_lists_and_gates(moe, name):
+    st, said = backward(moe, **{name: ctypes.c_void_p(0x10002)}, ws=None)
+    assert st == INVALID and "is not 4-byte aligned" in said and name in said
+
+
+def test_product_refuses_misaligned_offsets(moe):
+    lib = moe.binding.raw_lib()
+    assert lib.moe_grouped_gemm(GOOD, 5, ctypes.c_void_p(0x10002), 3, 40, 64, GOOD, None, 0, None, GOOD, 0, None, 0, None) == INVALID
+    assert "offsets is not 4-byte aligned" in lib.moe_last_error().decode()
+
+
 def test_nothing_to_do(moe):
     """No token: no buffer is looked at (but the weights' gradients, which would be cleared)."""
     assert train(moe, shape=(0, 16, 2, 512, 256), x=None, y=None, kept=None, ws=None)[0] == 0
