@@ -470,7 +470,9 @@ moe_status moe_balance_backward(const float* logits, const float* stats, const i
 
 /* The experts' gated feed-forward block with what its backward pass needs, and
  * that pass: the gradients of x, of the router's gates and of the three
- * matrices.  The pages do not train their model.  Both calls work on the
+ * matrices.  The pages do not train their model.  Nothing records a graph: the
+ * caller makes the backward call, and adds the dW up where steps accumulate.
+ * perm, offsets, inv_perm, gates and d_gates need 4-byte alignment.  Both calls work on the
  * routed layer, or on a dense block (a shared expert): perm and offsets (and
  * inv_perm) NULL with E = 1 and k = 1, whose sorted rows are the rows of x.
  * The shape's fat_threshold and thin_mma_min do not apply.
@@ -498,7 +500,8 @@ typedef struct {
 /* Forward: for sorted position p of expert e and token t
  *   g = W_gate[e] . x[t],  u = W_up[e] . x[t],
  *   y_sorted[p] = bf16( W_down[e] . bf16( silu(g) * u ) )
- * with fp32 accumulation, g and u in `saved`.  perm, offsets as moe_permute
+ * with fp32 accumulation (tensor cores, whose additions truncate), the sigmoid
+ * within (3.5 + |g|) * 2^-23 of its value and 0 below -87.3, g and u in `saved`.  perm, offsets as moe_permute
  * wrote them.  Offsets that do not ascend from 0 to T*k set MOE_ERR_BAD_INDEX
  * in the workspace status; rows of no expert are then not written.  ws:
  * moe_expert_ffn_train_workspace_size() bytes, initialised once with
@@ -561,13 +564,16 @@ typedef enum {
 /* Grouped bf16 product with bias, activation and residual: for the rows
  * offsets[e] <= p < offsets[e + 1] of group e
  *   y[p, n] = act( sum_k x[p, k] W[e, n, k] + bias[e, n] ) + residual[p, n]
- * in fp32, rounded once where y is bf16.  A router's logits are E = 1 with
- * fp32 y; a shared expert's down product takes the routed output as residual.
- *   x [rows, K] bf16; W [E, N, K] bf16; offsets [E + 1] ascending from 0 to
+ * in fp32, rounded once where y is bf16 (four rows and more on the tensor
+ * cores, whose additions truncate: fp32 results of random terms are off by about
+ * 1e-9 K of their size, 4e-6 at K = 4096; up to three rows 1e-7).  A router's logits are E = 1 with fp32 y; a projection adds another
+ * path's output as its residual.  There is no backward form of this product.
+ *   rows: at most 2^31 - 129; x [rows, K] bf16; W [E, N, K] bf16; offsets [E + 1] ascending from 0 to
  *   rows (groups may be empty), or NULL with E = 1; bias [E, N] fp32 or NULL;
  *   residual [rows, N] bf16 or NULL; y [rows, N] bf16 (y_fp32 == 0) or fp32,
  *   may be the residual itself when bf16.  K: a positive multiple of 8 and N:
- *   positive, each at most 65536; E <= 1024, E * N < 2^31.  ws:
+ *   positive, each at most 65536; E <= 1024, E * N < 2^31.  offsets and bias
+ *   need 4-byte, the residual 2-byte alignment.  ws:
  *   moe_grouped_gemm_workspace_size() bytes, initialised once with
  *   moe_workspace_init().  Offsets that are not as stated set
  *   MOE_ERR_BAD_INDEX in the workspace status; rows of no group are then not
