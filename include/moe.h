@@ -472,10 +472,10 @@ moe_status moe_balance_backward(const float* logits, const float* stats, const i
  * that pass: the gradients of x, of the router's gates and of the three
  * matrices.  The pages do not train their model.  Nothing records a graph: the
  * caller makes the backward call, and adds the dW up where steps accumulate.
- * perm, offsets, inv_perm, gates and d_gates need 4-byte alignment.  Both calls work on the
- * routed layer, or on a dense block (a shared expert): perm and offsets (and
- * inv_perm) NULL with E = 1 and k = 1, whose sorted rows are the rows of x.
- * The shape's fat_threshold and thin_mma_min do not apply.
+ * Both calls work on the routed layer, or on a dense block (a shared expert):
+ * perm and offsets (and inv_perm) NULL with E = 1 and k = 1, whose sorted rows
+ * are the rows of x.  perm, offsets, inv_perm, gates and d_gates need 4-byte
+ * alignment.  The shape's fat_threshold and thin_mma_min do not apply.
  *
  * What the forward call keeps, and the backward call reads (P = T * k sorted
  * rows).  fp8 == 0: gate, up [P, I] bf16 hold g = x W_gate^T and u = x W_up^T
@@ -501,9 +501,10 @@ typedef struct {
  *   g = W_gate[e] . x[t],  u = W_up[e] . x[t],
  *   y_sorted[p] = bf16( W_down[e] . bf16( silu(g) * u ) )
  * with fp32 accumulation (tensor cores, whose additions truncate), the sigmoid
- * within (3.5 + |g|) * 2^-23 of its value and 0 below -87.3, g and u in `saved`.  perm, offsets as moe_permute
- * wrote them.  Offsets that do not ascend from 0 to T*k set MOE_ERR_BAD_INDEX
- * in the workspace status; rows of no expert are then not written.  ws:
+ * within (3.5 + |g|) * 2^-23 of its value and 0 below -87.3, g and u in `saved`.
+ * perm, offsets as moe_permute wrote them.  Offsets that do not ascend from 0 to
+ * T*k set MOE_ERR_BAD_INDEX in the workspace status; rows of no expert are then
+ * not written.  ws:
  * moe_expert_ffn_train_workspace_size() bytes, initialised once with
  * moe_workspace_init(). */
 size_t moe_expert_ffn_train_workspace_size(const moe_shape* shape);
@@ -564,12 +565,14 @@ typedef enum {
 /* Grouped bf16 product with bias, activation and residual: for the rows
  * offsets[e] <= p < offsets[e + 1] of group e
  *   y[p, n] = act( sum_k x[p, k] W[e, n, k] + bias[e, n] ) + residual[p, n]
- * in fp32, rounded once where y is bf16 (four rows and more on the tensor
- * cores, whose additions truncate: fp32 results of random terms are off by about
- * 1e-9 K of their size, 4e-6 at K = 4096; up to three rows 1e-7).  A router's logits are E = 1 with fp32 y; a projection adds another
- * path's output as its residual.  There is no backward form of this product.
- *   rows: at most 2^31 - 129; x [rows, K] bf16; W [E, N, K] bf16; offsets [E + 1] ascending from 0 to
- *   rows (groups may be empty), or NULL with E = 1; bias [E, N] fp32 or NULL;
+ * in fp32, rounded once where y is bf16.  A router's logits are E = 1 with
+ * fp32 y; a projection adds another path's output as its residual.  There is no
+ * backward form.  Tensor cores truncate in their additions: fp32 results of
+ * random terms are off by about 1e-9 K of their size (4e-6 at K = 4096); up to
+ * three rows without offsets, on the CUDA cores, by 1e-7.
+ *   rows: at most 2^31 - 129; x [rows, K] bf16; W [E, N, K] bf16; offsets
+ *   [E + 1] ascending from 0 to rows (groups may be empty), or NULL with E = 1;
+ *   bias [E, N] fp32 or NULL;
  *   residual [rows, N] bf16 or NULL; y [rows, N] bf16 (y_fp32 == 0) or fp32,
  *   may be the residual itself when bf16.  K: a positive multiple of 8 and N:
  *   positive, each at most 65536; E <= 1024, E * N < 2^31.  offsets and bias
